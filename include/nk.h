@@ -92,6 +92,7 @@ typedef enum {
                                        operands by powers of two, so no finite bf16 input
                                        leaves their range); rk8v4 append: a group scale
                                        saturated at the fp16 maximum, or a non-finite value */
+#define NK_DEVFLAG_NO_PAGES 0x20u   /* nk_step_tables: the free list is shorter than the step needs */
 
 /* Limits of the library. */
 #define NK_GROUP 64      /* channels per quantization group */
@@ -249,6 +250,94 @@ int nk_decode_step_host(const nk_kv_pool* pool, const int32_t* block_table_dev, 
  * bytes. Returns the total size in bytes (0 for an invalid shape). */
 size_t nk_step_host_layout(int32_t B, int32_t total_new, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
                            int32_t head_dim, size_t offsets[6]);
+
+/*
+ * What a serving step computes around its append and attention. These four
+ * (nk_step_tables, nk_mrope, nk_paged_window_attn, nk_paged_chunk_attn) have no
+ * counterpart on the pages; they follow from the formulas given with each.
+ *
+ * nk_step_tables -- the block tables, slot map and lengths of a step, built on
+ * the GPU from the requests' lengths and a list of free pages.
+ *   start_pos_dev  int32 [B]: tokens sequence b already holds; its pages
+ *                  block_table[b][0 .. ceil(start / P) - 1] are assigned.
+ *   new_lens_dev   int32 [B]: tokens it brings in this step (0 allowed).
+ *   free_pages_dev int32 [num_free]: pages to hand out, each listed once.
+ *   block_table_dev int32 [B][max_pages_per_seq], updated in place: entries
+ *                  ceil(start / P) .. ceil((start + new) / P) - 1 of sequence b
+ *                  take the next pages of the free list, sequence after
+ *                  sequence; every other entry stays as it was.
+ *   cu_new_dev     int32 [B+1]: exclusive prefix of the new lengths (the
+ *                  cu_new of nk_kv_append, the cu_q of nk_paged_chunk_attn).
+ *   ctx_lens_dev   int32 [B]: start + new.
+ *   slot_map_dev   int64 [max_rows]: pool slot page * P + offset of new row
+ *                  j = cu_new[b] + t, -1 where it has none.
+ *   positions_dev  int32 [max_rows] or NULL: the row's position start + t.
+ *   used_pages_dev int32 [1] or NULL: pages of the free list the step needs.
+ * Rows from cu_new[B] on stay as they were, so buffers (and a captured graph)
+ * may be sized for the largest step. start and new of a sequence that are
+ * negative or pass the table set NK_DEVFLAG_BAD_POS: it gets no page, context
+ * length 0, slots -1 and positions -1, and its rows still count in cu_new. A
+ * free list that is too short sets NK_DEVFLAG_NO_PAGES: the entries and slots
+ * past its end are -1, and used_pages says what was needed. A page id outside
+ * the pool sets NK_DEVFLAG_BAD_PAGE and gives -1. 2^31 - 1 new rows or more in
+ * all set NK_DEVFLAG_BAD_POS and assign nothing. More rows than max_rows set
+ * NK_DEVFLAG_BAD_POS; the first max_rows are written. B is at most 1,024. The
+ * outputs must not overlap the inputs (block_table_dev but for the update).
+ * The same call on the same start_pos writes the same results.
+ */
+int nk_step_tables(int32_t page_size, int32_t num_pages, const int32_t* start_pos_dev, const int32_t* new_lens_dev,
+                   int32_t B, const int32_t* free_pages_dev, int32_t num_free, int32_t* block_table_dev,
+                   int32_t max_pages_per_seq, int32_t* cu_new_dev, int32_t* ctx_lens_dev, int64_t* slot_map_dev,
+                   int32_t* positions_dev, int32_t max_rows, int32_t* used_pages_dev, int32_t* status_dev,
+                   void* stream);
+
+/*
+ * nk_mrope -- rotary positions with several axes (time, height, width, ...) on
+ * the query and key rows of a step, before the append takes the keys.
+ *   q_dev, k_dev    bf16 rows of num_q_heads (num_kv_heads) heads of head_dim,
+ *                   consecutive within a row; rows are *_row_stride elements
+ *                   apart (slices of a fused projection need no copy). Either
+ *                   head count may be 0 (that pair of pointers is not read).
+ *   q_out_dev, k_out_dev  results, with their own row strides; may be the
+ *                   inputs themselves (same stride), else must not overlap.
+ *   positions_dev   int32 [num_axes][positions_stride]: row j has position
+ *                   positions[a][j] on axis a (1 to 4 axes; any int32).
+ *   inv_freq_host   double [half]: radians per position of frequency i, on the
+ *                   host, read during the call.
+ *   sections_host   int32 [num_axes] on the host; half = their sum, a multiple
+ *                   of 8 with 2 * half <= head_dim. Frequency i belongs to the
+ *                   axis whose run of sections[a] frequencies it falls in, or,
+ *                   with `interleaved`, to axis i mod num_axes as long as
+ *                   i < num_axes * sections[that axis], else to axis 0.
+ *   num_rows_dev    int32 [1] or NULL: rows from *num_rows_dev on stay as they
+ *                   were (cu_new + B of nk_step_tables).
+ * With angle = positions[axis(i)][j] * inv_freq[i], channels i and i + half of
+ * every head become (a cos - b sin, b cos + a sin), in fp32 from an angle that
+ * is exact to 2^-23 turns at any position, rounded once to bf16; channels
+ * 2 * half and up are copied. Pointers 16-byte aligned, strides multiples of 8,
+ * head_dim a multiple of 8 (16 .. 256).
+ */
+int nk_mrope(const void* q_dev, const void* k_dev, void* q_out_dev, void* k_out_dev, int64_t q_row_stride,
+             int64_t k_row_stride, int64_t q_out_row_stride, int64_t k_out_row_stride, int32_t rows,
+             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const int32_t* positions_dev,
+             int64_t positions_stride, const double* inv_freq_host, const int32_t* sections_host, int32_t num_axes,
+             int32_t interleaved, const int32_t* num_rows_dev, void* stream);
+
+/*
+ * nk_paged_window_attn -- nk_paged_decode_attn over a sliding window with
+ * sinks: the query at position p (p = ctx_len - T + t for column t) sees key
+ * n <= p when n > p - window or n < sinks. window >= 1 (1: the token itself),
+ * sinks >= 0. Arguments, checks, workspace (nk_decode_workspace_bytes), device
+ * flags, ordering and ownership as nk_paged_decode_attn. Only the pages that
+ * hold a visible key are read, and only their block-table entries: the pages
+ * between the sinks and the window may have been given back. They run on the
+ * mma.sync kernel; a window of at least max_ctx is nk_paged_decode_attn itself.
+ */
+int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
+                         int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, int32_t B, int32_t T,
+                         int32_t num_q_heads, float sm_scale, int32_t max_ctx, int32_t window, int32_t sinks,
+                         int32_t num_ctas, void* workspace_dev, size_t workspace_bytes, void* out_dev,
+                         int32_t* status_dev, void* stream);
 
 /* Same contract and result, computed by the fp32 CUDA-core kernel that the
  * tensor-core path is measured against. */

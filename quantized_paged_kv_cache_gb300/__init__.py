@@ -18,6 +18,7 @@ NK_DEVFLAG_BAD_POS = 0x2
 NK_DEVFLAG_BAD_CTX = 0x4
 NK_DEVFLAG_TIMEOUT = 0x8
 NK_DEVFLAG_RANGE = 0x10
+NK_DEVFLAG_NO_PAGES = 0x20
 GROUP = 64
 MAX_T = 16
 
@@ -27,6 +28,7 @@ __all__ = [
     "attn_combine", "status_string", "decode_step", "rk8v4_chunk_bytes", "rk8v4_pool_bytes", "rk8v4_append",
     "rk8v4_decode_attn", "i8f16_chunk_bytes", "i8f16_pool_bytes", "i8f16_append", "i8f16_decode_attn",
     "bf16kv_chunk_bytes", "bf16kv_pool_bytes", "bf16kv_append", "bf16kv_decode_attn", "test_inject_copy_stall", "paged_prefill_attn",
+    "step_tables", "mrope", "paged_window_attn",
 ]
 
 
@@ -368,4 +370,111 @@ def paged_prefill_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, 
                                      _ptr(ctx_lens), B, T, Hq, float(sm_scale), int(max_ctx), _ptr(out), _ptr(status),
                                      _stream(stream))
     _check(rc, "nk_paged_prefill_attn")
+    return out
+
+
+def _need_dtype(dtype, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
+
+
+def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map,
+                positions=None, used=None, status=None, stream=None) -> None:
+    """The block tables, slot map and lengths of a step from its requests'
+    lengths and a list of free pages (nk_step_tables): ``block_table`` int32
+    [B][max_pages] is updated in place; ``cu_new`` int32 [B+1], ``ctx_lens``
+    int32 [B], ``slot_map`` int64 [max_rows], ``positions`` int32 [max_rows]
+    and ``used`` int32 [1] are written."""
+    import torch
+
+    _need_cuda(start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map, positions, used, status)
+    _need_dtype(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
+    _need_dtype(torch.int64, slot_map)
+    B, rows = start_pos.numel(), slot_map.numel()
+    if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or block_table.dim() != 2 \
+            or block_table.shape[0] != B:
+        raise ValueError("start_pos, new_lens, ctx_lens and block_table hold one entry (row) per sequence, cu_new one more")
+    if positions is not None and positions.numel() < rows:
+        raise ValueError("positions must hold an entry for every one of slot_map")
+    rc = lib().nk_step_tables(page_size, num_pages, _ptr(start_pos), _ptr(new_lens), B, _ptr(free_pages),
+                              free_pages.numel(), _ptr(block_table), block_table.shape[1], _ptr(cu_new),
+                              _ptr(ctx_lens), _ptr(slot_map), _ptr(positions), rows, _ptr(used), _ptr(status),
+                              _stream(stream))
+    _check(rc, "nk_step_tables")
+
+
+def _rows(t, what: str):
+    """(heads, head_dim, row stride) of [rows][heads][head_dim] bf16 rows whose heads are consecutive."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a row of {what} must be consecutive")
+    return h, d, (t.stride(0) if n > 1 else h * d)
+
+
+def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=None, k_out=None, num_rows=None,
+          stream=None):
+    """Rotary positions with several axes on query and key rows (nk_mrope):
+    ``q`` bf16 [rows][Hq][D] and ``k`` [rows][Hkv][D] (rows may be strided),
+    ``positions`` int32 [axes][rows], ``inv_freq`` float64 [half] on the host,
+    ``sections`` the frequencies of each axis. Returns (q_out, k_out); pass
+    q and k themselves to rotate in place."""
+    import torch
+
+    rows = q.shape[0]
+    if k.shape[0] != rows or k.shape[2] != q.shape[2]:
+        raise ValueError("q and k must have the same rows and head_dim")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    _need_dtype(torch.bfloat16, q, k, q_out, k_out)
+    _need_cuda(positions, num_rows)
+    _need_dtype(torch.int32, positions, num_rows)
+    if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 host tensor")
+    sections = tuple(int(x) for x in sections)
+    if positions.dim() != 2 or positions.shape[0] != len(sections) or positions.shape[1] < rows:
+        raise ValueError("positions must hold one row of positions per section (axis)")
+    if inv_freq.numel() != sum(sections):
+        raise ValueError("inv_freq must hold one frequency for every one of the sections")
+    Hq, D, qs = _rows(q, "q")
+    Hkv, _, ks = _rows(k, "k")
+    qos, kos = _rows(q_out, "q_out")[2], _rows(k_out, "k_out")[2]
+    rc = lib().nk_mrope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), qs, ks, qos, kos, rows, Hq, Hkv, D,
+                        _ptr(positions), positions.shape[1], inv_freq.data_ptr(),
+                        (ctypes.c_int32 * len(sections))(*sections), len(sections), int(bool(interleaved)),
+                        _ptr(num_rows), _stream(stream))
+    _check(rc, "nk_mrope")
+    return q_out, k_out
+
+
+def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, max_ctx: int, window: int,
+                      sinks: int = 0, num_ctas: int = 0, workspace=None, out=None, status=None, stream=None):
+    """Decode / verify attention over a sliding window and the first ``sinks``
+    tokens (nk_paged_window_attn); returns out bf16 [B][T][Hq][D]."""
+    import torch
+
+    _need_cuda(q, block_table, ctx_lens, workspace, out, status)
+    pool.need("int8")
+    B, T, Hq, D = q.shape
+    if D != pool.head_dim or block_table.shape[0] != B or ctx_lens.numel() != B:
+        raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
+    _need_dtype(torch.bfloat16, q, out)
+    _need_dtype(torch.int32, block_table, ctx_lens, status)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        nbytes = decode_workspace_bytes(B, T, Hq, pool.num_kv_heads, D, num_ctas)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+    ps = pool.c_struct()
+    wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_paged_window_attn(ctypes.byref(ps), _ptr(q), _ptr(block_table), block_table.shape[-1],
+                                    _ptr(ctx_lens), B, T, Hq, float(sm_scale), max_ctx, window, sinks, num_ctas,
+                                    _ptr(workspace), wbytes, _ptr(out), _ptr(status), _stream(stream))
+    _check(rc, "nk_paged_window_attn")
     return out

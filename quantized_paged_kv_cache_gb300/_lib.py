@@ -65,6 +65,9 @@ EXPORTS = (
     "nk_version",
     "nk_test_inject_copy_stall",
     "nk_paged_prefill_attn",
+    "nk_step_tables",
+    "nk_mrope",
+    "nk_paged_window_attn",
 )
 
 
@@ -114,6 +117,13 @@ def lib() -> ctypes.CDLL:
                     fn.argtypes, fn.restype = args, res
             L.nk_paged_prefill_attn.argtypes = [pool_p, P, P, I32, P, I32, I32, I32, F, I32, P, P, P]
             L.nk_paged_prefill_attn.restype = ctypes.c_int
+            L.nk_step_tables.argtypes = [I32, I32, P, P, I32, P, I32, P, I32, P, P, P, P, I32, P, P, P]
+            L.nk_step_tables.restype = ctypes.c_int
+            I64 = ctypes.c_int64
+            L.nk_mrope.argtypes = [P, P, P, P, I64, I64, I64, I64, I32, I32, I32, I32, P, I64, P, P, I32, I32, P, P]
+            L.nk_mrope.restype = ctypes.c_int
+            L.nk_paged_window_attn.argtypes = [pool_p, P, P, I32, P, I32, I32, I32, F, I32, I32, I32, I32, P, Z, P, P, P]
+            L.nk_paged_window_attn.restype = ctypes.c_int
             L.nk_attn_combine.argtypes = [P, P, I32, I32, I32, P, P]
             L.nk_attn_combine.restype = ctypes.c_int
             L.nk_status_string.argtypes, L.nk_status_string.restype = [ctypes.c_int], ctypes.c_char_p

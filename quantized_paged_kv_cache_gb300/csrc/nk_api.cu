@@ -58,6 +58,15 @@ int64_t max_items(int32_t B, int32_t Hkv, int32_t max_ctx, int32_t P) {
   return (int64_t)B * Hkv * ((max_ctx + P - 1) / P);
 }
 
+// Keys of a sequence in pages that the T columns of a call can see, at most:
+// all of them, or those in the pages of a sliding window (its W + T - 1
+// positions touch at most one page more than they fill) and of the sinks.
+int32_t visible_keys(int32_t max_ctx, int32_t P, int32_t T, int32_t window, int32_t sinks) {
+  if (window < 1) return max_ctx;
+  const int64_t pages = ((int64_t)window + T - 1 + P - 2) / P + 1 + ((int64_t)sinks + P - 1) / P;
+  return pages * P < max_ctx ? (int32_t)(pages * P) : max_ctx;
+}
+
 int32_t default_ctas(int32_t B, int32_t Hkv, int32_t max_ctx, int32_t P, int per_sm) {
   const int sms = sm_count();
   // at most two CTAs per SM: the default workspace size assumes that bound
@@ -106,7 +115,8 @@ int chunk_cols(bool simt, int fmt, int D, int T, int G, int P) {
 // kernels on a pool of the pages' INT8 layout (fp16 scales) or of bf16 rows,
 // or on an rk8v4 pool the tensor-core kernel (up to 32 rows per kv-head) or
 // the rk8v4 CUDA-core kernel.
-enum class Path { kTensor, kSimt, kRk8v4, kTensorF16, kBf16 };
+// A sliding window (kWindow) runs on the mma.sync kernel's window instances.
+enum class Path { kTensor, kSimt, kRk8v4, kTensorF16, kBf16, kWindow };
 
 int path_fmt(Path path) {
   switch (path) {
@@ -118,13 +128,30 @@ int path_fmt(Path path) {
 }
 
 // the paths on the tensor-core kernels (tcgen05 / mma.sync)
-bool tensor_path(Path path) { return path == Path::kTensor || path == Path::kTensorF16 || path == Path::kBf16; }
+bool tensor_path(Path path) {
+  return path == Path::kTensor || path == Path::kTensorF16 || path == Path::kBf16 || path == Path::kWindow;
+}
+
+// columns per launch of a call on `path`
+int cols_of(Path path, int fmt, int D, int T, int G, int P) {
+  if (path != Path::kWindow) return chunk_cols(!tensor_path(path), fmt, D, T, G, P);
+  int c = 48 / G;
+  if (c < 1) c = 1;
+  if (c > T) c = T;
+  while (c > 1 && !decode_mma_supported(fmt, D, c, G, P)) --c;
+  return c;
+}
+
+// whether a launch of T columns runs on the tcgen05 kernel
+bool on_tc(Path path, int fmt, int D, int T, int G, int P) {
+  return path != Path::kWindow && decode_tc_supported(fmt, D, T, G, P);
+}
 
 // Checks the decode arguments and fills `p`; *empty = nothing to launch.
 int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int32_t max_pages, const int32_t* ctx,
                    int32_t B, int32_t T, int32_t Hq, float sm_scale, int32_t max_ctx, int32_t num_ctas,
                    void* workspace, size_t workspace_bytes, void* out, int32_t* status, Path path, DecodeParams* pp,
-                   bool* empty) {
+                   bool* empty, int32_t window = 0, int32_t sinks = 0) {
   const bool simt = !tensor_path(path);
   *empty = true;
   int err = NK_OK;
@@ -140,17 +167,18 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   if (!isfinite(sm_scale)) return NK_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(out, 16)) return NK_ERR_SHAPE;
   const int fmt = path_fmt(path);
-  const int Tc = chunk_cols(simt, fmt, D, T, G, P);
+  const int Tc = cols_of(path, fmt, D, T, G, P);
   const bool rk_tc = path == Path::kRk8v4 && decode_mma_supported(fmt, D, Tc, G, P);
   if (simt && !rk_tc) {
     if (G > 8) return NK_ERR_UNSUPPORTED;
   } else if (!rk_tc) {
-    if (!decode_tc_supported(fmt, D, Tc, G, P) && !decode_mma_supported(fmt, D, Tc, G, P)) return NK_ERR_UNSUPPORTED;
+    if (!on_tc(path, fmt, D, Tc, G, P) && !decode_mma_supported(fmt, D, Tc, G, P)) return NK_ERR_UNSUPPORTED;
   }
   const int per_sm = rk_tc ? decode_mma_ctas_per_sm(D, T, G)
                      : path == Path::kRk8v4 ? decode_rk8v4_ctas_per_sm(D, G)
                      : (simt ? decode_simt_ctas_per_sm(D, G) : decode_mma_ctas_per_sm(D, T, G));
-  const int32_t n = num_ctas > 0 ? num_ctas : default_ctas(B, Hkv, max_ctx, P, per_sm);
+  const int32_t seen = visible_keys(max_ctx, P, T, window, sinks);  // max_ctx without a window
+  const int32_t n = num_ctas > 0 ? num_ctas : default_ctas(B, Hkv, seen, P, per_sm);
   // The fp32 sums of mma.sync are not rounded to nearest, and their error
   // grows with the keys of one kv-head that a CTA runs through its
   // accumulators. The tcgen05 kernel folds them (its FOLD instance); the
@@ -161,9 +189,9 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   if (!simt || rk_tc) {
     const int Tl = T - (T - 1) / Tc * Tc;  // columns of the last chunk
     const bool mma_kernel =
-        rk_tc || !decode_tc_supported(fmt, D, Tc, G, P) || !decode_tc_supported(fmt, D, Tl, G, P);
-    const int64_t unit = ((int64_t)max_ctx + P - 1) / P;
-    const int64_t per_cta = (max_items(B, Hkv, max_ctx, P) + n - 1) / n;
+        rk_tc || !on_tc(path, fmt, D, Tc, G, P) || !on_tc(path, fmt, D, Tl, G, P);
+    const int64_t unit = ((int64_t)seen + P - 1) / P;
+    const int64_t per_cta = (max_items(B, Hkv, seen, P) + n - 1) / n;
     if (mma_kernel && (per_cta < unit ? per_cta : unit) * P > kMaxMmaRunKeys) return NK_ERR_UNSUPPORTED;
   }
   const size_t need = nk_decode_workspace_bytes(B, T, Hq, Hkv, D, n);
@@ -178,6 +206,8 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   p.D = D;
   p.lay = layout_of(fmt, P, D);
   p.fmt = fmt;
+  p.window = window;
+  p.sinks = sinks;
   p.q = reinterpret_cast<const uint16_t*>(q);
   p.bt = bt;
   p.max_pages = max_pages;
@@ -206,8 +236,7 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
 }
 
 int launch_decode(const DecodeParams& p0, Path path, cudaStream_t st) {
-  const bool simt = !tensor_path(path);
-  const int Tc = chunk_cols(simt, p0.fmt, p0.D, p0.T, p0.G, p0.P);
+  const int Tc = cols_of(path, p0.fmt, p0.D, p0.T, p0.G, p0.P);
   const int64_t slots = (int64_t)p0.n_ctas + (int64_t)p0.B * p0.Hkv;
   for (int t0 = 0; t0 < p0.T; t0 += Tc) {
     DecodeParams p = p0;
@@ -223,8 +252,7 @@ int launch_decode(const DecodeParams& p0, Path path, cudaStream_t st) {
     cudaError_t e = path == Path::kRk8v4 ? (decode_mma_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_mma(p, st)
                                                                                           : launch_decode_rk8v4(p, st))
                     : path == Path::kSimt   ? launch_decode_simt(p, st)
-                    : (decode_tc_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st)
-                                                                     : launch_decode_mma(p, st));
+                    : (on_tc(path, p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st) : launch_decode_mma(p, st));
     if (e != cudaSuccess) return NK_ERR_CUDA;
     e = launch_decode_combine(p, st);
     if (e != cudaSuccess) return NK_ERR_CUDA;
@@ -396,6 +424,25 @@ int nk_paged_decode_attn_simt(const nk_kv_pool* pool, const void* q_dev, const i
                               void* stream) {
   return paged_decode(pool, q_dev, block_table_dev, max_pages_per_seq, ctx_lens_dev, B, T, num_q_heads, sm_scale,
                       max_ctx, num_ctas, workspace_dev, workspace_bytes, out_dev, status_dev, stream, Path::kSimt);
+}
+
+int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
+                         int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, int32_t B, int32_t T,
+                         int32_t num_q_heads, float sm_scale, int32_t max_ctx, int32_t window, int32_t sinks,
+                         int32_t num_ctas, void* workspace_dev, size_t workspace_bytes, void* out_dev,
+                         int32_t* status_dev, void* stream) {
+  if (window < 1 || sinks < 0) return NK_ERR_SHAPE;
+  // a window as long as the longest context hides no key: whole-context attention
+  if (window >= max_ctx)
+    return paged_decode(pool, q_dev, block_table_dev, max_pages_per_seq, ctx_lens_dev, B, T, num_q_heads, sm_scale,
+                        max_ctx, num_ctas, workspace_dev, workspace_bytes, out_dev, status_dev, stream, Path::kTensor);
+  DecodeParams p;
+  bool empty = true;
+  const int err = prepare_decode(pool, q_dev, block_table_dev, max_pages_per_seq, ctx_lens_dev, B, T, num_q_heads,
+                                 sm_scale, max_ctx, num_ctas, workspace_dev, workspace_bytes, out_dev, status_dev,
+                                 Path::kWindow, &p, &empty, window, sinks < max_ctx ? sinks : max_ctx);
+  if (err != NK_OK || empty) return err;
+  return launch_decode(p, Path::kWindow, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t nk_rk8v4_chunk_bytes(int32_t page_size, int32_t head_dim) {

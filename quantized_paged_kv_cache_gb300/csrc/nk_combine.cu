@@ -118,12 +118,13 @@ __device__ __forceinline__ void merge_row(int S, LseFn lse_of, RowFn row_of, uin
 // written directly by that CTA; the others merge the partial slots c + u of
 // the CTAs c their pages span (CTAs with an empty range wrote nothing).
 // Block = one (unit, row) and a slice of C channels.
-template <int D, int C>
+// WIN: the units' pages are those of a sliding window with sinks.
+template <int D, int C, bool WIN>
 __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const DecodeParams p) {
   static_assert(D % C == 0, "whole slices");
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int warp_tot[8];
-  const SplitShape sh = p.shape();
+  const auto sh = p.shape_of<WIN>();
   // The page prefix runs before the wait for the split kernel: this kernel
   // only ever follows the split kernel of the same call, which could start
   // only once its own predecessor had passed its wait (that predecessor is
@@ -176,12 +177,17 @@ __global__ void __launch_bounds__(kCombThreads) attn_combine_kernel(const float*
 // kSliceRows: more blocks in flight, fewer partials per thread.
 constexpr int kSliceRows = 256;
 
-template <int D>
-static cudaError_t launch_combine_d(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
+template <int D, bool WIN>
+static cudaError_t launch_combine_w(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
   const dim3 b(kCombThreads);
   if (D > 64 && rows < kSliceRows)
-    return launch_chained(decode_combine_kernel<D, 64>, dim3((unsigned)(rows * (D / 64))), b, 0, stream, p);
-  return launch_chained(decode_combine_kernel<D, D>, dim3((unsigned)rows), b, 0, stream, p);
+    return launch_chained(decode_combine_kernel<D, 64, WIN>, dim3((unsigned)(rows * (D / 64))), b, 0, stream, p);
+  return launch_chained(decode_combine_kernel<D, D, WIN>, dim3((unsigned)rows), b, 0, stream, p);
+}
+
+template <int D>
+static cudaError_t launch_combine_d(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
+  return p.window > 0 ? launch_combine_w<D, true>(p, rows, stream) : launch_combine_w<D, false>(p, rows, stream);
 }
 
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {

@@ -170,6 +170,32 @@ __device__ __forceinline__ int pages_of_len(const SplitShape& s, int L) {
   return (L + s.P - 1) / s.P;
 }
 
+// The same split over a sliding window with sinks: query column t at position
+// p_t = L - T + t sees key n <= p_t when n > p_t - window or n < sinks. A unit
+// then owns only the pages that hold a key its first column (or a later one)
+// can see: the sink pages before the window's first page, then the window's
+// pages. Page number i of a unit is the logical page i, shifted past the gap
+// from the first window page on.
+struct WindowShape : SplitShape {
+  int window, sinks;
+};
+
+// First window page of a sequence of (valid) length L, and the sink pages before it.
+__host__ __device__ __forceinline__ void window_pages(const WindowShape& s, int L, int& first, int& lead) {
+  const int64_t lo = (int64_t)L - s.T - s.window + 1;
+  first = lo > 0 ? (int)(lo / s.P) : 0;
+  const int sp = (int)(((int64_t)s.sinks + s.P - 1) / s.P);
+  lead = sp < first ? sp : first;
+}
+
+__device__ __forceinline__ int pages_of_len(const WindowShape& s, int L) {
+  const int all = pages_of_len(static_cast<const SplitShape&>(s), L);
+  if (all == 0) return 0;
+  int first, lead;
+  window_pages(s, L, first, lead);
+  return all - first + lead;
+}
+
 __device__ __forceinline__ int64_t cta_begin(int64_t W, int n, int c) { return (int64_t)c * W / n; }
 
 // Largest CTA index whose range starts at or before item x (x < W).
@@ -189,8 +215,8 @@ constexpr int kMaxBatch = 1024;  // sequences per call (prefix sums live in shar
 // context lengths are also kept in shared memory (lens[b] = ctx_lens[b]), so
 // the kernel reads no length from global memory after its page loads start.
 // kL2Only reads the lengths at L2 (ld.global.cg), bypassing this SM's L1.
-template <bool kL2Only = false>
-__device__ __forceinline__ void block_page_prefix(const SplitShape& s, const int32_t* ctx_lens, int trim, int* pre,
+template <bool kL2Only = false, class Shape>
+__device__ __forceinline__ void block_page_prefix(const Shape& s, const int32_t* ctx_lens, int trim, int* pre,
                                                   int* warp_tot, int* lens = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int v[4];

@@ -35,6 +35,7 @@ struct DecodeParams {
   // this kernel could start.
   int early;
   int fmt;  // KvFmt of the pool (the rk8v4 kernel ignores it)
+  int window, sinks;  // sliding window and sinks (window 0: the whole context)
   // Failure-detection tests (nk_test_inject_copy_stall): every bounded wait
   // gives up after wait_cycles, and the page copies of CTA page numbers
   // >= withhold are never issued (-1: all issued).
@@ -42,6 +43,18 @@ struct DecodeParams {
   int withhold;
   __host__ __device__ bool issuable(int q) const { return withhold < 0 || q < withhold; }
   __host__ __device__ SplitShape shape() const { return SplitShape{B, Hkv, P, T, max_ctx, max_pages}; }
+  __host__ __device__ WindowShape window_shape() const {
+    WindowShape s;
+    static_cast<SplitShape&>(s) = shape();
+    s.window = window;
+    s.sinks = sinks;
+    return s;
+  }
+  template <bool WIN>
+  __host__ __device__ auto shape_of() const {
+    if constexpr (WIN) return window_shape();
+    else return shape();
+  }
 };
 
 // Flag invalid ctx lengths once (block 0 of a kernel).

@@ -309,6 +309,28 @@ __device__ __forceinline__ int page_coord(const DecodeParams& p, const SplitShap
   return (page < 0 || page >= p.num_pages) ? -1 : page * p.Hkv + h;
 }
 
+// The same over a sliding window with sinks (lens: the sequences' lengths).
+__device__ __forceinline__ int page_coord(const DecodeParams& p, const WindowShape& sh, const int* pre, const int* lens,
+                                          int64_t x_begin, int q) {
+  const int64_t x = x_begin + q;
+  int lo = 0, hi = sh.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)pre[mid] * sh.Hkv <= x) lo = mid; else hi = mid;
+  }
+  const int pages = pre[lo + 1] - pre[lo];
+  const int64_t off = x - (int64_t)pre[lo] * sh.Hkv;
+  const int h = (int)(off / pages), pi = (int)(off % pages);
+  int first, lead;
+  window_pages(sh, lens[lo], first, lead);
+  const int page = __ldg(p.bt + (int64_t)lo * p.max_pages + (pi < lead ? pi : pi - lead + first));
+  return (page < 0 || page >= p.num_pages) ? -1 : page * p.Hkv + h;
+}
+__device__ __forceinline__ int page_coord(const DecodeParams& p, const SplitShape& sh, const int* pre, const int*,
+                                          int64_t x_begin, int q) {
+  return page_coord(p, sh, pre, x_begin, q);
+}
+
 // Load the CTA's page number q into its stage: TMA boxes of the K|V codes
 // plus bulk copies of the two scale arrays, all completing on full_bar.
 template <int D, bool BF = false>
@@ -379,7 +401,10 @@ __device__ __forceinline__ void issue_page_rk(const DecodeParams& p, const CUten
 // the other formats tmapv is unused); each query row is rotated by H64 / 8
 // and enters the QK product as fp16 hi + lo; the 4-bit values are widened
 // from their nibbles; P' carries one scale per 32 value channels.
-template <int D, int NT, int CS, int FMT>
+// WIN: sliding window with sinks. The units' pages are the visible ones
+// (WindowShape), blocks that straddle an end of the window or the sinks are
+// masked per column, blocks no column sees are passed over.
+template <int D, int NT, int CS, int FMT, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                  const __grid_constant__ CUtensorMap tmapv,
                                                                  const DecodeParams p) {
@@ -427,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = p.P, BPP = P / 16;
   const int per_stage = BPP * CS;  // consumer-warp arrivals per page
-  const SplitShape sh = p.shape();
+  const auto sh = p.shape_of<WIN>();
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -694,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   bool have = next_segment(sh, pre, x, x_end, seg);
   if (have) fetch_q(seg);
   const int ncache = total < kPidCache ? total : kPidCache;
-  for (int q = tid; q < ncache; q += kThreads) pid[q] = page_coord(p, sh, pre, x_begin, q);
+  for (int q = tid; q < ncache; q += kThreads) pid[q] = page_coord(p, sh, pre, lens, x_begin, q);
   if (have) stage_q();
   __syncthreads();
   if (p.early) chain_wait();  // the pages may hold the preceding append's rows
@@ -755,10 +780,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
     // this team's blocks of the segment: CTA-wide block numbers jn = team,
     // team + NTEAMS, ... (4 blocks of 16 keys per 64-key page)
     const int seg_first = page_seq, seg_pages = seg.page_end - seg.page_begin;
+    // WIN: logical page of the unit's page number i: i, or i + gap from page `lead` on
+    int lead = 0, gap = 0;
+    if constexpr (WIN) {
+      int first;
+      window_pages(sh, L, first, lead);
+      gap = first - lead;
+    }
     for (; jn < (seg_first + seg_pages) * BPP; jn += NTEAMS) {
       const int q = bpp_sh >= 0 ? jn >> bpp_sh : jn / BPP;  // CTA page number
       const int kb = jn - q * BPP;                           // block in page
-      const int pi = seg.page_begin + (q - seg_first);
+      int pi = seg.page_begin + (q - seg_first);
+      if constexpr (WIN) pi += pi >= lead ? gap : 0;
       while (q_cur < q) {  // stage and phase of page q, advanced without a division
         ++q_cur;
         if (++s_cur == S) {
@@ -782,7 +815,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
         }
         const int key0 = kb * 16;
         const int pos0 = pi * P + key0;  // sequence position of the block's key 0
-        if (pos0 < L) {
+        bool seen = pos0 < L;
+        // the first column's window starts after L - T - window
+        if constexpr (WIN) seen = seen && (pos0 + 15 > L - T - sh.window || pos0 < sh.sinks);
+        if (seen) {
           // ---- QK: per-group fp32 partial dot products (GW*NT independent accumulators)
           float acc[GW][NT][4];
 #pragma unroll
@@ -883,6 +919,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
                 const int key = g + (k >> 1) * 8;
                 if (pos0 + key > L - T + row_t[nt][k & 1]) sc[nt][k] = -INFINITY;
               }
+          }
+          if constexpr (WIN) {
+            // blocks with a key before the last column's window, past the sinks
+            if (pos0 <= L - 1 - sh.window && pos0 + 15 >= sh.sinks) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int n = pos0 + g + (k >> 1) * 8;
+                  if (n >= sh.sinks && n <= L - T + row_t[nt][k & 1] - sh.window) sc[nt][k] = -INFINITY;
+                }
+            }
           }
 
           // ---- online softmax (base 2). The reference m_run is raised only when a
@@ -1111,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
             if (qn < total && p.issuable(qn) && !*abort_flag) {
               // every reader arrived before its increment: the phase is complete
               if (mbar_wait(smem_u32(&empty_bar[s]), par, p.wait_cycles)) {
-                const int zn = qn < kPidCache ? pid[qn] : page_coord(p, sh, pre, x_begin, qn);
+                const int zn = qn < kPidCache ? pid[qn] : page_coord(p, sh, pre, lens, x_begin, qn);
                 if constexpr (RK)
                   issue_page_rk<D>(p, &tmap, &tmapv, zn, st, smem_u32(&full_bar[s]));
                 else

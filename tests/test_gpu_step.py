@@ -1,0 +1,212 @@
+"""nk_step_tables and nk_mrope on the GPU against plain 64-bit forms, and one
+serving step (tables, rotary positions, append, attention) run together."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_paged_kv_cache_gb300 as nk
+
+import _ref
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32), device="cuda")
+
+
+def run_tables(P, num_pages, start, new, free, table, max_rows, with_pos=True, graph=False):
+    B = len(start)
+    t = dict(start=i32(start), new=i32(new), free=i32(free), table=i32(table), cu=i32([-5] * (B + 1)), ctx=i32([-5] * B),
+             slots=torch.full((max_rows,), -7, dtype=torch.int64, device="cuda"),
+             pos=i32([-7] * max_rows) if with_pos else None, used=i32([-5]), status=i32([0]))
+
+    def call():
+        nk.step_tables(P, num_pages, t["start"], t["new"], t["free"], t["table"], t["cu"], t["ctx"], t["slots"],
+                       positions=t["pos"], used=t["used"], status=t["status"])
+
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        g.replay()
+        g.replay()
+    else:
+        call()
+    torch.cuda.synchronize()
+    return t
+
+
+def make(B, P, seed, start_hi, new_hi, spare=3, slack=5):
+    rng = np.random.RandomState(seed)
+    start = rng.randint(0, start_hi + 1, B)
+    new = rng.randint(0, new_hi + 1, B)
+    held = -(-start // P)
+    need = -(-(start + new) // P) - held
+    num_pages = int(held.sum() + need.sum()) + spare
+    perm = rng.permutation(num_pages)
+    width = int((held + need).max()) + 2
+    table = np.full((B, width), -1)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    return start.tolist(), new.tolist(), perm[at:], table, num_pages, int(new.sum()) + slack
+
+
+def check_tables(t, want, with_pos=True):
+    table, cu, ctx, slots, pos, used = want
+    assert np.array_equal(t["table"].cpu().numpy(), table)
+    assert np.array_equal(t["cu"].cpu().numpy(), cu)
+    assert np.array_equal(t["ctx"].cpu().numpy(), ctx)
+    assert np.array_equal(t["slots"].cpu().numpy(), slots)
+    assert int(t["used"].item()) == used
+    if with_pos:
+        assert np.array_equal(t["pos"].cpu().numpy(), pos)
+
+
+@pytest.mark.parametrize("B,P,start_hi,new_hi", [
+    (1, 64, 0, 1), (1, 16, 1000, 1), (8, 64, 5000, 1), (3, 48, 100, 200), (33, 16, 70, 5), (257, 64, 300, 300),
+    (1023, 32, 64, 40), (1024, 256, 600, 17), (5, 1, 7, 9)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_tables(B, P, start_hi, new_hi, graph):
+    start, new, free, table, pages, rows = make(B, P, 7 * B + P, start_hi, new_hi)
+    if B == 1 and new_hi == 1:
+        new, rows = [1], 6
+    t = run_tables(P, pages, start, new, free, table, rows, graph=graph)
+    want = _ref.tables(P, pages, start, new, free, table, rows, np.full(rows, -7), np.full(rows, -7))
+    check_tables(t, want)
+    assert int(t["status"].item()) == 0
+
+
+def test_tables_without_positions_and_with_nothing_new():
+    start, new, free, table, pages, rows = make(9, 16, 3, 60, 30)
+    t = run_tables(16, pages, start, new, free, table, rows, with_pos=False)
+    check_tables(t, _ref.tables(16, pages, start, new, free, table, rows, np.full(rows, -7), np.full(rows, -7)), False)
+    t = run_tables(16, pages, start, [0] * 9, free, table, 4)
+    check_tables(t, _ref.tables(16, pages, start, [0] * 9, free, table, 4, np.full(4, -7), np.full(4, -7)))
+    assert int(t["used"].item()) == 0 and int(t["status"].item()) == 0
+
+
+@pytest.mark.parametrize("case", ["negative_start", "negative_new", "past_table", "short_free", "no_free", "bad_free_page",
+                                  "bad_held_page", "rows_past_buffer", "too_many_rows"])
+def test_tables_bad_data_is_flagged(case):
+    start, new, free, table, pages, rows = make(7, 16, 11, 60, 50)
+    new[3], start[3] = 20, 21  # a partly filled page with new rows behind it
+    held = -(-21 // 16)
+    start2, new2, free2, table2, rows2 = list(start), list(new), free.copy(), table.copy(), sum(new) + 5
+    table2[3, :held] = [0, 1][:held]
+    width = table2.shape[1]
+    flagged = nk.NK_DEVFLAG_BAD_POS
+    if case == "negative_start":
+        start2[2] = -1
+    elif case == "negative_new":
+        new2[2] = -4
+    elif case == "past_table":
+        new2[5] = width * 16 - start2[5] + 1
+        rows2 = sum(new2) + 5
+    elif case == "short_free":
+        free2, flagged = free2[:3], nk.NK_DEVFLAG_NO_PAGES
+    elif case == "no_free":
+        free2, flagged = free2[:0], nk.NK_DEVFLAG_NO_PAGES
+    elif case == "bad_free_page":
+        free2[1], flagged = pages, nk.NK_DEVFLAG_BAD_PAGE
+    elif case == "bad_held_page":
+        table2[3, held - 1], flagged = -3, nk.NK_DEVFLAG_BAD_PAGE
+    elif case == "rows_past_buffer":
+        rows2 = sum(new2) - 6
+    elif case == "too_many_rows":
+        new2[1] = new2[4] = 2 ** 31 - 1
+        t = run_tables(16, pages, start2, new2, free2, table2, rows2)
+        assert int(t["status"].item()) & nk.NK_DEVFLAG_BAD_POS
+        assert torch.all(t["slots"] == -7) and np.array_equal(t["table"].cpu().numpy(), table2)
+        assert t["cu"].tolist()[5:] == [2 ** 31 - 1] * 3
+        return
+    want = _ref.tables(16, pages, start2, new2, free2, table2, rows2, np.full(rows2, -7), np.full(rows2, -7))
+    t = run_tables(16, pages, start2, new2, free2, table2, rows2)
+    check_tables(t, want)
+    assert int(t["status"].item()) == flagged
+
+
+# A bf16 result is off by its rounding (2^-8 of the value, half a step) and by what the fp32 rotation leaves: the angle
+# (2^-23 turns from the frequency's double at position 2^31, 2^-25 from the fp32 fraction: together below 1e-6 radians,
+# and 3e-7 of the reference's own 64-bit angle there) and sincospi and two fp32 roundings (3e-7), times |a| + |b|.
+ROPE_ABS = 2.0 ** -19
+
+
+def check_rope(got, x, pos, inv, sections, interleaved):
+    want, size = _ref.mrope(x, pos, inv, sections, interleaved)
+    err = (got.double() - want).abs()
+    assert torch.all(err <= 2.0 ** -8 * want.abs() + ROPE_ABS * size), float((err - 2.0 ** -8 * want.abs()).max())
+    rot = 2 * len(inv)
+    assert torch.equal(got[..., rot:], x[..., rot:])
+
+
+def rope_case(rows, Hq, Hkv, D, sections, far, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    qkv = torch.randn((rows, Hq + 2 * Hkv, D), generator=g, device="cuda").bfloat16()
+    pos = torch.randint(0, far, (len(sections), rows), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    half = sum(sections)
+    inv = 1e6 ** (-torch.arange(half, dtype=torch.float64) / half)
+    return qkv, pos, inv
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,D,sections,interleaved,far", [
+    (1, 24, 4, 256, (32, 48, 48), False, 1000),
+    (8, 24, 4, 256, (32, 48, 48), False, 262144),
+    (37, 16, 2, 128, (12, 10, 10), True, 262144),
+    (1000, 8, 8, 64, (32,), False, 2 ** 31 - 1),
+    (5, 3, 1, 64, (0, 8, 0), False, 5000),
+    (9, 2, 1, 256, (100, 10, 10, 8), True, 100000),
+    (2049, 5, 5, 128, (24, 20, 20), True, 100000),
+    (6, 7, 3, 40, (8,), False, 64),
+    (4, 24, 0, 256, (128,), False, 64),
+])
+def test_mrope(rows, Hq, Hkv, D, sections, interleaved, far):
+    qkv, pos, inv = rope_case(rows, Hq, Hkv, D, sections, far, rows)
+    q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv]
+    before = qkv.clone()
+    qo, ko = nk.mrope(q, k, pos, inv, sections, interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert torch.equal(qkv, before)
+    check_rope(qo, q, pos, inv, sections, interleaved)
+    if Hkv:
+        check_rope(ko, k, pos, inv, sections, interleaved)
+    # in place, inside the fused rows: the same values, and the value rows untouched
+    nk.mrope(q, k, pos, inv, sections, interleaved=interleaved, q_out=q, k_out=k)
+    torch.cuda.synchronize()
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    assert torch.equal(qkv[:, Hq + Hkv:], before[:, Hq + Hkv:])
+
+
+def test_mrope_negative_positions_and_non_finite_rows():
+    qkv, pos, inv = rope_case(12, 2, 1, 64, (16, 8, 8), 1000, 5)
+    pos[0, ::2] = -pos[0, ::2] - 2 ** 30
+    q, k = qkv[:, :2], qkv[:, 2:3]
+    qo, _ = nk.mrope(q, k, pos, inv, (16, 8, 8))
+    check_rope(qo, q, pos, inv, (16, 8, 8), False)
+    q[3, 1, 5] = float("nan")
+    q[4, 0, 9] = float("inf")
+    qo2, _ = nk.mrope(q, k, pos, inv, (16, 8, 8))
+    bad = torch.zeros_like(qo, dtype=torch.bool)
+    bad[3, 1, [5, 37]] = True
+    bad[4, 0, [9, 41]] = True
+    assert torch.equal(qo2[~bad], qo[~bad]) and not torch.isfinite(qo2[bad]).any()
+
+
+def test_mrope_rows_behind_the_last_stay_and_graphs_replay():
+    qkv, pos, inv = rope_case(40, 4, 2, 128, (24, 20, 20), 9000, 6)
+    q, k = qkv[:, :4], qkv[:, 4:6]
+    n = i32([40])
+    full_q, full_k = nk.mrope(q, k, pos, inv, (24, 20, 20))
+    qo, ko = torch.full_like(full_q, 7.0), torch.full_like(full_k, 7.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nk.mrope(q, k, pos, inv, (24, 20, 20), q_out=qo, k_out=ko, num_rows=n)
+    for rows in (0, 1, 23, 40, 1000):
+        qo.fill_(7.0), ko.fill_(7.0), n.fill_(rows)
+        g.replay()
+        torch.cuda.synchronize()
+        m = min(rows, 40)
+        assert torch.equal(qo[:m], full_q[:m]) and torch.equal(ko[:m], full_k[:m])
+        assert torch.all(qo[m:] == 7.0) and torch.all(ko[m:] == 7.0)
