@@ -339,6 +339,36 @@ int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
                          int32_t num_ctas, void* workspace_dev, size_t workspace_bytes, void* out_dev,
                          int32_t* status_dev, void* stream);
 
+/*
+ * nk_paged_chunk_attn -- attention of ragged chunks of new tokens over the
+ * paged cache: sequence b brings the query rows cu_q[b] .. cu_q[b+1]-1 (none,
+ * one for a decoding sequence, thousands for a prompt), whose K/V the step's
+ * nk_kv_append already stored.
+ *   q_dev        bf16 [total_q][Hq][D];  out_dev bf16 [total_q][Hq][D] (not q)
+ *   cu_q_dev     int32 [B+1]: cu_q[0] >= 0, not decreasing, cu_q[B] <= total_q
+ *   ctx_lens_dev int32 [B]: tokens of sequence b, its new ones included
+ *   window, sinks  window 0: a token at position p sees keys 0 .. p; else as
+ *                nk_paged_window_attn, with the same promise on pages
+ *   num_ctas     <= 0 for the default (one per SM)
+ *   workspace_dev  nk_chunk_workspace_bytes(head_dim, num_ctas) bytes, 16-byte
+ *                aligned; scratch, contents on entry do not matter. Calls that
+ *                may overlap on the GPU need one each.
+ * Rows outside every sequence's range stay as they were. A sequence whose
+ * cu_q or ctx_len is out of range (ctx_len below its new tokens, above max_ctx
+ * or past the table) sets NK_DEVFLAG_BAD_CTX and is skipped. Keys in a page
+ * whose id is outside the pool (NK_DEVFLAG_BAD_PAGE) and groups whose scale is
+ * not finite (NK_DEVFLAG_RANGE) count as zeros. K and V enter the products as
+ * fp16: an output differs from the exact one by its bf16 rounding plus at most
+ * a few 2^-11 of the values it averages. B is at most 1,024 and
+ * total_q * Hq / Hkv below 2^31 - 128.
+ */
+size_t nk_chunk_workspace_bytes(int32_t head_dim, int32_t num_ctas);
+int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* cu_q_dev,
+                        const int32_t* block_table_dev, int32_t max_pages_per_seq, const int32_t* ctx_lens_dev,
+                        int32_t B, int32_t total_q, int32_t num_q_heads, float sm_scale, int32_t max_ctx,
+                        int32_t window, int32_t sinks, int32_t num_ctas, void* workspace_dev, size_t workspace_bytes,
+                        void* out_dev, int32_t* status_dev, void* stream);
+
 /* Same contract and result, computed by the fp32 CUDA-core kernel that the
  * tensor-core path is measured against. */
 int nk_paged_decode_attn_simt(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,

@@ -28,7 +28,7 @@ __all__ = [
     "attn_combine", "status_string", "decode_step", "rk8v4_chunk_bytes", "rk8v4_pool_bytes", "rk8v4_append",
     "rk8v4_decode_attn", "i8f16_chunk_bytes", "i8f16_pool_bytes", "i8f16_append", "i8f16_decode_attn",
     "bf16kv_chunk_bytes", "bf16kv_pool_bytes", "bf16kv_append", "bf16kv_decode_attn", "test_inject_copy_stall", "paged_prefill_attn",
-    "step_tables", "mrope", "paged_window_attn",
+    "step_tables", "mrope", "paged_window_attn", "chunk_workspace_bytes", "paged_chunk_attn",
 ]
 
 
@@ -477,4 +477,36 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
                                     _ptr(ctx_lens), B, T, Hq, float(sm_scale), max_ctx, window, sinks, num_ctas,
                                     _ptr(workspace), wbytes, _ptr(out), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_window_attn")
+    return out
+
+
+def chunk_workspace_bytes(head_dim: int, num_ctas: int = 0) -> int:
+    return int(lib().nk_chunk_workspace_bytes(head_dim, num_ctas))
+
+
+def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: float, max_ctx: int, window: int = 0,
+                     sinks: int = 0, num_ctas: int = 0, workspace=None, out=None, status=None, stream=None):
+    """Attention of ragged chunks of new tokens over the paged cache
+    (nk_paged_chunk_attn): ``q`` bf16 [total_q][Hq][D], the rows of sequence b
+    at cu_q[b] .. cu_q[b+1]-1; returns out bf16 [total_q][Hq][D]."""
+    import torch
+
+    _need_cuda(q, cu_q, block_table, ctx_lens, workspace, out, status)
+    pool.need("int8")
+    total, Hq, D = q.shape
+    B = ctx_lens.numel()
+    if D != pool.head_dim or block_table.shape[0] != B or cu_q.numel() != B + 1:
+        raise ValueError("q, cu_q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
+    _need_dtype(torch.bfloat16, q, out)
+    _need_dtype(torch.int32, cu_q, block_table, ctx_lens, status)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = torch.empty(chunk_workspace_bytes(D, num_ctas), dtype=torch.uint8, device=q.device)
+    ps = pool.c_struct()
+    wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_paged_chunk_attn(ctypes.byref(ps), _ptr(q), _ptr(cu_q), _ptr(block_table), block_table.shape[-1],
+                                   _ptr(ctx_lens), B, total, Hq, float(sm_scale), max_ctx, window, sinks, num_ctas,
+                                   _ptr(workspace), wbytes, _ptr(out), _ptr(status), _stream(stream))
+    _check(rc, "nk_paged_chunk_attn")
     return out

@@ -68,6 +68,8 @@ EXPORTS = (
     "nk_step_tables",
     "nk_mrope",
     "nk_paged_window_attn",
+    "nk_chunk_workspace_bytes",
+    "nk_paged_chunk_attn",
 )
 
 
@@ -124,6 +126,9 @@ def lib() -> ctypes.CDLL:
             L.nk_mrope.restype = ctypes.c_int
             L.nk_paged_window_attn.argtypes = [pool_p, P, P, I32, P, I32, I32, I32, F, I32, I32, I32, I32, P, Z, P, P, P]
             L.nk_paged_window_attn.restype = ctypes.c_int
+            L.nk_chunk_workspace_bytes.argtypes, L.nk_chunk_workspace_bytes.restype = [I32, I32], Z
+            L.nk_paged_chunk_attn.argtypes = [pool_p, P, P, P, I32, P, I32, I32, I32, F, I32, I32, I32, I32, P, Z, P, P, P]
+            L.nk_paged_chunk_attn.restype = ctypes.c_int
             L.nk_attn_combine.argtypes = [P, P, I32, I32, I32, P, P]
             L.nk_attn_combine.restype = ctypes.c_int
             L.nk_status_string.argtypes, L.nk_status_string.restype = [ctypes.c_int], ctypes.c_char_p

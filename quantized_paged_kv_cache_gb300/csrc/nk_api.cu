@@ -5,6 +5,7 @@
 
 #include <atomic>
 
+#include "nk_chunk.cuh"
 #include "nk_decode.cuh"
 #include "nk_ptx.cuh"
 #include "nk_rk8v4.cuh"
@@ -589,6 +590,68 @@ int nk_paged_prefill_attn(const nk_kv_pool* pool, const void* q_dev, const int32
   p.wait_cycles = wc > 0 ? wc : kWaitCycles;
   p.withhold = g_withhold.load(std::memory_order_relaxed);
   return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NK_OK : NK_ERR_CUDA;
+}
+
+size_t nk_chunk_workspace_bytes(int32_t head_dim, int32_t num_ctas) {
+  if (!(head_dim == 64 || head_dim == 128 || head_dim == 256)) return 0;
+  const int sms = sm_count();
+  const size_t n = num_ctas > 0 ? (size_t)num_ctas : (size_t)(sms > 0 ? sms : 152);
+  return (n * (2 * chunk::kRows * ((size_t)head_dim + 1) * 4 + sizeof(int4)) + 255) / 256 * 256;
+}
+
+int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* cu_q_dev,
+                        const int32_t* block_table_dev, int32_t max_pages_per_seq, const int32_t* ctx_lens_dev,
+                        int32_t B, int32_t total_q, int32_t num_q_heads, float sm_scale, int32_t max_ctx,
+                        int32_t window, int32_t sinks, int32_t num_ctas, void* workspace_dev, size_t workspace_bytes,
+                        void* out_dev, int32_t* status_dev, void* stream) {
+  int err = NK_OK;
+  if (!pool_ok(pool, &err)) return err;
+  if (B < 0 || total_q < 0 || num_q_heads < 1 || window < 0 || sinks < 0) return NK_ERR_SHAPE;
+  if (B == 0 || total_q == 0) return NK_OK;
+  if (!q_dev || !cu_q_dev || !block_table_dev || !ctx_lens_dev || !out_dev) return NK_ERR_NULL;
+  const int Hkv = pool->num_kv_heads, D = pool->head_dim, P = pool->page_size;
+  if (num_q_heads % Hkv != 0) return NK_ERR_SHAPE;
+  if (B > kMaxBatch) return NK_ERR_UNSUPPORTED;
+  if (max_pages_per_seq < 1 || max_ctx < 1 || (int64_t)max_ctx > (int64_t)max_pages_per_seq * P) return NK_ERR_SHAPE;
+  if (!isfinite(sm_scale)) return NK_ERR_SHAPE;
+  if (!aligned(q_dev, 16) || !aligned(out_dev, 16)) return NK_ERR_SHAPE;
+  const int G = num_q_heads / Hkv;
+  if ((int64_t)total_q * G > 0x7fffffff - chunk::kRows) return NK_ERR_SHAPE;  // rows of a unit in 32 bits
+  const int sms = sm_count();
+  const int n = num_ctas > 0 ? num_ctas : (sms > 0 ? sms : 152);
+  if (n > (1 << 20)) return NK_ERR_SHAPE;
+  if (!workspace_dev || workspace_bytes < nk_chunk_workspace_bytes(D, n) || !aligned(workspace_dev, 16))
+    return NK_ERR_WORKSPACE;
+  chunk::Params p = {};
+  p.pool = reinterpret_cast<const uint8_t*>(pool->base_dev);
+  p.num_pages = pool->num_pages;
+  p.P = P;
+  p.Hkv = Hkv;
+  p.lay = ChunkLayout::make(P, D);
+  p.q = reinterpret_cast<const uint16_t*>(q_dev);
+  p.cu = cu_q_dev;
+  p.bt = block_table_dev;
+  p.max_pages = max_pages_per_seq;
+  p.ctx = ctx_lens_dev;
+  p.B = B;
+  p.total_q = total_q;
+  p.Hq = num_q_heads;
+  p.G = G;
+  p.scale2 = sm_scale * kLog2e;
+  p.max_ctx = max_ctx;
+  p.window = window < max_ctx ? window : 0;  // as long as the longest context: hides no key
+  p.sinks = sinks < max_ctx ? sinks : max_ctx;
+  p.n_ctas = n;
+  const size_t slots = 2 * (size_t)n * chunk::kRows;
+  p.part_o = reinterpret_cast<float*>(workspace_dev);
+  p.part_lse = p.part_o + slots * D;
+  p.desc = reinterpret_cast<int4*>(p.part_lse + slots);
+  p.out = reinterpret_cast<uint16_t*>(out_dev);
+  p.status = status_dev;
+  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
+  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
+  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  return chunk::launch(p, D, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
 int nk_attn_combine(const float* part_o_dev, const float* part_lse_dev, int32_t num_splits, int32_t rows,

@@ -83,3 +83,22 @@ def test_binding_refusals():
         nk.mrope(x, x[:, :1], torch.zeros(3, 2, dtype=torch.int32), torch.ones(64, dtype=torch.float64), (32, 16, 16))
     with pytest.raises(ValueError):
         nk.mrope(x, x[:1, :1], torch.zeros(3, 2, dtype=torch.int32), torch.ones(64, dtype=torch.float64), (32, 16, 16))
+
+
+def test_chunk_refusals():
+    need = nk.chunk_workspace_bytes(64, 4)
+    assert need >= 4 * 2 * 128 * 65 * 4 and nk.chunk_workspace_bytes(96, 4) == 0
+
+    def call(p=pool(), q=FAKE, cu=FAKE, B=1, total=5, Hq=2, max_ctx=64, window=0, sinks=0, n=4, ws=FAKE, wsb=need, out=FAKE,
+             scale=0.1, pages=4):
+        return nk.lib().nk_paged_chunk_attn(ctypes.byref(p) if p is not None else None, q, cu, FAKE, pages, FAKE, B, total,
+                                            Hq, scale, max_ctx, window, sinks, n, ws, wsb, out, None, None)
+
+    assert call(p=None) == 1 and call(q=None) == 1 and call(cu=None) == 1 and call(out=None) == 1
+    assert call(B=-1) == 2 and call(total=-1) == 2 and call(window=-1) == 2 and call(sinks=-1) == 2
+    assert call(Hq=3, p=pool(H=2)) == 2 and call(Hq=0) == 2 and call(max_ctx=65) == 2 and call(max_ctx=0) == 2
+    assert call(pages=0) == 2 and call(scale=float("inf")) == 2 and call(q=FAKE + 8) == 2 and call(p=pool(P=24)) == 2
+    assert call(total=1 << 30, Hq=4) == 2 and call(n=1 << 21) == 2
+    assert call(B=1025) == 3
+    assert call(ws=None) == 4 and call(wsb=need - 1) == 4 and call(ws=FAKE + 4) == 4
+    assert call(B=0) == 0 and call(total=0) == 0
