@@ -24,17 +24,18 @@
 //               lazy reference (moved only when a score passes it by more than
 //               8, so the accumulator is rarely rescaled), P back to tensor
 //               memory over S, row sums, and the tile's output;
-//   warps 4-7   K blocks, warps 8-11 V blocks: codes and scales by 16-byte
-//               loads into registers one block ahead, widened to fp16, scaled,
-//               stored to one of two 128-byte-swizzled buffers;
-//   warp 12     (13-15 idle) issues the MMAs: QK of block j + 1 goes out before PV of block
-//               j, so the tensor cores work while the softmax does.
+//   warps 4-7   K blocks, warps 8-11 V blocks: codes and scales from the ring,
+//               widened to fp16, scaled, stored to one of two
+//               128-byte-swizzled operand buffers;
+//   warp 12     issues the MMAs: QK of block j + 1 goes out before PV of block
+//               j, so the tensor cores work while the softmax does;
+//   warp 13     looks up the pages and fills a two-stage ring of raw blocks
+//               with bulk asynchronous copies (14 and 15 are idle).
 //
-// Why no TMA copy of the pages: every byte has to pass the registers to be
-// widened, and shared memory is what bounds the kernel -- per 64-key block at
-// head dim 256 the fp16 tiles are written (64 KB) and read by the MMAs (64 KB),
-// about 1,000 cycles of its 128 bytes a cycle against 1,024 cycles of MMAs;
-// staging the codes there would add 68 KB.
+// Loading the codes straight into the convert warps' registers, one block
+// ahead, spared the ring's shared-memory traffic but left the page lookup and
+// the loads' latency in their path: 7,345 us against 4,720 on eight chunks of
+// 1,024 tokens at 8K to 32K (24 q-heads over 4 kv-heads, head dim 256).
 //
 // Work split (stream-K): the blocks of all tiles form one list, cut into equal
 // contiguous ranges, one per CTA, whatever the sequences' lengths. A tile cut
@@ -69,6 +70,7 @@ constexpr int kThreads = (kMmaWarp + 4) * 32;  // whole warpgroups, for setmaxnr
 constexpr int kLaunchRegs = 128, kRegsSoft = 200, kRegsConv = 136, kRegsMma = 40;
 static_assert(kRegsSoft + 2 * kRegsConv + kRegsMma == 4 * kLaunchRegs, "shares = the launch's registers");
 constexpr int kTmemCols = 512;
+constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256)
 constexpr int kMinBlocks = 4;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
 
 template <int D>
@@ -76,7 +78,9 @@ struct Smem {
   static constexpr int kTile = kKeys * D * 2;  // one fp16 K or V block
   static constexpr int off_k = 0;              // [2]
   static constexpr int off_v = 2 * kTile;      // [2]
-  static constexpr int off_pre = 4 * kTile;    // int64 [kMaxBatch + 1]: blocks before sequence b
+  static constexpr int kStage = kKeys * (2 * D + 2 * (D / 64) * 4);  // raw block: K codes | K scales | V codes | V scales
+  static constexpr int off_ring = 4 * kTile;                         // [kStages]
+  static constexpr int off_pre = off_ring + kStages * kStage;        // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_lens = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch]
   static constexpr int off_cu = off_lens + kMaxBatch * 4;         // int [kMaxBatch + 1]
   static constexpr int off_misc = off_cu + (kMaxBatch + 4) * 4;
@@ -210,17 +214,6 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32])
       : "memory");
 }
 
-// Codes and scales of the 16 keys a convert warp takes of a block, in flight
-// in registers: lane c = lane % LPK holds channels 16 c .. 16 c + 15 of key
-// i * KPI + lane / LPK for i < NI.
-template <int D>
-struct Raw {
-  static constexpr int LPK = D / 16, KPI = 32 / LPK, NI = 16 / KPI;
-  uint4 w[NI];
-  float s[NI];
-  bool first;  // the first block of its segment
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params p) {
   using SM = Smem<D>;
@@ -240,7 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   uint64_t* pfull = bars + 8;    // [2] P written (4 warps)
   uint64_t* qfull = bars + 10;   // Q of a tile written (4 warps)
   uint64_t* ofree = bars + 11;   // accumulator of a tile read (4 warps)
-  int* misc = reinterpret_cast<int*>(bars + 12);
+  uint64_t* rfull = bars + 12;   // [kStages] raw block in the ring (bytes)
+  uint64_t* rfree = bars + 12 + kStages;  // [kStages] read by the 8 convert warps
+  int* misc = reinterpret_cast<int*>(bars + 12 + 2 * kStages);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
   int* last_mma = misc + 2;                             // block number of the last MMAs committed to pvdone / qkdone
@@ -249,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   float* maxima = reinterpret_cast<float*>(misc + 24);  // [2 operands][4 warps][4 groups]
   float* kfac = reinterpret_cast<float*>(misc + 56);    // [4] 2^e of a K block
   volatile int* seg_blocks = misc + 92;                 // [2] blocks of a segment, for the MMA warp
+  volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | bad 16-key groups << 16
+  int* last_raw = misc + 100;                           // raw blocks issued
   float* vhdr = reinterpret_cast<float*>(misc + 60);    // [2][16]: moved | 4 beta | 4 of 2^e
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -262,10 +259,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(smem_u32(&pvdone[i]), 1);
       mbar_init(smem_u32(&pfull[i]), kSoftWarps);
     }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&rfull[i]), 1);
+      mbar_init(smem_u32(&rfree[i]), 2 * kConvWarps);
+    }
     mbar_init(smem_u32(qfull), kSoftWarps);
     mbar_init(smem_u32(ofree), kSoftWarps);
     *abort_flag = 0;
     last_mma[0] = last_mma[1] = -1;
+    *last_raw = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -415,8 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(x4[i])), fabsf(bf16_hi(x4[i]))));
         }
       }
+      // the sign of sm_scale goes into Q, so that scores scale by a positive factor
       const int e = q_norm_exp(m);
-      const float qs = pow2i(e);
+      const float qs = p.scale2 < 0.f ? -pow2i(e) : (p.scale2 > 0.f ? pow2i(e) : 0.f);
 #pragma unroll 1
       for (int g = 0; g < G64; ++g) {
         uint32_t r32[32];
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       ++q_seg;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(qfull));
-      return p.scale2 * pow2i(-e);
+      return p.scale2 == 0.f ? 1.f : fabsf(p.scale2) * pow2i(-e);
     };
     float kq = load_q();
     while (more) {
@@ -455,16 +458,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         wait_bar(&qkdone[j & 1], (j >> 1) & 1);
         fence_after();
         const uint32_t scol = lane_base + kColS + (j & 1) * 64;
-        uint32_t raw0[32], raw1[32];
-        tm_ld32(scol, raw0);
-        tm_ld32(scol + 32, raw1);
+        uint32_t lo[32], hi[32];
+        tm_ld32(scol, lo);
+        tm_ld32(scol + 32, hi);
+        // the factor of the raw scores, kept a normal number (a masked -inf times 0 would be NaN)
+        const float f = fminf(fmaxf(kq * kfac[j & 3], 1.2e-38f), 3.4e38f);
         wait_ld();
-        const float f = kq * kfac[j & 3];
         float s[64];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          s[c] = __uint_as_float(raw0[c]) * f;
-          s[32 + c] = __uint_as_float(raw1[c]) * f;
+          s[c] = __uint_as_float(lo[c]);
+          s[32 + c] = __uint_as_float(hi[c]);
         }
         if (key0 + kKeys - 1 > w.s.p0) {
           const int lim = pos - key0;
@@ -478,9 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           for (int c = 0; c < 64; ++c)
             if (c <= lim && c >= sk) s[c] = -INFINITY;
         }
-        float mx = fmaxf(s[0], s[1]);
+        float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 2; c < 64; ++c) mx = fmaxf(mx, s[c]);
+        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[c + i]), s[c + 4 + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[60 + i]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
         // the reference moves at a row's first key and when a score passes it by more than 8
         const bool raise = mx > m_ref + 8.f;
         wait_bar(&vfull[j & 1], (j >> 1) & 1);  // the block's V exponents
@@ -513,16 +522,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           for (int g = 0; g < G64; ++g) unscale[g] = vh[5 + g];
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        // p = 2^(score f - m), two at a time; four partial sums
+        const float2 f2 = make_float2(f, f), mu2 = make_float2(-mu, -mu);
         uint32_t pk[32];
-        float l0 = 0.f, l1 = 0.f;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          const float a = ex2(s[2 * c] - mu), b = ex2(s[2 * c + 1] - mu);
-          l0 += a;
-          l1 += b;
-          pk[c] = pack_f16(a, b);
+          const float2 t2 = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), f2, mu2);
+          const float2 e2 = make_float2(ex2(t2.x), ex2(t2.y));
+          sum[c & 1] = __fadd2_rn(sum[c & 1], e2);
+          pk[c] = pack_f16(e2.x, e2.y);
         }
-        l += l0 + l1;
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tm_st32(scol, pk);
         wait_st();
         fence_before();
@@ -594,71 +605,70 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConv) : "memory");
     const bool isv = warp >= kSoftWarps + kConvWarps;
     const int cw = (warp - kSoftWarps) & 3;  // keys 16 cw .. 16 cw + 15 of a block
-    using R = Raw<D>;
-    const int ck = lane % R::LPK, kk = lane / R::LPK;  // 16-channel piece, key within a load
+    // Lane -> (key, 16-channel piece) of a load: a quarter warp takes four
+    // pieces of two neighbouring keys, the odd key's in the other half of the
+    // 128 bytes, so that neither its 16-byte reads of the raw rows nor its
+    // swizzled stores meet in a bank.
+    constexpr int KPI = 512 / D, NI = 16 / KPI;  // keys of a load, loads of a block
+    const int qt = lane >> 3, kp = (lane >> 2) & 1;
+    const int kk = D == 256 ? kp : (D == 128 ? (qt >> 1) * 2 + kp : qt * 2 + kp);
+    const int ck = D == 64 ? lane & 3 : ((lane & 3) | (((qt ^ kp) & 1) << 2) | (D == 256 ? (qt >> 1) << 3 : 0));
     const int grp = ck >> 2;
-    const int64_t code_off = isv ? p.lay.vc : 0, scale_off = isv ? p.lay.vs : p.lay.ks;
+    const int raw_off = isv ? kKeys * (D + G64 * 4) : 0;
     uint64_t* full = isv ? vfull : kfull;
     uint64_t* done = isv ? pvdone : qkdone;
     const uint32_t buf = isv ? vbuf : kbuf;
-    Walk w = w0;
-    bool more = true;
-    // page of this warp's 16 keys in w's block (P is a multiple of 16: one page holds them all)
-    auto page_of = [&]() -> int {
-      const int pos = block_of(w) * kKeys + cw * 16;
-      if (pos >= w.L) return -2;  // nothing there
-      return __ldg(p.bt + (int64_t)w.b * p.max_pages + pos / p.P);
-    };
-    bool bad_page = false, bad_scale = false;
-    auto load = [&](Raw<D>& x, int page, bool first) {
-      x.first = first;
-      const int pos = block_of(w) * kKeys + cw * 16;
-      const bool ok = page >= 0 && page < p.num_pages;
-      if (!ok && page != -2) bad_page = true;
-      const int slot = pos % p.P;
-      const uint8_t* chunk = p.pool + ((int64_t)(ok ? page : 0) * p.Hkv + w.h) * p.lay.chunk;
-#pragma unroll
-      for (int i = 0; i < R::NI; ++i) {
-        const int key = i * R::KPI + kk;
-        x.w[i] = make_uint4(0u, 0u, 0u, 0u);
-        x.s[i] = 0.f;
-        if (ok && pos + key < w.L) {
-          x.w[i] = __ldg(reinterpret_cast<const uint4*>(chunk + code_off + (int64_t)(slot + key) * D + ck * 16));
-          x.s[i] = __ldg(reinterpret_cast<const float*>(chunk + scale_off) + (slot + key) * G64 + grp);
-        }
-      }
-    };
+    int* votes_w = votes + (isv ? 8 : 0);
+    const int bar_id = isv ? 2 : 1;
+    const int total = (int)(w0.end - w0.x);
+    bool bad_scale = false;
     int ev[4] = {kEvUnset, kEvUnset, kEvUnset, kEvUnset};
-    int j = 0;
-    auto convert = [&](Raw<D>& x) {
-      // ---- exponents: a group moves when a scale passes 2^6 of it, or none of the block's reaches 2^-10
-      constexpr int NG = G64;
-      if (isv && x.first) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) ev[g] = kEvUnset;
-      }
+    int my = kEvUnset;  // the exponent of this thread's group
+    int st = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < total; ++j) {
+      wait_bar(&rfull[st], ph);
+      const uint8_t* raw = smem + SM::off_ring + st * SM::kStage + raw_off;
+      const int inf = info[st];
+      const bool first = (inf >> 8) & 1;
+      const int there = ((inf >> (16 + cw)) & 1) ? 0 : (inf & 0xff) - cw * 16;  // keys of this warp's 16 that exist
+      uint4 w[NI];
+      float s[NI];
       float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < R::NI; ++i) {
-        if (!(x.s[i] <= 3.0e38f)) {  // the append of a non-finite row: counts as zero, flagged
-          x.s[i] = 0.f;
+      for (int i = 0; i < NI; ++i) {
+        const int key = cw * 16 + i * KPI + kk;
+        s[i] = *reinterpret_cast<const float*>(raw + kKeys * D + (key * G64 + grp) * 4);
+        w[i] = *reinterpret_cast<const uint4*>(raw + key * D + ck * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (i * KPI + kk >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
+        if (!(s[i] <= 3.0e38f)) {               // the append of a non-finite row: zeros too, flagged
+          s[i] = 0.f;
           bad_scale = true;
         }
-        mx = fmaxf(mx, x.s[i]);
+        mx = fmaxf(mx, s[i]);
       }
-      const int eg = isv ? grp : 0;
-      int my = ev[0];
+      // ---- exponents: a group moves when a scale passes 2^6 of it, or none of the block's reaches 2^-10
+      constexpr int NG = G64;
+      if (isv && first) {
 #pragma unroll
-      for (int g = 1; g < NG; ++g) my = eg == g ? ev[g] : my;
+        for (int g = 0; g < 4; ++g) ev[g] = kEvUnset;
+        my = kEvUnset;
+      }
       uint32_t bits = 0u;
       if (my != kEvUnset) {
         const float t = mx * pow2i(-my);
-        bits = ((t > 64.f ? 1u : 0u) | (t >= 0.0009765625f ? 16u : 0u)) << eg;
+        bits = ((t > 64.f ? 1u : 0u) | (t >= 0.0009765625f ? 16u : 0u)) << (isv ? grp : 0);
       }
       bits = __reduce_or_sync(0xffffffffu, bits);
-      int* vote = votes + (isv ? 8 : 0) + (j & 1) * 4;
-      if (lane == 0) vote[cw] = (int)bits;
-      named_bar(1 + (isv ? 1 : 0), kConvWarps * 32);
+      int* vote = votes_w + (j & 1) * 4;
+      if (lane == 0) {
+        vote[cw] = (int)bits;
+        mbar_arrive(smem_u32(&rfree[st]));  // the raw block is in registers (every lane has passed the reduction)
+      }
+      named_bar(bar_id, kConvWarps * 32);
       bits = (uint32_t)(vote[0] | vote[1] | vote[2] | vote[3]);
       constexpr uint32_t all = (1u << NG) - 1u;
       const uint32_t moving = ((bits & 15u) | (~(bits >> 4) & 15u)) & (isv ? all : 1u);
@@ -670,17 +680,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const uint32_t v = __reduce_max_sync(0xffffffffu, (!isv || grp == g) ? __float_as_uint(mx) : 0u);
           if (lane == 0) mxs[cw * 4 + g] = __uint_as_float(v);
         }
-        named_bar(1 + (isv ? 1 : 0), kConvWarps * 32);
+        named_bar(bar_id, kConvWarps * 32);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (!((moving >> g) & 1u)) continue;
-          const float m4 = fmaxf(fmaxf(mxs[g], mxs[4 + g]), fmaxf(mxs[8 + g], mxs[12 + g]));
+          const float m4 = isv ? fmaxf(fmaxf(mxs[g], mxs[4 + g]), fmaxf(mxs[8 + g], mxs[12 + g]))
+                               : fmaxf(fmaxf(mxs[0], mxs[4]), fmaxf(mxs[8], mxs[12]));
           if (m4 > 0.f) (void)ev_update(ev[g], exp_of(m4), beta[g]);
         }
-        named_bar(1 + (isv ? 1 : 0), kConvWarps * 32);  // maxima read before a later block writes them
+        named_bar(bar_id, kConvWarps * 32);  // maxima read before a later block writes them
         my = ev[0];
+        if (isv) {
 #pragma unroll
-        for (int g = 1; g < NG; ++g) my = eg == g ? ev[g] : my;
+          for (int g = 1; g < NG; ++g) my = grp == g ? ev[g] : my;
+        }
       }
       const float down = my == kEvUnset ? 1.f : pow2i(-my);
       // ---- the buffer's previous block has been multiplied
@@ -688,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       if (cw == 0 && lane == 0) {
         if (isv) {
           float* vh = vhdr + (j & 1) * 16;
-          const bool tell = moving != 0 || x.first;
+          const bool tell = moving != 0 || first;
           reinterpret_cast<int*>(vh)[0] = tell ? 1 : 0;
           if (tell) {
 #pragma unroll
@@ -701,13 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           kfac[j & 3] = my == kEvUnset ? 1.f : pow2i(my);
         }
       }
-      const uint32_t dst = buf + (j & 1) * SM::kTile + grp * (kKeys * 128);
+      const uint32_t dst = buf + (j & 1) * SM::kTile + grp * (kKeys * 128) + (cw * 16 + kk) * 128;
 #pragma unroll
-      for (int i = 0; i < R::NI; ++i) {
-        const int key = cw * 16 + i * R::KPI + kk;
-        const __half2 sc = __float2half2_rn(x.s[i] * down);
-        const uint32_t w4[4] = {x.w[i].x ^ 0x80808080u, x.w[i].y ^ 0x80808080u, x.w[i].z ^ 0x80808080u,
-                                x.w[i].w ^ 0x80808080u};
+      for (int i = 0; i < NI; ++i) {
+        const __half2 sc = __float2half2_rn(s[i] * down);
+        const uint32_t w4[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
         uint32_t h[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -717,58 +728,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           h[2 * k] = *reinterpret_cast<const uint32_t*>(&pa);
           h[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&pb);
         }
-        // two 16-byte chunks; odd groups store the second first, so that the
-        // eight lanes of a key hit distinct banks
-        const int c0 = (ck & 3) * 2, odd = grp & 1;
-        const uint32_t row = dst + key * 128;
-        const uint32_t a0 = row + (((c0 + odd) ^ (key & 7)) << 4), a1 = row + (((c0 + 1 - odd) ^ (key & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(odd ? h[4] : h[0]), "r"(odd ? h[5] : h[1]),
-                     "r"(odd ? h[6] : h[2]), "r"(odd ? h[7] : h[3])
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(odd ? h[0] : h[4]), "r"(odd ? h[1] : h[5]),
-                     "r"(odd ? h[2] : h[6]), "r"(odd ? h[3] : h[7])
-                     : "memory");
+        // i * KPI is a multiple of 8 at head dim 64, else the row moves within its group of eight
+        const int r7 = (i * KPI + kk) & 7, c0 = (ck & 3) * 2;
+        const uint32_t row = dst + i * (KPI * 128);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c0 ^ r7) << 4)), "r"(h[0]), "r"(h[1]),
+                     "r"(h[2]), "r"(h[3]));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c0 + 1) ^ r7) << 4)), "r"(h[4]),
+                     "r"(h[5]), "r"(h[6]), "r"(h[7]));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0 && (p.withhold < 0 || j < p.withhold)) mbar_arrive(smem_u32(&full[j & 1]));
-      ++j;
-    };
-    // two blocks in flight: while one is converted the next is being loaded,
-    // and the page id of the one after that
-    Raw<D> ra, rb;
-    load(ra, page_of(), true);
-    int tile_seen = w.tile, h_seen = w.h, b_seen = w.b;
-    int page = -2;
-    bool first = false;
-    auto advance = [&]() {  // to the next block: its page id goes out
-      more = step(p, tab, w);
-      if (more) {
-        first = w.tile != tile_seen || w.h != h_seen || w.b != b_seen;
-        tile_seen = w.tile;
-        h_seen = w.h;
-        b_seen = w.b;
-        page = page_of();
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
       }
-    };
-    advance();
-    while (true) {
-      const bool next_b = more;
-      if (next_b) {
-        load(rb, page, first);
-        advance();
-      }
-      convert(ra);
-      if (!next_b) break;
-      const bool next_a = more;
-      if (next_a) {
-        load(ra, page, first);
-        advance();
-      }
-      convert(rb);
-      if (!next_a) break;
     }
-    if (__any_sync(0xffffffffu, bad_page) && lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) flag(p.status, NK_DEVFLAG_RANGE);
   } else {
     // ======================================================= MMA warp
@@ -813,9 +788,66 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         ++seg;
       }
     }
+    if (warp == kMmaWarp + 1) {
+      // ===================================================== producer warp
+      // lanes 0-3 take 16 keys of a block each (P is a multiple of 16: one
+      // page holds them); with pages of whole blocks lane 0 takes all 64
+      const int per = p.P % kKeys == 0 ? kKeys : 16;
+      constexpr int kKeyBytes = 2 * D + 2 * G64 * 4;
+      Walk w = w0;
+      int st = 0, page = -2;
+      uint32_t ph = 1u;  // a fresh ring is free
+      bool first = true;
+      auto look = [&]() {  // page id of the lane's keys (-2: no such keys)
+        const int pos = block_of(w) * kKeys + lane * per;
+        page = -2;
+        if (lane * per < kKeys && pos < w.L) page = __ldg(p.bt + (int64_t)w.b * p.max_pages + pos / p.P);
+      };
+      look();
+      for (int q = 0;; ++q) {
+        const int key0 = block_of(w) * kKeys, pos = key0 + lane * per, h = w.h;
+        const int keys = w.L - key0 < kKeys ? w.L - key0 : kKeys;
+        const int cur = page;
+        const bool was_first = first;
+        const int b = w.b, tile = w.tile;
+        const bool more = step(p, tab, w);
+        if (more) {
+          first = w.b != b || w.h != h || w.tile != tile;
+          look();
+        }
+        const bool ok = cur >= 0 && cur < p.num_pages;
+        const unsigned copies = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, !ok && cur != -2);
+        wait_bar(&rfree[st], ph);
+        const bool stop = *abort_flag;
+        if (__any_sync(0xffffffffu, stop)) break;
+        const uint32_t bar = smem_u32(&rfull[st]);
+        if (lane == 0) {
+          info[st] = keys | (was_first ? 256 : 0) | ((per == kKeys ? (bad ? 15u : 0u) : (bad & 15u)) << 16);
+          if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+          mbar_arrive_expect_tx(bar, __popc(copies) * per * kKeyBytes);
+          *last_raw = q + 1;
+        }
+        __syncwarp();
+        if (ok) {
+          const int slot = pos % p.P;
+          const uint8_t* c = p.pool + ((int64_t)cur * p.Hkv + h) * p.lay.chunk;
+          const uint32_t dst = smem_u32(smem + SM::off_ring + st * SM::kStage);
+          const int k0 = lane * per;
+          bulk_load(dst + k0 * D, c + (int64_t)slot * D, per * D, bar);
+          bulk_load(dst + kKeys * D + k0 * G64 * 4, c + p.lay.ks + slot * G64 * 4, per * G64 * 4, bar);
+          bulk_load(dst + kKeys * (D + G64 * 4) + k0 * D, c + p.lay.vc + (int64_t)slot * D, per * D, bar);
+          bulk_load(dst + kKeys * (2 * D + G64 * 4) + k0 * G64 * 4, c + p.lay.vs + slot * G64 * 4, per * G64 * 4, bar);
+        }
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (!more) break;
+      }
+    }
     __syncwarp();
   }
-  // ---- every MMA that was issued completes before the tensor memory is released
+  // ---- every MMA and copy that was issued completes before the tensor memory is released
   fence_before();
   __syncthreads();
   if (tid == 0) {
@@ -824,6 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       uint64_t* bar = i ? pvdone : qkdone;
       if (q >= 0) (void)mbar_wait(smem_u32(&bar[q & 1]), (q >> 1) & 1, p.wait_cycles);
     }
+    for (int q = *last_raw - kStages > 0 ? *last_raw - kStages : 0; q < *last_raw; ++q)
+      (void)mbar_wait(smem_u32(&rfull[q % kStages]), (q / kStages) & 1, p.wait_cycles);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
