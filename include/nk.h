@@ -330,8 +330,8 @@ int nk_mrope(const void* q_dev, const void* k_dev, void* q_out_dev, void* k_out_
  * sinks >= 0. Arguments, checks, workspace (nk_decode_workspace_bytes), device
  * flags, ordering and ownership as nk_paged_decode_attn. Only the pages that
  * hold a visible key are read, and only their block-table entries: the pages
- * between the sinks and the window may have been given back. They run on the
- * mma.sync kernel; a window of at least max_ctx is nk_paged_decode_attn itself.
+ * between the sinks and the window may have been given back. A window of at
+ * least max_ctx is nk_paged_decode_attn itself.
  */
 int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
                          int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, int32_t B, int32_t T,

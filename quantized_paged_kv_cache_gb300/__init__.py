@@ -9,6 +9,7 @@ int32 ``status`` tensor (``NK_DEVFLAG_*`` bits).
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 from ._lib import NKError, lib, nk_kv_pool, status_string  # noqa: F401
@@ -36,12 +37,30 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream():
+    """torch's call for the current stream's handle, without the Stream object
+    around it (2.9 us of a call's host time on a Grace core, against 0.2)."""
+    import torch
+
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
+_current = None
+
+
 def _stream(stream) -> int:
     if stream is not None:
         return int(getattr(stream, "cuda_stream", stream))
-    import torch
+    global _current
+    if _current is None:
+        import torch
 
-    return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # CUDA is up before the raw handle is asked for
+        _current = _raw_stream()
+    return _current()
 
 
 def _check(rc: int, where: str) -> None:
@@ -373,9 +392,11 @@ def paged_prefill_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, 
     return out
 
 
-def _need_dtype(dtype, *tensors) -> None:
+def _need(dtype, *tensors) -> None:
+    """CUDA, contiguous and of one type (None: an optional argument that is not given)."""
     for t in tensors:
-        if t is not None and t.dtype != dtype:
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype == dtype):
+            _need_cuda(t)
             raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
 
 
@@ -388,30 +409,35 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
     and ``used`` int32 [1] are written."""
     import torch
 
-    _need_cuda(start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map, positions, used, status)
-    _need_dtype(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
-    _need_dtype(torch.int64, slot_map)
-    B, rows = start_pos.numel(), slot_map.numel()
-    if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or block_table.dim() != 2 \
-            or block_table.shape[0] != B:
+    _need(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
+    _need(torch.int64, slot_map)
+    B, rows, shape = start_pos.numel(), slot_map.numel(), block_table.shape
+    if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
         raise ValueError("start_pos, new_lens, ctx_lens and block_table hold one entry (row) per sequence, cu_new one more")
     if positions is not None and positions.numel() < rows:
         raise ValueError("positions must hold an entry for every one of slot_map")
-    rc = lib().nk_step_tables(page_size, num_pages, _ptr(start_pos), _ptr(new_lens), B, _ptr(free_pages),
-                              free_pages.numel(), _ptr(block_table), block_table.shape[1], _ptr(cu_new),
-                              _ptr(ctx_lens), _ptr(slot_map), _ptr(positions), rows, _ptr(used), _ptr(status),
+    rc = lib().nk_step_tables(page_size, num_pages, start_pos.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
+                              free_pages.numel(), block_table.data_ptr(), shape[1], cu_new.data_ptr(),
+                              ctx_lens.data_ptr(), slot_map.data_ptr(), _ptr(positions), rows, _ptr(used), _ptr(status),
                               _stream(stream))
     _check(rc, "nk_step_tables")
 
 
-def _rows(t, what: str):
-    """(heads, head_dim, row stride) of [rows][heads][head_dim] bf16 rows whose heads are consecutive."""
-    if not t.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+@functools.lru_cache(maxsize=64)
+def _sections(sections: tuple):
+    """(the sections as a C array, its address, their count, their sum); the array is only ever read."""
+    values = tuple(int(x) for x in sections)
+    array = (ctypes.c_int32 * len(values))(*values)
+    return array, ctypes.addressof(array), len(values), sum(values)
+
+
+def _row_stride(t, shape, what: str) -> int:
+    """Row stride of [rows][heads][head_dim] rows whose heads are consecutive."""
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
         raise ValueError(f"the heads of a row of {what} must be consecutive")
-    return h, d, (t.stride(0) if n > 1 else h * d)
+    return s0 if n > 1 else h * d
 
 
 def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=None, k_out=None, num_rows=None,
@@ -423,32 +449,38 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
     q and k themselves to rotate in place."""
     import torch
 
-    rows = q.shape[0]
-    if k.shape[0] != rows or k.shape[2] != q.shape[2]:
-        raise ValueError("q and k must have the same rows and head_dim")
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    _need_dtype(torch.bfloat16, q, k, q_out, k_out)
-    _need_cuda(positions, num_rows)
-    _need_dtype(torch.int32, positions, num_rows)
+    qs, ks, ps = q.shape, k.shape, positions.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError("q and k must be [rows][heads][head_dim] with the same rows and head_dim")
+    _need(torch.int32, positions, num_rows)
+    bf16 = torch.bfloat16
+    for t in (q, k, q_out, k_out):
+        if t is not None and not (t.is_cuda and t.dtype == bf16):
+            raise ValueError("q, k and their outputs must be bfloat16 CUDA tensors (there is no CPU path)")
     if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 host tensor")
-    sections = tuple(int(x) for x in sections)
-    if positions.dim() != 2 or positions.shape[0] != len(sections) or positions.shape[1] < rows:
+    _, array, axes, half = _sections(tuple(sections))
+    rows, Hq, D = qs
+    Hkv = ks[1]
+    if len(ps) != 2 or ps[0] != axes or ps[1] < rows:
         raise ValueError("positions must hold one row of positions per section (axis)")
-    if inv_freq.numel() != sum(sections):
+    if inv_freq.numel() != half:
         raise ValueError("inv_freq must hold one frequency for every one of the sections")
-    Hq, D, qs = _rows(q, "q")
-    Hkv, _, ks = _rows(k, "k")
-    qos, kos = _rows(q_out, "q_out")[2], _rows(k_out, "k_out")[2]
-    rc = lib().nk_mrope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), qs, ks, qos, kos, rows, Hq, Hkv, D,
-                        _ptr(positions), positions.shape[1], inv_freq.data_ptr(),
-                        (ctypes.c_int32 * len(sections))(*sections), len(sections), int(bool(interleaved)),
-                        _ptr(num_rows), _stream(stream))
+    if q_out is None:
+        q_out, qos = torch.empty(qs, dtype=bf16, device=q.device), Hq * D
+    elif q_out.shape == qs:
+        qos = _row_stride(q_out, qs, "q_out")
+    else:
+        raise ValueError("q_out must have the shape of q")
+    if k_out is None:
+        k_out, kos = torch.empty(ks, dtype=bf16, device=k.device), Hkv * D
+    elif k_out.shape == ks:
+        kos = _row_stride(k_out, ks, "k_out")
+    else:
+        raise ValueError("k_out must have the shape of k")
+    rc = lib().nk_mrope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _row_stride(q, qs, "q"),
+                        _row_stride(k, ks, "k"), qos, kos, rows, Hq, Hkv, D, positions.data_ptr(), ps[1],
+                        inv_freq.data_ptr(), array, axes, 1 if interleaved else 0, _ptr(num_rows), _stream(stream))
     _check(rc, "nk_mrope")
     return q_out, k_out
 
@@ -459,23 +491,26 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
     tokens (nk_paged_window_attn); returns out bf16 [B][T][Hq][D]."""
     import torch
 
-    _need_cuda(q, block_table, ctx_lens, workspace, out, status)
+    _need(torch.bfloat16, q, out)
+    _need(torch.int32, block_table, ctx_lens, status)
+    _need_cuda(workspace)
     pool.need("int8")
     B, T, Hq, D = q.shape
-    if D != pool.head_dim or block_table.shape[0] != B or ctx_lens.numel() != B:
+    shape = block_table.shape
+    if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
         raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
-    _need_dtype(torch.bfloat16, q, out)
-    _need_dtype(torch.int32, block_table, ctx_lens, status)
     if out is None:
         out = torch.empty_like(q)
+    elif out.numel() != q.numel():
+        raise ValueError("out must have the shape of q")
     if workspace is None:
-        nbytes = decode_workspace_bytes(B, T, Hq, pool.num_kv_heads, D, num_ctas)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
-    ps = pool.c_struct()
-    wbytes = workspace.numel() * workspace.element_size()
-    rc = lib().nk_paged_window_attn(ctypes.byref(ps), _ptr(q), _ptr(block_table), block_table.shape[-1],
-                                    _ptr(ctx_lens), B, T, Hq, float(sm_scale), max_ctx, window, sinks, num_ctas,
-                                    _ptr(workspace), wbytes, _ptr(out), _ptr(status), _stream(stream))
+        wbytes = max(lib().nk_decode_workspace_bytes(B, T, Hq, pool.num_kv_heads, D, num_ctas), 256)
+        workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_paged_window_attn(pool.c_struct(), q.data_ptr(), block_table.data_ptr(), shape[1],
+                                    ctx_lens.data_ptr(), B, T, Hq, sm_scale, max_ctx, window, sinks, num_ctas,
+                                    workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_window_attn")
     return out
 
@@ -491,22 +526,25 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
     at cu_q[b] .. cu_q[b+1]-1; returns out bf16 [total_q][Hq][D]."""
     import torch
 
-    _need_cuda(q, cu_q, block_table, ctx_lens, workspace, out, status)
+    _need(torch.bfloat16, q, out)
+    _need(torch.int32, cu_q, block_table, ctx_lens, status)
+    _need_cuda(workspace)
     pool.need("int8")
     total, Hq, D = q.shape
-    B = ctx_lens.numel()
-    if D != pool.head_dim or block_table.shape[0] != B or cu_q.numel() != B + 1:
+    B, shape = ctx_lens.numel(), block_table.shape
+    if D != pool.head_dim or len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:
         raise ValueError("q, cu_q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
-    _need_dtype(torch.bfloat16, q, out)
-    _need_dtype(torch.int32, cu_q, block_table, ctx_lens, status)
     if out is None:
         out = torch.empty_like(q)
+    elif out.numel() != q.numel():
+        raise ValueError("out must have the shape of q")
     if workspace is None:
-        workspace = torch.empty(chunk_workspace_bytes(D, num_ctas), dtype=torch.uint8, device=q.device)
-    ps = pool.c_struct()
-    wbytes = workspace.numel() * workspace.element_size()
-    rc = lib().nk_paged_chunk_attn(ctypes.byref(ps), _ptr(q), _ptr(cu_q), _ptr(block_table), block_table.shape[-1],
-                                   _ptr(ctx_lens), B, total, Hq, float(sm_scale), max_ctx, window, sinks, num_ctas,
-                                   _ptr(workspace), wbytes, _ptr(out), _ptr(status), _stream(stream))
+        wbytes = lib().nk_chunk_workspace_bytes(D, num_ctas)
+        workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_paged_chunk_attn(pool.c_struct(), q.data_ptr(), cu_q.data_ptr(), block_table.data_ptr(), shape[1],
+                                   ctx_lens.data_ptr(), B, total, Hq, sm_scale, max_ctx, window, sinks, num_ctas,
+                                   workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_chunk_attn")
     return out

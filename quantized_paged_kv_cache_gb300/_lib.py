@@ -76,6 +76,8 @@ EXPORTS = (
 def lib() -> ctypes.CDLL:
     """Load libnk.so, building it first when the sources are newer."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()

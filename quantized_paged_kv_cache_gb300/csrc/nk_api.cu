@@ -116,7 +116,7 @@ int chunk_cols(bool simt, int fmt, int D, int T, int G, int P) {
 // kernels on a pool of the pages' INT8 layout (fp16 scales) or of bf16 rows,
 // or on an rk8v4 pool the tensor-core kernel (up to 32 rows per kv-head) or
 // the rk8v4 CUDA-core kernel.
-// A sliding window (kWindow) runs on the mma.sync kernel's window instances.
+// A sliding window (kWindow) runs on the window instances of both.
 enum class Path { kTensor, kSimt, kRk8v4, kTensorF16, kBf16, kWindow };
 
 int path_fmt(Path path) {
@@ -131,21 +131,6 @@ int path_fmt(Path path) {
 // the paths on the tensor-core kernels (tcgen05 / mma.sync)
 bool tensor_path(Path path) {
   return path == Path::kTensor || path == Path::kTensorF16 || path == Path::kBf16 || path == Path::kWindow;
-}
-
-// columns per launch of a call on `path`
-int cols_of(Path path, int fmt, int D, int T, int G, int P) {
-  if (path != Path::kWindow) return chunk_cols(!tensor_path(path), fmt, D, T, G, P);
-  int c = 48 / G;
-  if (c < 1) c = 1;
-  if (c > T) c = T;
-  while (c > 1 && !decode_mma_supported(fmt, D, c, G, P)) --c;
-  return c;
-}
-
-// whether a launch of T columns runs on the tcgen05 kernel
-bool on_tc(Path path, int fmt, int D, int T, int G, int P) {
-  return path != Path::kWindow && decode_tc_supported(fmt, D, T, G, P);
 }
 
 // Checks the decode arguments and fills `p`; *empty = nothing to launch.
@@ -168,12 +153,12 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   if (!isfinite(sm_scale)) return NK_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(out, 16)) return NK_ERR_SHAPE;
   const int fmt = path_fmt(path);
-  const int Tc = cols_of(path, fmt, D, T, G, P);
+  const int Tc = chunk_cols(simt, fmt, D, T, G, P);
   const bool rk_tc = path == Path::kRk8v4 && decode_mma_supported(fmt, D, Tc, G, P);
   if (simt && !rk_tc) {
     if (G > 8) return NK_ERR_UNSUPPORTED;
   } else if (!rk_tc) {
-    if (!on_tc(path, fmt, D, Tc, G, P) && !decode_mma_supported(fmt, D, Tc, G, P)) return NK_ERR_UNSUPPORTED;
+    if (!decode_tc_supported(fmt, D, Tc, G, P) && !decode_mma_supported(fmt, D, Tc, G, P)) return NK_ERR_UNSUPPORTED;
   }
   const int per_sm = rk_tc ? decode_mma_ctas_per_sm(D, T, G)
                      : path == Path::kRk8v4 ? decode_rk8v4_ctas_per_sm(D, G)
@@ -190,7 +175,7 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   if (!simt || rk_tc) {
     const int Tl = T - (T - 1) / Tc * Tc;  // columns of the last chunk
     const bool mma_kernel =
-        rk_tc || !on_tc(path, fmt, D, Tc, G, P) || !on_tc(path, fmt, D, Tl, G, P);
+        rk_tc || !decode_tc_supported(fmt, D, Tc, G, P) || !decode_tc_supported(fmt, D, Tl, G, P);
     const int64_t unit = ((int64_t)seen + P - 1) / P;
     const int64_t per_cta = (max_items(B, Hkv, seen, P) + n - 1) / n;
     if (mma_kernel && (per_cta < unit ? per_cta : unit) * P > kMaxMmaRunKeys) return NK_ERR_UNSUPPORTED;
@@ -237,7 +222,7 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
 }
 
 int launch_decode(const DecodeParams& p0, Path path, cudaStream_t st) {
-  const int Tc = cols_of(path, p0.fmt, p0.D, p0.T, p0.G, p0.P);
+  const int Tc = chunk_cols(!tensor_path(path), p0.fmt, p0.D, p0.T, p0.G, p0.P);
   const int64_t slots = (int64_t)p0.n_ctas + (int64_t)p0.B * p0.Hkv;
   for (int t0 = 0; t0 < p0.T; t0 += Tc) {
     DecodeParams p = p0;
@@ -253,7 +238,7 @@ int launch_decode(const DecodeParams& p0, Path path, cudaStream_t st) {
     cudaError_t e = path == Path::kRk8v4 ? (decode_mma_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_mma(p, st)
                                                                                           : launch_decode_rk8v4(p, st))
                     : path == Path::kSimt   ? launch_decode_simt(p, st)
-                    : (on_tc(path, p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st) : launch_decode_mma(p, st));
+                    : (decode_tc_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st) : launch_decode_mma(p, st));
     if (e != cudaSuccess) return NK_ERR_CUDA;
     e = launch_decode_combine(p, st);
     if (e != cudaSuccess) return NK_ERR_CUDA;

@@ -62,6 +62,10 @@ namespace mma {
 constexpr int kConsumerWarps = 8;
 constexpr int kThreads = kConsumerWarps * 32;
 constexpr int kSmemLimit = 232448;  // opt-in shared memory per block on sm_100/103
+// Pages in flight, at most. Eight 64-key pages fill shared memory at head dim
+// 256; a ring of small pages (16 keys: one block, so one team's step) needs
+// more of them to cover a load's latency.
+constexpr int kMaxStages = 32;
 
 struct Geometry {
   int stage_bytes;   // one page: K|V boxes, then Ks, Vs (rounded to 1 KB)
@@ -90,11 +94,11 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   g.xch_bytes = CS > 1 ? nteams * 2 * CS * NT * 4 * 32 * 4 : 0;
   const int mrows = NT * 8;
   g.merge_bytes = mrows * (D + 4) * 4 + 3 * nteams * mrows * 4 + mrows * 4;
-  const int pre_bytes = round_up((2 * B + 33) * 4, 16);  // pre[B+1], warp_tot, flags, lens[B], icnt[8]
+  const int pre_bytes = round_up((2 * B + 10 + 2 * kMaxStages) * 4, 16);  // pre[B+1], warp_tot[8], abort, cnt, lens[B], icnt
   const int pid_bytes = 1024 * 4;
-  const int fixed = g.xch_bytes + g.merge_bytes + pre_bytes + pid_bytes + 8 * 2 * 8 + 1024;
+  const int fixed = g.xch_bytes + g.merge_bytes + pre_bytes + pid_bytes + 2 * kMaxStages * 8 + 1024;
   int s = (kSmemLimit - fixed) / g.stage_bytes;
-  if (s > 8) s = 8;
+  if (s > kMaxStages) s = kMaxStages;
   g.stages = s;
   int off = g.stages * g.stage_bytes;
   g.xch_off = off;
@@ -106,7 +110,7 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   g.pid_off = off;
   off += pid_bytes;
   g.bar_off = off;
-  off += 2 * 8 * 8;
+  off += 2 * kMaxStages * 8;
   g.total = off + 1024;  // slack to align the dynamic base to 1 KB
   return g;
 }
@@ -438,12 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   int* pre = reinterpret_cast<int*>(smem + geo.pre_off);
   int* warp_tot = pre + (p.B + 1);
   volatile int* abort_flag = pre + (p.B + 1) + 8;
-  int* cnt = pre + (p.B + 1) + 9;  // [8] consumer count per stage
-  int* lens = pre + (p.B + 1) + 24;  // [B] context lengths
-  int* icnt = lens + p.B;            // [8] copies issued into each stage
+  int* cnt = pre + (p.B + 1) + 9;    // [kMaxStages] consumer count per stage
+  int* lens = cnt + kMaxStages;      // [B] context lengths
+  int* icnt = lens + p.B;            // [kMaxStages] copies issued into each stage
   int* pid = reinterpret_cast<int*>(smem + geo.pid_off);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + geo.bar_off);
-  uint64_t* empty_bar = full_bar + 8;
+  uint64_t* empty_bar = full_bar + kMaxStages;
   float* xch = reinterpret_cast<float*>(smem + geo.xch_off);
   float* mo = reinterpret_cast<float*>(smem + geo.merge_off);
   float* tm_m = mo + MROWS * (D + 4);

@@ -203,7 +203,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // SB: bytes of a group scale (4: fp32 scales; 2: the pages' fp16 scales).
 // FOLD: the PV accumulators are folded into a tensor-memory total every
 // kFoldPages pages.
-template <int W, int NT, int SB, bool FOLD>
+// WIN: sliding window with sinks (nk_common.cuh, WindowShape): the units own
+// the visible pages only, and pages that straddle an end of a column's window
+// or the sinks are masked per column.
+template <int W, int NT, int SB, bool FOLD, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                 const DecodeParams p) {
   // the tensor map is a launch parameter: its descriptor fetch can start
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int role = warp < kConvWarps ? 0 : (warp < kConvWarps + kScoreWarps ? 1 : 2);  // convert | score | PV
   const int quad = warp & 3;  // tensor-memory lane quadrant this warp may access
-  const SplitShape sh = p.shape();
+  const auto sh = p.shape_of<WIN>();
   const int G = p.G, T = p.T, M = G * T;
 
   if (tid == 0) {
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   // Every global read of the prologue (page coordinates up to the cache
   // size, the first unit's Q lines) goes out before the first page load.
   const int ncache = total < kPidCache ? total : kPidCache;
-  for (int q = tid; q < ncache; q += kThreads) pid[q] = page_coord(p, sh, pre, x_begin, q);
+  for (int q = tid; q < ncache; q += kThreads) pid[q] = page_coord(p, sh, pre, lens, x_begin, q);
   if (role == 0 && total > 0) {
     int64_t x0 = x_begin;
     Segment s0;
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const int qn = q + S;
         if (qn < total && p.issuable(qn) && !*abort_flag) {
           if (mbar_wait(smem_u32(&empty_bar[s]), ph, p.wait_cycles)) {
-            issue_page<kD>(p, &tmap, qn < kPidCache ? pid[qn] : page_coord(p, sh, pre, x_begin, qn),
+            issue_page<kD>(p, &tmap, qn < kPidCache ? pid[qn] : page_coord(p, sh, pre, lens, x_begin, qn),
                            stage0 + s * kStageBytes, smem_u32(&full_bar[s]));
             ++icnt[s];
           } else {
@@ -519,13 +522,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         named_bar(2, kScoreWarps * 32);
         kq = p.scale2 * pow2i(-q_norm_exp(fmaxf(fmaxf(qmx[4], qmx[5]), fmaxf(qmx[6], qmx[7]))));
       }
+      // WIN: logical page of the unit's page number i: i, or i + gap from page `lead` on
+      int lead = 0, gap = 0;
+      if constexpr (WIN) {
+        int first;
+        window_pages(sh, L, first, lead);
+        gap = first - lead;
+      }
       for (int j = 0; j < npages; ++j) {
         const int q = q0 + j;
+        int lp = seg.page_begin + j;  // logical page
+        if constexpr (WIN) lp += lp >= lead ? gap : 0;
         wait_bar(&full_bar[s], ph);  // scale arrays of the page visible
         const uint8_t* st = smem + s * kStageBytes;
         const uint8_t* ks_s = st + 2 * kP * kD;           // [64 keys][4 groups], fp32 or fp16
         const uint8_t* vs_s = ks_s + kP * (kD / kGroup) * sb;
-        const int pos = (seg.page_begin + j) * kP + key;
+        const int pos = lp * kP + key;
         const bool key_valid = pos < L;
         // P' window of each group, while the page's QK runs: bit g set when a
         // key's Vs 2^-ev passes 2^6 (p Vs 2^-ev could reach 2^15), bit 4 + g
@@ -602,11 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
         // ---- causal / context mask: only pages that reach past L - T (padding rows
         // hold zero queries and are never written out, so they need no mask)
-        if ((seg.page_begin + j + 1) * kP > L - T) {
+        if ((lp + 1) * kP > L - T) {
           const int lim = pos - (L - T);  // visible to column t when lim <= t
 #pragma unroll
           for (int i = 0; i < NR; ++i)
             if (lim > row_t[8 * (i >> 2) + 4 * half + (i & 3)]) sc[i] = -INFINITY;
+        }
+        if constexpr (WIN) {
+          // pages with a key before the last column's window, past the sinks
+          if (lp * kP <= L - 1 - sh.window && lp * kP + kP - 1 >= sh.sinks && pos >= sh.sinks) {
+            const int lim = pos + sh.window - (L - T);  // hidden from column t when lim <= t
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+              if (lim <= row_t[8 * (i >> 2) + 4 * half + (i & 3)]) sc[i] = -INFINITY;
+          }
         }
         // ---- lazy reference: raised when a score passes it by more than 8
         bool over = false;
@@ -947,29 +968,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
   }
 }
 
-template <int W, int NT, int SB, bool FOLD>
+template <int W, int NT, int SB, bool FOLD, bool WIN = false>
 static cudaError_t launch_tsf(const CUtensorMap& map, const DecodeParams& p, cudaStream_t st) {
   const Layout LY = layout(W, NT, SB);
   if (LY.stages < 2 || LY.total > kSmemLimit) return cudaErrorInvalidConfiguration;
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(decode_tc_kernel<W, NT, SB, FOLD>), LY.total);
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(decode_tc_kernel<W, NT, SB, FOLD, WIN>), LY.total);
   if (e != cudaSuccess) return e;
   // the register shares assume the launch count they were split from
   static int regs = -1;
   if (regs < 0) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, decode_tc_kernel<W, NT, SB, FOLD>);
+    e = cudaFuncGetAttributes(&fa, decode_tc_kernel<W, NT, SB, FOLD, WIN>);
     if (e != cudaSuccess) return e;
     regs = fa.numRegs;
   }
   if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_chained(decode_tc_kernel<W, NT, SB, FOLD>, dim3(p.n_ctas), dim3(kThreads), LY.total, st, map, p);
+  return launch_chained(decode_tc_kernel<W, NT, SB, FOLD, WIN>, dim3(p.n_ctas), dim3(kThreads), LY.total, st, map, p);
 }
 
 // The most pages of one kv-head a CTA may run: a CTA takes at most
 // ceil(items / CTAs) consecutive (page, kv-head) items, and a kv-head of a
 // sequence holds at most ceil(max_ctx / P) pages.
 static int64_t max_run_pages(const DecodeParams& p) {
-  const int64_t unit = ((int64_t)p.max_ctx + kP - 1) / kP;
+  int64_t unit = ((int64_t)p.max_ctx + kP - 1) / kP;
+  if (p.window > 0) {  // the window's pages and the sinks'
+    const int64_t seen = ((int64_t)p.window + p.T - 1 + kP - 2) / kP + 1 + ((int64_t)p.sinks + kP - 1) / kP;
+    if (seen < unit) unit = seen;
+  }
   const int64_t items = unit * p.B * p.Hkv;
   const int64_t per_cta = (items + p.n_ctas - 1) / p.n_ctas;
   return per_cta < unit ? per_cta : unit;
@@ -983,6 +1008,9 @@ static cudaError_t launch_ts(const CUtensorMap& map, const DecodeParams& p, cuda
 
 template <int W, int NT>
 static cudaError_t launch_t(const CUtensorMap& map, const DecodeParams& p, cudaStream_t st) {
+  if (p.window > 0)  // fp32 scales only (nk_paged_window_attn)
+    return max_run_pages(p) > kNoFoldPages ? launch_tsf<W, NT, 4, true, true>(map, p, st)
+                                           : launch_tsf<W, NT, 4, false, true>(map, p, st);
   return scale_bytes(p.fmt) == 2 ? launch_ts<W, NT, 2>(map, p, st) : launch_ts<W, NT, 4>(map, p, st);
 }
 
