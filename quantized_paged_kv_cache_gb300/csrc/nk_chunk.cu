@@ -14,10 +14,12 @@
 // Operands: Q (bf16, scaled per row by a power of two into the fp16 range) and
 // P are A operands in tensor memory; K and V are B operands in shared memory,
 // dequantized to fp16: code * fp16(scale * 2^-e), two roundings of at most
-// 2^-11 relative each where the output's bf16 rounding is 2^-8. The exponent e
-// keeps the products inside the fp16 range for any pool: one per block for K
-// (undone on the scores), one per 64-channel group for V, moved only when a
-// block's scales leave its window (the accumulator is then rescaled).
+// 2^-11 relative each where the output's bf16 rounding is 2^-8 (a row whose
+// scale is below 2^-8 of its block's largest keeps fewer bits, never fewer
+// than 2^-25 of that largest). The exponent e keeps the products inside the
+// fp16 range for any pool: one per block for K (undone on the scores), one per
+// 64-channel group for V, moved only when a block's scales leave its window
+// (the accumulator is then rescaled).
 //
 // 16 warps in four warpgroups, one CTA per SM:
 //   warps 0-3   softmax: S from tensor memory, masks, running maximum with a
@@ -51,8 +53,6 @@ namespace chunk {
 
 using mma::ex2;
 using mma::exp_of;
-using mma::ev_update;
-using mma::i8x2_to_f16x2;
 using mma::kEvUnset;
 using mma::kSmemLimit;
 using mma::named_bar;
@@ -67,7 +67,14 @@ constexpr int kThreads = (kMmaWarp + 4) * 32;  // whole warpgroups, for setmaxnr
 // Registers per thread: launched with 128 (512 threads, the whole file); the
 // shares below add up to 4 * 128, so no increase waits for registers that are
 // not there (checked on the host against the compiled count).
-constexpr int kLaunchRegs = 128, kRegsSoft = 200, kRegsConv = 136, kRegsMma = 40;
+constexpr int kLaunchRegs = 128, kRegsSoft = 184, kRegsConv = 128, kRegsMma = 72;
+// setmaxnreg.inc must not lower a count, .dec must not raise one (an illegal instruction otherwise).
+template <int N>
+__device__ __forceinline__ void set_regs() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg takes multiples of 8");
+  if constexpr (N > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+  if constexpr (N < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
 static_assert(kRegsSoft + 2 * kRegsConv + kRegsMma == 4 * kLaunchRegs, "shares = the launch's registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256)
@@ -80,7 +87,8 @@ struct Smem {
   static constexpr int off_v = 2 * kTile;      // [2]
   static constexpr int kStage = kKeys * (2 * D + 2 * (D / 64) * 4);  // raw block: K codes | K scales | V codes | V scales
   static constexpr int off_ring = 4 * kTile;                         // [kStages]
-  static constexpr int off_pre = off_ring + kStages * kStage;        // int64 [kMaxBatch + 1]: blocks before sequence b
+  static constexpr int off_tab = off_ring + kStages * kStage;        // [8 convert warps][16 keys][D / 64] scales
+  static constexpr int off_pre = off_tab + 8 * 16 * (D / 64) * 8;    // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_lens = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch]
   static constexpr int off_cu = off_lens + kMaxBatch * 4;         // int [kMaxBatch + 1]
   static constexpr int off_misc = off_cu + (kMaxBatch + 4) * 4;
@@ -212,6 +220,25 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32])
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+// Two codes as fp16: u = code + 128 in the low byte of each half is, read as
+// fp16, the subnormal u 2^-24; one fma forms (u - 128) 2^-24 S from S and
+// -S 2^-17 with a single rounding.
+__device__ __forceinline__ uint32_t scale_codes(uint32_t u2, __half2 s, __half2 bias) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u2), s, bias);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+constexpr float kOperand = 32768.f;  // 2^15: an operand holds its value times 2^-(ev + 15)
+
+// New exponent of a group whose largest scale has exponent E: S = s 2^(9 - ev)
+// then lies in [2^11, 2^12), two octaves below where the group moves up and
+// five above where it moves down. beta = 2^(ev_old - ev_new).
+__device__ __forceinline__ void move_exponent(int& ev, int E, float& beta) {
+  const int ne = E - 2 < -110 ? -110 : E - 2;
+  const int d = ev == kEvUnset ? 0 : ev - ne;
+  beta = d < -126 ? 0.f : pow2i(d > 127 ? 127 : d);
+  ev = ne;
 }
 
 template <int D>
@@ -393,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (tid == 0 && cta < p.n_ctas) p.desc[cta] = make_int4(0, -1, 0, 0);
   } else if (warp < kSoftWarps) {
     // ======================================================= softmax warps
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft) : "memory");
+    set_regs<kRegsSoft>();
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const int row = warp * 32 + lane;
     Walk w = w0;
@@ -462,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         tm_ld32(scol, lo);
         tm_ld32(scol + 32, hi);
         // the factor of the raw scores, kept a normal number (a masked -inf times 0 would be NaN)
-        const float f = fminf(fmaxf(kq * kfac[j & 3], 1.2e-38f), 3.4e38f);
+        const float f = fminf(fmaxf(kq * kfac[j & 3] * kOperand, 1.2e-38f), 3.4e38f);
         wait_ld();
         float s[64];
 #pragma unroll
@@ -546,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       if (more) kq = load_q();
       wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1);
       fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l > 0.f ? kOperand / l : 0.f;
       bool finite = true;
       const int64_t slot = 2 * (int64_t)cta + (head ? 1 : 0);
       uint16_t* orow = p.out + ((int64_t)(base_row + (live ? r : 0) / p.G) * p.Hq + at.h * p.G + (live ? r : 0) % p.G) * D;
@@ -602,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (!have_desc && row == 0) p.desc[cta] = make_int4(0, -1, 0, 0);
   } else if (warp < kMmaWarp) {
     // ======================================================= convert warps
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConv) : "memory");
+    set_regs<kRegsConv>();
     const bool isv = warp >= kSoftWarps + kConvWarps;
     const int cw = (warp - kSoftWarps) & 3;  // keys 16 cw .. 16 cw + 15 of a block
     // Lane -> (key, 16-channel piece) of a load: a quarter warp takes four
@@ -614,88 +641,107 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int kk = D == 256 ? kp : (D == 128 ? (qt >> 1) * 2 + kp : qt * 2 + kp);
     const int ck = D == 64 ? lane & 3 : ((lane & 3) | (((qt ^ kp) & 1) << 2) | (D == 256 ? (qt >> 1) << 3 : 0));
     const int grp = ck >> 2;
-    const int raw_off = isv ? kKeys * (D + G64 * 4) : 0;
+    // raw rows and scales of this warp's keys in a stage
+    const uint32_t raw0 = smem_u32(smem + SM::off_ring) + (isv ? kKeys * (D + G64 * 4) : 0);
+    const uint32_t codes0 = raw0 + (cw * 16 + kk) * D + ck * 16, scales0 = raw0 + kKeys * D + (cw * 16 * G64 + lane) * 4;
+    // this warp's table of scales: (S, -S 2^-17) as fp16 pairs, [16 keys][G64]
+    const uint32_t tab0 = smem_u32(smem + SM::off_tab) + (warp - kSoftWarps) * (16 * G64 * 8);
+    constexpr int NS = (16 * G64 + 31) / 32;  // scales of a lane (group lane % G64; one of two lanes at head dim 64)
+    const bool has_scale = D > 64 || lane < 16;
+    const int sgrp = isv ? lane % G64 : 0;    // group whose exponent they follow
+    // store addresses: row (i KPI + kk) of the buffer, chunks 2 (ck & 3) and + 1 swizzled by the row mod 8; rows
+    // repeat their swizzle every 8 / KPI loads
+    constexpr int NA = 8 / KPI > 1 ? 8 / KPI : 1;
+    uint32_t sa[NA][2];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        sa[i][c] = (isv ? vbuf : kbuf) + grp * (kKeys * 128) + (cw * 16 + i * KPI + kk) * 128 +
+                   ((((ck & 3) * 2 + c) ^ ((i * KPI + kk) & 7)) << 4);
     uint64_t* full = isv ? vfull : kfull;
     uint64_t* done = isv ? pvdone : qkdone;
-    const uint32_t buf = isv ? vbuf : kbuf;
     int* votes_w = votes + (isv ? 8 : 0);
     const int bar_id = isv ? 2 : 1;
     const int total = (int)(w0.end - w0.x);
     bool bad_scale = false;
     int ev[4] = {kEvUnset, kEvUnset, kEvUnset, kEvUnset};
-    int my = kEvUnset;  // the exponent of this thread's group
+    float inv_e = 0.f;  // 2^-ev of the lane's group (0: not set)
     int st = 0;
     uint32_t ph = 0;
     for (int j = 0; j < total; ++j) {
       wait_bar(&rfull[st], ph);
-      const uint8_t* raw = smem + SM::off_ring + st * SM::kStage + raw_off;
       const int inf = info[st];
       const bool first = (inf >> 8) & 1;
       const int there = ((inf >> (16 + cw)) & 1) ? 0 : (inf & 0xff) - cw * 16;  // keys of this warp's 16 that exist
       uint4 w[NI];
-      float s[NI];
+      float s[NS];
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[i]) : "r"(scales0 + st * SM::kStage + i * 128));
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                     : "r"(codes0 + st * SM::kStage + i * (KPI * D)));
       float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int key = cw * 16 + i * KPI + kk;
-        s[i] = *reinterpret_cast<const float*>(raw + kKeys * D + (key * G64 + grp) * 4);
-        w[i] = *reinterpret_cast<const uint4*>(raw + key * D + ck * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        if (i * KPI + kk >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
-        if (!(s[i] <= 3.0e38f)) {               // the append of a non-finite row: zeros too, flagged
+      for (int i = 0; i < NS; ++i) {
+        if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
+        if (!(s[i] <= 3.0e38f)) {  // the append of a non-finite row: zeros too, flagged
           s[i] = 0.f;
           bad_scale = true;
         }
         mx = fmaxf(mx, s[i]);
       }
-      // ---- exponents: a group moves when a scale passes 2^6 of it, or none of the block's reaches 2^-10
-      constexpr int NG = G64;
-      if (isv && first) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) ev[g] = kEvUnset;
-        my = kEvUnset;
-      }
-      uint32_t bits = 0u;
-      if (my != kEvUnset) {
-        const float t = mx * pow2i(-my);
-        bits = ((t > 64.f ? 1u : 0u) | (t >= 0.0009765625f ? 16u : 0u)) << (isv ? grp : 0);
-      }
-      bits = __reduce_or_sync(0xffffffffu, bits);
+      // ---- exponents: a group moves when a scale passes 2^6 of it, or none of the block's reaches 2^-2
+      if (isv && first) inv_e = 0.f;
+      const float t = mx * inv_e;
+      const uint32_t bits =
+          __reduce_or_sync(0xffffffffu, ((t > 64.f ? 1u : 0u) | (t >= 0.25f ? 16u : 0u)) << sgrp);
       int* vote = votes_w + (j & 1) * 4;
-      if (lane == 0) {
-        vote[cw] = (int)bits;
-        mbar_arrive(smem_u32(&rfree[st]));  // the raw block is in registers (every lane has passed the reduction)
-      }
+      if (lane == 0) vote[cw] = (int)bits;
       named_bar(bar_id, kConvWarps * 32);
-      bits = (uint32_t)(vote[0] | vote[1] | vote[2] | vote[3]);
-      constexpr uint32_t all = (1u << NG) - 1u;
-      const uint32_t moving = ((bits & 15u) | (~(bits >> 4) & 15u)) & (isv ? all : 1u);
+      const int4 v4 = *reinterpret_cast<const int4*>(vote);
+      const uint32_t seen = (uint32_t)(v4.x | v4.y | v4.z | v4.w);
+      const uint32_t moving = ((seen & 15u) | (~(seen >> 4) & 15u)) & (isv ? (1u << G64) - 1u : 1u);
       float beta[4] = {1.f, 1.f, 1.f, 1.f};
       if (moving) {
         float* mxs = maxima + (isv ? 16 : 0);
+        if (isv && first) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t v = __reduce_max_sync(0xffffffffu, (!isv || grp == g) ? __float_as_uint(mx) : 0u);
+          for (int g = 0; g < 4; ++g) ev[g] = kEvUnset;
+        }
+#pragma unroll
+        for (int g = 0; g < G64; ++g) {
+          const uint32_t v = __reduce_max_sync(0xffffffffu, (!isv || sgrp == g) ? __float_as_uint(mx) : 0u);
           if (lane == 0) mxs[cw * 4 + g] = __uint_as_float(v);
         }
         named_bar(bar_id, kConvWarps * 32);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < G64; ++g) {
           if (!((moving >> g) & 1u)) continue;
-          const float m4 = isv ? fmaxf(fmaxf(mxs[g], mxs[4 + g]), fmaxf(mxs[8 + g], mxs[12 + g]))
-                               : fmaxf(fmaxf(mxs[0], mxs[4]), fmaxf(mxs[8], mxs[12]));
-          if (m4 > 0.f) (void)ev_update(ev[g], exp_of(m4), beta[g]);
+          const float m4 = fmaxf(fmaxf(mxs[g], mxs[4 + g]), fmaxf(mxs[8 + g], mxs[12 + g]));
+          if (m4 > 0.f) move_exponent(ev[g], exp_of(m4), beta[g]);
         }
         named_bar(bar_id, kConvWarps * 32);  // maxima read before a later block writes them
-        my = ev[0];
-        if (isv) {
+        int e = ev[0];
 #pragma unroll
-          for (int g = 1; g < NG; ++g) my = grp == g ? ev[g] : my;
-        }
+        for (int g = 1; g < G64; ++g) e = sgrp == g ? ev[g] : e;
+        inv_e = e == kEvUnset ? 0.f : pow2i(-e);
       }
-      const float down = my == kEvUnset ? 1.f : pow2i(-my);
+      // ---- the scales as fp16: S = s 2^(9 - ev) (zero where there is none)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const __half2 sc = __float2half2_rn(s[i] * inv_e * 512.f);
+        const __half2 bias = __hmul2(sc, __float2half2_rn(-7.62939453125e-6f));  // -S 2^-17
+        if (has_scale)
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tab0 + (lane + 32 * i) * 8),
+                       "r"(*reinterpret_cast<const uint32_t*>(&sc)), "r"(*reinterpret_cast<const uint32_t*>(&bias))
+                       : "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&rfree[st]));  // every lane holds its part of the raw block
       // ---- the buffer's previous block has been multiplied
       wait_bar(&done[j & 1], ((j >> 1) & 1) ^ 1);
       if (cw == 0 && lane == 0) {
@@ -711,30 +757,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
           }
         } else {
-          kfac[j & 3] = my == kEvUnset ? 1.f : pow2i(my);
+          kfac[j & 3] = ev[0] == kEvUnset ? 1.f : pow2i(ev[0]);
         }
       }
-      const uint32_t dst = buf + (j & 1) * SM::kTile + grp * (kKeys * 128) + (cw * 16 + kk) * 128;
+      const uint32_t half_off = (j & 1) * SM::kTile;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const __half2 sc = __float2half2_rn(s[i] * down);
+        uint32_t scu, biu;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(scu), "=r"(biu)
+                     : "r"(tab0 + ((i * KPI + kk) * G64 + grp) * 8)
+                     : "memory");
+        const __half2 sc = *reinterpret_cast<const __half2*>(&scu), bi = *reinterpret_cast<const __half2*>(&biu);
         const uint32_t w4[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
         uint32_t h[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t a = i8x2_to_f16x2(w4[k], 0x4140), b = i8x2_to_f16x2(w4[k], 0x4342);
-          const __half2 pa = __hmul2(*reinterpret_cast<const __half2*>(&a), sc);
-          const __half2 pb = __hmul2(*reinterpret_cast<const __half2*>(&b), sc);
-          h[2 * k] = *reinterpret_cast<const uint32_t*>(&pa);
-          h[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&pb);
+          h[2 * k] = scale_codes(mma::prmt(w4[k], 0u, 0x4140), sc, bi);
+          h[2 * k + 1] = scale_codes(mma::prmt(w4[k], 0u, 0x4342), sc, bi);
         }
-        // i * KPI is a multiple of 8 at head dim 64, else the row moves within its group of eight
-        const int r7 = (i * KPI + kk) & 7, c0 = (ck & 3) * 2;
-        const uint32_t row = dst + i * (KPI * 128);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c0 ^ r7) << 4)), "r"(h[0]), "r"(h[1]),
+        const uint32_t o = half_off + (i / NA) * (NA * KPI * 128);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sa[i % NA][0] + o), "r"(h[0]), "r"(h[1]),
                      "r"(h[2]), "r"(h[3]));
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c0 + 1) ^ r7) << 4)), "r"(h[4]),
-                     "r"(h[5]), "r"(h[6]), "r"(h[7]));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sa[i % NA][1] + o), "r"(h[4]), "r"(h[5]),
+                     "r"(h[6]), "r"(h[7]));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -747,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) flag(p.status, NK_DEVFLAG_RANGE);
   } else {
     // ======================================================= MMA warp
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma) : "memory");
+    set_regs<kRegsMma>();
     if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t id_qk = idesc_f16_f32(kRows, kKeys, false), id_pv = idesc_f16_f32(kRows, D, true);
       const int total = (int)(w0.end - w0.x);
