@@ -167,7 +167,9 @@ __device__ __forceinline__ int blocks_left(const Walk& w) {
   return w.s.blocks - w.v < left ? w.s.blocks - w.v : (int)left;
 }
 
-__device__ __forceinline__ int block_of(const Walk& w) { return w.v < w.s.lead ? w.v : w.v - w.s.lead + w.s.first; }
+// Key block number v of a tile.
+__device__ __forceinline__ int block_at(const TileSpan& s, int v) { return v < s.lead ? v : v - s.lead + s.first; }
+__device__ __forceinline__ int block_of(const Walk& w) { return block_at(w.s, w.v); }
 
 // ---------------------------------------------------------------------------
 // PTX
@@ -176,21 +178,24 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 128-byte-swizzled operand in shared memory, atoms of 8 rows of 128 bytes.
-// K-major (K: a row is a key, 64 channels wide): `step8` bytes between groups
-// of 8 keys; `wide` is not used. MN-major (V: a row is a key, 64 channels of
-// the N dimension wide): step8 between groups of 8 keys, wide between groups
-// of 64 channels.
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t wide, uint32_t step8) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((wide >> 4) & 0x3fff) << 16) |
-         ((uint64_t)((step8 >> 4) & 0x3fff) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// 128-byte-swizzled operand in shared memory, atoms of 8 rows (keys) of 128
+// bytes (64 channels), 1,024 bytes apart. K-major (K): `wide` is not used.
+// MN-major (V, channels are the N dimension): wide bytes between groups of 64
+// channels.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr, uint32_t wide) { return (addr >> 4) | ((wide >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // 1,024 bytes between groups of 8 keys; swizzle
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = *tslot;  // 0: all of the SM's columns
   const Tables tab{pre, lens, cus};
   if (!idle) {
     w0.b = start[0];
@@ -406,12 +411,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const bool work = !idle && w0.x < w0.end;
 
   // A bounded wait; once one has run out no wait blocks any more, no MMA is
-  // issued, and the end of the kernel waits for those that were.
+  // issued, and the end of the kernel waits for those that were. (The flag is
+  // read only while a wait blocks: a read of shared memory in front of every
+  // wait was a tenth of a block's time.)
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) {
-    if (*abort_flag) return;
-    if (!mbar_wait(smem_u32(bar), parity, p.wait_cycles)) {
-      if (lane == 0) flag(p.status, NK_DEVFLAG_TIMEOUT);
-      *abort_flag = 1;
+    const uint32_t at = smem_u32(bar);
+    if (mbar_try_wait(at, parity)) return;
+    const unsigned long long t0 = clock64();
+    while (!mbar_try_wait(at, parity)) {
+      if (*abort_flag) return;
+      if (clock64() - t0 > p.wait_cycles) {
+        if (lane == 0) flag(p.status, NK_DEVFLAG_TIMEOUT);
+        *abort_flag = 1;
+        return;
+      }
     }
   };
   const uint32_t kbuf = smem_u32(smem + SM::off_k), vbuf = smem_u32(smem + SM::off_v);
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       float unscale[G64];
       const Walk at = w;  // the tile, for the output
       for (int i = 0; i < nblk; ++i, ++j) {
-        const int key0 = block_of(w) * kKeys;
+        const int key0 = block_at(w.s, w.v + i) * kKeys;
         wait_bar(&qkdone[j & 1], (j >> 1) & 1);
         fence_after();
         const uint32_t scol = lane_base + kColS + (j & 1) * 64;
@@ -566,8 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&pfull[j & 1]));
-        more = step(p, tab, w);
       }
+      w.x += nblk;
+      w.v += nblk;
+      more = w.x < w.end;
+      if (more) next_tile(p, tab, w);
       // the next tile's Q while the last products run (its QKs wait for it;
       // this tile's have all completed)
       if (more) kq = load_q();
@@ -794,43 +810,58 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   } else {
     // ======================================================= MMA warp
     set_regs<kRegsMma>();
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
+      // The whole warp runs the loop and one elected lane issues. All 512
+      // columns are this CTA's, so tensor memory starts at address 0: with
+      // that and the warp's uniform loop every operand of an MMA is a uniform
+      // register (a lane on its own paid some 75 cycles an MMA to move them).
       constexpr uint32_t id_qk = idesc_f16_f32(kRows, kKeys, false), id_pv = idesc_f16_f32(kRows, D, true);
+      const bool leader = elect_one();
       const int total = (int)(w0.end - w0.x);
-      int j = 0, seg = 0;
-      auto pv = [&](int q, bool accumulate) {
+      const uint32_t k_lo = sdesc_lo(kbuf, 16), v_lo = sdesc_lo(vbuf, kKeys * 128);
+      int j = 0, seg = 0, left = 0;  // blocks, segments, blocks left of the segment
+      bool fresh = true;             // the segment's first PV is still to come
+      auto pv = [&](int q) {
         wait_bar(&vfull[q & 1], (q >> 1) & 1);
         wait_bar(&pfull[q & 1], (q >> 1) & 1);
-        if (!*abort_flag) {
+        if (*abort_flag) return;
+        if (leader) {
           fence_after();
-          const uint32_t a = tmem + kColS + (q & 1) * 64, v0 = vbuf + (q & 1) * SM::kTile;
+          const uint32_t a = kColS + (q & 1) * 64, v0 = v_lo + (q & 1) * (SM::kTile >> 4);
 #pragma unroll
           for (int ks = 0; ks < kKeys / 16; ++ks)
-            mma_ts(tmem + kColO, a + ks * 8, sdesc(v0 + ks * 2048, kKeys * 128, 1024), id_pv, accumulate || ks > 0);
+            mma_ts(kColO, a + ks * 8, v0 + ks * (2048 >> 4), id_pv, ks > 0 || !fresh);
           mma_commit(smem_u32(&pvdone[q & 1]));
           last_mma[1] = q;
         }
+        fresh = false;
       };
       while (j < total) {
         wait_bar(qfull, seg & 1);
-        const int nblk = *abort_flag ? total - j : seg_blocks[seg & 1];
-        for (int i = 0; i < nblk; ++i, ++j) {
+        left = *abort_flag ? total - j : seg_blocks[seg & 1];
+        for (int i = 0; i < left; ++i, ++j) {
           wait_bar(&kfull[j & 1], (j >> 1) & 1);
-          if (!*abort_flag) {
+          if (!*abort_flag && leader) {
             fence_after();
-            const uint32_t k0 = kbuf + (j & 1) * SM::kTile;
+            const uint32_t k0 = k_lo + (j & 1) * (SM::kTile >> 4), d = kColS + (j & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              mma_ts(tmem + kColS + (j & 1) * 64, tmem + kColQ + ks * 8,
-                     sdesc(k0 + (ks / 4) * (kKeys * 128) + (ks % 4) * 32, 16, 1024), id_qk, ks > 0);
+              mma_ts(d, kColQ + ks * 8, k0 + (((ks / 4) * (kKeys * 128) + (ks % 4) * 32) >> 4), id_qk, ks > 0);
             mma_commit(smem_u32(&qkdone[j & 1]));
             last_mma[0] = j;
           }
+          __syncwarp();
+          if (i == 0) {
+            fresh = true;
+            continue;  // the first product of a segment goes out after its second QK
+          }
           if (i == 1 && seg > 0) wait_bar(ofree, (seg - 1) & 1);
-          if (i > 0) pv(j - 1, i > 1);
+          pv(j - 1);
+          __syncwarp();
         }
-        if (nblk == 1 && seg > 0) wait_bar(ofree, (seg - 1) & 1);
-        pv(j - 1, nblk > 1);
+        if (left == 1 && seg > 0) wait_bar(ofree, (seg - 1) & 1);
+        pv(j - 1);
+        __syncwarp();
         ++seg;
       }
     }
