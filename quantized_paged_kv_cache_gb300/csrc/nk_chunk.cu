@@ -17,22 +17,23 @@
 // 2^-11 relative each where the output's bf16 rounding is 2^-8 (a row whose
 // scale is below 2^-8 of its block's largest keeps fewer bits, never fewer
 // than 2^-25 of that largest). The exponent e keeps the products inside the
-// fp16 range for any pool: one per block for K (undone on the scores), one per
-// 64-channel group for V, moved only when a block's scales leave its window
-// (the accumulator is then rescaled).
+// fp16 range for any pool. It is one of 16 keys, undone on the scores for K and
+// put into the weights for V (P carries 2^(e - e_ref) beside exp2(S - m)).
 //
-// 16 warps in four warpgroups, one CTA per SM:
-//   warps 0-3   softmax: S from tensor memory, masks, running maximum with a
+// 28 warps in seven warpgroups, one CTA per SM:
+//   warps 0-7   softmax, two threads a row, 32 keys each: S from tensor memory, masks, running maximum with a
 //               lazy reference (moved only when a score passes it by more than
 //               8, so the accumulator is rarely rescaled), P back to tensor
 //               memory over S, row sums, and the tile's output;
-//   warps 4-7   K blocks, warps 8-11 V blocks: codes and scales from the ring,
-//               widened to fp16, scaled, stored to one of two
-//               128-byte-swizzled operand buffers;
-//   warp 12     issues the MMAs: QK of block j + 1 goes out before PV of block
+//   warps 8-23  K and V blocks, of even and of odd number (four warps each):
+//               codes and scales from the ring, widened to fp16, scaled,
+//               stored to the operand buffer of that parity; a warp's chain of
+//               waits, loads and stores is longer than a block's time, so two
+//               blocks are under way;
+//   warp 24     issues the MMAs: QK of block j + 1 goes out before PV of block
 //               j, so the tensor cores work while the softmax does;
-//   warp 13     looks up the pages and fills a two-stage ring of raw blocks
-//               with bulk asynchronous copies (14 and 15 are idle).
+//   warp 25     looks up the pages and fills a two-stage ring of raw blocks
+//               with bulk asynchronous copies (26 and 27 are idle).
 //
 // Loading the codes straight into the convert warps' registers, one block
 // ahead, spared the ring's shared-memory traffic but left the page lookup and
@@ -53,7 +54,6 @@ namespace chunk {
 
 using mma::ex2;
 using mma::exp_of;
-using mma::kEvUnset;
 using mma::kSmemLimit;
 using mma::named_bar;
 using mma::pack_f16;
@@ -61,13 +61,13 @@ using mma::pow2i;
 using mma::q_norm_exp;
 
 constexpr int kKeys = 64;   // keys of a block
-constexpr int kSoftWarps = 4, kConvWarps = 4;  // convert warps per operand
-constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps;
+constexpr int kSoftWarps = 8, kConvWarps = 8;  // half of each for blocks of even number, half for odd
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;  // whole warpgroups, for setmaxnreg
-// Registers per thread: launched with 128 (512 threads, the whole file); the
-// shares below add up to 4 * 128, so no increase waits for registers that are
-// not there (checked on the host against the compiled count).
-constexpr int kLaunchRegs = 128, kRegsSoft = 184, kRegsConv = 128, kRegsMma = 72;
+// Registers per thread: launched with 96 (640 threads); the shares below add
+// up to 5 * 96, so no increase waits for registers that are not there (checked
+// on the host against the compiled count).
+constexpr int kLaunchRegs = 96, kRegsSoft = 128, kRegsConv = 80, kRegsMma = 64;
 // setmaxnreg.inc must not lower a count, .dec must not raise one (an illegal instruction otherwise).
 template <int N>
 __device__ __forceinline__ void set_regs() {
@@ -75,10 +75,26 @@ __device__ __forceinline__ void set_regs() {
   if constexpr (N > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
   if constexpr (N < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
 }
-static_assert(kRegsSoft + 2 * kRegsConv + kRegsMma == 4 * kLaunchRegs, "shares = the launch's registers");
+static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsMma == 5 * kLaunchRegs, "shares = the launch's registers");
 constexpr int kTmemCols = 512;
-constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256)
+constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256), one of each parity
 constexpr int kMinBlocks = 4;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
+
+// A segment: the blocks of one tile that fall into the CTA's range. The
+// producer warp, which walks the list, leaves them for the softmax and MMA
+// warps; it is at most 8 blocks, so 9 segments, ahead of the softmax.
+struct Seg {
+  int blocks, v, lead, first;  // blocks; number of the first in its tile; the tile's TileSpan
+  int p0, p1;                  // positions of the tile's first and last token
+  int r0, rows;                // its first row in the unit, its rows
+  int pos0;                    // position of the unit's first token
+  int base, h;                 // query row of that token, kv-head
+  int flags;                   // 1: begins the tile, 2: is all of it, 4: the CTA's last
+  int join;                    // CTAs that work on the tile
+  int pad[3];
+};
+static_assert(sizeof(Seg) == 64, "a slot of the ring");
+constexpr int kSegs = 16;
 
 template <int D>
 struct Smem {
@@ -87,12 +103,14 @@ struct Smem {
   static constexpr int off_v = 2 * kTile;      // [2]
   static constexpr int kStage = kKeys * (2 * D + 2 * (D / 64) * 4);  // raw block: K codes | K scales | V codes | V scales
   static constexpr int off_ring = 4 * kTile;                         // [kStages]
-  static constexpr int off_tab = off_ring + kStages * kStage;        // [8 convert warps][16 keys][D / 64] scales
-  static constexpr int off_pre = off_tab + 8 * 16 * (D / 64) * 8;    // int64 [kMaxBatch + 1]: blocks before sequence b
+  static constexpr int off_tab = off_ring + kStages * kStage;        // [8 convert warps][K | V][16 keys][D / 64] scales
+  static constexpr int off_pre = off_tab + 16 * 16 * (D / 64) * 8;   // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_lens = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch]
   static constexpr int off_cu = off_lens + kMaxBatch * 4;         // int [kMaxBatch + 1]
-  static constexpr int off_misc = off_cu + (kMaxBatch + 4) * 4;
-  static constexpr int total = off_misc + 1024 + 1024;  // slack to align the base
+  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [4][128]: what the two threads of a row hand each other
+  static constexpr int off_segs = off_pair + 4 * kRows * 4;       // [kSegs] segments
+  static constexpr int off_misc = off_segs + kSegs * 64;
+  static constexpr int total = off_misc + 1280 + 1024;  // slack to align the base
 };
 
 // The blocks of a tile: `lead` sink blocks, then the blocks from `first` on.
@@ -234,16 +252,26 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t u2, __half2 s, __half2 
   const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u2), s, bias);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-constexpr float kOperand = 32768.f;  // 2^15: an operand holds its value times 2^-(ev + 15)
+constexpr int kNoExp = -1000;  // 16 keys that are all zero, or not there
+constexpr int kOperand = 15;  // an operand holds its value times 2^-(e + 15)
 
-// New exponent of a group whose largest scale has exponent E: S = s 2^(9 - ev)
-// then lies in [2^11, 2^12), two octaves below where the group moves up and
-// five above where it moves down. beta = 2^(ev_old - ev_new).
-__device__ __forceinline__ void move_exponent(int& ev, int E, float& beta) {
-  const int ne = E - 2 < -110 ? -110 : E - 2;
-  const int d = ev == kEvUnset ? 0 : ev - ne;
-  beta = d < -126 ? 0.f : pow2i(d > 127 ? 127 : d);
-  ev = ne;
+// 2^x for any whole x (0 or infinity past the range).
+__device__ __forceinline__ float pow2_any(int x) { return x < -126 ? 0.f : (x > 127 ? INFINITY : pow2i(x)); }
+
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 template <int D>
@@ -257,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int64_t* pre = reinterpret_cast<int64_t*>(smem + SM::off_pre);
   int* lens = reinterpret_cast<int*>(smem + SM::off_lens);
   int* cus = reinterpret_cast<int*>(smem + SM::off_cu);
+  float* pair_x = reinterpret_cast<float*>(smem + SM::off_pair);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::off_misc);
   uint64_t* kfull = bars;        // [2] K block in shared memory (4 warps)
   uint64_t* vfull = bars + 2;    // [2] V block (4 warps)
@@ -267,33 +296,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   uint64_t* ofree = bars + 11;   // accumulator of a tile read (4 warps)
   uint64_t* rfull = bars + 12;   // [kStages] raw block in the ring (bytes)
   uint64_t* rfree = bars + 12 + kStages;  // [kStages] read by the 8 convert warps
-  int* misc = reinterpret_cast<int*>(bars + 12 + 2 * kStages);
+  uint64_t* segfull = bars + 12 + 2 * kStages;  // [kSegs]
+  uint64_t* handed = bars + 12 + 2 * kStages + kSegs;  // [2][4] references after a block, per 32 rows
+  int* misc = reinterpret_cast<int*>(bars + 20 + 2 * kStages + kSegs);
+  Seg* segs = reinterpret_cast<Seg*>(smem + SM::off_segs);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = misc + 1;
   int* last_mma = misc + 2;                             // block number of the last MMAs committed to pvdone / qkdone
   int* start = misc + 4;                                // [4] b, h, tile, v of the CTA's first block
-  int* votes = misc + 8;                                // [2 operands][2][4 warps]
-  float* maxima = reinterpret_cast<float*>(misc + 24);  // [2 operands][4 warps][4 groups]
-  float* kfac = reinterpret_cast<float*>(misc + 56);    // [4] 2^e of a K block
-  volatile int* seg_blocks = misc + 92;                 // [2] blocks of a segment, for the MMA warp
+  int* exps = misc + 32;                                // [4][K | V][4]: e of 16 keys of a block
+  int* e_pub = misc + 72;                               // [2][4] what the softmax hands on beside pair_x
   volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | bad 16-key groups << 16
   int* last_raw = misc + 100;                           // raw blocks issued
-  float* vhdr = reinterpret_cast<float*>(misc + 60);    // [2][16]: moved | 4 beta | 4 of 2^e
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   chain_wait();
   chain_release();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&kfull[i]), kConvWarps);
-      mbar_init(smem_u32(&vfull[i]), kConvWarps);
+      mbar_init(smem_u32(&kfull[i]), kConvWarps / 2);
+      mbar_init(smem_u32(&vfull[i]), kConvWarps / 2);
       mbar_init(smem_u32(&qkdone[i]), 1);
       mbar_init(smem_u32(&pvdone[i]), 1);
-      mbar_init(smem_u32(&pfull[i]), kSoftWarps);
+      mbar_init(smem_u32(&pfull[i]), kSoftWarps / 2);
+      for (int k = 0; k < 4; ++k) mbar_init(smem_u32(&handed[i * 4 + k]), 1);
     }
+    for (int i = 0; i < kSegs; ++i) mbar_init(smem_u32(&segfull[i]), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&rfull[i]), 1);
-      mbar_init(smem_u32(&rfree[i]), 2 * kConvWarps);
+      mbar_init(smem_u32(&rfree[i]), kConvWarps / 2);
     }
     mbar_init(smem_u32(qfull), kSoftWarps);
     mbar_init(smem_u32(ofree), kSoftWarps);
@@ -351,13 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   __syncthreads();
   const int64_t W = pre[p.B];
   const int64_t most = (W + kMinBlocks - 1) / kMinBlocks;
-  const int n = most < p.n_ctas ? (int)most : p.n_ctas;  // CTAs that take part
+  const int nctas = most < p.n_ctas ? (int)most : p.n_ctas;  // CTAs that take part
   const int cta = blockIdx.x;
-  const bool idle = cta >= n;
+  const bool idle = cta >= nctas;
   Walk w0 = {};
   if (!idle) {
-    w0.x = cta_begin(W, n, cta);
-    w0.end = cta_begin(W, n, cta + 1);
+    w0.x = cta_begin(W, nctas, cta);
+    w0.end = cta_begin(W, nctas, cta + 1);
     if (warp == 0) {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
@@ -427,6 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     }
   };
+  // The segments come from the producer warp, which leaves them all even after
+  // a wait has run out (its own waits then return at once): the softmax warps
+  // meet in barriers and have to agree on the blocks they go through.
+  auto wait_seg = [&](int sg) {
+    const unsigned long long t0 = clock64();
+    while (!mbar_try_wait(smem_u32(&segfull[sg % kSegs]), (sg / kSegs) & 1))
+      if (clock64() - t0 > 16 * p.wait_cycles) break;
+  };
   const uint32_t kbuf = smem_u32(smem + SM::off_k), vbuf = smem_u32(smem + SM::off_v);
 
   if (!work) {
@@ -434,22 +473,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   } else if (warp < kSoftWarps) {
     // ======================================================= softmax warps
     set_regs<kRegsSoft>();
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const int row = warp * 32 + lane;
-    Walk w = w0;
-    int j = 0, q_seg = 0;
+    const int quad = warp & 3, half = warp >> 2;  // rows (tensor-memory lanes); blocks of even or odd number
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const int row = quad * 32 + lane;
+    int j0 = 0;  // number of the segment's first block
     bool have_desc = false;
-    bool more = true;
-    // Q of w's tile into tensor memory; returns sm_scale log2(e) 2^-e of the thread's row
-    auto load_q = [&]() -> float {
-      const int r = w.tile * kRows + row;
-      const bool live = r < w.s.r1;
-      const int rr = live ? r : 0;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((int64_t)(cus[w.b] + rr / p.G) * p.Hq + w.h * p.G + rr % p.G) * D);
+    // Q of segment sg's tile into tensor memory (this warp: every other 64
+    // channels); returns |sm_scale| log2(e) 2^-e of the thread's row
+    auto load_q = [&](int sg) -> float {
+      wait_seg(sg);
+      const Seg& sd = segs[sg % kSegs];
+      const bool live = row < sd.rows;
+      const int rr = live ? sd.r0 + row : 0;
+      const uint4* src =
+          reinterpret_cast<const uint4*>(p.q + ((int64_t)(sd.base + rr / p.G) * p.Hq + sd.h * p.G + rr % p.G) * D);
       float m = 0.f;
       if (live) {
-#pragma unroll 8
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 x = __ldg(src + c);
           const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
@@ -461,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int e = q_norm_exp(m);
       const float qs = p.scale2 < 0.f ? -pow2i(e) : (p.scale2 > 0.f ? pow2i(e) : 0.f);
 #pragma unroll 1
-      for (int g = 0; g < G64; ++g) {
+      for (int g = half; g < G64; g += 2) {
         uint32_t r32[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -475,34 +515,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       wait_st();
       fence_before();
-      if (row == 0) seg_blocks[q_seg & 1] = blocks_left(w);
-      ++q_seg;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(qfull));
       return p.scale2 == 0.f ? 1.f : fabsf(p.scale2) * pow2i(-e);
     };
-    float kq = load_q();
-    while (more) {
-      // one segment: the CTA's blocks of w's tile
-      const int nblk = blocks_left(w);
-      const bool head = w.v == 0, whole = head && nblk == w.s.blocks;
-      const int r = w.tile * kRows + row;
-      const bool live = r < w.s.r1;
-      const int pos = w.L - w.T + (live ? r : w.s.r1 - 1) / p.G;
-      const int base_row = cus[w.b];
+    float kq = load_q(0);
+    bool more = true;
+    for (int sg = 0; more; ++sg) {
+      const Seg& sd = segs[sg % kSegs];
+      const int nblk = sd.blocks;
+      const int v0 = sd.v, lead = sd.lead, shift = sd.first - lead;
+      const int pos = sd.pos0 + (sd.r0 + (row < sd.rows ? row : sd.rows - 1)) / p.G;
+      const int causal = sd.p0 - (kKeys - 1);                               // blocks past it hold hidden keys
+      const int behind = p.window > 0 ? sd.p1 - p.window : -0x7fffffff - 1;  // blocks up to it may
+      // The two warpgroups take the blocks in turn, so that two are under way.
+      // The reference of a row's weights (and of the values' exponents) goes
+      // from block to block through shared memory; a thread's row sum follows
+      // its own copy of the reference.
       float m_ref = -INFINITY, l = 0.f;
-      float unscale[G64];
-      const Walk at = w;  // the tile, for the output
-      for (int i = 0; i < nblk; ++i, ++j) {
-        const int key0 = block_at(w.s, w.v + i) * kKeys;
-        wait_bar(&qkdone[j & 1], (j >> 1) & 1);
+      int e_ref = kNoExp;  // the accumulator holds O 2^-(e_ref + 15)
+      for (int i = (half ^ j0) & 1; i < nblk; i += 2) {
+        const int j = j0 + i;
+        const int key0 = (v0 + i < lead ? v0 + i : v0 + i + shift) * kKeys;
+        wait_bar(&qkdone[half], (j >> 1) & 1);
         fence_after();
-        const uint32_t scol = lane_base + kColS + (j & 1) * 64;
+        const uint32_t scol = lane_base + kColS + half * 64;
         uint32_t lo[32], hi[32];
         tm_ld32(scol, lo);
         tm_ld32(scol + 32, hi);
-        // the factor of the raw scores, kept a normal number (a masked -inf times 0 would be NaN)
-        const float f = fminf(fmaxf(kq * kfac[j & 3] * kOperand, 1.2e-38f), 3.4e38f);
+        // the factors of the raw scores (16 keys each), kept normal numbers (a masked -inf times 0 would be NaN)
+        const int4 ke = *reinterpret_cast<const int4*>(exps + (j & 3) * 8), ve = *reinterpret_cast<const int4*>(exps + (j & 3) * 8 + 4);
+        auto factor = [&](int e) { return fminf(fmaxf(kq * pow2_any(e + kOperand), 1.2e-38f), 3.4e38f); };
+        const float f[4] = {factor(ke.x), factor(ke.y), factor(ke.z), factor(ke.w)};
+        const int vmax = max(max(ve.x, ve.y), max(ve.z, ve.w));
         wait_ld();
         float s[64];
 #pragma unroll
@@ -510,103 +555,131 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s[c] = __uint_as_float(lo[c]);
           s[32 + c] = __uint_as_float(hi[c]);
         }
-        if (key0 + kKeys - 1 > w.s.p0) {
+        if (key0 > causal) {
           const int lim = pos - key0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c > lim) s[c] = -INFINITY;
         }
-        if (p.window > 0 && key0 <= w.s.p1 - p.window && key0 + kKeys - 1 >= p.sinks) {
+        if (key0 <= behind && key0 + kKeys - 1 >= p.sinks) {
           const int lim = pos - p.window - key0, sk = p.sinks - key0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c <= lim && c >= sk) s[c] = -INFINITY;
         }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
+        float m4[4];
 #pragma unroll
-        for (int c = 4; c < 60; c += 8)
+        for (int g = 0; g < 4; ++g) {
+          float a = fmaxf(s[16 * g], s[16 * g + 1]), b = fmaxf(s[16 * g + 2], s[16 * g + 3]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[c + i]), s[c + 4 + i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[60 + i]);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
-        // the reference moves at a row's first key and when a score passes it by more than 8
-        const bool raise = mx > m_ref + 8.f;
-        wait_bar(&vfull[j & 1], (j >> 1) & 1);  // the block's V exponents
-        const float* vh = vhdr + (j & 1) * 16;
-        const bool moved = reinterpret_cast<const int*>(vh)[0] != 0;
-        const bool any = __any_sync(0xffffffffu, raise);
-        float alpha = 1.f;
-        if (raise) {
-          alpha = ex2(m_ref - mx);  // 0 while the row was empty
-          l *= alpha;
-          m_ref = mx;
+          for (int c = 4; c < 16; c += 4) {
+            a = fmaxf(fmaxf(a, s[16 * g + c]), s[16 * g + c + 1]);
+            b = fmaxf(fmaxf(b, s[16 * g + c + 2]), s[16 * g + c + 3]);
+          }
+          m4[g] = fmaxf(a, b) * f[g];
         }
-        if (i > 0 && (any || moved)) {
-          wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // ---- the references after the block before
+        const float m_own = m_ref;
+        if (j > 0) wait_bar(&handed[(1 - half) * 4 + quad], ((j - 1) >> 1) & 1);
+        if (i > 0) {
+          m_ref = pair_x[(1 - half) * kRows + row];
+          e_ref = e_pub[(1 - half) * 4 + quad];
+        }
+        // The reference moves at a row's first key and when a score passes it
+        // by more than 8. The weights of 16 keys carry their values' exponent,
+        // p 2^(ve - e_ref): e_ref follows the blocks' largest ve, moved when a
+        // weight could pass 2^14 or the block's largest value drops 2^4 below.
+        const bool moved = vmax > e_ref + 6 || (vmax < e_ref - 4 && vmax != kNoExp);
+        const bool change = __any_sync(0xffffffffu, moved || mx > m_ref + 8.f);  // rare
+        float a = 1.f;
+        if (change) {
+          if (mx > m_ref + 8.f) {
+            a = ex2(m_ref - mx);  // 0 while the row was empty
+            m_ref = mx;
+          }
+          if (moved) {
+            a *= pow2_any(e_ref - vmax);
+            e_ref = vmax;
+          }
+        }
+        pair_x[half * kRows + row] = m_ref;
+        if (lane == 0) e_pub[half * 4 + quad] = e_ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&handed[half * 4 + quad]));
+        if (__any_sync(0xffffffffu, m_ref != m_own)) l *= m_own == -INFINITY ? 0.f : ex2(m_own - m_ref);
+        if (change && i > 0) {  // the accumulator follows
+          wait_bar(&pvdone[1 - half], ((j - 1) >> 1) & 1);
           fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            const float a = moved ? alpha * vh[1 + c / 2] : alpha;
-            uint32_t o[32];
-            tm_ld32(lane_base + kColO + c * 32, o);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tm_ld16(lane_base + kColO + c * 16, o);
             wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            tm_st32(lane_base + kColO + c * 32, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tm_st16(lane_base + kColO + c * 16, o);
           }
           wait_st();
         }
-        if (moved) {
-#pragma unroll
-          for (int g = 0; g < G64; ++g) unscale[g] = vh[5 + g];
-        }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        // p = 2^(score f - m), two at a time; four partial sums
-        const float2 f2 = make_float2(f, f), mu2 = make_float2(-mu, -mu);
+        // ---- p 2^d = 2^(score f - m + d), two at a time, d of 16 keys each; the row sum is of p
+        const int vd[4] = {ve.x, ve.y, ve.z, ve.w};
         uint32_t pk[32];
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 t2 = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), f2, mu2);
-          const float2 e2 = make_float2(ex2(t2.x), ex2(t2.y));
-          sum[c & 1] = __fadd2_rn(sum[c & 1], e2);
-          pk[c] = pack_f16(e2.x, e2.y);
+        for (int g = 0; g < 4; ++g) {
+          const int d = max(vd[g] - e_ref, -60);  // 2^-60 of the weights is nothing in fp16
+          const float2 mu2 = make_float2((float)d - mu, (float)d - mu), f2 = make_float2(f[g], f[g]);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 8 * g; c < 8 * g + 8; ++c) {
+            const float2 t2 = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), f2, mu2);
+            const float2 e2 = make_float2(ex2(t2.x), ex2(t2.y));
+            sum = __fadd2_rn(sum, e2);
+            pk[c] = pack_f16(e2.x, e2.y);
+          }
+          l = fmaf(sum.x + sum.y, pow2i(-d), l);
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tm_st32(scol, pk);
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&pfull[j & 1]));
+        if (lane == 0) mbar_arrive(smem_u32(&pfull[half]));
       }
-      w.x += nblk;
-      w.v += nblk;
-      more = w.x < w.end;
-      if (more) next_tile(p, tab, w);
+      j0 += nblk;
+      more = !(sd.flags & 4);
       // the next tile's Q while the last products run (its QKs wait for it;
       // this tile's have all completed)
-      if (more) kq = load_q();
-      wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1);
+      wait_bar(&qkdone[(j0 - 1) & 1], ((j0 - 1) >> 1) & 1);  // (the other threads' block, maybe)
+      if (more) kq = load_q(sg + 1);
+      // ---- both threads of a row: the last block's references, the whole row sum
+      wait_bar(&handed[((j0 - 1) & 1) * 4 + quad], ((j0 - 1) >> 1) & 1);
+      const float m_end = pair_x[((j0 - 1) & 1) * kRows + row];
+      e_ref = e_pub[((j0 - 1) & 1) * 4 + quad];
+      if (l > 0.f) l *= ex2(m_ref - m_end);
+      m_ref = m_end;
+      pair_x[(2 + half) * kRows + row] = l;
+      named_bar(1 + quad, 64);
+      l += pair_x[(3 - half) * kRows + row];
+      wait_bar(&pvdone[(j0 - 1) & 1], ((j0 - 1) >> 1) & 1);
       fence_after();
-      const float inv = l > 0.f ? kOperand / l : 0.f;
+      // back to O: 2^(e_ref + 15) / l (the power in two steps, each a normal number)
+      const float up = e_ref == kNoExp ? 1.f : pow2i(e_ref), inv = l > 0.f ? 32768.f / l : 0.f;
       bool finite = true;
+      const bool head = sd.flags & 1, whole = sd.flags & 2, live = row < sd.rows;
       const int64_t slot = 2 * (int64_t)cta + (head ? 1 : 0);
-      uint16_t* orow = p.out + ((int64_t)(base_row + (live ? r : 0) / p.G) * p.Hq + at.h * p.G + (live ? r : 0) % p.G) * D;
+      const int rr = live ? sd.r0 + row : 0;
+      uint16_t* orow = p.out + ((int64_t)(sd.base + rr / p.G) * p.Hq + sd.h * p.G + rr % p.G) * D;
       float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kRows + row;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = half; c < D / 32; c += 2) {
         uint32_t o[32];
         tm_ld32(lane_base + kColO + c * 32, o);
         wait_ld();
-        float un = unscale[0];
-#pragma unroll
-        for (int g = 1; g < G64; ++g) un = c / 2 == g ? unscale[g] : un;
-        const float sc = inv * un;
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          v[k] = __uint_as_float(o[k]) * sc;
+          v[k] = __uint_as_float(o[k]) * inv * up;
           finite &= isfinite(v[k]) != 0;
         }
         if (whole) {
@@ -628,26 +701,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       if (live && !finite) flag(p.status, NK_DEVFLAG_RANGE);
       if (!whole) {
-        p.part_lse[slot * kRows + row] = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        if (half == 0) p.part_lse[slot * kRows + row] = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
         if (head) {
           // the tile's first blocks: this CTA leaves what the join needs
           have_desc = true;
-          if (row == 0) {
-            const int last = cta_of_item(W, n, at.x - at.v + at.s.blocks - 1);
-            p.desc[cta] = make_int4(base_row, at.h, at.tile * kRows, (at.s.r1 - at.tile * kRows) | ((last - cta + 1) << 8));
-          }
+          if (tid == 0) p.desc[cta] = make_int4(sd.base, sd.h, sd.r0, sd.rows | (sd.join << 8));
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(ofree));
+      named_bar(1 + quad, 64);  // the row sums and references are read before the next segment's are written
     }
-    if (!have_desc && row == 0) p.desc[cta] = make_int4(0, -1, 0, 0);
+    if (!have_desc && tid == 0) p.desc[cta] = make_int4(0, -1, 0, 0);
   } else if (warp < kMmaWarp) {
     // ======================================================= convert warps
     set_regs<kRegsConv>();
-    const bool isv = warp >= kSoftWarps + kConvWarps;
-    const int cw = (warp - kSoftWarps) & 3;  // keys 16 cw .. 16 cw + 15 of a block
+    const int odd = (warp - kSoftWarps) >> 2;  // the blocks, ring stage and operand buffers of this warp
+    const int cw = (warp - kSoftWarps) & 3;    // keys 16 cw .. 16 cw + 15 of a block
     // Lane -> (key, 16-channel piece) of a load: a quarter warp takes four
     // pieces of two neighbouring keys, the odd key's in the other half of the
     // 128 bytes, so that neither its 16-byte reads of the raw rows nor its
@@ -657,153 +728,111 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int kk = D == 256 ? kp : (D == 128 ? (qt >> 1) * 2 + kp : qt * 2 + kp);
     const int ck = D == 64 ? lane & 3 : ((lane & 3) | (((qt ^ kp) & 1) << 2) | (D == 256 ? (qt >> 1) << 3 : 0));
     const int grp = ck >> 2;
-    // raw rows and scales of this warp's keys in a stage
-    const uint32_t raw0 = smem_u32(smem + SM::off_ring) + (isv ? kKeys * (D + G64 * 4) : 0);
+    // raw rows and scales of this warp's keys in its stage (K; V lies kRawV bytes on)
+    constexpr int kRawV = kKeys * (D + G64 * 4);
+    const uint32_t raw0 = smem_u32(smem + SM::off_ring) + odd * SM::kStage;
     const uint32_t codes0 = raw0 + (cw * 16 + kk) * D + ck * 16, scales0 = raw0 + kKeys * D + (cw * 16 * G64 + lane) * 4;
-    // this warp's table of scales: (S, -S 2^-17) as fp16 pairs, [16 keys][G64]
-    const uint32_t tab0 = smem_u32(smem + SM::off_tab) + (warp - kSoftWarps) * (16 * G64 * 8);
-    constexpr int NS = (16 * G64 + 31) / 32;  // scales of a lane (group lane % G64; one of two lanes at head dim 64)
+    // this warp's tables of scales: (S, -S 2^-17) as fp16 pairs, [K | V][16 keys][G64]
+    constexpr int kTab = 16 * G64 * 8;
+    const uint32_t tab0 = smem_u32(smem + SM::off_tab) + (warp - kSoftWarps) * (2 * kTab);
+    const uint32_t tabp = tab0 + (kk * G64 + grp) * 8;
+    constexpr int NS = (16 * G64 + 31) / 32;  // scales of a lane (one of two lanes at head dim 64)
     const bool has_scale = D > 64 || lane < 16;
-    const int sgrp = isv ? lane % G64 : 0;    // group whose exponent they follow
-    // store addresses: row (i KPI + kk) of the buffer, chunks 2 (ck & 3) and + 1 swizzled by the row mod 8; rows
-    // repeat their swizzle every 8 / KPI loads
-    constexpr int NA = 8 / KPI > 1 ? 8 / KPI : 1;
-    uint32_t sa[NA][2];
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        sa[i][c] = (isv ? vbuf : kbuf) + grp * (kKeys * 128) + (cw * 16 + i * KPI + kk) * 128 +
-                   ((((ck & 3) * 2 + c) ^ ((i * KPI + kk) & 7)) << 4);
-    uint64_t* full = isv ? vfull : kfull;
-    uint64_t* done = isv ? pvdone : qkdone;
-    int* votes_w = votes + (isv ? 8 : 0);
-    const int bar_id = isv ? 2 : 1;
+    // the first row's store address; rows i KPI further on add i KPI 128 and xor (i KPI mod 8) into the 16-byte chunk
+    const uint32_t sa = kbuf + odd * SM::kTile + grp * (kKeys * 128) + (cw * 16 + kk) * 128 + ((((ck & 3) * 2) ^ (kk & 7)) << 4);
     const int total = (int)(w0.end - w0.x);
     bool bad_scale = false;
-    int ev[4] = {kEvUnset, kEvUnset, kEvUnset, kEvUnset};
-    float inv_e = 0.f;  // 2^-ev of the lane's group (0: not set)
-    int st = 0;
-    uint32_t ph = 0;
-    for (int j = 0; j < total; ++j) {
-      wait_bar(&rfull[st], ph);
-      const int inf = info[st];
-      const bool first = (inf >> 8) & 1;
+    uint32_t ph = 0;  // phase of the stage and (inverted) of the operand buffers
+    static_assert(kStages == 2, "a stage per parity");
+    for (int j = odd; j < total; j += 2, ph ^= 1u) {
+      wait_bar(&rfull[odd], ph);
+      const int inf = info[odd];
       const int there = ((inf >> (16 + cw)) & 1) ? 0 : (inf & 0xff) - cw * 16;  // keys of this warp's 16 that exist
-      uint4 w[NI];
-      float s[NS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[i]) : "r"(scales0 + st * SM::kStage + i * 128));
+      for (int v = 0; v < 2; ++v) {  // K, V
+        uint4 w[NI];
+        float s[NS], mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                     : "r"(codes0 + st * SM::kStage + i * (KPI * D)));
-      float mx = 0.f;
+        for (int i = 0; i < NS; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[i]) : "r"(scales0 + v * kRawV + i * 128));
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
-        if (!(s[i] <= 3.0e38f)) {  // the append of a non-finite row: zeros too, flagged
-          s[i] = 0.f;
-          bad_scale = true;
-        }
-        mx = fmaxf(mx, s[i]);
-      }
-      // ---- exponents: a group moves when a scale passes 2^6 of it, or none of the block's reaches 2^-2
-      if (isv && first) inv_e = 0.f;
-      const float t = mx * inv_e;
-      const uint32_t bits =
-          __reduce_or_sync(0xffffffffu, ((t > 64.f ? 1u : 0u) | (t >= 0.25f ? 16u : 0u)) << sgrp);
-      int* vote = votes_w + (j & 1) * 4;
-      if (lane == 0) vote[cw] = (int)bits;
-      named_bar(bar_id, kConvWarps * 32);
-      const int4 v4 = *reinterpret_cast<const int4*>(vote);
-      const uint32_t seen = (uint32_t)(v4.x | v4.y | v4.z | v4.w);
-      const uint32_t moving = ((seen & 15u) | (~(seen >> 4) & 15u)) & (isv ? (1u << G64) - 1u : 1u);
-      float beta[4] = {1.f, 1.f, 1.f, 1.f};
-      if (moving) {
-        float* mxs = maxima + (isv ? 16 : 0);
-        if (isv && first) {
+        for (int i = 0; i < NI; ++i)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(codes0 + v * kRawV + i * (KPI * D)));
 #pragma unroll
-          for (int g = 0; g < 4; ++g) ev[g] = kEvUnset;
-        }
-#pragma unroll
-        for (int g = 0; g < G64; ++g) {
-          const uint32_t v = __reduce_max_sync(0xffffffffu, (!isv || sgrp == g) ? __float_as_uint(mx) : 0u);
-          if (lane == 0) mxs[cw * 4 + g] = __uint_as_float(v);
-        }
-        named_bar(bar_id, kConvWarps * 32);
-#pragma unroll
-        for (int g = 0; g < G64; ++g) {
-          if (!((moving >> g) & 1u)) continue;
-          const float m4 = fmaxf(fmaxf(mxs[g], mxs[4 + g]), fmaxf(mxs[8 + g], mxs[12 + g]));
-          if (m4 > 0.f) move_exponent(ev[g], exp_of(m4), beta[g]);
-        }
-        named_bar(bar_id, kConvWarps * 32);  // maxima read before a later block writes them
-        int e = ev[0];
-#pragma unroll
-        for (int g = 1; g < G64; ++g) e = sgrp == g ? ev[g] : e;
-        inv_e = e == kEvUnset ? 0.f : pow2i(-e);
-      }
-      // ---- the scales as fp16: S = s 2^(9 - ev) (zero where there is none)
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const __half2 sc = __float2half2_rn(s[i] * inv_e * 512.f);
-        const __half2 bias = __hmul2(sc, __float2half2_rn(-7.62939453125e-6f));  // -S 2^-17
-        if (has_scale)
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tab0 + (lane + 32 * i) * 8),
-                       "r"(*reinterpret_cast<const uint32_t*>(&sc)), "r"(*reinterpret_cast<const uint32_t*>(&bias))
-                       : "memory");
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&rfree[st]));  // every lane holds its part of the raw block
-      // ---- the buffer's previous block has been multiplied
-      wait_bar(&done[j & 1], ((j >> 1) & 1) ^ 1);
-      if (cw == 0 && lane == 0) {
-        if (isv) {
-          float* vh = vhdr + (j & 1) * 16;
-          const bool tell = moving != 0 || first;
-          reinterpret_cast<int*>(vh)[0] = tell ? 1 : 0;
-          if (tell) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              vh[1 + g] = beta[g];
-              vh[5 + g] = ev[g] == kEvUnset ? 1.f : pow2i(ev[g]);
-            }
+        for (int i = 0; i < NS; ++i) {
+          if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
+          if (!(s[i] <= 3.0e38f)) {  // the append of a non-finite row: zeros too, flagged
+            s[i] = 0.f;
+            bad_scale = true;
           }
-        } else {
-          kfac[j & 3] = ev[0] == kEvUnset ? 1.f : pow2i(ev[0]);
+          mx = fmaxf(mx, s[i]);
         }
-      }
-      const uint32_t half_off = (j & 1) * SM::kTile;
+        // the 16 keys take the exponent of their own largest scale: S = s 2^(9 - e) lies below 2^12
+        const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+        const int e = m > 0.f ? max(exp_of(m) - 2, -110) : kNoExp;
+        const float down = m > 0.f ? pow2i(9 - e) : 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        uint32_t scu, biu;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                     : "=r"(scu), "=r"(biu)
-                     : "r"(tab0 + ((i * KPI + kk) * G64 + grp) * 8)
-                     : "memory");
-        const __half2 sc = *reinterpret_cast<const __half2*>(&scu), bi = *reinterpret_cast<const __half2*>(&biu);
-        const uint32_t w4[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          h[2 * k] = scale_codes(mma::prmt(w4[k], 0u, 0x4140), sc, bi);
-          h[2 * k + 1] = scale_codes(mma::prmt(w4[k], 0u, 0x4342), sc, bi);
+        for (int i = 0; i < NS; ++i) {
+          const __half2 sc = __float2half2_rn(s[i] * down);
+          const __half2 bias = __hmul2(sc, __float2half2_rn(-7.62939453125e-6f));  // -S 2^-17
+          if (has_scale)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tab0 + v * kTab + (lane + 32 * i) * 8),
+                         "r"(*reinterpret_cast<const uint32_t*>(&sc)), "r"(*reinterpret_cast<const uint32_t*>(&bias))
+                         : "memory");
         }
-        const uint32_t o = half_off + (i / NA) * (NA * KPI * 128);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sa[i % NA][0] + o), "r"(h[0]), "r"(h[1]),
-                     "r"(h[2]), "r"(h[3]));
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sa[i % NA][1] + o), "r"(h[4]), "r"(h[5]),
-                     "r"(h[6]), "r"(h[7]));
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0 && (p.withhold < 0 || j < p.withhold)) mbar_arrive(smem_u32(&full[j & 1]));
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1u;
+        // Both exponents have to be there with the scores, so V's is told before
+        // K is handed over: K's pass looks at V's scales, too.
+        if (v == 0) {
+          float vm = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(scales0 + kRawV + i * 128));
+            if (has_scale && (lane + 32 * i) / G64 < there && x <= 3.0e38f) vm = fmaxf(vm, x);
+          }
+          vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+          // (the slot's last reader, the softmax of block j - 4, is done: its PV was waited for at block j - 2)
+          if (lane == 0) {
+            exps[(j & 3) * 8 + cw] = e;
+            exps[(j & 3) * 8 + 4 + cw] = vm > 0.f ? max(exp_of(vm) - 2, -110) : kNoExp;
+          }
+        }
+        __syncwarp();
+        if (v == 1 && lane == 0) mbar_arrive(smem_u32(&rfree[odd]));  // every lane holds its part of the raw block
+        // ---- the buffer's previous block has been multiplied
+        wait_bar((v ? pvdone : qkdone) + odd, ph ^ 1u);
+        constexpr int NH = NI < 4 ? NI : 4;  // loads whose scales are in registers at once
+#pragma unroll
+        for (int i0 = 0; i0 < NI; i0 += NH) {
+          uint32_t scu[NH], biu[NH];
+#pragma unroll
+          for (int i = 0; i < NH; ++i)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(scu[i]), "=r"(biu[i])
+                         : "r"(tabp + v * kTab + (i0 + i) * (KPI * G64 * 8))
+                         : "memory");
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            const uint4 x = w[i0 + i];
+            const __half2 sc = *reinterpret_cast<const __half2*>(&scu[i]), bi = *reinterpret_cast<const __half2*>(&biu[i]);
+            const uint32_t w4[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = scale_codes(mma::prmt(w4[k], 0u, 0x4140), sc, bi);
+              h[2 * k + 1] = scale_codes(mma::prmt(w4[k], 0u, 0x4342), sc, bi);
+            }
+            const uint32_t a0 = (sa ^ ((((i0 + i) * KPI) & 7) << 4)), at = v * (2 * SM::kTile) + (i0 + i) * (KPI * 128);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + at), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                         "r"(h[3]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((a0 ^ 16u) + at), "r"(h[4]), "r"(h[5]),
+                         "r"(h[6]), "r"(h[7]));
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && (p.withhold < 0 || j < p.withhold)) mbar_arrive(smem_u32((v ? vfull : kfull) + odd));
       }
     }
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) flag(p.status, NK_DEVFLAG_RANGE);
@@ -838,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       };
       while (j < total) {
         wait_bar(qfull, seg & 1);
-        left = *abort_flag ? total - j : seg_blocks[seg & 1];
+        left = *abort_flag ? total - j : segs[seg % kSegs].blocks;
         for (int i = 0; i < left; ++i, ++j) {
           wait_bar(&kfull[j & 1], (j >> 1) & 1);
           if (!*abort_flag && leader) {
@@ -867,59 +896,104 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     if (warp == kMmaWarp + 1) {
       // ===================================================== producer warp
-      // lanes 0-3 take 16 keys of a block each (P is a multiple of 16: one
-      // page holds them); with pages of whole blocks lane 0 takes all 64
-      const int per = p.P % kKeys == 0 ? kKeys : 16;
+      // Lane -> (array, group of keys): K codes, K scales, V codes, V scales of
+      // a whole block where pages hold whole blocks, else of 16 keys each (P
+      // is a multiple of 16: one page holds them). The page ids come 32 (8)
+      // blocks at a time, a lane each, one batch ahead.
+      const bool whole = p.P % kKeys == 0;
+      const int per = whole ? kKeys : 16, batch = whole ? 32 : 8;
       constexpr int kKeyBytes = 2 * D + 2 * G64 * 4;
-      Walk w = w0;
-      int st = 0, page = -2;
-      uint32_t ph = 1u;  // a fresh ring is free
-      bool first = true;
-      auto look = [&]() {  // page id of the lane's keys (-2: no such keys)
-        const int pos = block_of(w) * kKeys + lane * per;
+      const int arr = lane & 3, kg = lane >> 2;
+      const bool copier = kg * per < kKeys;
+      const int width = (arr & 1) ? G64 * 4 : D;  // bytes of a key in the array
+      const int64_t src_off = arr == 0 ? 0 : (arr == 1 ? p.lay.ks : (arr == 2 ? p.lay.vc : p.lay.vs));
+      const uint32_t dst0 = smem_u32(smem + SM::off_ring) + (arr == 0 ? 0 : (arr == 1 ? kKeys * D : (arr == 2 ? kKeys * (D + G64 * 4) : kKeys * (2 * D + G64 * 4)))) +
+                            kg * per * width;
+      // page (-1: outside the pool, -2: no such keys) and slot of the lane's keys in the batch of w's tile from block v on
+      auto look = [&](const Walk& w, int v, int n, int& page, int& slot) {
+        const int i = whole ? lane : lane >> 2;
+        const int pos = block_at(w.s, v + i) * kKeys + (whole ? 0 : (lane & 3) * 16);
         page = -2;
-        if (lane * per < kKeys && pos < w.L) page = __ldg(p.bt + (int64_t)w.b * p.max_pages + pos / p.P);
+        slot = 0;
+        if (i < n && pos < w.L) {
+          const int pi = pos / p.P;
+          slot = pos - pi * p.P;
+          page = __ldg(p.bt + (int64_t)w.b * p.max_pages + pi);
+          if (page < 0 || page >= p.num_pages) page = -1;
+        }
       };
-      look();
-      for (int q = 0;; ++q) {
-        const int key0 = block_of(w) * kKeys, pos = key0 + lane * per, h = w.h;
-        const int keys = w.L - key0 < kKeys ? w.L - key0 : kKeys;
-        const int cur = page;
-        const bool was_first = first;
-        const int b = w.b, tile = w.tile;
-        const bool more = step(p, tab, w);
-        if (more) {
-          first = w.b != b || w.h != h || w.tile != tile;
-          look();
-        }
-        const bool ok = cur >= 0 && cur < p.num_pages;
-        const unsigned copies = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, !ok && cur != -2);
-        wait_bar(&rfree[st], ph);
-        const bool stop = *abort_flag;
-        if (__any_sync(0xffffffffu, stop)) break;
-        const uint32_t bar = smem_u32(&rfull[st]);
+      Walk w = w0;
+      int page, slot, q = 0, sg = 0;
+      look(w, w.v, blocks_left(w), page, slot);
+      bool more = true;
+      while (more) {
+        // one segment
+        const int n = blocks_left(w), v0 = w.v, L = w.L, h = w.h;
+        const TileSpan span = w.s;
+        Walk ahead = w;
+        ahead.x += n;
+        ahead.v += n;
+        more = ahead.x < ahead.end;
+        if (more) next_tile(p, tab, ahead);
         if (lane == 0) {
-          info[st] = keys | (was_first ? 256 : 0) | ((per == kKeys ? (bad ? 15u : 0u) : (bad & 15u)) << 16);
-          if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
-          mbar_arrive_expect_tx(bar, __popc(copies) * per * kKeyBytes);
-          *last_raw = q + 1;
+          Seg& s = segs[sg % kSegs];
+          const int r0 = w.tile * kRows;
+          const bool head = v0 == 0, all = head && n == span.blocks;
+          s.blocks = n;
+          s.v = v0;
+          s.lead = span.lead;
+          s.first = span.first;
+          s.p0 = span.p0;
+          s.p1 = span.p1;
+          s.r0 = r0;
+          s.rows = span.r1 - r0;
+          s.pos0 = L - w.T;
+          s.base = cus[w.b];
+          s.h = h;
+          s.flags = (head ? 1 : 0) | (all ? 2 : 0) | (more ? 0 : 4);
+          s.join = head ? cta_of_item(W, nctas, w.x + span.blocks - 1) - cta + 1 : 0;
+          mbar_arrive(smem_u32(&segfull[sg % kSegs]));
         }
-        __syncwarp();
-        if (ok) {
-          const int slot = pos % p.P;
-          const uint8_t* c = p.pool + ((int64_t)cur * p.Hkv + h) * p.lay.chunk;
-          const uint32_t dst = smem_u32(smem + SM::off_ring + st * SM::kStage);
-          const int k0 = lane * per;
-          bulk_load(dst + k0 * D, c + (int64_t)slot * D, per * D, bar);
-          bulk_load(dst + kKeys * D + k0 * G64 * 4, c + p.lay.ks + slot * G64 * 4, per * G64 * 4, bar);
-          bulk_load(dst + kKeys * (D + G64 * 4) + k0 * D, c + p.lay.vc + (int64_t)slot * D, per * D, bar);
-          bulk_load(dst + kKeys * (2 * D + G64 * 4) + k0 * G64 * 4, c + p.lay.vs + slot * G64 * 4, per * G64 * 4, bar);
+        ++sg;
+        for (int i = 0; i < n; ++i, ++q) {
+          const int at = i % batch;
+          int next_page = -2, next_slot = 0;
+          const bool turn = at == batch - 1 || i == n - 1;  // the batch's last block: the next batch's ids go out
+          if (turn) {
+            if (i < n - 1) look(w, v0 + i + 1, n - i - 1, next_page, next_slot);
+            else if (more) look(ahead, ahead.v, blocks_left(ahead), next_page, next_slot);
+          }
+          const int from = whole ? at : at * 4 + (kg & 3);
+          const int pg = __shfl_sync(0xffffffffu, page, from), sl = __shfl_sync(0xffffffffu, slot, from);
+          const bool ok = copier && pg >= 0;
+          const unsigned okb = __ballot_sync(0xffffffffu, ok && arr == 0), badb = __ballot_sync(0xffffffffu, copier && arr == 0 && pg == -1);
+          const int st = q % kStages;
+          wait_bar(&rfree[st], ((q / kStages) & 1) ^ 1u);
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) {  // no more copies; the segments still go out
+            page = turn ? next_page : page;
+            slot = turn ? next_slot : slot;
+            continue;
+          }
+          const uint32_t bar = smem_u32(&rfull[st]);
+          if (lane == 0) {
+            const int left = L - block_at(span, v0 + i) * kKeys;
+            // bits 0, 4, 8, 12 of badb are the 16-key groups, bit 0 alone a whole block
+            const unsigned bad = whole ? (badb ? 15u : 0u) : ((badb & 1u) | ((badb >> 3) & 2u) | ((badb >> 6) & 4u) | ((badb >> 9) & 8u));
+            info[st] = (left < kKeys ? left : kKeys) | (i == 0 ? 256 : 0) | (bad << 16);
+            if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+            mbar_arrive_expect_tx(bar, __popc(okb) * per * kKeyBytes);
+            *last_raw = q + 1;
+          }
+          __syncwarp();
+          if (ok)
+            bulk_load(dst0 + st * SM::kStage,
+                      p.pool + ((int64_t)pg * p.Hkv + h) * p.lay.chunk + src_off + (int64_t)sl * width, per * width, bar);
+          if (turn) {
+            page = next_page;
+            slot = next_slot;
+          }
         }
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-        if (!more) break;
+        w = ahead;
       }
     }
     __syncwarp();
