@@ -78,7 +78,7 @@ __device__ __forceinline__ void set_regs() {
 static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsMma == 5 * kLaunchRegs, "shares = the launch's registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256), one of each parity
-constexpr int kMinBlocks = 4;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
+constexpr int kMinBlocks = 1;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
 
 // A segment: the blocks of one tile that fall into the CTA's range. The
 // producer warp, which walks the list, leaves them for the softmax and MMA
@@ -107,11 +107,19 @@ struct Smem {
   static constexpr int off_pre = off_tab + 16 * 16 * (D / 64) * 8;   // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_lens = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch]
   static constexpr int off_cu = off_lens + kMaxBatch * 4;         // int [kMaxBatch + 1]
-  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [4][128]: what the two threads of a row hand each other
-  static constexpr int off_segs = off_pair + 4 * kRows * 4;       // [kSegs] segments
+  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128]: what the two threads of a row hand each other
+  static constexpr int off_segs = off_pair + 6 * kRows * 4;       // [kSegs] segments
   static constexpr int off_misc = off_segs + kSegs * 64;
   static constexpr int total = off_misc + 1280 + 1024;  // slack to align the base
 };
+
+// Quotients of the block numbers, which fit 32 bits but for the largest
+// batches: a 64-bit division costs some hundred instructions.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+__device__ __forceinline__ int64_t range_begin(int64_t W, int n, int c) { return quot((int64_t)c * W, n); }
 
 // The blocks of a tile: `lead` sink blocks, then the blocks from `first` on.
 struct TileSpan {
@@ -381,22 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
   __syncthreads();
   const int64_t W = pre[p.B];
-  const int64_t most = (W + kMinBlocks - 1) / kMinBlocks;
+  const int64_t most = quot(W + kMinBlocks - 1, kMinBlocks);
   const int nctas = most < p.n_ctas ? (int)most : p.n_ctas;  // CTAs that take part
   const int cta = blockIdx.x;
   const bool idle = cta >= nctas;
   Walk w0 = {};
   if (!idle) {
-    w0.x = cta_begin(W, nctas, cta);
-    w0.end = cta_begin(W, nctas, cta + 1);
+    w0.x = range_begin(W, nctas, cta);
+    w0.end = range_begin(W, nctas, cta + 1);
     if (warp == 0) {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= w0.x) lo = mid; else hi = mid;
       }
-      const int64_t per_head = (pre[lo + 1] - pre[lo]) / p.Hkv, off = w0.x - pre[lo];
-      int64_t rem = off % per_head;
+      const int64_t per_head = quot(pre[lo + 1] - pre[lo], p.Hkv), off = w0.x - pre[lo], head = quot(off, per_head);
+      int64_t rem = off - head * per_head;
       const int T = cus[lo + 1] - cus[lo], tiles = tiles_of(p, T);
       int tile = 0;
       for (int t0 = 0; t0 < tiles; t0 += 32) {
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       if (lane == 0) {
         start[0] = lo;
-        start[1] = (int)(off / per_head);
+        start[1] = (int)head;
         start[2] = tile;
         start[3] = (int)rem;
       }
@@ -487,31 +495,40 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int rr = live ? sd.r0 + row : 0;
       const uint4* src =
           reinterpret_cast<const uint4*>(p.q + ((int64_t)(sd.base + rr / p.G) * p.Hq + sd.h * p.G + rr % p.G) * D);
+      // the thread's channels (every other 64) in one go, their largest |q|, then the row's
+      constexpr int NQ = (G64 + 1) / 2;
+      uint32_t q32[NQ][32];
       float m = 0.f;
-      if (live) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = __ldg(src + c);
-          const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(x4[i])), fabsf(bf16_hi(x4[i]))));
+      for (int k = 0; k < NQ; ++k)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int g = half + 2 * k;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (live && g < G64) x = __ldg(src + g * 8 + c);
+          q32[k][4 * c] = x.x;
+          q32[k][4 * c + 1] = x.y;
+          q32[k][4 * c + 2] = x.z;
+          q32[k][4 * c + 3] = x.w;
         }
-      }
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) m = fmaxf(m, fmaxf(fabsf(bf16_lo(q32[k][c])), fabsf(bf16_hi(q32[k][c]))));
+      pair_x[(4 + half) * kRows + row] = m;
+      named_bar(1 + quad, 64);
+      m = fmaxf(m, pair_x[(5 - half) * kRows + row]);
       // the sign of sm_scale goes into Q, so that scores scale by a positive factor
       const int e = q_norm_exp(m);
       const float qs = p.scale2 < 0.f ? -pow2i(e) : (p.scale2 > 0.f ? pow2i(e) : 0.f);
-#pragma unroll 1
-      for (int g = half; g < G64; g += 2) {
-        uint32_t r32[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (live) x = __ldg(src + g * 8 + c);
-          const uint32_t x4[4] = {x.x, x.y, x.z, x.w};
+      for (int k = 0; k < NQ; ++k) {
+        const int g = half + 2 * k;
+        if (g < G64) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r32[c * 4 + i] = pack_f16(bf16_lo(x4[i]) * qs, bf16_hi(x4[i]) * qs);
+          for (int c = 0; c < 32; ++c) q32[k][c] = pack_f16(bf16_lo(q32[k][c]) * qs, bf16_hi(q32[k][c]) * qs);
+          tm_st32(lane_base + kColQ + g * 32, q32[k]);
         }
-        tm_st32(lane_base + kColQ + g * 32, r32);
       }
       wait_st();
       fence_before();
@@ -951,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s.base = cus[w.b];
           s.h = h;
           s.flags = (head ? 1 : 0) | (all ? 2 : 0) | (more ? 0 : 4);
-          s.join = head ? cta_of_item(W, nctas, w.x + span.blocks - 1) - cta + 1 : 0;
+          s.join = head ? (int)quot((w.x + span.blocks) * nctas - 1, W) - cta + 1 : 0;
           mbar_arrive(smem_u32(&segfull[sg % kSegs]));
         }
         ++sg;
