@@ -194,6 +194,7 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   p.fmt = fmt;
   p.window = window;
   p.sinks = sinks;
+  p.sink_pages = (int)(((int64_t)sinks + P - 1) / P);
   p.q = reinterpret_cast<const uint16_t*>(q);
   p.bt = bt;
   p.max_pages = max_pages;

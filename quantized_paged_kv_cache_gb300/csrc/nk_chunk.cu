@@ -113,14 +113,6 @@ struct Smem {
   static constexpr int total = off_misc + 1280 + 1024;  // slack to align the base
 };
 
-// Quotients of the block numbers, which fit 32 bits but for the largest
-// batches: a 64-bit division costs some hundred instructions.
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-__device__ __forceinline__ int64_t range_begin(int64_t W, int n, int c) { return quot((int64_t)c * W, n); }
-
 // The blocks of a tile: `lead` sink blocks, then the blocks from `first` on.
 struct TileSpan {
   int r1;            // one past its last row
@@ -395,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const bool idle = cta >= nctas;
   Walk w0 = {};
   if (!idle) {
-    w0.x = range_begin(W, nctas, cta);
-    w0.end = range_begin(W, nctas, cta + 1);
+    w0.x = cta_begin(W, nctas, cta);
+    w0.end = cta_begin(W, nctas, cta + 1);
     if (warp == 0) {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
@@ -968,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s.base = cus[w.b];
           s.h = h;
           s.flags = (head ? 1 : 0) | (all ? 2 : 0) | (more ? 0 : 4);
-          s.join = head ? (int)quot((w.x + span.blocks) * nctas - 1, W) - cta + 1 : 0;
+          s.join = head ? cta_of_item(W, nctas, w.x + span.blocks - 1) - cta + 1 : 0;
           mbar_arrive(smem_u32(&segfull[sg % kSegs]));
         }
         ++sg;

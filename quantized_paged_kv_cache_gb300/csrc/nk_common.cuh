@@ -178,14 +178,14 @@ __device__ __forceinline__ int pages_of_len(const SplitShape& s, int L) {
 // from the first window page on.
 struct WindowShape : SplitShape {
   int window, sinks;
+  int sink_pages;  // ceil(sinks / P)
 };
 
 // First window page of a sequence of (valid) length L, and the sink pages before it.
 __host__ __device__ __forceinline__ void window_pages(const WindowShape& s, int L, int& first, int& lead) {
-  const int64_t lo = (int64_t)L - s.T - s.window + 1;
-  first = lo > 0 ? (int)(lo / s.P) : 0;
-  const int sp = (int)(((int64_t)s.sinks + s.P - 1) / s.P);
-  lead = sp < first ? sp : first;
+  const int lo = L - s.T - s.window + 1;  // L >= T, window >= 1: no overflow
+  first = lo > 0 ? (int)((unsigned)lo / (unsigned)s.P) : 0;
+  lead = s.sink_pages < first ? s.sink_pages : first;
 }
 
 __device__ __forceinline__ int pages_of_len(const WindowShape& s, int L) {
@@ -196,11 +196,19 @@ __device__ __forceinline__ int pages_of_len(const WindowShape& s, int L) {
   return all - first + lead;
 }
 
-__device__ __forceinline__ int64_t cta_begin(int64_t W, int n, int c) { return (int64_t)c * W / n; }
+// Quotient of two numbers that are not negative. They nearly always fit 32
+// bits, where a division costs a tenth of the 64-bit one's hundreds of cycles;
+// several stand in the prologue of every decode kernel.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((uint64_t)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+__device__ __forceinline__ int64_t cta_begin(int64_t W, int n, int c) { return quot((int64_t)c * W, n); }
 
 // Largest CTA index whose range starts at or before item x (x < W).
 __device__ __forceinline__ int cta_of_item(int64_t W, int n, int64_t x) {
-  return (int)(((x + 1) * (int64_t)n - 1) / W);
+  return (int)quot((x + 1) * (int64_t)n - 1, W);
 }
 
 }  // namespace nk
@@ -273,8 +281,8 @@ __device__ __forceinline__ bool next_segment(const SplitShape& s, const int* pre
   const int b = lo;
   const int pages = pre[b + 1] - pre[b];
   const int64_t off = x - (int64_t)pre[b] * s.Hkv;
-  const int h = (int)(off / pages);
-  const int p0 = (int)(off % pages);
+  const int h = (int)quot(off, pages);
+  const int p0 = (int)(off - (int64_t)h * pages);
   const int64_t unit_end = (int64_t)pre[b] * s.Hkv + (int64_t)(h + 1) * pages;
   const int64_t e = unit_end < x_end ? unit_end : x_end;
   seg.b = b;

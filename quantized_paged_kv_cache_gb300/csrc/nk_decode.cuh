@@ -36,6 +36,7 @@ struct DecodeParams {
   int early;
   int fmt;  // KvFmt of the pool (the rk8v4 kernel ignores it)
   int window, sinks;  // sliding window and sinks (window 0: the whole context)
+  int sink_pages;     // ceil(sinks / P)
   // Failure-detection tests (nk_test_inject_copy_stall): every bounded wait
   // gives up after wait_cycles, and the page copies of CTA page numbers
   // >= withhold are never issued (-1: all issued).
@@ -48,6 +49,7 @@ struct DecodeParams {
     static_cast<SplitShape&>(s) = shape();
     s.window = window;
     s.sinks = sinks;
+    s.sink_pages = sink_pages;
     return s;
   }
   template <bool WIN>

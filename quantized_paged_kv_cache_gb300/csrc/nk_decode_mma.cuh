@@ -308,7 +308,7 @@ __device__ __forceinline__ int page_coord(const DecodeParams& p, const SplitShap
   }
   const int pages = pre[lo + 1] - pre[lo];
   const int64_t off = x - (int64_t)pre[lo] * sh.Hkv;
-  const int h = (int)(off / pages), pi = (int)(off % pages);
+  const int h = (int)quot(off, pages), pi = (int)(off - (int64_t)h * pages);
   const int page = __ldg(p.bt + (int64_t)lo * p.max_pages + pi);
   return (page < 0 || page >= p.num_pages) ? -1 : page * p.Hkv + h;
 }
@@ -324,7 +324,7 @@ __device__ __forceinline__ int page_coord(const DecodeParams& p, const WindowSha
   }
   const int pages = pre[lo + 1] - pre[lo];
   const int64_t off = x - (int64_t)pre[lo] * sh.Hkv;
-  const int h = (int)(off / pages), pi = (int)(off % pages);
+  const int h = (int)quot(off, pages), pi = (int)(off - (int64_t)h * pages);
   int first, lead;
   window_pages(sh, lens[lo], first, lead);
   const int page = __ldg(p.bt + (int64_t)lo * p.max_pages + (pi < lead ? pi : pi - lead + first));
