@@ -187,13 +187,19 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesPa
 // double, at most 2^-54 turns, so 2^-23 turns at position 2^31.
 //
 // Bandwidth-bound: each row is read and written once, in 16-byte pieces. A
-// block takes `per` rows: it forms the rows' half cos/sin pairs once in shared
-// memory (all heads share them), then its threads run over (row, head, eight
-// channel pairs) items, two loads and two stores of 16 bytes each.
+// block takes `per` rows and forms their half cos/sin pairs once in shared
+// memory (all heads share them). A thread keeps one piece of the head (eight
+// channel pairs, or eight copied channels) and goes over (row, head) from its
+// first head on: no division in the loop (with one per item, 8,192 rows of 24
+// + 4 heads of 256 took 43.1 us against 39.7: 5.9 TB/s, 0.87 of a copy's rate;
+// 4,099 rows of 16 + 2 heads of 128, half of each turned, 11.4 against 7.6).
+// Many blocks in flight cover the loads' latency; two or four items of a
+// thread in flight, held in registers, were slower (60 and 87 us).
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxHalf = NK_MAX_HEAD_DIM / 2;
 constexpr int kRopeMaxRows = 8;  // rows of a block, at most
+constexpr int kRopeItems = 2;    // items of a thread, about (4: the same, 8: 42, 16: 50 us on the 8,192 rows)
 
 struct RopeParams {
   const uint16_t* q;
@@ -235,37 +241,40 @@ __global__ void __launch_bounds__(kRopeThreads) mrope_kernel(const __grid_consta
   }
   __syncthreads();
   const int heads = p.Hq + p.Hkv;
-  const int pieces = p.half / 8;                   // pairs of pieces that turn
-  const int tail = (p.D - 2 * p.half) / 8;         // pieces that are copied
-  const int per_head = pieces + tail;
-  const int per_row = heads * per_head;
-  const int items = n * per_row;
-#pragma unroll 2
-  for (int i = tid; i < items; i += kRopeThreads) {
-    const int r = i / per_row, x = i - r * per_row, h = x / per_head, c = x - h * per_head;
-    const bool isq = h < p.Hq;
-    const int64_t row = row0 + r;
-    const int hh = isq ? h : h - p.Hq;
-    const uint16_t* src = (isq ? p.q + row * p.q_stride : p.k + row * p.k_stride) + hh * p.D;
-    uint16_t* dst = (isq ? p.qo + row * p.qo_stride : p.ko + row * p.ko_stride) + hh * p.D;
-    if (c < pieces) {
-      const uint4 a4 = *reinterpret_cast<const uint4*>(src + c * 8);
-      const uint4 b4 = *reinterpret_cast<const uint4*>(src + p.half + c * 8);
-      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
-      uint32_t u[4], v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 co = *reinterpret_cast<const float2*>(&cs[r][c * 8 + 2 * j]);
-        const float2 si = *reinterpret_cast<const float2*>(&sn[r][c * 8 + 2 * j]);
-        const float a0 = bf16_lo(a[j]), a1 = bf16_hi(a[j]), b0 = bf16_lo(b[j]), b1 = bf16_hi(b[j]);
-        u[j] = pack_bf16(a0 * co.x - b0 * si.x, a1 * co.y - b1 * si.y);
-        v[j] = pack_bf16(b0 * co.x + a0 * si.x, b1 * co.y + a1 * si.y);
+  const int pieces = p.half / 8;               // pairs of pieces that turn
+  const int tail = (p.D - 2 * p.half) / 8;     // pieces that are copied
+  const int per_head = pieces + tail;          // threads of a head
+  const int lanes = kRopeThreads / per_head;   // heads at once
+  const int c = tid % per_head, h0 = tid / per_head;
+  if (h0 >= lanes) return;
+  const bool turns = c < pieces;
+  const int off_a = turns ? c * 8 : 2 * p.half + (c - pieces) * 8, off_b = turns ? p.half + c * 8 : off_a;
+  if (h0 >= heads) return;
+  for (int r = 0; r < n; ++r) {
+    const int64_t j = row0 + r;
+    for (int h = h0; h < heads; h += lanes) {
+      const bool isq = h < p.Hq;
+      const int hh = (isq ? h : h - p.Hq) * p.D;
+      const uint16_t* src = (isq ? p.q + j * p.q_stride : p.k + j * p.k_stride) + hh;
+      uint16_t* dst = (isq ? p.qo + j * p.qo_stride : p.ko + j * p.ko_stride) + hh;
+      const uint4 a4 = *reinterpret_cast<const uint4*>(src + off_a);
+      if (!turns) {
+        *reinterpret_cast<uint4*>(dst + off_a) = a4;
+        continue;
       }
-      *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(u[0], u[1], u[2], u[3]);
-      *reinterpret_cast<uint4*>(dst + p.half + c * 8) = make_uint4(v[0], v[1], v[2], v[3]);
-    } else if (dst != src) {
-      const int o = 2 * p.half + (c - pieces) * 8;
-      *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(src + o);
+      const uint4 b4 = *reinterpret_cast<const uint4*>(src + off_b);
+      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+      uint32_t x[4], y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 co = *reinterpret_cast<const float2*>(&cs[r][c * 8 + 2 * k]);
+        const float2 si = *reinterpret_cast<const float2*>(&sn[r][c * 8 + 2 * k]);
+        const float a0 = bf16_lo(a[k]), a1 = bf16_hi(a[k]), b0 = bf16_lo(b[k]), b1 = bf16_hi(b[k]);
+        x[k] = pack_bf16(a0 * co.x - b0 * si.x, a1 * co.y - b1 * si.y);
+        y[k] = pack_bf16(b0 * co.x + a0 * si.x, b1 * co.y + a1 * si.y);
+      }
+      *reinterpret_cast<uint4*>(dst + off_a) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(dst + off_b) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
 }
@@ -374,9 +383,9 @@ int nk_mrope(const void* q_dev, const void* k_dev, void* q_out_dev, void* k_out_
   p.Hkv = num_kv_heads;
   p.D = head_dim;
   p.half = half;
-  // about four items a thread, while every SM still gets a block
+  // rows of a block, while every SM still gets two blocks
   const int64_t per_row = (int64_t)(num_q_heads + num_kv_heads) * (head_dim / 8 - half / 8);
-  int64_t per = (4 * kRopeThreads + per_row - 1) / per_row;
+  int64_t per = (kRopeItems * kRopeThreads + per_row - 1) / per_row;
   if (per > kRopeMaxRows) per = kRopeMaxRows;
   while (per > 1 && (rows + per - 1) / per < 304) --per;
   p.per = (int)per;

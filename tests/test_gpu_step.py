@@ -210,3 +210,88 @@ def test_mrope_rows_behind_the_last_stay_and_graphs_replay():
         m = min(rows, 40)
         assert torch.equal(qo[:m], full_q[:m]) and torch.equal(ko[:m], full_k[:m])
         assert torch.all(qo[m:] == 7.0) and torch.all(ko[m:] == 7.0)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,P,window,sinks", [(256, 24, 4, 64, 0, 0), (128, 16, 2, 16, 100, 5)])
+def test_a_step_of_continuous_batching(D, Hq, Hkv, P, window, sinks):
+    """Three steps of a serving loop as a user writes them: tables and slot map, rotary positions, append, attention of the
+    step's ragged tokens, on one stream without a host synchronisation; against the 64-bit forms at the end of each step."""
+    rng = np.random.RandomState(5)
+    B, width, pages = 5, 24 * 64 // P, 140 * 64 // P
+    perm = rng.permutation(pages)
+    table, lens = i32(np.full((B, width), -1)), np.zeros(B, dtype=int)
+    pool = nk.KVPool.empty(pages, P, Hkv, D, fill=0xFF)
+    status = i32([0])
+    inv = 1e6 ** (-torch.arange(D // 4, dtype=torch.float64) * 4 / D)
+    sections = (D // 4 - 2 * (D // 12), D // 12, D // 12)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    keys = [torch.empty((0, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(B)]
+    taken = 0
+    for step_new in ([300, 0, 77, 1, 500], [1, 40, 1, 1, 1], [4, 4, 200, 0, 1]):
+        start, new = lens.copy(), np.asarray(step_new)
+        total, rows = int(new.sum()), int(new.sum()) + 9  # buffers for the largest step
+        free = i32(perm[taken:])
+        cu, ctx = i32([0] * (B + 1)), i32([0] * B)
+        slots, pos, used = torch.full((rows,), -7, dtype=torch.int64, device="cuda"), i32([0] * rows), i32([0])
+        qkv = torch.randn((rows, Hq + 2 * Hkv, D), generator=g, device="cuda").bfloat16()
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        startd, newd = i32(start), i32(new)
+        nk.step_tables(P, pages, startd, newd, free, table, cu, ctx, slots, positions=pos, used=used, status=status)
+        axes = torch.stack([pos, pos // 7, pos % 7]).contiguous()
+        qr, kr = nk.mrope(q, k, axes, inv, sections, interleaved=True, num_rows=cu[B:])
+        nk.kv_append(pool, table, startd, cu, kr[:total].contiguous(), v[:total].contiguous(), status=status)
+        out = nk.paged_chunk_attn(pool, qr, cu, table, ctx, 1 / D ** 0.5, width * P, window=window, sinks=sinks, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        taken += int(used.item())
+        lens = start + new
+        assert ctx.tolist() == lens.tolist() and cu.tolist() == [0] + np.cumsum(new).tolist()
+        # the slots are where the rows went
+        K, _ = _ref.dequantized(pool.storage, pages, Hkv, P, D)
+        flat = K.transpose(1, 2).reshape(pages * P, Hkv, D)[slots[:total]]
+        scale = kr[:total].double().unflatten(-1, (D // 64, 64)).abs().amax(-1, keepdim=True) / 127
+        # a code is off by half a step, of 127 (and the scale by its own rounding, below 2^-23 of the value)
+        assert torch.all((flat.unflatten(-1, (D // 64, 64)) - kr[:total].double().unflatten(-1, (D // 64, 64))).abs() <= scale * 0.5001)
+        check_rope(qr[:total], q[:total], axes[:, :total], inv, sections, True)
+        want = _ref.attention(pool.storage, pages, Hkv, P, D, table, lens.tolist(), new.tolist(), qr[:total], 1 / D ** 0.5, window, sinks)
+        # the chunk attention's tolerance: half a bf16 step and 4e-3 for its fp16 operands (tests/test_gpu_chunk.py)
+        err = (out[:total].double() - want).abs()
+        assert torch.all(err <= 2.0 ** -8 * want.abs() + 4e-3)
+        # a decoding batch: the same tokens through the windowed decode
+        if (new == new[0]).all():
+            continue
+        one = [b for b in range(B) if lens[b] > 0]
+        qd = qr[:len(one)].reshape(len(one), 1, Hq, D).contiguous()
+        args = (pool, qd, table[one].contiguous(), ctx[one].contiguous(), 1 / D ** 0.5, width * P)
+        got = nk.paged_window_attn(*args, window, sinks=sinks) if window else nk.paged_decode_attn(*args)
+        want = _ref.attention(pool.storage, pages, Hkv, P, D, table[one], lens[one].tolist(), [1] * len(one), qd, 1 / D ** 0.5,
+                              window, sinks).reshape(got.shape)
+        assert torch.all((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 4e-3)
+
+
+def test_step_operators_follow_the_stream_order():
+    """A side stream holds the whole step; the calls read what kernels before them on that stream wrote."""
+    P, D, Hq, Hkv, B = 16, 128, 8, 2, 3
+    pool = nk.KVPool.empty(64, P, Hkv, D, fill=0)
+    side = torch.cuda.Stream()
+    outs = []
+    for rep in range(2):
+        g = torch.Generator(device="cuda").manual_seed(3)
+        qkv = torch.randn((60, Hq + 2 * Hkv, D), generator=g, device="cuda").bfloat16()
+        src = i32([30, 1, 29])
+        torch.cuda.synchronize()
+        stream = side if rep else torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            if rep:
+                torch.cuda._sleep(20_000_000)  # everything below is enqueued long before it runs
+            start, new = torch.zeros(B, dtype=torch.int32, device="cuda"), src * 1
+            table = torch.full((B, 8), -1, dtype=torch.int32, device="cuda")
+            free = torch.arange(63, -1, -1, dtype=torch.int32, device="cuda")
+            cu, ctx = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+            slots, pos = torch.zeros(60, dtype=torch.int64, device="cuda"), torch.zeros(60, dtype=torch.int32, device="cuda")
+            nk.step_tables(P, 64, start, new, free, table, cu, ctx, slots, positions=pos)
+            q, k = nk.mrope(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], pos[None].contiguous(), torch.ones(64, dtype=torch.float64), (64,))
+            nk.kv_append(pool, table, start, cu, k, qkv[:, Hq + Hkv:].contiguous())
+            outs.append(nk.paged_chunk_attn(pool, q, cu, table, ctx, 0.1, 128))
+        stream.synchronize()
+    assert torch.equal(outs[0], outs[1])
