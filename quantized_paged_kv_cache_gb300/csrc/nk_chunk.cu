@@ -40,10 +40,16 @@
 // the loads' latency in their path: 7,345 us against 4,720 on eight chunks of
 // 1,024 tokens at 8K to 32K (24 q-heads over 4 kv-heads, head dim 256).
 //
-// Work split (stream-K): the blocks of all tiles form one list, cut into equal
-// contiguous ranges, one per CTA, whatever the sequences' lengths. A tile cut
-// by a range's end leaves fp32 partials with their log-sum-exp in the
-// workspace; a second kernel joins them. Every mbarrier wait is bounded.
+// Work split. The tiles are one list. With more than two tiles a CTA they are
+// first dealt out whole, in rounds of one tile each: neighbouring tiles, which
+// share their keys, then run side by side and read them from L2 (with every
+// CTA on its own stretch of the list instead, eight chunks of 1,024 tokens at
+// 8K to 32K read 11.3 GB from device memory). The blocks of the remaining
+// tiles, one to two a CTA, or of all tiles where there are fewer, are cut into
+// contiguous ranges that even out the CTAs' totals, whatever the sequences'
+// lengths (stream-K). A tile cut by a range's end leaves fp32 partials with
+// their log-sum-exp in the workspace; a second kernel joins them. Every
+// mbarrier wait is bounded.
 #include <math.h>
 
 #include "nk_chunk.cuh"
@@ -78,6 +84,7 @@ __device__ __forceinline__ void set_regs() {
 static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsMma == 5 * kLaunchRegs, "shares = the launch's registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256), one of each parity
+constexpr int kMaxSched = 160;  // CTAs of a call whose tiles are dealt out whole first (one per SM has fewer)
 constexpr int kMinBlocks = 1;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
 
 // A segment: the blocks of one tile that fall into the CTA's range. The
@@ -105,12 +112,12 @@ struct Smem {
   static constexpr int off_ring = 4 * kTile;                         // [kStages]
   static constexpr int off_tab = off_ring + kStages * kStage;        // [8 convert warps][K | V][16 keys][D / 64] scales
   static constexpr int off_pre = off_tab + 16 * 16 * (D / 64) * 8;   // int64 [kMaxBatch + 1]: blocks before sequence b
-  static constexpr int off_lens = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch]
-  static constexpr int off_cu = off_lens + kMaxBatch * 4;         // int [kMaxBatch + 1]
+  static constexpr int off_tiles = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch + 1]: tiles before sequence b
+  static constexpr int off_cu = off_tiles + (kMaxBatch + 4) * 4;  // int [kMaxBatch + 1]
   static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128]: what the two threads of a row hand each other
   static constexpr int off_segs = off_pair + 6 * kRows * 4;       // [kSegs] segments
   static constexpr int off_misc = off_segs + kSegs * 64;
-  static constexpr int total = off_misc + 1280 + 1024;  // slack to align the base
+  static constexpr int total = off_misc + 1408 + 1024;  // slack to align the base
 };
 
 // The blocks of a tile: `lead` sink blocks, then the blocks from `first` on.
@@ -150,9 +157,11 @@ struct Walk {
 __device__ __forceinline__ int tiles_of(const Params& p, int T) { return (int)(((int64_t)T * p.G + kRows - 1) / kRows); }
 
 struct Tables {
-  const int64_t* pre;
-  const int* lens;
+  const int64_t* pre;     // blocks before a sequence
+  const int* tiles;       // tiles before it (of all kv-heads)
   const int* cu;
+  const int32_t* ctx;     // in device memory
+  int B;
 };
 
 __device__ __forceinline__ void enter_tile(const Params& p, Walk& w) { w.s = span_of(p, w.L, w.T, w.tile); }
@@ -165,18 +174,30 @@ __device__ __forceinline__ void next_tile(const Params& p, const Tables& t, Walk
     if (++w.h == p.Hkv) {
       w.h = 0;
       do ++w.b; while (t.pre[w.b + 1] == t.pre[w.b]);
-      w.L = t.lens[w.b];
+      w.L = __ldg(t.ctx + w.b);
       w.T = t.cu[w.b + 1] - t.cu[w.b];
     }
   }
   enter_tile(p, w);
 }
 
-// Steps to the next block; false at the end of the CTA's range.
-__device__ __forceinline__ bool step(const Params& p, const Tables& t, Walk& w) {
-  if (++w.x >= w.end) return false;
-  if (++w.v == w.s.blocks) next_tile(p, t, w);
-  return true;
+// Tile number i of the list, whole.
+__device__ __forceinline__ void tile_at(const Params& p, const Tables& t, int i, Walk& w) {
+  int lo = 0, hi = t.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.tiles[mid] <= i) lo = mid; else hi = mid;
+  }
+  w.b = lo;
+  w.L = __ldg(t.ctx + lo);
+  w.T = t.cu[lo + 1] - t.cu[lo];
+  const int per = tiles_of(p, w.T), k = i - t.tiles[lo];
+  w.h = (unsigned)k / (unsigned)per;
+  w.tile = k - w.h * per;
+  w.v = 0;
+  enter_tile(p, w);
+  w.x = 0;
+  w.end = w.s.blocks;
 }
 
 // The CTA's blocks of w's tile from w on.
@@ -283,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int64_t* pre = reinterpret_cast<int64_t*>(smem + SM::off_pre);
-  int* lens = reinterpret_cast<int*>(smem + SM::off_lens);
+  int* tiles = reinterpret_cast<int*>(smem + SM::off_tiles);
   int* cus = reinterpret_cast<int*>(smem + SM::off_cu);
   float* pair_x = reinterpret_cast<float*>(smem + SM::off_pair);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::off_misc);
@@ -308,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int* e_pub = misc + 72;                               // [2][4] what the softmax hands on beside pair_x
   volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | bad 16-key groups << 16
   int* last_raw = misc + 100;                           // raw blocks issued
+  int* longest = misc + 101;                            // blocks of the longest tile
+  int* sched = misc + 104;                              // [kMaxSched + 1] where the CTAs' shares of the last tiles begin
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   chain_wait();
@@ -331,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     *abort_flag = 0;
     last_mma[0] = last_mma[1] = -1;
     *last_raw = 0;
+    *longest = 1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -340,56 +364,124 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     fence_before();
   }
-  // ---- the list of blocks: lengths, then the blocks of every sequence
+  // ---- the list of tiles and blocks
   for (int b = tid; b <= p.B; b += kThreads) cus[b] = p.cu[b];
-  for (int b = tid; b < p.B; b += kThreads) lens[b] = p.ctx[b];
   __syncthreads();
   for (int b = warp; b < p.B; b += kThreads / 32) {
-    const int c0 = cus[b], c1 = cus[b + 1], L = lens[b];
+    const int c0 = cus[b], c1 = cus[b + 1], L = __ldg(p.ctx + b);
     const int64_t T = (int64_t)c1 - c0;
     const bool ok = c0 >= 0 && T >= 0 && c1 <= p.total_q && T <= L && L <= p.max_ctx &&
                     (int64_t)L <= (int64_t)p.max_pages * p.P;
+    const int nt = ok ? tiles_of(p, (int)T) : 0;
     int64_t n = 0;
-    if (ok && T > 0) {
-      const int tiles = tiles_of(p, (int)T);
-      for (int t = lane; t < tiles; t += 32) n += span_of(p, L, (int)T, t).blocks;
+    int most = 0;
+    for (int t = lane; t < nt; t += 32) {
+      const int k = span_of(p, L, (int)T, t).blocks;
+      n += k;
+      most = max(most, k);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) {
       pre[b] = n * p.Hkv;
+      tiles[b] = nt;
+      atomicMax(longest, most);
       if (!ok && blockIdx.x == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
     }
   }
   __syncthreads();
-  if (warp == 0) {  // exclusive prefix
-    int64_t run = 0;
+  if (warp == 0) {  // exclusive prefixes
+    int64_t run = 0, trun = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
-      const int64_t n = b < p.B ? pre[b] : 0;
-      int64_t inc = n;
+      const int64_t n = b < p.B ? pre[b] : 0, nt = b < p.B ? (int64_t)tiles[b] * p.Hkv : 0;
+      int64_t inc = n, tinc = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, tinc, o);
+        if (lane >= o) {
+          inc += y;
+          tinc += z;
+        }
       }
       __syncwarp();
-      if (b < p.B) pre[b] = run + inc - n;
+      if (b < p.B) {
+        pre[b] = run + inc - n;
+        tiles[b] = (int)min(trun + tinc - nt, (int64_t)0x7fffffff);
+      }
       run += __shfl_sync(0xffffffffu, inc, 31);
+      trun += __shfl_sync(0xffffffffu, tinc, 31);
     }
-    if (lane == 0) pre[p.B] = run;
+    if (lane == 0) {
+      pre[p.B] = run;
+      tiles[p.B] = (int)min(trun, (int64_t)0x7fffffff);
+    }
   }
   __syncthreads();
+  const Tables tab{pre, tiles, cus, p.ctx, p.B};
   const int64_t W = pre[p.B];
   const int64_t most = quot(W + kMinBlocks - 1, kMinBlocks);
   const int nctas = most < p.n_ctas ? (int)most : p.n_ctas;  // CTAs that take part
   const int cta = blockIdx.x;
   const bool idle = cta >= nctas;
-  Walk w0 = {};
-  if (!idle) {
-    w0.x = cta_begin(W, nctas, cta);
-    w0.end = cta_begin(W, nctas, cta + 1);
+  // ---- whole tiles first: `waves` rounds of one tile a CTA
+  int waves = 0;
+  if (!idle && nctas <= kMaxSched && tiles[p.B] < 0x7fffffff && W < 0x7fffffff) {
+    waves = tiles[p.B] / nctas - 1;
+    waves = min(waves, (int)min(quot(quot(W, nctas), *longest), (int64_t)0x7fffffff));
+    waves = max(waves, 0);
+  }
+  const int first_split = waves * nctas;  // first tile of those that are split
+  int64_t split0 = 0;                     // its first block
+  if (waves > 0) {
+    // what the rounds give each CTA; the rest of its share comes from the
+    // split tiles (a block at least, so that no CTA between two is left out)
+    if (tid < nctas) {
+      int64_t got = 0;
+      Walk w;
+      for (int k = 0; k < waves; ++k) {
+        tile_at(p, tab, tid + k * nctas, w);
+        got += w.s.blocks;
+      }
+      sched[tid] = (int)max(quot(W, nctas) + 1 - got, (int64_t)1);
+    }
+    Walk w;
+    tile_at(p, tab, first_split, w);  // (there are at least nctas tiles after the rounds)
+    for (int k = lane; k < w.tile; k += 32) split0 += span_of(p, w.L, w.T, k).blocks;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) split0 += __shfl_xor_sync(0xffffffffu, split0, o);
+    split0 += pre[w.b] + w.h * quot(pre[w.b + 1] - pre[w.b], p.Hkv);
+    __syncthreads();
     if (warp == 0) {
+      int run = 0;
+      for (int c0 = 0; c0 <= nctas; c0 += 32) {
+        const int c = c0 + lane, v = c < nctas ? sched[c] : 0;
+        int inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        __syncwarp();
+        if (c <= nctas) sched[c] = run + inc - v;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    __syncthreads();
+  }
+  // ---- the CTA's blocks of the split tiles
+  Walk w0 = {};
+  int total = 0;
+  if (!idle) {
+    if (waves > 0) {
+      w0.x = min(split0 + sched[cta], W);
+      w0.end = min(split0 + sched[cta + 1], W);
+    } else {
+      w0.x = cta_begin(W, nctas, cta);
+      w0.end = cta_begin(W, nctas, cta + 1);
+    }
+    if (warp == 0 && w0.x < w0.end) {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -397,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       const int64_t per_head = quot(pre[lo + 1] - pre[lo], p.Hkv), off = w0.x - pre[lo], head = quot(off, per_head);
       int64_t rem = off - head * per_head;
-      const int T = cus[lo + 1] - cus[lo], tiles = tiles_of(p, T);
+      const int T = cus[lo + 1] - cus[lo], nt = tiles_of(p, T), L = __ldg(p.ctx + lo);
       int tile = 0;
-      for (int t0 = 0; t0 < tiles; t0 += 32) {
+      for (int t0 = 0; t0 < nt; t0 += 32) {
         const int t = t0 + lane;
-        const int nb = t < tiles ? span_of(p, lens[lo], T, t).blocks : 0;
+        const int nb = t < nt ? span_of(p, L, T, t).blocks : 0;
         int64_t inc = nb;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -425,21 +517,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         start[3] = (int)rem;
       }
     }
+    total = (int)(w0.end - w0.x);
+    Walk w;
+    for (int k = 0; k < waves; ++k) {
+      tile_at(p, tab, cta + k * nctas, w);
+      total += w.s.blocks;
+    }
   }
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tslot;  // 0: all of the SM's columns
-  const Tables tab{pre, lens, cus};
-  if (!idle) {
-    w0.b = start[0];
-    w0.h = start[1];
-    w0.tile = start[2];
-    w0.v = start[3];
-    w0.L = lens[w0.b];
-    w0.T = cus[w0.b + 1] - cus[w0.b];
-    enter_tile(p, w0);
-  }
-  const bool work = !idle && w0.x < w0.end;
+  const bool work = total > 0;
 
   // A bounded wait; once one has run out no wait blocks any more, no MMA is
   // issued, and the end of the kernel waits for those that were. (The flag is
@@ -749,7 +837,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const bool has_scale = D > 64 || lane < 16;
     // the first row's store address; rows i KPI further on add i KPI 128 and xor (i KPI mod 8) into the 16-byte chunk
     const uint32_t sa = kbuf + odd * SM::kTile + grp * (kKeys * 128) + (cw * 16 + kk) * 128 + ((((ck & 3) * 2) ^ (kk & 7)) << 4);
-    const int total = (int)(w0.end - w0.x);
     bool bad_scale = false;
     uint32_t ph = 0;  // phase of the stage and (inverted) of the operand buffers
     static_assert(kStages == 2, "a stage per parity");
@@ -855,7 +942,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // register (a lane on its own paid some 75 cycles an MMA to move them).
       constexpr uint32_t id_qk = idesc_f16_f32(kRows, kKeys, false), id_pv = idesc_f16_f32(kRows, D, true);
       const bool leader = elect_one();
-      const int total = (int)(w0.end - w0.x);
       const uint32_t k_lo = sdesc_lo(kbuf, 16), v_lo = sdesc_lo(vbuf, kKeys * 128);
       int j = 0, seg = 0, left = 0;  // blocks, segments, blocks left of the segment
       bool fresh = true;             // the segment's first PV is still to come
@@ -931,7 +1017,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (page < 0 || page >= p.num_pages) page = -1;
         }
       };
-      Walk w = w0;
+      // the tiles of the rounds, then the CTA's blocks of the split tiles
+      Walk w;
+      int wave = 0;
+      auto begin_split = [&](Walk& a) {
+        a = w0;
+        a.b = start[0];
+        a.h = start[1];
+        a.tile = start[2];
+        a.v = start[3];
+        a.L = __ldg(p.ctx + a.b);
+        a.T = cus[a.b + 1] - cus[a.b];
+        enter_tile(p, a);
+      };
+      if (waves > 0) tile_at(p, tab, cta, w);
+      else begin_split(w);
       int page, slot, q = 0, sg = 0;
       look(w, w.v, blocks_left(w), page, slot);
       bool more = true;
@@ -939,11 +1039,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         // one segment
         const int n = blocks_left(w), v0 = w.v, L = w.L, h = w.h;
         const TileSpan span = w.s;
+        const bool split = wave >= waves;
         Walk ahead = w;
-        ahead.x += n;
-        ahead.v += n;
-        more = ahead.x < ahead.end;
-        if (more) next_tile(p, tab, ahead);
+        if (++wave < waves) {
+          tile_at(p, tab, cta + wave * nctas, ahead);
+        } else if (!split) {
+          more = w0.x < w0.end;
+          if (more) begin_split(ahead);
+        } else {
+          ahead.x += n;
+          ahead.v += n;
+          more = ahead.x < ahead.end;
+          if (more) next_tile(p, tab, ahead);
+        }
         if (lane == 0) {
           Seg& s = segs[sg % kSegs];
           const int r0 = w.tile * kRows;
@@ -960,7 +1068,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s.base = cus[w.b];
           s.h = h;
           s.flags = (head ? 1 : 0) | (all ? 2 : 0) | (more ? 0 : 4);
-          s.join = head ? cta_of_item(W, nctas, w.x + span.blocks - 1) - cta + 1 : 0;
+          s.join = 0;
+          if (head && !all) {  // the CTA of the tile's last block
+            const int64_t last = w.x + span.blocks - 1;
+            int c = waves > 0 ? cta : cta_of_item(W, nctas, last);
+            while (waves > 0 && c + 1 < nctas && split0 + sched[c + 1] <= last) ++c;
+            s.join = c - cta + 1;
+          }
           mbar_arrive(smem_u32(&segfull[sg % kSegs]));
         }
         ++sg;

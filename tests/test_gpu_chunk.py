@@ -246,3 +246,21 @@ def test_chunk_wait_that_runs_out_is_reported():
     out = k.run(num_ctas=2, status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 5, 7, 0])
+def test_chunk_tiles_dealt_out_whole_and_split(ctas):
+    """More than two tiles a CTA: rounds of whole tiles, then split ones; tiles of very different lengths, sequences without
+    tokens between them."""
+    k = Chunk("rounds", [300, 0, 1, 1, 257, 0, 2, 128], [300, 7, 2500, 64, 1700, 90, 2, 1000], 8, 2, 64, 16, seed=77)
+    for window, sinks in ((0, 0), (333, 5)):
+        ref = k.ref(window, sinks)
+        out = k.run(window, sinks, num_ctas=ctas)
+        check(out, ref, f"ctas={ctas} window={window}")
+        assert torch.equal(out, k.run(window, sinks, num_ctas=ctas))
+
+
+def test_chunk_many_tiles_of_one_length():
+    """The default split with rounds: 4 x 24 tiles a kv-head."""
+    k = Chunk("even", [512] * 4, [1100, 700, 1024, 513], 20, 4, 128, 64, seed=78)
+    check(k.run(), k.ref(), "rounds over the default CTAs")
