@@ -1,7 +1,9 @@
 /*
  * nk.h -- C ABI of the paged INT8 group-64 KV cache for one GB300 (sm_103a).
  *
- * Three operations, all enqueued on a caller-supplied CUDA stream:
+ * Three operations on the cache, and beside them the operators of a serving
+ * step (tables, rotary positions, windowed and ragged attention; described at
+ * their declarations), all enqueued on a caller-supplied CUDA stream:
  *   nk_kv_append          quantize new bf16 K/V rows into 64-channel int8 groups
  *                         and scatter them into pages ("NInfer-3090" README,
  *                         introduction: the kv_cache_append Op owns KV

@@ -20,31 +20,43 @@
 // fp16 range for any pool. It is one of 16 keys, undone on the scores for K and
 // put into the weights for V (P carries 2^(e - e_ref) beside exp2(S - m)).
 //
-// 28 warps in seven warpgroups, one CTA per SM:
-//   warps 0-7   softmax, two threads a row, 32 keys each: S from tensor memory, masks, running maximum with a
-//               lazy reference (moved only when a score passes it by more than
-//               8, so the accumulator is rarely rescaled), P back to tensor
-//               memory over S, row sums, and the tile's output;
-//   warps 8-23  K and V blocks, of even and of odd number (four warps each):
-//               codes and scales from the ring, widened to fp16, scaled,
-//               stored to the operand buffer of that parity; a warp's chain of
-//               waits, loads and stores is longer than a block's time, so two
-//               blocks are under way;
-//   warp 24     issues the MMAs: QK of block j + 1 goes out before PV of block
+// 20 warps in five warpgroups, one CTA per SM:
+//   warps 0-7   softmax, two warpgroups that take the blocks of a tile in turn,
+//               one thread a row: S from tensor memory, masks, running maximum
+//               with a lazy reference (moved only when a score passes it by
+//               more than 8, so the accumulator is rarely rescaled; the two
+//               hand it to each other), P back to tensor memory over S, row
+//               sums, and the tile's output;
+//   warps 8-15  K, then V, of 16 keys a warp, four warps for the blocks of even
+//               number and four for the odd: codes and scales from the ring,
+//               widened to fp16, scaled, stored to the operand buffer of that
+//               parity; a warp's chain of waits, loads and stores is longer
+//               than a block's time, so two blocks are under way;
+//   warp 16     issues the MMAs: QK of block j + 1 goes out before PV of block
 //               j, so the tensor cores work while the softmax does;
-//   warp 25     looks up the pages and fills a two-stage ring of raw blocks
-//               with bulk asynchronous copies (26 and 27 are idle).
+//   warp 17     walks the list, looks up the pages and fills a two-stage ring of
+//               raw blocks with bulk asynchronous copies (18 and 19 are idle).
 //
-// Loading the codes straight into the convert warps' registers, one block
-// ahead, spared the ring's shared-memory traffic but left the page lookup and
-// the loads' latency in their path: 7,345 us against 4,720 on eight chunks of
-// 1,024 tokens at 8K to 32K (24 q-heads over 4 kv-heads, head dim 256).
+// What bounds it: per 64-key block at head dim 256 the MMAs take 1,026 cycles
+// of the tensor cores, the copies, codes, fp16 tiles and MMA operands about
+// 1,700 of shared memory, and about 4,800 warp instructions 1,200 issue slots
+// of each scheduler; a block takes about 2,050 cycles, so the hand-offs between
+// the roles count beside each of them. Eight chunks of 1,024 tokens at 8K to
+// 32K (24 q-heads over 4 kv-heads): 3,340 us, 1,118 TFLOP/s.
+//
+// Taken against, on those eight chunks: codes loaded straight into the convert
+// warps' registers instead of the ring, 7,345 us (4,720 with the ring, other
+// things equal); MMAs issued by one lane of a diverged warp 4,332 (3,518 from
+// a uniform one); two threads a row, 32 keys each, that exchange their maxima
+// for every block 3,880; 16 convert warps with K and V apart 3,757; the scores
+// of block j + 1 read while the weights of block j are formed 4,243 (3,418
+// otherwise).
 //
 // Work split. The tiles are one list. With more than two tiles a CTA they are
 // first dealt out whole, in rounds of one tile each: neighbouring tiles, which
 // share their keys, then run side by side and read them from L2 (with every
 // CTA on its own stretch of the list instead, eight chunks of 1,024 tokens at
-// 8K to 32K read 11.3 GB from device memory). The blocks of the remaining
+// 8K to 32K read 11.3 GB from device memory and took 3,418 us). The blocks of the remaining
 // tiles, one to two a CTA, or of all tiles where there are fewer, are cut into
 // contiguous ranges that even out the CTAs' totals, whatever the sequences'
 // lengths (stream-K). A tile cut by a range's end leaves fp32 partials with
@@ -114,7 +126,7 @@ struct Smem {
   static constexpr int off_pre = off_tab + 16 * 16 * (D / 64) * 8;   // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_tiles = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch + 1]: tiles before sequence b
   static constexpr int off_cu = off_tiles + (kMaxBatch + 4) * 4;  // int [kMaxBatch + 1]
-  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128]: what the two threads of a row hand each other
+  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128]: what the two softmax threads of a row hand each other
   static constexpr int off_segs = off_pair + 6 * kRows * 4;       // [kSegs] segments
   static constexpr int off_misc = off_segs + kSegs * 64;
   static constexpr int total = off_misc + 1408 + 1024;  // slack to align the base

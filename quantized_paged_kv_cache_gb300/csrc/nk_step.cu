@@ -19,8 +19,8 @@ namespace nk {
 // in a fresh page finds its page in the free list, not in the table another
 // block may be writing, so nothing a block reads is written in the launch.
 // Bounded by latency: one launch, the lengths' load, the block scan, one
-// dependent load per row and its stores. Measured (back-to-back calls): see
-// the launch below.
+// dependent load per row and its stores. Measured in a replayed graph: 4.0 us
+// for 8 sequences of one token, 7.4 us for 1,024 ragged ones (147K rows).
 // ---------------------------------------------------------------------------
 struct TablesParams {
   const int32_t* start;
