@@ -283,7 +283,8 @@ size_t nk_step_host_layout(int32_t B, int32_t total_new, int32_t T, int32_t num_
  * past its end are -1, and used_pages says what was needed. A page id outside
  * the pool sets NK_DEVFLAG_BAD_PAGE and gives -1. 2^31 - 1 new rows or more in
  * all set NK_DEVFLAG_BAD_POS and assign nothing. More rows than max_rows set
- * NK_DEVFLAG_BAD_POS; the first max_rows are written. B is at most 1,024. The
+ * NK_DEVFLAG_BAD_POS; the first max_rows are written. B is at most 1,024; with
+ * B 0 only cu_new[0] and used_pages are written (zeros). The
  * outputs must not overlap the inputs (block_table_dev but for the update).
  * The same call on the same start_pos writes the same results.
  */

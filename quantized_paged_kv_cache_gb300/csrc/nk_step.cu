@@ -303,13 +303,13 @@ int nk_step_tables(int32_t page_size, int32_t num_pages, const int32_t* start_po
                    void* stream) {
   if (page_size < 1 || num_pages < 1 || B < 0 || num_free < 0 || max_pages_per_seq < 1 || max_rows < 0)
     return NK_ERR_SHAPE;
-  if (B == 0) return NK_OK;
   if (B > kMaxBatch) return NK_ERR_UNSUPPORTED;
-  if (!start_pos_dev || !new_lens_dev || !block_table_dev || !cu_new_dev || !ctx_lens_dev ||
-      (num_free > 0 && !free_pages_dev) || (max_rows > 0 && !slot_map_dev))
+  // (a step of no sequences still tells that it has no rows and takes no page)
+  if (!cu_new_dev || (B > 0 && (!start_pos_dev || !new_lens_dev || !block_table_dev || !ctx_lens_dev ||
+                                (num_free > 0 && !free_pages_dev) || (max_rows > 0 && !slot_map_dev))))
     return NK_ERR_NULL;
   // every block reads the lengths while others write the results
-  if (ctx_lens_dev == start_pos_dev || ctx_lens_dev == new_lens_dev) return NK_ERR_SHAPE;
+  if (B > 0 && (ctx_lens_dev == start_pos_dev || ctx_lens_dev == new_lens_dev)) return NK_ERR_SHAPE;
   TablesParams p{start_pos_dev, new_lens_dev, B, page_size, num_pages, free_pages_dev, num_free, block_table_dev,
                  max_pages_per_seq, cu_new_dev, ctx_lens_dev, slot_map_dev, positions_dev, max_rows, used_pages_dev,
                  status_dev};

@@ -88,6 +88,13 @@ def test_tables_without_positions_and_with_nothing_new():
     assert int(t["used"].item()) == 0 and int(t["status"].item()) == 0
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_tables_of_no_sequences(graph):
+    t = run_tables(16, 8, [], [], [3, 1], np.zeros((0, 4)), 5, graph=graph)
+    assert t["cu"].tolist() == [0] and int(t["used"].item()) == 0 and int(t["status"].item()) == 0
+    assert t["slots"].tolist() == [-7] * 5 and t["pos"].tolist() == [-7] * 5  # rows behind the last stay
+
+
 @pytest.mark.parametrize("case", ["negative_start", "negative_new", "past_table", "short_free", "no_free", "bad_free_page",
                                   "bad_held_page", "rows_past_buffer", "too_many_rows"])
 def test_tables_bad_data_is_flagged(case):
