@@ -601,6 +601,7 @@ int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t
   if (max_pages_per_seq < 1 || max_ctx < 1 || (int64_t)max_ctx > (int64_t)max_pages_per_seq * P) return NK_ERR_SHAPE;
   if (!isfinite(sm_scale)) return NK_ERR_SHAPE;
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16)) return NK_ERR_SHAPE;
+  if (q_dev == out_dev) return NK_ERR_SHAPE;  // CTAs that share a tile read its queries at different times
   const int G = num_q_heads / Hkv;
   if ((int64_t)total_q * G > 0x7fffffff - chunk::kRows) return NK_ERR_SHAPE;  // rows of a unit in 32 bits
   const int sms = sm_count();

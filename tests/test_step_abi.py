@@ -89,7 +89,7 @@ def test_chunk_refusals():
     need = nk.chunk_workspace_bytes(64, 4)
     assert need >= 4 * 2 * 128 * 65 * 4 and nk.chunk_workspace_bytes(96, 4) == 0
 
-    def call(p=pool(), q=FAKE, cu=FAKE, B=1, total=5, Hq=2, max_ctx=64, window=0, sinks=0, n=4, ws=FAKE, wsb=need, out=FAKE,
+    def call(p=pool(), q=FAKE, cu=FAKE, B=1, total=5, Hq=2, max_ctx=64, window=0, sinks=0, n=4, ws=FAKE, wsb=need, out=FAKE * 2,
              scale=0.1, pages=4):
         return nk.lib().nk_paged_chunk_attn(ctypes.byref(p) if p is not None else None, q, cu, FAKE, pages, FAKE, B, total,
                                             Hq, scale, max_ctx, window, sinks, n, ws, wsb, out, None, None)
@@ -99,6 +99,7 @@ def test_chunk_refusals():
     assert call(Hq=3, p=pool(H=2)) == 2 and call(Hq=0) == 2 and call(max_ctx=65) == 2 and call(max_ctx=0) == 2
     assert call(pages=0) == 2 and call(scale=float("inf")) == 2 and call(q=FAKE + 8) == 2 and call(p=pool(P=24)) == 2
     assert call(total=1 << 30, Hq=4) == 2 and call(n=1 << 21) == 2
+    assert call(out=FAKE) == 2  # over the queries
     assert call(B=1025) == 3
     assert call(ws=None) == 4 and call(wsb=need - 1) == 4 and call(ws=FAKE + 4) == 4
     assert call(B=0) == 0 and call(total=0) == 0
