@@ -400,6 +400,21 @@ def _need(dtype, *tensors) -> None:
             raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
 
 
+def _empty(stream, shape, dtype, device):
+    """A call's own output or workspace, allocated on the stream the call runs
+    on: memory of another stream could still be in use there, or be handed out
+    again while the call uses it."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map,
                 positions=None, used=None, status=None, stream=None) -> None:
     """The block tables, slot map and lengths of a step from its requests'
@@ -467,13 +482,13 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
     if inv_freq.numel() != half:
         raise ValueError("inv_freq must hold one frequency for every one of the sections")
     if q_out is None:
-        q_out, qos = torch.empty(qs, dtype=bf16, device=q.device), Hq * D
+        q_out, qos = _empty(stream, qs, bf16, q.device), Hq * D
     elif q_out.shape == qs:
         qos = _row_stride(q_out, qs, "q_out")
     else:
         raise ValueError("q_out must have the shape of q")
     if k_out is None:
-        k_out, kos = torch.empty(ks, dtype=bf16, device=k.device), Hkv * D
+        k_out, kos = _empty(stream, ks, bf16, k.device), Hkv * D
     elif k_out.shape == ks:
         kos = _row_stride(k_out, ks, "k_out")
     else:
@@ -500,12 +515,12 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
         raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     elif out.numel() != q.numel():
         raise ValueError("out must have the shape of q")
     if workspace is None:
         wbytes = max(lib().nk_decode_workspace_bytes(B, T, Hq, pool.num_kv_heads, D, num_ctas), 256)
-        workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, wbytes, torch.uint8, q.device)
     else:
         wbytes = workspace.numel() * workspace.element_size()
     rc = lib().nk_paged_window_attn(pool.c_struct(), q.data_ptr(), block_table.data_ptr(), shape[1],
@@ -535,12 +550,12 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:
         raise ValueError("q, cu_q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     elif out.numel() != q.numel():
         raise ValueError("out must have the shape of q")
     if workspace is None:
         wbytes = lib().nk_chunk_workspace_bytes(D, num_ctas)
-        workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, wbytes, torch.uint8, q.device)
     else:
         wbytes = workspace.numel() * workspace.element_size()
     rc = lib().nk_paged_chunk_attn(pool.c_struct(), q.data_ptr(), cu_q.data_ptr(), block_table.data_ptr(), shape[1],

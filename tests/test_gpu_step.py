@@ -302,3 +302,27 @@ def test_step_operators_follow_the_stream_order():
             outs.append(nk.paged_chunk_attn(pool, q, cu, table, ctx, 0.1, 128))
         stream.synchronize()
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_of_a_call_belongs_to_its_stream(raw, monkeypatch):
+    pool = nk.KVPool.empty(4, 16, 1, 64, fill=0)
+    q, k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, ctx, cu = i32([[0, 1]]), i32([20]), i32([0, 3])
+    pos, inv = i32([[0, 1, 2]]), torch.ones(32, dtype=torch.float64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    arg, seen, empty = side.cuda_stream if raw else side, [], torch.empty
+
+    def watched(*a, **kw):
+        if "cuda" in str(kw.get("device", "")):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", watched)
+    nk.mrope(q, k, pos, inv, (32,), stream=arg)
+    nk.paged_window_attn(pool, q[:1].view(1, 1, 2, 64), table, ctx, 0.1, 32, 8, stream=arg)
+    nk.paged_chunk_attn(pool, q, cu, table, ctx, 0.1, 32, stream=arg)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert len(seen) == 6 and set(seen) == {side.cuda_stream}
