@@ -392,12 +392,42 @@ def paged_prefill_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, 
     return out
 
 
+_I32_MAX = 2**31 - 1
+
+
+def _here() -> int:
+    """Index of the device that launches go to."""
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _need_here(*tensors) -> None:
+    """On the current device, where the kernels run (None: an optional argument that is not given)."""
+    here = _here()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor lies on {t.device}, the call runs on the current device, cuda:{here}")
+
+
 def _need(dtype, *tensors) -> None:
     """CUDA, contiguous and of one type (None: an optional argument that is not given)."""
     for t in tensors:
         if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype == dtype):
             _need_cuda(t)
             raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
+
+
+def _one(t, what: str) -> None:
+    if t is not None and t.numel() < 1:
+        raise ValueError(f"{what} must hold an entry")
+
+
+def _context(max_ctx: int, window: int, sinks: int) -> tuple:
+    """The three as the C calls take them: a window or sinks past 2^31 - 1 tokens mean the same as that many."""
+    if max_ctx > _I32_MAX:
+        raise ValueError("max_ctx must be below 2^31")
+    return max_ctx, min(window, _I32_MAX), min(sinks, _I32_MAX)
 
 
 def _empty(stream, shape, dtype, device):
@@ -426,13 +456,15 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
 
     _need(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
     _need(torch.int64, slot_map)
-    B, rows, shape = start_pos.numel(), slot_map.numel(), block_table.shape
+    _need_here(start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map, positions, used, status)
+    _one(used, "used")
+    B, rows, shape = start_pos.numel(), min(slot_map.numel(), _I32_MAX), block_table.shape
     if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
         raise ValueError("start_pos, new_lens, ctx_lens and block_table hold one entry (row) per sequence, cu_new one more")
     if positions is not None and positions.numel() < rows:
         raise ValueError("positions must hold an entry for every one of slot_map")
     rc = lib().nk_step_tables(page_size, num_pages, start_pos.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
-                              free_pages.numel(), block_table.data_ptr(), shape[1], cu_new.data_ptr(),
+                              min(free_pages.numel(), _I32_MAX), block_table.data_ptr(), shape[1], cu_new.data_ptr(),
                               ctx_lens.data_ptr(), slot_map.data_ptr(), _ptr(positions), rows, _ptr(used), _ptr(status),
                               _stream(stream))
     _check(rc, "nk_step_tables")
@@ -441,9 +473,8 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
 @functools.lru_cache(maxsize=64)
 def _sections(sections: tuple):
     """(the sections as a C array, its address, their count, their sum); the array is only ever read."""
-    values = tuple(int(x) for x in sections)
-    array = (ctypes.c_int32 * len(values))(*values)
-    return array, ctypes.addressof(array), len(values), sum(values)
+    array = (ctypes.c_int32 * len(sections))(*sections)
+    return array, ctypes.addressof(array), len(sections), sum(sections)
 
 
 def _row_stride(t, shape, what: str) -> int:
@@ -474,8 +505,12 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
             raise ValueError("q, k and their outputs must be bfloat16 CUDA tensors (there is no CPU path)")
     if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 host tensor")
-    _, array, axes, half = _sections(tuple(sections))
+    _need_here(q, k, positions, q_out, k_out, num_rows)
+    _one(num_rows, "num_rows")
+    _, array, axes, half = _sections(tuple(map(int, sections)))
     rows, Hq, D = qs
+    if rows > _I32_MAX:
+        raise ValueError("q and k must have fewer than 2^31 rows")
     Hkv = ks[1]
     if len(ps) != 2 or ps[0] != axes or ps[1] < rows:
         raise ValueError("positions must hold one row of positions per section (axis)")
@@ -509,7 +544,9 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
     _need(torch.bfloat16, q, out)
     _need(torch.int32, block_table, ctx_lens, status)
     _need_cuda(workspace)
+    _need_here(pool.storage, q, block_table, ctx_lens, workspace, out, status)
     pool.need("int8")
+    max_ctx, window, sinks = _context(max_ctx, window, sinks)
     B, T, Hq, D = q.shape
     shape = block_table.shape
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
@@ -544,7 +581,9 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
     _need(torch.bfloat16, q, out)
     _need(torch.int32, cu_q, block_table, ctx_lens, status)
     _need_cuda(workspace)
+    _need_here(pool.storage, q, cu_q, block_table, ctx_lens, workspace, out, status)
     pool.need("int8")
+    max_ctx, window, sinks = _context(max_ctx, window, sinks)
     total, Hq, D = q.shape
     B, shape = ctx_lens.numel(), block_table.shape
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:

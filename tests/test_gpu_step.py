@@ -326,3 +326,37 @@ def test_memory_of_a_call_belongs_to_its_stream(raw, monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert len(seen) == 6 and set(seen) == {side.cuda_stream}
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    pool = nk.KVPool.empty(4, 16, 1, 64, fill=0)
+    x, y = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, ctx, cu, z, slots = i32([[0, 1]]), i32([20]), i32([0, 3]), i32([0]), torch.zeros(4, dtype=torch.int64, device="cuda")
+    monkeypatch.setattr(nk, "_here", lambda: torch.cuda.current_device() + 1)  # as if that one were current
+    for call in (lambda: nk.step_tables(16, 4, z, z, z, table, cu, ctx, slots),
+                 lambda: nk.mrope(x, y, i32([[0, 1, 2]]), torch.ones(32, dtype=torch.float64), (32,)),
+                 lambda: nk.paged_window_attn(pool, x[:1].view(1, 1, 2, 64), table, ctx, 0.1, 32, 8),
+                 lambda: nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_arguments_past_32_bits():
+    pool = nk.KVPool.empty(4, 16, 1, 64, fill=0)
+    x = torch.randn(3, 2, 64, device="cuda").bfloat16()
+    v = torch.randn(20, 1, 64, device="cuda").bfloat16()
+    table, ctx, cu = i32([[0, 1]]), i32([20]), i32([0, 3])
+    nk.kv_append(pool, table, i32([0]), i32([0, 20]), v, v)
+    whole = nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32)
+    assert torch.equal(nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32, window=2**32 + 3), whole)
+    assert torch.equal(nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32, window=1, sinks=2**32), whole)
+    q = x.view(1, 3, 2, 64)
+    all_keys = nk.paged_decode_attn(pool, q, table, ctx, 0.1, 32)
+    assert torch.equal(nk.paged_window_attn(pool, q, table, ctx, 0.1, 32, 2**32 + 3), all_keys)
+    for attn in (lambda m: nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, m),
+                 lambda m: nk.paged_window_attn(pool, q, table, ctx, 0.1, m, 8)):
+        with pytest.raises(ValueError):
+            attn(2**32 + 32)
+    pos, inv = i32([[0, 1, 2]]), torch.ones(32, dtype=torch.float64)
+    with pytest.raises(ValueError):  # no row count in it
+        nk.mrope(x, x[:, :1], pos, inv, (32,), num_rows=cu[2:])
