@@ -316,7 +316,8 @@ int nk_step_tables(int32_t page_size, int32_t num_pages, const int32_t* start_po
  *                   were (cu_new + B of nk_step_tables).
  * With angle = positions[axis(i)][j] * inv_freq[i], channels i and i + half of
  * every head become (a cos - b sin, b cos + a sin), in fp32 from an angle that
- * is exact to 2^-23 turns at any position, rounded once to bf16; channels
+ * is exact to 2^-23 turns at any position (for frequencies of up to 2 pi; their
+ * doubles carry no more beyond), rounded once to bf16; channels
  * 2 * half and up are copied. Pointers 16-byte aligned, strides multiples of 8,
  * head_dim a multiple of 8 (16 .. 256).
  */
@@ -362,7 +363,8 @@ int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
  * whose id is outside the pool (NK_DEVFLAG_BAD_PAGE) and groups whose scale is
  * not finite (NK_DEVFLAG_RANGE) count as zeros. K and V enter the products as
  * fp16: an output differs from the exact one by its bf16 rounding plus at most
- * a few 2^-11 of the values it averages. B is at most 1,024 and
+ * a few 2^-11 of the values it averages (and, where neighbouring keys differ in
+ * size by more than 2^14, 2^-25 of the largest of the 16 around a key). B is at most 1,024 and
  * total_q * Hq / Hkv below 2^31 - 128.
  */
 size_t nk_chunk_workspace_bytes(int32_t head_dim, int32_t num_ctas);

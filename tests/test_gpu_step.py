@@ -1,5 +1,9 @@
 """nk_step_tables and nk_mrope on the GPU against plain 64-bit forms, and one
 serving step (tables, rotary positions, append, attention) run together."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -360,3 +364,79 @@ def test_arguments_past_32_bits():
     pos, inv = i32([[0, 1, 2]]), torch.ones(32, dtype=torch.float64)
     with pytest.raises(ValueError):  # no row count in it
         nk.mrope(x, x[:, :1], pos, inv, (32,), num_rows=cu[2:])
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """Kernels whose code is not loaded yet, in a graph capture."""
+    code = """
+import torch, quantized_paged_kv_cache_gb300 as nk
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+for D, P, Hq in ((256, 64, 24), (64, 16, 4)):
+    pool = nk.KVPool.empty(4, P, 2, D, fill=0)
+    x = torch.ones(3, Hq, D, dtype=torch.bfloat16, device="cuda")
+    start, new, free, table = i32([5]), i32([3]), i32([1, 2]), i32([[0, -1]])
+    cu, ctx, slots = i32([0, 0]), i32([0]), torch.zeros(3, dtype=torch.int64, device="cuda")
+    pos, inv = i32([[5, 6, 7]]), torch.ones(32, dtype=torch.float64)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nk.step_tables(P, 4, start, new, free, table, cu, ctx, slots)
+        q, k = nk.mrope(x, x[:, :2], pos, inv, (32,))
+        nk.kv_append(pool, table, start, cu, k, k)
+        a = nk.paged_chunk_attn(pool, q, cu, table, ctx, 0.1, 2 * P, window=8)
+        b = nk.paged_window_attn(pool, q.view(1, 3, Hq, D), table, ctx, 0.1, 2 * P, 8)
+    g.replay()
+    torch.cuda.synchronize()
+    assert (a.float() - b.view_as(a).float()).abs().max().item() < 2e-2 and a.float().abs().max().item() > 0.5
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)
+
+
+def test_two_graphs_with_workspaces_of_their_own_run_at_once():
+    rng = np.random.RandomState(8)
+    D, P, Hq, Hkv = 128, 16, 16, 2
+    calls = []
+    for i in range(2):
+        L = [int(x) for x in rng.randint(200, 3000, 6)]
+        pages = [-(-n // P) for n in L]
+        pool = nk.KVPool.empty(sum(pages), P, Hkv, D, fill=0)
+        table = np.full((6, max(pages)), -1)
+        at = 0
+        for b, n in enumerate(pages):
+            table[b, :n] = np.arange(at, at + n)
+            at += n
+        table = i32(table)
+        rows = sum(L)
+        k, v = (torch.randn(rows, Hkv, D, device="cuda").bfloat16() for _ in range(2))
+        nk.kv_append(pool, table, i32([0] * 6), i32(np.concatenate(([0], np.cumsum(L)))), k, v)
+        new = [1, 40, 3, 0, 17, 150]
+        q = torch.randn(sum(new), Hq, D, device="cuda").bfloat16()
+        cu, ctx = i32(np.concatenate(([0], np.cumsum(new)))), i32(L)
+        qd = torch.randn(6, 2, Hq, D, device="cuda").bfloat16()
+        ws = [torch.empty(nk.chunk_workspace_bytes(D), dtype=torch.uint8, device="cuda"),
+              torch.empty(nk.decode_workspace_bytes(6, 2, Hq, Hkv, D), dtype=torch.uint8, device="cuda")]
+        out = [torch.zeros_like(q), torch.zeros_like(qd)]
+
+        def call(pool=pool, table=table, q=q, cu=cu, ctx=ctx, qd=qd, ws=ws, out=out, top=max(L)):
+            nk.paged_chunk_attn(pool, q, cu, table, ctx, 0.1, top, window=500, sinks=3, workspace=ws[0], out=out[0])
+            nk.paged_window_attn(pool, qd, table, ctx, 0.1, top, 150, 5, workspace=ws[1], out=out[1])
+
+        call()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in out]
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=s):
+            call()
+        calls.append((g, s, out, want, call))  # (call holds the tensors that the graph works on)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s, out, want, _ in calls:
+            with torch.cuda.stream(s):
+                for o in out:
+                    o.zero_()
+                for _ in range(4):
+                    g.replay()
+        torch.cuda.synchronize()
+        for g, s, out, want, _ in calls:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
