@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import numbers
 from dataclasses import dataclass
 
 from ._lib import NKError, lib, nk_kv_pool, status_string  # noqa: F401
@@ -395,27 +396,47 @@ def paged_prefill_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, 
 _I32_MAX = 2**31 - 1
 
 
+_device = None
+
+
 def _here() -> int:
-    """Index of the device that launches go to."""
-    import torch
+    """Index of the device that launches go to (-2 without a GPU: no tensor lies there)."""
+    global _device
+    if _device is None:
+        import torch
 
-    return torch.cuda.current_device()
+        if not torch.cuda.is_available():
+            return -2
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        torch.cuda.current_device()  # CUDA is up before the raw call
+    return _device()
 
 
-def _need_here(*tensors) -> None:
-    """On the current device, where the kernels run (None: an optional argument that is not given)."""
-    here = _here()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor lies on {t.device}, the call runs on the current device, cuda:{here}")
+def _refuse(t, here: int, dtype=None) -> None:
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    if t.get_device() != here:
+        raise ValueError(f"a tensor lies on {t.device}, the call runs on the current device, cuda:{here}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
+    raise ValueError("all tensors must be contiguous")
 
 
 def _need(dtype, *tensors) -> None:
-    """CUDA, contiguous and of one type (None: an optional argument that is not given)."""
+    """On the current device, where the kernels run, contiguous and of one type (None: an argument that is not given)."""
+    here = _here()
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype == dtype):
-            _need_cuda(t)
-            raise ValueError(f"expected a {dtype} tensor, not a {t.dtype} one")
+        if t is not None and not (t.get_device() == here and t.dtype == dtype and t.is_contiguous()):
+            _refuse(t, here, dtype)
+
+
+def _need_scratch(storage, workspace) -> None:
+    """The pool's memory and the workspace: of any type."""
+    here = _here()
+    if not (storage.get_device() == here and storage.is_contiguous()):
+        _refuse(storage, here)
+    if workspace is not None and not (workspace.get_device() == here and workspace.is_contiguous()):
+        _refuse(workspace, here)
 
 
 def _one(t, what: str) -> None:
@@ -456,7 +477,6 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
 
     _need(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
     _need(torch.int64, slot_map)
-    _need_here(start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map, positions, used, status)
     _one(used, "used")
     B, rows, shape = start_pos.numel(), min(slot_map.numel(), _I32_MAX), block_table.shape
     if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
@@ -473,7 +493,9 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
 @functools.lru_cache(maxsize=64)
 def _sections(sections: tuple):
     """(the sections as a C array, its address, their count, their sum); the array is only ever read."""
-    array = (ctypes.c_int32 * len(sections))(*sections)
+    if not all(isinstance(x, numbers.Integral) for x in sections):
+        raise ValueError("sections must be whole numbers")
+    array = (ctypes.c_int32 * len(sections))(*map(int, sections))
     return array, ctypes.addressof(array), len(sections), sum(sections)
 
 
@@ -499,15 +521,14 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
     if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
         raise ValueError("q and k must be [rows][heads][head_dim] with the same rows and head_dim")
     _need(torch.int32, positions, num_rows)
-    bf16 = torch.bfloat16
+    bf16, here = torch.bfloat16, _here()
     for t in (q, k, q_out, k_out):
-        if t is not None and not (t.is_cuda and t.dtype == bf16):
-            raise ValueError("q, k and their outputs must be bfloat16 CUDA tensors (there is no CPU path)")
+        if t is not None and not (t.get_device() == here and t.dtype == bf16):
+            _refuse(t, here, bf16)
     if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 host tensor")
-    _need_here(q, k, positions, q_out, k_out, num_rows)
     _one(num_rows, "num_rows")
-    _, array, axes, half = _sections(tuple(map(int, sections)))
+    _, array, axes, half = _sections(tuple(sections))
     rows, Hq, D = qs
     if rows > _I32_MAX:
         raise ValueError("q and k must have fewer than 2^31 rows")
@@ -543,8 +564,7 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
 
     _need(torch.bfloat16, q, out)
     _need(torch.int32, block_table, ctx_lens, status)
-    _need_cuda(workspace)
-    _need_here(pool.storage, q, block_table, ctx_lens, workspace, out, status)
+    _need_scratch(pool.storage, workspace)
     pool.need("int8")
     max_ctx, window, sinks = _context(max_ctx, window, sinks)
     B, T, Hq, D = q.shape
@@ -580,8 +600,7 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
 
     _need(torch.bfloat16, q, out)
     _need(torch.int32, cu_q, block_table, ctx_lens, status)
-    _need_cuda(workspace)
-    _need_here(pool.storage, q, cu_q, block_table, ctx_lens, workspace, out, status)
+    _need_scratch(pool.storage, workspace)
     pool.need("int8")
     max_ctx, window, sinks = _context(max_ctx, window, sinks)
     total, Hq, D = q.shape

@@ -164,7 +164,7 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
                      : path == Path::kRk8v4 ? decode_rk8v4_ctas_per_sm(D, G)
                      : (simt ? decode_simt_ctas_per_sm(D, G) : decode_mma_ctas_per_sm(D, T, G));
   const int32_t seen = visible_keys(max_ctx, P, T, window, sinks);  // max_ctx without a window
-  const int32_t n = num_ctas > 0 ? num_ctas : default_ctas(B, Hkv, seen, P, per_sm);
+  int32_t n = num_ctas > 0 ? num_ctas : default_ctas(B, Hkv, seen, P, per_sm);
   // The fp32 sums of mma.sync are not rounded to nearest, and their error
   // grows with the keys of one kv-head that a CTA runs through its
   // accumulators. The tcgen05 kernel folds them (its FOLD instance); the
@@ -176,6 +176,17 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
     const int Tl = T - (T - 1) / Tc * Tc;  // columns of the last chunk
     const bool mma_kernel =
         rk_tc || !decode_tc_supported(fmt, D, Tc, G, P) || !decode_tc_supported(fmt, D, Tl, G, P);
+    // A window gives most sequences the same number of pages, so with as many
+    // CTAs as divide evenly over the units few CTAs change units in the middle,
+    // which costs the mma.sync kernel some thirty 16-key pages. Taken where it
+    // leaves at most a fifth of the CTAs out: 64 sequences with windows of
+    // 1,000 on 16-key pages (128 CTAs for 152) 39.9 -> 32.5 us, 8 with 8,192 on
+    // 64-key pages 49.0 -> 46.2; half of the 64 shorter than their window 51.0
+    // -> 51.5. (The tcgen05 kernel changes units cheaply: 79.7 -> 80.1, T = 4.)
+    if (path == Path::kWindow && num_ctas <= 0 && mma_kernel && seen <= kMaxMmaRunKeys) {
+      const int64_t units = (int64_t)B * Hkv, even = units <= n ? n / units * units : 0;
+      if (5 * even >= 4 * (int64_t)n) n = (int32_t)even;
+    }
     const int64_t unit = ((int64_t)seen + P - 1) / P;
     const int64_t per_cta = (max_items(B, Hkv, seen, P) + n - 1) / n;
     if (mma_kernel && (per_cta < unit ? per_cta : unit) * P > kMaxMmaRunKeys) return NK_ERR_UNSUPPORTED;
@@ -239,7 +250,8 @@ int launch_decode(const DecodeParams& p0, Path path, cudaStream_t st) {
     cudaError_t e = path == Path::kRk8v4 ? (decode_mma_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_mma(p, st)
                                                                                           : launch_decode_rk8v4(p, st))
                     : path == Path::kSimt   ? launch_decode_simt(p, st)
-                    : (decode_tc_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st) : launch_decode_mma(p, st));
+                    : (decode_tc_supported(p.fmt, p.D, p.T, p.G, p.P) ? launch_decode_tc(p, st)
+                                                                     : launch_decode_mma(p, st));
     if (e != cudaSuccess) return NK_ERR_CUDA;
     e = launch_decode_combine(p, st);
     if (e != cudaSuccess) return NK_ERR_CUDA;

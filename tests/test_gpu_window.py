@@ -52,6 +52,17 @@ def test_window_matches_reference(shape):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("B,T", [(64, 1), (70, 2), (33, 1)])
+def test_a_batch_of_windows_split_evenly_over_its_units(B, T):
+    lens = [150 + 37 * b % 260 for b in range(B)]
+    lens[1], lens[B // 2] = T, 60  # (most units have the window's pages, some fewer)
+    w = wl.custom(f"even{B}", B=B, T=T, Hq=16, Hkv=2, D=128, P=16, ctx_lens=lens, seed=94,
+                  num_pages=sum((L + 15) // 16 for L in lens) + 2, outlier_channels=2, outlier_scale=8.0)
+    c = build(w, fill=0xFF, oracle_pool=False)
+    for window, sinks in ((100, 5), (40, 0)):
+        compare(call(c, window, sinks), reference(c, window, sinks), f"{B} sequences, window {window}")
+
+
 def test_a_window_over_everything_is_the_whole_context():
     w = wl.custom("win_all", B=2, T=4, Hq=24, Hkv=4, D=256, P=64, ctx_lens=[900, 333], seed=92)
     c = build(w, oracle_pool=False)
