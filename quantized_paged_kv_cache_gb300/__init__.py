@@ -145,6 +145,9 @@ class KVPool:
 
     def c_struct(self) -> nk_kv_pool:
         _need_cuda(self.storage)
+        return self._struct()
+
+    def _struct(self) -> nk_kv_pool:  # (of storage that was checked)
         return nk_kv_pool(self.storage.data_ptr(), self.num_pages, self.page_size, self.num_kv_heads, self.head_dim)
 
 
@@ -444,26 +447,27 @@ def _one(t, what: str) -> None:
         raise ValueError(f"{what} must hold an entry")
 
 
-def _context(max_ctx: int, window: int, sinks: int) -> tuple:
-    """The three as the C calls take them: a window or sinks past 2^31 - 1 tokens mean the same as that many."""
+def _clamped(max_ctx: int, window: int, sinks: int) -> tuple:
+    """A window or sinks past 2^31 - 1 tokens, which the C calls cannot take, mean the same as that many."""
     if max_ctx > _I32_MAX:
         raise ValueError("max_ctx must be below 2^31")
-    return max_ctx, min(window, _I32_MAX), min(sinks, _I32_MAX)
+    return min(window, _I32_MAX), min(sinks, _I32_MAX)
 
 
-def _empty(stream, shape, dtype, device):
+def _empty(stream, like, shape, dtype=None):
     """A call's own output or workspace, allocated on the stream the call runs
     on: memory of another stream could still be in use there, or be handed out
     again while the call uses it."""
     import torch
 
+    dtype = dtype or like.dtype
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = _stream(stream)
-        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+        stream = torch.cuda.ExternalStream(raw, device=like.device) if raw else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map,
@@ -538,13 +542,13 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
     if inv_freq.numel() != half:
         raise ValueError("inv_freq must hold one frequency for every one of the sections")
     if q_out is None:
-        q_out, qos = _empty(stream, qs, bf16, q.device), Hq * D
+        q_out, qos = _empty(stream, q, qs), Hq * D
     elif q_out.shape == qs:
         qos = _row_stride(q_out, qs, "q_out")
     else:
         raise ValueError("q_out must have the shape of q")
     if k_out is None:
-        k_out, kos = _empty(stream, ks, bf16, k.device), Hkv * D
+        k_out, kos = _empty(stream, k, ks), Hkv * D
     elif k_out.shape == ks:
         kos = _row_stride(k_out, ks, "k_out")
     else:
@@ -566,21 +570,22 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
     _need(torch.int32, block_table, ctx_lens, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    max_ctx, window, sinks = _context(max_ctx, window, sinks)
+    if max_ctx > _I32_MAX or window > _I32_MAX or sinks > _I32_MAX:
+        window, sinks = _clamped(max_ctx, window, sinks)
     B, T, Hq, D = q.shape
     shape = block_table.shape
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
         raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
     if out is None:
-        out = _empty(stream, q.shape, q.dtype, q.device)
+        out = _empty(stream, q, q.shape)
     elif out.numel() != q.numel():
         raise ValueError("out must have the shape of q")
     if workspace is None:
         wbytes = max(lib().nk_decode_workspace_bytes(B, T, Hq, pool.num_kv_heads, D, num_ctas), 256)
-        workspace = _empty(stream, wbytes, torch.uint8, q.device)
+        workspace = _empty(stream, q, wbytes, torch.uint8)
     else:
         wbytes = workspace.numel() * workspace.element_size()
-    rc = lib().nk_paged_window_attn(pool.c_struct(), q.data_ptr(), block_table.data_ptr(), shape[1],
+    rc = lib().nk_paged_window_attn(pool._struct(), q.data_ptr(), block_table.data_ptr(), shape[1],
                                     ctx_lens.data_ptr(), B, T, Hq, sm_scale, max_ctx, window, sinks, num_ctas,
                                     workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_window_attn")
@@ -602,21 +607,22 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
     _need(torch.int32, cu_q, block_table, ctx_lens, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    max_ctx, window, sinks = _context(max_ctx, window, sinks)
+    if max_ctx > _I32_MAX or window > _I32_MAX or sinks > _I32_MAX:
+        window, sinks = _clamped(max_ctx, window, sinks)
     total, Hq, D = q.shape
     B, shape = ctx_lens.numel(), block_table.shape
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:
         raise ValueError("q, cu_q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
     if out is None:
-        out = _empty(stream, q.shape, q.dtype, q.device)
+        out = _empty(stream, q, q.shape)
     elif out.numel() != q.numel():
         raise ValueError("out must have the shape of q")
     if workspace is None:
         wbytes = lib().nk_chunk_workspace_bytes(D, num_ctas)
-        workspace = _empty(stream, wbytes, torch.uint8, q.device)
+        workspace = _empty(stream, q, wbytes, torch.uint8)
     else:
         wbytes = workspace.numel() * workspace.element_size()
-    rc = lib().nk_paged_chunk_attn(pool.c_struct(), q.data_ptr(), cu_q.data_ptr(), block_table.data_ptr(), shape[1],
+    rc = lib().nk_paged_chunk_attn(pool._struct(), q.data_ptr(), cu_q.data_ptr(), block_table.data_ptr(), shape[1],
                                    ctx_lens.data_ptr(), B, total, Hq, sm_scale, max_ctx, window, sinks, num_ctas,
                                    workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_chunk_attn")
