@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesPa
 // memory (all heads share them). A thread keeps one piece of the head (eight
 // channel pairs, or eight copied channels) and goes over (row, head) from its
 // first head on: no division in the loop (with one per item, 8,192 rows of 24
-// + 4 heads of 256 took 43.1 us against 39.7: 5.9 TB/s, 0.87 of a copy's rate;
-// 4,099 rows of 16 + 2 heads of 128, half of each turned, 11.4 against 7.6).
+// + 4 heads of 256 took 43.1 us against 39.1: 6.0 TB/s, 0.89 of a copy's rate;
+// 4,099 rows of 16 + 2 heads of 128, half of each turned, 11.4 against 7.3).
 // Many blocks in flight cover the loads' latency; two or four items of a
 // thread in flight, held in registers, were slower (60 and 87 us).
 // ---------------------------------------------------------------------------
