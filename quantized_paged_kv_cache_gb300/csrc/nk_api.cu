@@ -56,7 +56,7 @@ int sm_count() {
 constexpr int64_t kMaxMmaRunKeys = 262144;
 
 int64_t max_items(int32_t B, int32_t Hkv, int32_t max_ctx, int32_t P) {
-  return (int64_t)B * Hkv * ((max_ctx + P - 1) / P);
+  return (int64_t)B * Hkv * (((int64_t)max_ctx + P - 1) / P);
 }
 
 // Keys of a sequence in pages that the T columns of a call can see, at most:

@@ -167,7 +167,7 @@ struct SplitShape {
 // Pages of a sequence of context length L (0 for an invalid length).
 __device__ __forceinline__ int pages_of_len(const SplitShape& s, int L) {
   if (L < s.T || L > s.max_ctx || (int64_t)L > (int64_t)s.max_pages * s.P) return 0;
-  return (L + s.P - 1) / s.P;
+  return (L - 1) / s.P + 1;  // (T >= 1; L + P - 1 may pass 31 bits)
 }
 
 // The same split over a sliding window with sinks: query column t at position

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         }
         // ---- causal / context mask: only pages that reach past L - T (padding rows
         // hold zero queries and are never written out, so they need no mask)
-        if ((lp + 1) * kP > L - T) {
+        if (lp * kP > L - T - kP) {
           const int lim = pos - (L - T);  // visible to column t when lim <= t
 #pragma unroll
           for (int i = 0; i < NR; ++i)
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         if constexpr (WIN) {
           // pages with a key before the last column's window, past the sinks
           if (lp * kP <= L - 1 - sh.window && lp * kP + kP - 1 >= sh.sinks && pos >= sh.sinks) {
-            const int lim = pos + sh.window - (L - T);  // hidden from column t when lim <= t
+            const int lim = pos - (L - T) + sh.window;  // hidden from column t when lim <= t
 #pragma unroll
             for (int i = 0; i < NR; ++i)
               if (lim <= row_t[8 * (i >> 2) + 4 * half + (i & 3)]) sc[i] = -INFINITY;

@@ -440,3 +440,22 @@ def test_two_graphs_with_workspaces_of_their_own_run_at_once():
         torch.cuda.synchronize()
         for g, s, out, want, _ in calls:
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_slots_and_rows_past_32_bits():
+    # the last pages of a pool of 2^33 slots
+    pages = 2**27
+    t = run_tables(64, pages, [130, 0], [70, 65], [pages - 1, 3, pages - 2], [[5, 6, pages - 3, -1], [-1] * 4], 135)
+    want = [(pages - 3) * 64 + 2 + i for i in range(62)] + [(pages - 1) * 64 + i for i in range(8)]
+    want += [3 * 64 + i for i in range(64)] + [(pages - 2) * 64]
+    assert t["slots"].tolist() == want and int(t["status"].item()) == 0
+    # rows of a buffer further apart than 2^31 elements in all
+    stride, Hq, D = 2**30, 3, 64
+    buf = torch.empty(2 * stride + 4 * D, dtype=torch.bfloat16, device="cuda")
+    q, k = buf.as_strided((3, Hq, D), (stride, D, 1)), buf.as_strided((3, 1, D), (stride, D, 1), Hq * D)
+    x, y = torch.randn(3, Hq, D, device="cuda").bfloat16(), torch.randn(3, 1, D, device="cuda").bfloat16()
+    q.copy_(x), k.copy_(y)
+    pos, inv = i32([[1, 50, 9000]]), 10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)
+    want = nk.mrope(x, y, pos, inv, (32,))
+    nk.mrope(q, k, pos, inv, (32,), q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])

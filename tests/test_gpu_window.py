@@ -122,3 +122,57 @@ def test_window_replays_in_a_graph_on_a_side_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D,P,T", [(256, 64, 1), (256, 64, 4), (128, 16, 2)])
+def test_the_last_positions_that_32_bits_hold(D, P, T):
+    """A context of 2^31 - 1 tokens (its pages far from the window were given back) is the one of 2,047 tokens."""
+    Hq, Hkv, near, far = 24, 4, 2047, 2**31 - 1
+    shift = (far - near) // P
+    pool = nk.KVPool.empty(2048 // P, P, Hkv, D, fill=0)
+    table = torch.randperm(2048 // P, device="cuda").int().view(1, -1)
+    k, v = (torch.randn(near, Hkv, D, device="cuda").bfloat16() for _ in range(2))
+    lens = [torch.tensor([n], dtype=torch.int32, device="cuda") for n in (near, far, 0)]
+    cu = torch.tensor([0, near], dtype=torch.int32, device="cuda")
+    nk.kv_append(pool, table, lens[2], cu, k, v)
+    long = torch.full((1, shift + 2048 // P), -1, dtype=torch.int32, device="cuda")
+    long[:, shift:] = table
+    q = torch.randn(1, T, Hq, D, device="cuda").bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for window in (1, 100, 1500):
+        a = nk.paged_window_attn(pool, q, table, lens[0], 0.1, near, window, status=status)
+        b = nk.paged_window_attn(pool, q, long, lens[1], 0.1, far, window, status=status)
+        assert torch.equal(a, b), f"window {window}"
+        rows = torch.randn(70, Hq, D, device="cuda").bfloat16()
+        cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+        a = nk.paged_chunk_attn(pool, rows, cu, table, lens[0], 0.1, near, window=window, status=status)
+        b = nk.paged_chunk_attn(pool, rows, cu, long, lens[1], 0.1, far, window=window, status=status)
+        assert torch.equal(a, b), f"chunk, window {window}"
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("D,P", [(256, 64), (128, 16)])
+def test_pages_and_rows_past_4_gib(D, P):
+    """Pages at the end of a pool of more than 2^32 bytes, query rows past 2^32 bytes."""
+    Hq, Hkv, n = 24, 4, 1000
+    used = -(-n // P)
+    big_pages = 2**32 // (nk.kv_chunk_bytes(P, D) * Hkv) + used + 1
+    k, v = (torch.randn(n, Hkv, D, device="cuda").bfloat16() for _ in range(2))
+    start, cu, ctx = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0], [0, n], [n]))
+    at = torch.arange(used, dtype=torch.int32, device="cuda").view(1, -1)
+    pools = [(nk.KVPool.empty(used, P, Hkv, D), at), (nk.KVPool.empty(big_pages, P, Hkv, D), at + (big_pages - used))]
+    base = 2**32 // (Hq * D * 2) + 1
+    q = torch.randn(33, Hq, D, device="cuda").bfloat16()
+    far, out = (torch.empty(base + 33, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    far[base:] = q
+    got = []
+    for pool, table in pools:
+        nk.kv_append(pool, table, start, cu, k, v)
+        for window in (300, n):
+            got.append(nk.paged_window_attn(pool, q[:2].unsqueeze(0), table, ctx, 0.1, n, window))
+            got.append(nk.paged_chunk_attn(pool, q, torch.tensor([0, 33], dtype=torch.int32, device="cuda"), table, ctx, 0.1, n,
+                                           window=window))
+            nk.paged_chunk_attn(pool, far, torch.tensor([base, base + 33], dtype=torch.int32, device="cuda"), table, ctx, 0.1,
+                                n, window=window, out=out)
+            assert torch.equal(out[base:], got[-1])
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], got[4:]))
