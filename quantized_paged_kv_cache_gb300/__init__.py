@@ -443,7 +443,7 @@ def _need_scratch(storage, workspace) -> None:
 
 
 def _one(t, what: str) -> None:
-    if t is not None and t.numel() < 1:
+    if t.numel() < 1:
         raise ValueError(f"{what} must hold an entry")
 
 
@@ -460,14 +460,13 @@ def _empty(stream, like, shape, dtype=None):
     again while the call uses it."""
     import torch
 
-    dtype = dtype or like.dtype
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is None:  # (rows of consecutive heads: dense ones, whatever the rows of `like` are apart)
+        return torch.empty_like(like) if dtype is None else torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
         raw = _stream(stream)
         stream = torch.cuda.ExternalStream(raw, device=like.device) if raw else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, slot_map,
@@ -481,7 +480,8 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
 
     _need(torch.int32, start_pos, new_lens, free_pages, block_table, cu_new, ctx_lens, positions, used, status)
     _need(torch.int64, slot_map)
-    _one(used, "used")
+    if used is not None:
+        _one(used, "used")
     B, rows, shape = start_pos.numel(), min(slot_map.numel(), _I32_MAX), block_table.shape
     if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
         raise ValueError("start_pos, new_lens, ctx_lens and block_table hold one entry (row) per sequence, cu_new one more")
@@ -531,7 +531,8 @@ def mrope(q, k, positions, inv_freq, sections, interleaved: bool = False, q_out=
             _refuse(t, here, bf16)
     if inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 host tensor")
-    _one(num_rows, "num_rows")
+    if num_rows is not None:
+        _one(num_rows, "num_rows")
     _, array, axes, half = _sections(tuple(sections))
     rows, Hq, D = qs
     if rows > _I32_MAX:
