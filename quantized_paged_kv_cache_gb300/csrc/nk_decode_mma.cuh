@@ -730,9 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   // The first S pages, issued in order by one thread (the copy unit then
   // completes page 0 first). Each issue waits until the unit accepts the
   // copy, so the issuer is the last warp, whose first block is in page 1.
-  if (tid == kThreads - 32) {
-    const int n0 = total < S ? total : S;
-    for (int q = 0; q < n0; ++q) {
+  // WIN: with many small pages (or few in all) the issue itself is what the
+  // start waits for, and the lanes of four warps share it: 64 sequences with
+  // windows of 1,000 on 16-key pages 32.5 -> 27.3 us, 8 with 3,000 on 128-key
+  // pages 15.9 -> 14.5. With a ring of few large pages and more to come they
+  // would all land late together (8 windows of 8,192 on 64-key pages 46.4 us in
+  // order, 47.7 shared out).
+  const int n0 = total < S ? total : S;
+  const bool shared_out = WIN && (S > 8 || total <= S);
+  constexpr int kIssuers = 4;
+  if (shared_out ? warp >= kConsumerWarps - kIssuers : tid == kThreads - 32) {
+    const int q0 = shared_out ? lane * kIssuers + warp % kIssuers : 0, step = shared_out ? 32 * kIssuers : 1;
+    for (int q = q0; q < n0; q += step) {
       if (!p.issuable(q)) break;
       if constexpr (RK)
         issue_page_rk<D>(p, &tmap, &tmapv, pid[q], stage0 + q * geo.stage_bytes, smem_u32(&full_bar[q]));
