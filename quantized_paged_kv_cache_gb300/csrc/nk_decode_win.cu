@@ -10,7 +10,7 @@ namespace mma {
 
 template <int D, int NT, int CS>
 static cudaError_t launch_w(const CUtensorMap& map, const DecodeParams& p, cudaStream_t st) {
-  const Geometry geo = geometry(kFmtI8F32, D, NT, CS, p.P, p.B);
+  const Geometry geo = geometry(kFmtI8F32, D, NT, CS, p.P, p.B, true);
   if (geo.stages < 2 || geo.total > kSmemLimit) return cudaErrorInvalidConfiguration;
   cudaError_t e =
       set_smem_limit(reinterpret_cast<const void*>(decode_mma_kernel<D, NT, CS, kFmtI8F32, true>), geo.total);
