@@ -178,11 +178,11 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
         rk_tc || !decode_tc_supported(fmt, D, Tc, G, P) || !decode_tc_supported(fmt, D, Tl, G, P);
     // A window gives most sequences the same number of pages, so with as many
     // CTAs as divide evenly over the units few CTAs change units in the middle,
-    // which costs the mma.sync kernel some thirty 16-key pages. Taken where it
-    // leaves at most a fifth of the CTAs out: 64 sequences with windows of
-    // 1,000 on 16-key pages (128 CTAs for 152) 39.9 -> 32.5 us, 8 with 8,192 on
-    // 64-key pages 49.0 -> 46.2; half of the 64 shorter than their window 51.0
-    // -> 51.5. (The tcgen05 kernel changes units cheaply: 79.7 -> 80.1, T = 4.)
+    // which costs the mma.sync kernel the time of some twenty 16-key pages. Taken
+    // where it leaves at most a fifth of the CTAs out: 64 sequences with windows
+    // of 1,000 on 16-key pages (128 CTAs for 152) 33.2 -> 27.3 us, 8 with 8,192
+    // on 64-key pages 49.1 -> 46.9; half of the 64 shorter than their window
+    // 40.3 -> 40.5. (The tcgen05 kernel changes units cheaply: 79.7 -> 80.1, T = 4.)
     if (path == Path::kWindow && num_ctas <= 0 && mma_kernel && seen <= kMaxMmaRunKeys) {
       const int64_t units = (int64_t)B * Hkv, even = units <= n ? n / units * units : 0;
       if (5 * even >= 4 * (int64_t)n) n = (int32_t)even;
