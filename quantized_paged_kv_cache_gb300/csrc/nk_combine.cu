@@ -160,6 +160,86 @@ __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const Deco
   merge_row<C>(c1 - c0 + 1, lse_of, row_of, p.out + (((int64_t)b * p.qT + t) * p.Hq + h * p.G + hg) * D + c_off);
 }
 
+// The same for windows whose units span few CTAs: a warp per row, a lane for
+// its channels (D / 32 of them), partial after partial. A block per row merges
+// with most of its threads idle then, and a batch's rows need several rounds of
+// blocks, each with the page prefix to form first; here eight rows share one.
+template <int D>
+__global__ void __launch_bounds__(kCombThreads) window_combine_kernel(const DecodeParams p) {
+  constexpr int V = D < 128 ? 2 : 4;  // channels of a load
+  constexpr int NL = D / (32 * V);    // loads of a lane and partial
+  constexpr int U = 4;                // partials in flight
+  __shared__ int pre[kMaxBatch + 1];
+  __shared__ int warp_tot[8];
+  const auto sh = p.shape_of<true>();
+  block_page_prefix<true>(sh, p.ctx, p.trim, pre, warp_tot);  // before the wait, as above
+  chain_wait();
+  chain_release();
+  const int64_t W = (int64_t)pre[p.B] * p.Hkv;
+  const int M = p.G * p.T, lane = threadIdx.x & 31;
+  const int64_t ur = (int64_t)blockIdx.x * (kCombThreads / 32) + (threadIdx.x >> 5);
+  if (ur >= (int64_t)p.B * p.Hkv * M || W == 0) return;
+  const int u = (int)quot(ur, M), r = (int)(ur - (int64_t)u * M);
+  const int b = u / p.Hkv, h = u % p.Hkv;
+  const int pages = pre[b + 1] - pre[b];
+  if (pages == 0) return;
+  const int64_t x0 = (int64_t)pre[b] * p.Hkv + (int64_t)h * pages;
+  const int n = p.n_ctas, c0 = cta_of_item(W, n, x0), c1 = cta_of_item(W, n, x0 + pages - 1);
+  if (c0 == c1) return;
+  const int S = c1 - c0 + 1;
+  float m = -INFINITY, l = 0.f, acc[NL][V];
+#pragma unroll
+  for (int k = 0; k < NL; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[k][j] = 0.f;
+  for (int s0 = 0; s0 < S; s0 += U) {
+    float ls[U], v[U][NL][V];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int s = s0 + i, c = c0 + s;
+      // a CTA can own no item only when there are fewer items than CTAs
+      const bool there = s < S && !(W < n && cta_begin(W, n, c) == cta_begin(W, n, c + 1));
+      const int64_t row = ((int64_t)c + u) * M + r;
+      ls[i] = there ? p.part_lse[row] : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < NL; ++k) {
+        const float* src = p.part_o + row * D + (k * 32 + lane) * V;
+        if constexpr (V == 4) {
+          const float4 x = there ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[i][k][0] = x.x, v[i][k][1] = x.y, v[i][k][2] = x.z, v[i][k][3] = x.w;
+        } else {
+          const float2 x = there ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
+          v[i][k][0] = x.x, v[i][k][1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (ls[i] == -INFINITY) continue;
+      const float mx = fmaxf(m, ls[i]), a = expf(m - mx), w = expf(ls[i] - mx);  // a: 0 while nothing was merged
+      m = mx;
+      l = fmaf(l, a, w);
+#pragma unroll
+      for (int k = 0; k < NL; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[k][j] = fmaf(w, v[i][k][j], acc[k][j] * a);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int t = r / p.G, hg = r % p.G;
+  uint16_t* out = p.out + (((int64_t)b * p.qT + t) * p.Hq + h * p.G + hg) * D;
+#pragma unroll
+  for (int k = 0; k < NL; ++k) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j)
+      w[j] = f32_to_bf16(acc[k][2 * j] * inv) | ((uint32_t)f32_to_bf16(acc[k][2 * j + 1] * inv) << 16);
+    uint16_t* dst = out + (k * 32 + lane) * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
+}
+
 // Standalone combine: part_o [S][R][D], part_lse [S][R] -> out [R][D]; block = row.
 template <int D>
 __global__ void __launch_bounds__(kCombThreads) attn_combine_kernel(const float* part_o, const float* part_lse, int S,
@@ -176,6 +256,11 @@ __global__ void __launch_bounds__(kCombThreads) attn_combine_kernel(const float*
 // Rows are split into 64-channel slices when there are fewer rows than
 // kSliceRows: more blocks in flight, fewer partials per thread.
 constexpr int kSliceRows = 256;
+// Windows: a warp per row where a unit spans about so many CTAs at most (64
+// sequences on 16-key pages, a span of 1: 40.6 -> 34.4 us; 8 with windows of
+// 1,024, a span of 5: 20.3 -> 14.6; T = 4 74.4 -> 68.4; 8 on 128-key pages, a
+// span of 10: 14.6 -> 14.0; one sequence, a span of 38: 12.1 -> 21.5).
+constexpr int kRowWarpSpan = 12;
 
 template <int D, bool WIN>
 static cudaError_t launch_combine_w(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
@@ -187,6 +272,11 @@ static cudaError_t launch_combine_w(const DecodeParams& p, int64_t rows, cudaStr
 
 template <int D>
 static cudaError_t launch_combine_d(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
+  if (p.window > 0 && p.n_ctas <= kRowWarpSpan * p.B * p.Hkv) {
+    const int64_t per = kCombThreads / 32;
+    return launch_chained(window_combine_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kCombThreads), 0,
+                          stream, p);
+  }
   return p.window > 0 ? launch_combine_w<D, true>(p, rows, stream) : launch_combine_w<D, false>(p, rows, stream);
 }
 
