@@ -428,8 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   // descriptor fetch can start before the wait for the previous kernel
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
   if constexpr (RK) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmapv)) : "memory");
-  if (!p.early) chain_wait();  // (early: waits below, before the first page load)
-  chain_release();
   constexpr int NTEAMS = kConsumerWarps / CS;
   constexpr int DW = D / CS;        // channels per warp
   constexpr int NCH = DW / 16;      // 16-channel chunks per warp
@@ -467,16 +465,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   const int per_stage = BPP * CS;  // consumer-warp arrivals per page
   const auto sh = p.shape_of<WIN>();
 
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
-      mbar_init(smem_u32(&empty_bar[s]), per_stage);
-      cnt[s] = 0;
-      icnt[s] = 0;
-    }
-    *abort_flag = 0;
+  if (tid < S) {
+    mbar_init(smem_u32(&full_bar[tid]), 1);
+    mbar_init(smem_u32(&empty_bar[tid]), per_stage);
+    cnt[tid] = 0;
+    icnt[tid] = 0;
+    if (tid == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // (only shared memory and launch parameters so far: beside the previous
+  // kernel, a thread per stage, 2 to 3 % of a short window's time)
+  if (!p.early) chain_wait();  // (early: waits below, before the first page load)
+  chain_release();
   flag_bad_ctx(p);
   block_page_prefix(sh, p.ctx, p.trim, pre, warp_tot, lens);  // ends with __syncthreads
 
