@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kCombThreads) window_combine_kernel(const Deco
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int warp_tot[8];
   const auto sh = p.shape_of<true>();
-  block_page_prefix<true>(sh, p.ctx, p.trim, pre, warp_tot);  // before the wait, as above
+  block_page_prefix_short<true>(sh, p.ctx, p.trim, pre, warp_tot);  // before the wait, as above
   chain_wait();
   chain_release();
   const int64_t W = (int64_t)pre[p.B] * p.Hkv;

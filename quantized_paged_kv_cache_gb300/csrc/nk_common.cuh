@@ -259,6 +259,46 @@ __device__ __forceinline__ void block_page_prefix(const Shape& s, const int32_t*
   __syncthreads();
 }
 
+// The same with a sequence per thread while the batch allows it, and by one
+// warp for up to 32: the prologue of a short window's kernel waits for it (64
+// sequences 21.9 -> 20.0 us, 8 with 3,000 keys on 128-key pages 13.5 -> 12.4,
+// one 11.7 -> 11.6; the combine alone 21.2 -> 20.1 of the first, where behind
+// the tcgen05 kernel it loses, 68.3 -> 69.7, T = 4; that kernel itself does not
+// gain and keeps the other).
+template <bool kL2Only = false, class Shape>
+__device__ __forceinline__ void block_page_prefix_short(const Shape& s, const int32_t* ctx_lens, int trim, int* pre,
+                                                        int* warp_tot, int* lens = nullptr) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (s.B > 256) {
+    block_page_prefix<kL2Only>(s, ctx_lens, trim, pre, warp_tot, lens);
+    return;
+  }
+  const bool one_warp = s.B <= 32;
+  if (!one_warp || wid == 0) {
+    int v = 0;
+    if (tid < s.B) {
+      const int L = (kL2Only ? __ldcg(ctx_lens + tid) : ctx_lens[tid]) - trim;
+      v = pages_of_len(s, L);
+      if (lens) lens[tid] = L;
+    }
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int base = 0;
+    if (!one_warp) {
+      if (lane == 31 && wid < 8) warp_tot[wid] = incl;
+      __syncthreads();
+      for (int w = 0; w < wid && w < 8; ++w) base += warp_tot[w];
+    }
+    if (tid < s.B) pre[tid] = base + incl - v;
+    if (tid == s.B - 1) pre[s.B] = base + incl;
+  }
+  __syncthreads();
+}
+
 // Segment of unit items handled by one CTA.
 struct Segment {
   int b, h, u;           // sequence, kv-head, unit index b*Hkv + h

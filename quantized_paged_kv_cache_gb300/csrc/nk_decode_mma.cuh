@@ -478,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   if (!p.early) chain_wait();  // (early: waits below, before the first page load)
   chain_release();
   flag_bad_ctx(p);
-  block_page_prefix(sh, p.ctx, p.trim, pre, warp_tot, lens);  // ends with __syncthreads
+  // (both end with __syncthreads)
+  if constexpr (WIN) block_page_prefix_short(sh, p.ctx, p.trim, pre, warp_tot, lens);
+  else block_page_prefix(sh, p.ctx, p.trim, pre, warp_tot, lens);
 
   const int64_t W = (int64_t)pre[p.B] * p.Hkv;
   if (W == 0) {
