@@ -52,7 +52,7 @@ def test_window_matches_reference(shape):
     assert int(status.item()) == 0
 
 
-@pytest.mark.parametrize("B,T", [(64, 1), (70, 2), (33, 1)])
+@pytest.mark.parametrize("B,T", [(64, 1), (70, 2), (33, 1), (32, 2), (300, 1)])
 def test_a_batch_of_windows_split_evenly_over_its_units(B, T):
     lens = [150 + 37 * b % 260 for b in range(B)]
     lens[1], lens[B // 2] = T, 60  # (most units have the window's pages, some fewer)
