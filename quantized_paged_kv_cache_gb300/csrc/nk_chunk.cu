@@ -558,9 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     }
   };
-  // The segments come from the producer warp, which leaves them all even after
-  // a wait has run out (its own waits then return at once): the softmax warps
-  // meet in barriers and have to agree on the blocks they go through.
+  // The segments come from the producer warp. The softmax warps meet in
+  // barriers, so all of them have to go through the same segments, also after a
+  // wait has run out: the producer then leaves one more, marked as the CTA's
+  // last, and stops. While nothing has run out the ring of raw blocks keeps it
+  // 8 blocks, so 9 segments, ahead at most; with that one they are 10 of the 16
+  // slots, and no slot is written that a softmax warp may still have to read.
   auto wait_seg = [&](int sg) {
     const unsigned long long t0 = clock64();
     while (!mbar_try_wait(smem_u32(&segfull[sg % kSegs]), (sg / kSegs) & 1))
@@ -1053,6 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const TileSpan span = w.s;
         const bool split = wave >= waves;
         Walk ahead = w;
+        const bool ends = __any_sync(0xffffffffu, *abort_flag != 0);  // a wait has run out: this segment is the last
         if (++wave < waves) {
           tile_at(p, tab, cta + wave * nctas, ahead);
         } else if (!split) {
@@ -1064,6 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           more = ahead.x < ahead.end;
           if (more) next_tile(p, tab, ahead);
         }
+        if (ends) more = false;
         if (lane == 0) {
           Seg& s = segs[sg % kSegs];
           const int r0 = w.tile * kRows;
@@ -1104,11 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const unsigned okb = __ballot_sync(0xffffffffu, ok && arr == 0), badb = __ballot_sync(0xffffffffu, copier && arr == 0 && pg == -1);
           const int st = q % kStages;
           wait_bar(&rfree[st], ((q / kStages) & 1) ^ 1u);
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) {  // no more copies; the segments still go out
-            page = turn ? next_page : page;
-            slot = turn ? next_slot : slot;
-            continue;
-          }
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // no more copies
           const uint32_t bar = smem_u32(&rfull[st]);
           if (lane == 0) {
             const int left = L - block_at(span, v0 + i) * kKeys;
