@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int* start = misc + 4;                                // [4] b, h, tile, v of the CTA's first block
   int* exps = misc + 32;                                // [4][K | V][4]: e of 16 keys of a block
   int* e_pub = misc + 72;                               // [2][4] what the softmax hands on beside pair_x
-  volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | bad 16-key groups << 16
+  volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | 16-key groups that were not copied << 16
   int* last_raw = misc + 100;                           // raw blocks issued
   int* longest = misc + 101;                            // blocks of the longest tile
   int* sched = misc + 104;                              // [kMaxSched + 1] where the CTAs' shares of the last tiles begin
@@ -1019,17 +1019,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int64_t src_off = arr == 0 ? 0 : (arr == 1 ? p.lay.ks : (arr == 2 ? p.lay.vc : p.lay.vs));
       const uint32_t dst0 = smem_u32(smem + SM::off_ring) + (arr == 0 ? 0 : (arr == 1 ? kKeys * D : (arr == 2 ? kKeys * (D + G64 * 4) : kKeys * (2 * D + G64 * 4)))) +
                             kg * per * width;
-      // page (-1: outside the pool, -2: no such keys) and slot of the lane's keys in the batch of w's tile from block v on
+      // Page and slot of the lane's keys in the batch of w's tile from block v on. Page -1: outside the pool; -2: no such
+      // keys; -3: before the window of the tile's first token and behind the sinks, so nobody sees them and their page
+      // may have been given back: neither the entry nor the page is read (in a whole-block page some key is seen).
       auto look = [&](const Walk& w, int v, int n, int& page, int& slot) {
         const int i = whole ? lane : lane >> 2;
         const int pos = block_at(w.s, v + i) * kKeys + (whole ? 0 : (lane & 3) * 16);
         page = -2;
         slot = 0;
         if (i < n && pos < w.L) {
-          const int pi = pos / p.P;
-          slot = pos - pi * p.P;
-          page = __ldg(p.bt + (int64_t)w.b * p.max_pages + pi);
-          if (page < 0 || page >= p.num_pages) page = -1;
+          if (!whole && p.window > 0 && pos + 15 <= w.s.p0 - p.window && pos >= p.sinks) {
+            page = -3;
+          } else {
+            const int pi = pos / p.P;
+            slot = pos - pi * p.P;
+            page = __ldg(p.bt + (int64_t)w.b * p.max_pages + pi);
+            if (page < 0 || page >= p.num_pages) page = -1;
+          }
         }
       };
       // the tiles of the rounds, then the CTA's blocks of the split tiles
@@ -1106,16 +1112,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const int from = whole ? at : at * 4 + (kg & 3);
           const int pg = __shfl_sync(0xffffffffu, page, from), sl = __shfl_sync(0xffffffffu, slot, from);
           const bool ok = copier && pg >= 0;
-          const unsigned okb = __ballot_sync(0xffffffffu, ok && arr == 0), badb = __ballot_sync(0xffffffffu, copier && arr == 0 && pg == -1);
+          const unsigned okb = __ballot_sync(0xffffffffu, ok && arr == 0);
+          const unsigned outb = __ballot_sync(0xffffffffu, copier && arr == 0 && (pg == -1 || pg == -3));  // not copied: zeros
+          const bool bad = __any_sync(0xffffffffu, copier && arr == 0 && pg == -1);
           const int st = q % kStages;
           wait_bar(&rfree[st], ((q / kStages) & 1) ^ 1u);
           if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // no more copies
           const uint32_t bar = smem_u32(&rfull[st]);
           if (lane == 0) {
             const int left = L - block_at(span, v0 + i) * kKeys;
-            // bits 0, 4, 8, 12 of badb are the 16-key groups, bit 0 alone a whole block
-            const unsigned bad = whole ? (badb ? 15u : 0u) : ((badb & 1u) | ((badb >> 3) & 2u) | ((badb >> 6) & 4u) | ((badb >> 9) & 8u));
-            info[st] = (left < kKeys ? left : kKeys) | (i == 0 ? 256 : 0) | (bad << 16);
+            // bits 0, 4, 8, 12 of outb are the 16-key groups, bit 0 alone a whole block
+            const unsigned out = whole ? (outb ? 15u : 0u) : ((outb & 1u) | ((outb >> 3) & 2u) | ((outb >> 6) & 4u) | ((outb >> 9) & 8u));
+            info[st] = (left < kKeys ? left : kKeys) | (i == 0 ? 256 : 0) | (out << 16);
             if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
             mbar_arrive_expect_tx(bar, __popc(okb) * per * kKeyBytes);
             *last_raw = q + 1;
