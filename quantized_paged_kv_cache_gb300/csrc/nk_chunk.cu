@@ -17,7 +17,8 @@
 // 2^-11 relative each where the output's bf16 rounding is 2^-8 (a row whose
 // scale is below 2^-8 of its block's largest keeps fewer bits, never fewer
 // than 2^-25 of that largest). The exponent e keeps the products inside the
-// fp16 range for any pool. It is one of 16 keys, undone on the scores for K and
+// fp16 range for any pool. It is one of 16 keys
+// (of their largest scale, groups of zeros left out), undone on the scores for K and
 // put into the weights for V (P carries 2^(e - e_ref) beside exp2(S - m)).
 //
 // 20 warps in five warpgroups, one CTA per SM:
@@ -859,17 +860,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       wait_bar(&rfull[odd], ph);
       const int inf = info[odd];
       const int there = ((inf >> (16 + cw)) & 1) ? 0 : (inf & 0xff) - cw * 16;  // keys of this warp's 16 that exist
+      // ---- scales of K and V, and the exponents, which have to be there with the scores
+      int es[2];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {  // K, V
-        uint4 w[NI];
-        float s[NS], mx = 0.f;
+      for (int v = 0; v < 2; ++v) {
+        float s[NS];
 #pragma unroll
         for (int i = 0; i < NS; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[i]) : "r"(scales0 + v * kRawV + i * 128));
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                       : "r"(codes0 + v * kRawV + i * (KPI * D)));
+        float mx = 0.f, mn = INFINITY;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
@@ -878,11 +876,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             bad_scale = true;
           }
           mx = fmaxf(mx, s[i]);
+          if (s[i] > 0.f) mn = fminf(mn, s[i]);
+        }
+        float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+        const float lo = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(mn)));
+        // The scale of a group whose codes are all zero says nothing of a size (the append writes 1): it must not set the
+        // exponent of the 16 keys. Looked for where the largest scale could be such a one: at exactly 1, or far above the
+        // smallest; elsewhere it costs no bits.
+        if (m == 1.f || m > 256.f * lo) {
+          mx = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            if (s[i] > 0.f) {
+              uint32_t any = 0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint4 x;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                             : "r"(raw0 + v * kRawV + cw * 16 * D + (lane + 32 * i) * 64 + c * 16));
+                any |= x.x | x.y | x.z | x.w;
+              }
+              if (any == 0) s[i] = 0.f;
+            }
+            mx = fmaxf(mx, s[i]);
+          }
+          m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
         }
         // the 16 keys take the exponent of their own largest scale: S = s 2^(9 - e) lies below 2^12
-        const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-        const int e = m > 0.f ? max(exp_of(m) - 2, -110) : kNoExp;
-        const float down = m > 0.f ? pow2i(9 - e) : 0.f;
+        es[v] = m > 0.f ? max(exp_of(m) - 2, -110) : kNoExp;
+        const float down = m > 0.f ? pow2i(9 - es[v]) : 0.f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const __half2 sc = __float2half2_rn(s[i] * down);
@@ -892,23 +915,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                          "r"(*reinterpret_cast<const uint32_t*>(&sc)), "r"(*reinterpret_cast<const uint32_t*>(&bias))
                          : "memory");
         }
-        // Both exponents have to be there with the scores, so V's is told before
-        // K is handed over: K's pass looks at V's scales, too.
-        if (v == 0) {
-          float vm = 0.f;
+      }
+      // (the slot's last reader, the softmax of block j - 4, is done: its PV was waited for at block j - 2)
+      if (lane == 0) {
+        exps[(j & 3) * 8 + cw] = es[0];
+        exps[(j & 3) * 8 + 4 + cw] = es[1];
+      }
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            float x;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(scales0 + kRawV + i * 128));
-            if (has_scale && (lane + 32 * i) / G64 < there && x <= 3.0e38f) vm = fmaxf(vm, x);
-          }
-          vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
-          // (the slot's last reader, the softmax of block j - 4, is done: its PV was waited for at block j - 2)
-          if (lane == 0) {
-            exps[(j & 3) * 8 + cw] = e;
-            exps[(j & 3) * 8 + 4 + cw] = vm > 0.f ? max(exp_of(vm) - 2, -110) : kNoExp;
-          }
-        }
+      for (int v = 0; v < 2; ++v) {  // K, V
+        uint4 w[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(codes0 + v * kRawV + i * (KPI * D)));
         __syncwarp();
         if (v == 1 && lane == 0) mbar_arrive(smem_u32(&rfree[odd]));  // every lane holds its part of the raw block
         // ---- the buffer's previous block has been multiplied

@@ -1,0 +1,80 @@
+"""nk_paged_chunk_attn on caches whose keys and channel groups differ widely in size, and with all-zero ones among them:
+against the plain 64-bit form over the pool's own bytes.
+
+The roundings (half a step each): the output to bf16, 2^-8 of the value; code * fp16(scale) in fp16, 2^-11 each of the value,
+or, for values far below the largest of the 16 keys they share an exponent with, 2^-20 of that largest; a weight in fp16,
+2^-11 of it, or 2^-33 of the reference weight (that of a key at most 2^4 below the row's largest), as far as the values of
+the visible keys reach. Scores enter as in test_gpu_chunk.py; where only values are looked at, q is zero and the scores are
+exact."""
+import math
+
+import pytest
+import torch
+
+import quantized_paged_kv_cache_gb300 as nk
+
+import _ref
+from test_gpu_chunk import check
+
+pytestmark = pytest.mark.gpu
+
+
+class Cache:
+    """One sequence whose rows [L][Hkv][D] went through the append; the last T tokens are the chunk."""
+
+    def __init__(self, k, v, q, P=64, window=0, sinks=0):
+        L, self.Hkv, self.D = k.shape
+        self.P, self.L, self.T, self.q, self.window, self.sinks = P, L, q.shape[0], q.bfloat16(), window, sinks
+        self.pages = -(-L // P) + 1
+        self.pool = nk.KVPool.empty(self.pages, P, self.Hkv, self.D)
+        self.pool.storage.fill_(0xFF)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.bt = torch.arange(self.pages - 1, -1, -1, dtype=torch.int32, device="cuda")[:-1].view(1, -1).contiguous()
+        self.ctx, self.cu = i32([L]), i32([0, self.T])
+        nk.kv_append(self.pool, self.bt, i32([0]), i32([0, L]), k.bfloat16(), v.bfloat16())
+        self.scale = 1 / math.sqrt(self.D)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def parts(self):
+        """The pool's scales of K and V, [pages][Hkv][P][D/64], writable."""
+        raw = self.pool.storage.view(self.pages, self.Hkv, -1)
+        n, sc = self.P * self.D, self.P * (self.D // 64) * 4
+        return [raw[..., a:a + sc].view(torch.float32).unflatten(-1, (self.P, self.D // 64)) for a in (n, 2 * n + sc)]
+
+    def run(self, **kw):
+        return nk.paged_chunk_attn(self.pool, self.q, self.cu, kw.pop("bt", self.bt), self.ctx, self.scale, self.L,
+                                   window=self.window, sinks=self.sinks, status=self.status, **kw)
+
+    def ref(self):
+        return _ref.attention(self.pool.storage, self.pages, self.Hkv, self.P, self.D, self.bt, [self.L], [self.T], self.q,
+                              self.scale, self.window, self.sinks)
+
+
+def rows(seed, L, T, Hq, Hkv, D):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    return r(L, Hkv, D), r(L, Hkv, D), r(T, Hq, D)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("s", [-3, -6, -12, -30])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64), (256, 48), (256, 64)])
+def test_zero_tokens_and_zero_channel_groups(which, s, D, P):
+    """The append gives an all-zero group the scale 1: it must not set the exponent of the small rows beside it, whether the
+    zero row is visible or still to come."""
+    k, v, q = rows(5, 300, 40, 8, 2, D)
+    unit = 1.0
+    if which == "k":
+        k, q = k * 2.0 ** s, q * 2.0 ** -s
+    else:
+        v, unit = v * 2.0 ** s, 2.0 ** s
+    x = k if which == "k" else v
+    x[7::16] = 0       # a token of every 16
+    x[290:293] = 0     # hidden from most of the chunk's rows
+    x[100:140, 1] = 0  # two whole groups of 16 keys of one kv-head
+    if D > 64:
+        x[3::5, :, 64:128] = 0  # a channel group of a fifth of the tokens
+        x[:, 0, :64] = 0        # a channel group that is dead throughout
+    c = Cache(k, v, q, P)
+    check(c.run(), c.ref(), f"{which} 2^{s}", unit=unit)
+    assert int(c.status.item()) == 0
