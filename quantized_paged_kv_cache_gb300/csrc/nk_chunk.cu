@@ -871,12 +871,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
-          if (!(s[i] <= 3.0e38f)) {  // the append of a non-finite row: zeros too, flagged
-            s[i] = 0.f;
+          float a = fabsf(s[i]);
+          if (!(a <= 3.4028234e38f)) {  // infinite of either sign or NaN, the append of a non-finite row: zeros too, flagged
+            s[i] = a = 0.f;
             bad_scale = true;
           }
-          mx = fmaxf(mx, s[i]);
-          if (s[i] > 0.f) mn = fminf(mn, s[i]);
+          mx = fmaxf(mx, a);
+          if (a > 0.f) mn = fminf(mn, a);
         }
         float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
         const float lo = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(mn)));
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           mx = 0.f;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            if (s[i] > 0.f) {
+            if (s[i] != 0.f) {
               uint32_t any = 0;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               }
               if (any == 0) s[i] = 0.f;
             }
-            mx = fmaxf(mx, s[i]);
+            mx = fmaxf(mx, fabsf(s[i]));
           }
           m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
         }

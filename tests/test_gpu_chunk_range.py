@@ -78,3 +78,31 @@ def test_zero_tokens_and_zero_channel_groups(which, s, D, P):
     c = Cache(k, v, q, P)
     check(c.run(), c.ref(), f"{which} 2^{s}", unit=unit)
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("which", [0, 1])
+def test_groups_whose_scale_is_not_finite_count_as_zeros(which, value):
+    k, v, q = rows(6, 200, 100, 8, 2, 128)
+    c = Cache(k, v, q, 16)
+    pos = 150
+    x = c.parts()[which][int(c.bt[0, pos // 16]), :, pos % 16]
+    x[:, 1] = 0.0
+    want = c.ref()
+    x[:, 1] = value
+    out = c.run()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == nk.NK_DEVFLAG_RANGE
+    check(out, want, f"{value}")
+
+
+def test_groups_with_a_negative_scale():
+    k, v, q = rows(7, 200, 50, 8, 2, 128)
+    c = Cache(k, v, q, 16)
+    for x in c.parts():
+        x[:, :, 3:9] *= -1.0
+        x[:, :, 12] *= -4.0
+    # One key in 16 has K and V rows of four times N(0, 1): its score is off by four times the 5e-4 that the 4e-3 of `check`
+    # stand on, and moves O by that times a |v - O| four times as large, so the bound is 4 * 4 times the one for unit rows.
+    check(c.run(), c.ref(), "negative scales", unit=16.0)
+    assert int(c.status.item()) == 0
