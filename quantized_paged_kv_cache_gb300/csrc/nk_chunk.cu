@@ -127,8 +127,8 @@ struct Smem {
   static constexpr int off_pre = off_tab + 16 * 16 * (D / 64) * 8;   // int64 [kMaxBatch + 1]: blocks before sequence b
   static constexpr int off_tiles = off_pre + (kMaxBatch + 2) * 8;  // int [kMaxBatch + 1]: tiles before sequence b
   static constexpr int off_cu = off_tiles + (kMaxBatch + 4) * 4;  // int [kMaxBatch + 1]
-  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128]: what the two softmax threads of a row hand each other
-  static constexpr int off_segs = off_pair + 6 * kRows * 4;       // [kSegs] segments
+  static constexpr int off_pair = off_cu + (kMaxBatch + 4) * 4;   // float [6][128], int16 [2][128]: what the two softmax threads of a row hand each other
+  static constexpr int off_segs = off_pair + 6 * kRows * 4 + 2 * kRows * 2;       // [kSegs] segments
   static constexpr int off_misc = off_segs + kSegs * 64;
   static constexpr int total = off_misc + 1408 + 1024;  // slack to align the base
 };
@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int* tiles = reinterpret_cast<int*>(smem + SM::off_tiles);
   int* cus = reinterpret_cast<int*>(smem + SM::off_cu);
   float* pair_x = reinterpret_cast<float*>(smem + SM::off_pair);
+  int16_t* pair_e = reinterpret_cast<int16_t*>(pair_x + 6 * kRows);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::off_misc);
   uint64_t* kfull = bars;        // [2] K block in shared memory (4 warps)
   uint64_t* vfull = bars + 2;    // [2] V block (4 warps)
@@ -339,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int* last_mma = misc + 2;                             // block number of the last MMAs committed to pvdone / qkdone
   int* start = misc + 4;                                // [4] b, h, tile, v of the CTA's first block
   int* exps = misc + 32;                                // [4][K | V][4]: e of 16 keys of a block
-  int* e_pub = misc + 72;                               // [2][4] what the softmax hands on beside pair_x
   volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | 16-key groups that were not copied << 16
   int* last_raw = misc + 100;                           // raw blocks issued
   int* longest = misc + 101;                            // blocks of the longest tile
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int causal = sd.p0 - (kKeys - 1);                               // blocks past it hold hidden keys
       const int behind = p.window > 0 ? sd.p1 - p.window : -0x7fffffff - 1;  // blocks up to it may
       // The two warpgroups take the blocks in turn, so that two are under way.
-      // The reference of a row's weights (and of the values' exponents) goes
+      // The references of a row's weights and of its values' exponents go
       // from block to block through shared memory; a thread's row sum follows
       // its own copy of the reference.
       float m_ref = -INFINITY, l = 0.f;
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int4 ke = *reinterpret_cast<const int4*>(exps + (j & 3) * 8), ve = *reinterpret_cast<const int4*>(exps + (j & 3) * 8 + 4);
         auto factor = [&](int e) { return fminf(fmaxf(kq * pow2_any(e + kOperand), 1.2e-38f), 3.4e38f); };
         const float f[4] = {factor(ke.x), factor(ke.y), factor(ke.z), factor(ke.w)};
-        const int vmax = max(max(ve.x, ve.y), max(ve.z, ve.w));
+        const int vd[4] = {ve.x, ve.y, ve.z, ve.w};
         wait_ld();
         float s[64];
 #pragma unroll
@@ -668,13 +668,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s[c] = __uint_as_float(lo[c]);
           s[32 + c] = __uint_as_float(hi[c]);
         }
-        if (key0 > causal) {
+        int vmax = max(max(ve.x, ve.y), max(ve.z, ve.w));  // of the keys that the row sees
+        const bool late = key0 > causal, early = key0 <= behind && key0 + kKeys - 1 >= p.sinks;
+        if (late || early) {
+          vmax = kNoExp;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int k0 = key0 + 16 * g;
+            if (k0 <= pos && (!early || k0 + 15 > pos - p.window || k0 < p.sinks)) vmax = max(vmax, vd[g]);
+          }
+        }
+        if (late) {
           const int lim = pos - key0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c > lim) s[c] = -INFINITY;
         }
-        if (key0 <= behind && key0 + kKeys - 1 >= p.sinks) {
+        if (early) {
           const int lim = pos - p.window - key0, sk = p.sinks - key0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -697,13 +707,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (j > 0) wait_bar(&handed[(1 - half) * 4 + quad], ((j - 1) >> 1) & 1);
         if (i > 0) {
           m_ref = pair_x[(1 - half) * kRows + row];
-          e_ref = e_pub[(1 - half) * 4 + quad];
+          e_ref = pair_e[(1 - half) * kRows + row];
         }
         // The reference moves at a row's first key and when a score passes it
         // by more than 8. The weights of 16 keys carry their values' exponent,
-        // p 2^(ve - e_ref): e_ref follows the blocks' largest ve, moved when a
-        // weight could pass 2^14 or the block's largest value drops 2^4 below.
-        const bool moved = vmax > e_ref + 6 || (vmax < e_ref - 4 && vmax != kNoExp);
+        // p 2^(ve - e_ref). e_ref follows the largest ve that the row has seen
+        // (hidden keys must not cost it bits) and never falls, so that what is
+        // in the accumulator only ever shrinks; it moves when a weight could
+        // pass 2^14.
+        const bool moved = vmax > e_ref + 6;
         const bool change = __any_sync(0xffffffffu, moved || mx > m_ref + 8.f);  // rare
         float a = 1.f;
         if (change) {
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
         }
         pair_x[half * kRows + row] = m_ref;
-        if (lane == 0) e_pub[half * 4 + quad] = e_ref;
+        pair_e[half * kRows + row] = (int16_t)e_ref;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&handed[half * 4 + quad]));
         if (__any_sync(0xffffffffu, m_ref != m_own)) l *= m_own == -INFINITY ? 0.f : ex2(m_own - m_ref);
@@ -737,11 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         // ---- p 2^d = 2^(score f - m + d), two at a time, d of 16 keys each; the row sum is of p
-        const int vd[4] = {ve.x, ve.y, ve.z, ve.w};
         uint32_t pk[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int d = max(vd[g] - e_ref, -60);  // 2^-60 of the weights is nothing in fp16
+          const int d = min(max(vd[g] - e_ref, -60), 6);  // 2^-60 of the weights is nothing in fp16; above 6: hidden keys, p 0
           const float2 mu2 = make_float2((float)d - mu, (float)d - mu), f2 = make_float2(f[g], f[g]);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -768,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // ---- both threads of a row: the last block's references, the whole row sum
       wait_bar(&handed[((j0 - 1) & 1) * 4 + quad], ((j0 - 1) >> 1) & 1);
       const float m_end = pair_x[((j0 - 1) & 1) * kRows + row];
-      e_ref = e_pub[((j0 - 1) & 1) * 4 + quad];
+      e_ref = pair_e[((j0 - 1) & 1) * kRows + row];
       if (l > 0.f) l *= ex2(m_ref - m_end);
       m_ref = m_end;
       pair_x[(2 + half) * kRows + row] = l;

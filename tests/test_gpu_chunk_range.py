@@ -106,3 +106,32 @@ def test_groups_with_a_negative_scale():
     # stand on, and moves O by that times a |v - O| four times as large, so the bound is 4 * 4 times the one for unit rows.
     check(c.run(), c.ref(), "negative scales", unit=16.0)
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("r", [8, 12, 16, 20, 24, 40])
+@pytest.mark.parametrize("G", [1, 6])
+def test_a_row_does_not_see_the_size_of_hidden_keys(r, G):
+    """Later tokens, and tokens before the window, whose values are 2^r times as large (in 16 keys of their own)."""
+    k, v, q = rows(8, 128, 64, 4 * G, 4, 256)
+    v[112:] *= 2.0 ** r
+    c = Cache(k, v, q)
+    ref = c.ref()
+    check(c.run()[:48], ref[:48], "later tokens")
+    check(c.run()[48:], ref[48:], "the tokens themselves", unit=2.0 ** r)
+    v[112:] *= 2.0 ** -r
+    v[:80] *= 2.0 ** r
+    c = Cache(k, v, q, window=20)  # rows from position 99 on see none of the first 80 tokens
+    check(c.run()[36:], c.ref()[36:], "tokens before the window")
+    c = Cache(k, v, q, window=20, sinks=3)  # sinks among the loud ones: what the row sees is loud
+    check(c.run(), c.ref(), "loud sinks", unit=2.0 ** r)
+    assert int(c.status.item()) == 0
+
+
+def test_values_that_fall_by_more_than_the_fp32_range():
+    """V from 2^100 down to 2^-100: what the early blocks left must not overflow while the later ones are added."""
+    k, v, q = rows(9, 64 * 5, 8, 8, 2, 128)
+    for i, e in enumerate((100, -100, 0, -100, -20)):
+        v[64 * i:64 * i + 64] *= 2.0 ** e
+    c = Cache(k, v, q)
+    check(c.run(num_ctas=1), c.ref(), "falling values", unit=2.0 ** 100)
+    assert int(c.status.item()) == 0
