@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int4 ke = *reinterpret_cast<const int4*>(exps + (j & 3) * 8), ve = *reinterpret_cast<const int4*>(exps + (j & 3) * 8 + 4);
         auto factor = [&](int e) { return fminf(fmaxf(kq * pow2_any(e + kOperand), 1.2e-38f), 3.4e38f); };
         const float f[4] = {factor(ke.x), factor(ke.y), factor(ke.z), factor(ke.w)};
-        const int vd[4] = {ve.x, ve.y, ve.z, ve.w};
+        int vd[4] = {ve.x, ve.y, ve.z, ve.w};
         wait_ld();
         float s[64];
 #pragma unroll
@@ -668,24 +668,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           s[c] = __uint_as_float(lo[c]);
           s[32 + c] = __uint_as_float(hi[c]);
         }
-        int vmax = max(max(ve.x, ve.y), max(ve.z, ve.w));  // of the keys that the row sees
-        const bool late = key0 > causal, early = key0 <= behind && key0 + kKeys - 1 >= p.sinks;
-        if (late || early) {
-          vmax = kNoExp;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int k0 = key0 + 16 * g;
-            if (k0 <= pos && (!early || k0 + 15 > pos - p.window || k0 < p.sinks)) vmax = max(vmax, vd[g]);
-          }
-        }
-        if (late) {
+        // hidden scores; 16 keys that are all hidden from the row must not set its exponents either
+        if (key0 > causal) {
           const int lim = pos - key0;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (16 * g > lim) vd[g] = kNoExp;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c > lim) s[c] = -INFINITY;
         }
-        if (early) {
+        if (key0 <= behind && key0 + kKeys - 1 >= p.sinks) {
           const int lim = pos - p.window - key0, sk = p.sinks - key0;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (16 * g + 15 <= lim && 16 * g >= sk) vd[g] = kNoExp;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c <= lim && c >= sk) s[c] = -INFINITY;
@@ -702,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           m4[g] = fmaxf(a, b) * f[g];
         }
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const int vmax = max(max(vd[0], vd[1]), max(vd[2], vd[3]));
         // ---- the references after the block before
         const float m_own = m_ref;
         if (j > 0) wait_bar(&handed[(1 - half) * 4 + quad], ((j - 1) >> 1) & 1);
@@ -752,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         uint32_t pk[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int d = min(max(vd[g] - e_ref, -60), 6);  // 2^-60 of the weights is nothing in fp16; above 6: hidden keys, p 0
+          const int d = max(vd[g] - e_ref, -60);  // 2^-60 of the weights is nothing in fp16
           const float2 mu2 = make_float2((float)d - mu, (float)d - mu), f2 = make_float2(f[g], f[g]);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
