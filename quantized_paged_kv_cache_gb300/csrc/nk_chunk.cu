@@ -288,6 +288,14 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t u2, __half2 s, __half2 
 }
 constexpr int kNoExp = -1000;  // 16 keys that are all zero, or not there
 constexpr int kOperand = 15;  // an operand holds its value times 2^-(e + 15)
+// Weights are held 2^kUp up. A score may pass its reference by kScoreSlack
+// before that moves (by 4 only, and the accumulator is rescaled so often that
+// four chunks in a window take 556 us instead of about 480), so the largest fp16 weight is
+// 2^15, and one of 2^-32 of the reference weight still counts: without the 2^7,
+// 131,072 keys 2^-25.5 below a dominant one were lost from the product, but not
+// from the row sum (0.3 % of the result).
+constexpr int kUp = 7, kScoreSlack = 8;
+static_assert(kUp + kScoreSlack <= 15, "fp16 weights");
 
 // 2^x for any whole x (0 or infinity past the range).
 __device__ __forceinline__ float pow2_any(int x) { return x < -126 ? 0.f : (x > 127 ? INFINITY : pow2i(x)); }
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       // from block to block through shared memory; a thread's row sum follows
       // its own copy of the reference.
       float m_ref = -INFINITY, l = 0.f;
-      int e_ref = kNoExp;  // the accumulator holds O 2^-(e_ref + 15)
+      int e_ref = kNoExp;  // the accumulator holds l O 2^(kUp - e_ref - kOperand)
       for (int i = (half ^ j0) & 1; i < nblk; i += 2) {
         const int j = j0 + i;
         const int key0 = (v0 + i < lead ? v0 + i : v0 + i + shift) * kKeys;
@@ -708,16 +716,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           e_ref = pair_e[(1 - half) * kRows + row];
         }
         // The reference moves at a row's first key and when a score passes it
-        // by more than 8. The weights of 16 keys carry their values' exponent,
+        // by more than kScoreSlack. The weights of 16 keys carry their values' exponent,
         // p 2^(ve - e_ref). e_ref follows the largest ve that the row has seen
         // (hidden keys must not cost it bits) and never falls, so that what is
-        // in the accumulator only ever shrinks; it moves when a weight could
-        // pass 2^14.
-        const bool moved = vmax > e_ref + 6;
-        const bool change = __any_sync(0xffffffffu, moved || mx > m_ref + 8.f);  // rare
+        // in the accumulator only ever shrinks.
+        const bool moved = vmax > e_ref;
+        const bool change = __any_sync(0xffffffffu, moved || mx > m_ref + (float)kScoreSlack);  // rare
         float a = 1.f;
         if (change) {
-          if (mx > m_ref + 8.f) {
+          if (mx > m_ref + (float)kScoreSlack) {
             a = ex2(m_ref - mx);  // 0 while the row was empty
             m_ref = mx;
           }
@@ -746,11 +753,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           wait_st();
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        // ---- p 2^d = 2^(score f - m + d), two at a time, d of 16 keys each; the row sum is of p
+        // ---- p 2^d = 2^(score f - m + d), two at a time, d = kUp + ve - e_ref of 16 keys each; the row sum is of p
         uint32_t pk[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int d = max(vd[g] - e_ref, -60);  // 2^-60 of the weights is nothing in fp16
+          const int d = max(vd[g] - e_ref, -60) + kUp;  // 2^-60 of the weights is nothing in fp16
           const float2 mu2 = make_float2((float)d - mu, (float)d - mu), f2 = make_float2(f[g], f[g]);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -785,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       l += pair_x[(3 - half) * kRows + row];
       wait_bar(&pvdone[(j0 - 1) & 1], ((j0 - 1) >> 1) & 1);
       fence_after();
-      // back to O: 2^(e_ref + 15) / l (the power in two steps, each a normal number)
-      const float up = e_ref == kNoExp ? 1.f : pow2i(e_ref), inv = l > 0.f ? 32768.f / l : 0.f;
+      // back to O: 2^(e_ref + 15 - kUp) / l (the power in two steps, each a normal number)
+      const float up = e_ref == kNoExp ? 1.f : pow2i(e_ref), inv = l > 0.f ? pow2i(kOperand - kUp) / l : 0.f;
       bool finite = true;
       const bool head = sd.flags & 1, whole = sd.flags & 2, live = row < sd.rows;
       const int64_t slot = 2 * (int64_t)cta + (head ? 1 : 0);

@@ -3,8 +3,8 @@ against the plain 64-bit form over the pool's own bytes.
 
 The roundings (half a step each): the output to bf16, 2^-8 of the value; code * fp16(scale) in fp16, 2^-11 each of the value,
 or, for values far below the largest of the 16 keys they share an exponent with, 2^-20 of that largest; a weight in fp16,
-2^-11 of it, or 2^-33 of the reference weight (that of a key at most 2^4 below the row's largest), as far as the values of
-the visible keys reach. Scores enter as in test_gpu_chunk.py; where only values are looked at, q is zero and the scores are
+2^-11 of it, or 2^-32 of the reference weight (that of a key at most 2^8 below the row's largest; fp16's half step of 2^-25
+is 2^-32 of it, because it is held as 2^7). Scores enter as in test_gpu_chunk.py; where only values are looked at, q is zero and the scores are
 exact."""
 import math
 
@@ -135,3 +135,25 @@ def test_values_that_fall_by_more_than_the_fp32_range():
     c = Cache(k, v, q)
     check(c.run(num_ctas=1), c.ref(), "falling values", unit=2.0 ** 100)
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("octaves", [20, 25, 26, 28])
+@pytest.mark.parametrize("where", [0, 40000])
+def test_many_keys_far_below_one_dominant_key(octaves, where):
+    """131,072 keys whose weights lie 2^-octaves below one key's, which has no value: their sum is the result. The head's
+    row 127 * 2^-k and the zero rows are exact in the cache, so the scores are, too: sm_scale * 256 * 127 * 2^-k * q."""
+    L, D = 131072, 256
+    k = torch.zeros(L, 1, D, device="cuda")
+    k[where] = 127 * 2.0 ** -10
+    v = torch.rand(L, 1, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)) * 0.25 + 0.75
+    v[where] = 0
+    qv = octaves * math.log(2) / (256 * 127 * 2.0 ** -10 / 16)
+    q = torch.full((1, 2, D), qv, device="cuda")
+    c = Cache(k, v, q)
+    ref, out = c.ref(), c.run(num_ctas=1).double()  # (one CTA: its own sums meet the dominant key)
+    # each weight is off by at most 2^-32 of the dominant one (half a step of fp16, which holds that one as 2^7), all of them
+    # the same way here. The rest: bf16, V's and the scale's fp16 roundings.
+    p = 2.0 ** -(octaves * float(q.bfloat16()[0, 0, 0]) / qv)
+    tol = 2.0 ** -8 + 2.0 ** -32 / p + 3 * 2.0 ** -11 + 1e-3
+    rel = float(((out - ref).abs() / ref).max())
+    assert rel <= tol, f"relative error {rel:.3e}, bound {tol:.3e}"
