@@ -14,12 +14,15 @@
 // Operands: Q (bf16, scaled per row by a power of two into the fp16 range) and
 // P are A operands in tensor memory; K and V are B operands in shared memory,
 // dequantized to fp16: code * fp16(scale * 2^-e), two roundings of at most
-// 2^-11 relative each where the output's bf16 rounding is 2^-8 (a row whose
-// scale is below 2^-8 of its block's largest keeps fewer bits, never fewer
-// than 2^-25 of that largest). The exponent e keeps the products inside the
-// fp16 range for any pool. It is one of 16 keys
-// (of their largest scale, groups of zeros left out), undone on the scores for K and
-// put into the weights for V (P carries 2^(e - e_ref) beside exp2(S - m)).
+// 2^-11 relative each where the output's bf16 rounding is 2^-8. The exponent e
+// keeps the products inside the fp16 range for any pool. It is one of 16 keys
+// and all their channels (of their largest scale, groups of zeros left out),
+// undone on the scores for K and put into the weights for V (P carries
+// 2^(e - e_ref) beside exp2(S - m)). A value far below the largest of those 16
+// keys is off by the fp16 steps at the bottom of the range instead, at most
+// 2^-20 of that largest: scales are brought up to 2^15, where the operand's
+// largest is above 2^-4 and two half steps of 2^-25 are what the fma and its
+// rounded second operand can lose.
 //
 // 20 warps in five warpgroups, one CTA per SM:
 //   warps 0-7   softmax, two warpgroups that take the blocks of a tile in turn,
@@ -287,7 +290,7 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t u2, __half2 s, __half2 
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 constexpr int kNoExp = -1000;  // 16 keys that are all zero, or not there
-constexpr int kOperand = 15;  // an operand holds its value times 2^-(e + 15)
+constexpr int kOperand = 12;  // an operand holds its value times 2^-(e + kOperand)
 // Weights are held 2^kUp up. A score may pass its reference by kScoreSlack
 // before that moves (by 4 only, and the accumulator is rescaled so often that
 // four chunks in a window take 556 us instead of about 480), so the largest fp16 weight is
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       l += pair_x[(3 - half) * kRows + row];
       wait_bar(&pvdone[(j0 - 1) & 1], ((j0 - 1) >> 1) & 1);
       fence_after();
-      // back to O: 2^(e_ref + 15 - kUp) / l (the power in two steps, each a normal number)
+      // back to O: 2^(e_ref + kOperand - kUp) / l (the power in two steps, each a normal number)
       const float up = e_ref == kNoExp ? 1.f : pow2i(e_ref), inv = l > 0.f ? pow2i(kOperand - kUp) / l : 0.f;
       bool finite = true;
       const bool head = sd.flags & 1, whole = sd.flags & 2, live = row < sd.rows;
@@ -920,9 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           }
           m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
         }
-        // the 16 keys take the exponent of their own largest scale: S = s 2^(9 - e) lies below 2^12
+        // the 16 keys take the exponent of their own largest scale: S = s 2^(24 - kOperand - e) lies below 2^15
         es[v] = m > 0.f ? max(exp_of(m) - 2, -110) : kNoExp;
-        const float down = m > 0.f ? pow2i(9 - es[v]) : 0.f;
+        const float down = m > 0.f ? pow2i(24 - kOperand - es[v]) : 0.f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const __half2 sc = __float2half2_rn(s[i] * down);

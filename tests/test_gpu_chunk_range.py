@@ -137,6 +137,50 @@ def test_values_that_fall_by_more_than_the_fp32_range():
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("r", [4, 8, 11, 12, 13, 14])
+@pytest.mark.parametrize("loud", ["group", "key"])
+def test_neighbours_of_different_size(loud, r):
+    """Channel groups, or keys, of one 16 whose values differ by 2^r. The first token sees itself alone, the second itself
+    and the first: nothing averages the roundings out."""
+    L, Hkv, D = 64, 2, 256
+    k, v, _ = rows(10 + r, L, L, 2, Hkv, D)
+    if loud == "group":
+        v[:, :, 64:128] *= 2.0 ** r
+        quiet = [g for g in range(4) if g != 1]
+    else:
+        v[15::16] *= 2.0 ** r
+        quiet = range(4)
+    c = Cache(k, v, torch.zeros(L, 2, D, device="cuda"))
+    K, V = _ref.dequantized(c.pool.storage, c.pages, Hkv, c.P, D)
+    ref, out = c.ref(), c.run().double()
+    V = V[int(c.bt[0, 0])]                                                 # [Hkv][64][D]
+    largest = V.abs().amax(-1).view(Hkv, 4, 16).amax(-1)                   # of each 16 keys
+    mean = lambda x: x.cumsum(1) / torch.arange(1, L + 1, device="cuda")[:, None]  # noqa: E731  (equal weights)
+    near = mean(largest.repeat_interleave(16, 1)[..., None].expand(Hkv, L, 1)).transpose(0, 1)
+    bound = 2.0 ** -8 * ref.abs() + 3 * 2.0 ** -11 * mean(V.abs()).transpose(0, 1) + 2.0 ** -20 * near
+    err = (out - ref).abs()
+    # (the weights' own step, for the largest value of all: 64 keys of 2^-32)
+    bound = bound + 64 * 2.0 ** -32 * float(largest.max())
+    assert torch.all(err <= bound), f"{loud} 2^{r}: {float((err - bound).max()):.3e} past the bound"
+    first = out[0].view(Hkv, 4, 64)[:, list(quiet)], ref[0].view(Hkv, 4, 64)[:, list(quiet)]
+    rel = float((first[0] - first[1]).norm() / first[1].norm())
+    # bf16 1.65e-3, three fp16 roundings; 2^-25 of the operand's unit twice, uniform: 2^-20 2^r (4 sigma) / sqrt(12) at most
+    assert rel <= math.hypot(2.5e-3, 2.0 ** (r - 18) / math.sqrt(12)), f"{loud} 2^{r}: relative norm {rel:.3e}"
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_scores_beside_a_loud_channel_group_of_k(D):
+    """K with a channel group 2^8 times as large as the others, which q leaves out. The operand of a quiet channel is off by
+    two half steps of 2^-25 where the largest is 2^-3 at least: of rows of N(0, 1), with that largest at four times 2^8, by
+    2^-24 2^3 4 2^8 / sqrt(12) = 2^-12.8 in the mean square, less than the 2^-11 sqrt(2/3) that `check` allows for already."""
+    k, v, q = rows(12, 300, 60, 8, 2, D)
+    k[:, :, 64:128] *= 2.0 ** 8
+    q[:, :, 64:128] = 0
+    c = Cache(k, v, q)
+    check(c.run(), c.ref(), "loud group of K")
+    assert int(c.status.item()) == 0
+
+
 @pytest.mark.parametrize("octaves", [20, 25, 26, 28])
 @pytest.mark.parametrize("where", [0, 40000])
 def test_many_keys_far_below_one_dominant_key(octaves, where):
