@@ -63,13 +63,21 @@ constexpr int kConsumerWarps = 8;
 constexpr int kThreads = kConsumerWarps * 32;
 constexpr int kSmemLimit = 232448;  // opt-in shared memory per block on sm_100/103
 // Pages in flight, at most. Eight 64-key pages fill shared memory at head dim
-// 256; a ring of small pages (16 keys: one block, so one team's step) needs
-// more of them to cover a load's latency.
-constexpr int kMaxStages = 32;
+// 256. A sliding window over small pages (16 keys: one block, so one team's
+// step) takes up to 32, filled by four warps (64 windows of 1,000 keys on
+// 16-key pages 51.5 -> 45.7 us with them). Over the whole context, where one
+// thread fills the ring in order, more than eight only delay its warp: with 32,
+// 64 sequences of 2,000 tokens on 16-key pages took 44.5 us (40.3 with 8; head
+// dim 128), 8 of 1,000 21.8 (18.3; head dim 64). A ring that does not hold more
+// than eight keeps no room for their barriers: at head dim 256, 128-key pages
+// with fp16 scales leave two stages beside 33 to 40 rows, and a few hundred
+// bytes more would cost one of them, so the shape.
+constexpr int kStagesWhole = 8, kStagesWindow = 32;
 
 struct Geometry {
   int stage_bytes;   // one page: K|V boxes, then Ks, Vs (rounded to 1 KB)
   int stages;
+  int max_stages;    // that barriers and counters have room for
   int park_off;      // the teams' accumulators at a segment's end, -1: no room beside the ring
   int xch_off, xch_bytes;
   int merge_off, merge_bytes;
@@ -97,15 +105,22 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   g.xch_bytes = CS > 1 ? nteams * 2 * CS * NT * 4 * 32 * 4 : 0;
   const int mrows = NT * 8;
   g.merge_bytes = mrows * (D + 4) * 4 + 3 * nteams * mrows * 4 + mrows * 4;
-  const int pre_bytes = round_up((2 * B + 10 + 2 * kMaxStages) * 4, 16);  // pre[B+1], warp_tot[8], abort, cnt, lens[B], icnt
   const int pid_bytes = 1024 * 4;
-  const int fixed = g.xch_bytes + g.merge_bytes + pre_bytes + pid_bytes + 2 * kMaxStages * 8 + 1024;
-  int s = (kSmemLimit - fixed) / g.stage_bytes;
+  const int base = g.xch_bytes + g.merge_bytes + pid_bytes + 1024;
   const int park_bytes = nteams * mrows * (D + 4) * 4;
-  const int sp = (kSmemLimit - fixed - park_bytes) / g.stage_bytes;
-  const bool park = win && sp > 8;
-  if (park) s = sp;
-  if (s > kMaxStages) s = kMaxStages;
+  int s = 0, pre_bytes = 0;
+  bool park = false;
+  for (int ms = win ? kStagesWindow : kStagesWhole;; ms = kStagesWhole) {
+    pre_bytes = round_up((2 * B + 10 + 2 * ms) * 4, 16);  // pre[B+1], warp_tot[8], abort, cnt[ms], lens[B], icnt[ms]
+    const int left = kSmemLimit - (base + pre_bytes + 2 * ms * 8);
+    s = left / g.stage_bytes;
+    const int sp = (left - park_bytes) / g.stage_bytes;
+    park = win && sp > 8;
+    if (park) s = sp;
+    if (s > ms) s = ms;
+    g.max_stages = ms;
+    if (ms == kStagesWhole || s > kStagesWhole) break;
+  }
   g.stages = s;
   int off = g.stages * g.stage_bytes;
   g.park_off = park ? off : -1;
@@ -119,7 +134,7 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   g.pid_off = off;
   off += pid_bytes;
   g.bar_off = off;
-  off += 2 * kMaxStages * 8;
+  off += 2 * g.max_stages * 8;
   g.total = off + 1024;  // slack to align the dynamic base to 1 KB
   return g;
 }
@@ -449,12 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   int* pre = reinterpret_cast<int*>(smem + geo.pre_off);
   int* warp_tot = pre + (p.B + 1);
   volatile int* abort_flag = pre + (p.B + 1) + 8;
-  int* cnt = pre + (p.B + 1) + 9;    // [kMaxStages] consumer count per stage
-  int* lens = cnt + kMaxStages;      // [B] context lengths
-  int* icnt = lens + p.B;            // [kMaxStages] copies issued into each stage
+  const int ms = WIN ? geo.max_stages : kStagesWhole;
+  int* cnt = pre + (p.B + 1) + 9;  // [ms] consumer count per stage
+  int* lens = cnt + ms;            // [B] context lengths
+  int* icnt = lens + p.B;          // [ms] copies issued into each stage
   int* pid = reinterpret_cast<int*>(smem + geo.pid_off);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + geo.bar_off);
-  uint64_t* empty_bar = full_bar + kMaxStages;
+  uint64_t* empty_bar = full_bar + ms;
   float* xch = reinterpret_cast<float*>(smem + geo.xch_off);
   float* mo = reinterpret_cast<float*>(smem + geo.merge_off);
   float* tm_m = mo + MROWS * (D + 4);

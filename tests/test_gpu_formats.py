@@ -190,3 +190,18 @@ def test_full_size_c1(name):
     out = DECODE[w.fmt](c.pool, c.q, c.bt, c.ctx, w.sm_scale, w.max_ctx)
     torch.cuda.synchronize()
     compare(out, oracle_out(w.fmt, c), name)
+
+
+@pytest.mark.parametrize("heads,T", [(33, 1), (40, 1), (6, 6), (8, 5), (4, 10), (37, 2)])
+def test_33_to_40_rows_on_128_key_pages(heads, T):
+    """Head dim 256, fp16 scales: two stages of the ring are all that fits beside so many rows."""
+    lens = [T, 300, 1100]
+    w = wl.custom(f"rows{heads}x{T}", B=3, T=T, Hq=heads, Hkv=1, D=256, P=128, ctx_lens=lens, seed=12,
+                  num_pages=sum((L + 127) // 128 for L in lens) + 3, outlier_channels=2, outlier_scale=8.0)
+    c = build_fmt("i8f16", w, fill=0xFF)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for n in (0, 1, 7):
+        out = nk.i8f16_decode_attn(c.pool, c.q, c.bt, c.ctx, w.sm_scale, w.max_ctx, num_ctas=n, status=status)
+        torch.cuda.synchronize()
+        compare(out, oracle_out("i8f16", c), f"{w.name}/ctas={n}")
+    assert int(status.item()) == 0
