@@ -334,7 +334,10 @@ int nk_mrope(const void* q_dev, const void* k_dev, void* q_out_dev, void* k_out_
  * sinks >= 0. Arguments, checks, workspace (nk_decode_workspace_bytes), device
  * flags, ordering and ownership as nk_paged_decode_attn. Only the pages that
  * hold a visible key are read, and only their block-table entries: the pages
- * between the sinks and the window may have been given back. A window of at
+ * between the sinks and the window may have been given back. Keys that no
+ * column of the call sees do not enter the result, whatever their bits; one that
+ * some column sees sets the others' precision, as in nk_paged_decode_attn, and
+ * makes all columns of its sequence NaN when its V is not finite. A window of at
  * least max_ctx is nk_paged_decode_attn itself.
  */
 int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,

@@ -963,6 +963,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
           if constexpr (WIN) {
             // blocks with a key before the last column's window, past the sinks
             if (pos0 <= L - 1 - sh.window && pos0 + 15 >= sh.sinks) {
+              // a key that no column sees: its V counts as zero, whatever its
+              // size or bits (0 times infinity, and the exponent of P')
+              const int none = L - T - sh.window, n0 = pos0 + g, n1 = n0 + 8;
+              valid0 = valid0 && (n0 > none || n0 < sh.sinks);
+              valid1 = valid1 && (n1 > none || n1 < sh.sinks);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

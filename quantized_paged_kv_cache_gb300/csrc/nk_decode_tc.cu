@@ -538,7 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(const __grid_con
         const uint8_t* ks_s = st + 2 * kP * kD;           // [64 keys][4 groups], fp32 or fp16
         const uint8_t* vs_s = ks_s + kP * (kD / kGroup) * sb;
         const int pos = lp * kP + key;
-        const bool key_valid = pos < L;
+        bool key_valid = pos < L;
+        // a key that no column sees: its V counts as zero, whatever its size or bits
+        if constexpr (WIN) key_valid = key_valid && (pos > L - T - sh.window || pos < sh.sinks);
         // P' window of each group, while the page's QK runs: bit g set when a
         // key's Vs 2^-ev passes 2^6 (p Vs 2^-ev could reach 2^15), bit 4 + g
         // when one is at least 2^-10; a group whose ev is not set yet has
