@@ -367,12 +367,13 @@ int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
  * not finite (NK_DEVFLAG_RANGE) count as zeros. K and V enter the products as
  * fp16, where the other attention calls keep the codes exact. A value of K or V
  * is off by at most 2^-10 of itself, plus 2^-20 of the largest value of its
- * kv-head among the 16 tokens (positions 16 i .. 16 i + 15, hidden ones
- * included) it lies in; a weight by 2^-11 of itself, plus 2^-32 of the weight of
- * the row's largest score or of one up to 2^8 below it. So an output differs
- * from the exact one by its bf16 rounding plus a few 2^-11 of the values it
- * averages, and more only where neighbouring tokens, or channel groups, differ
- * in size by more than about 2^10. B is at most 1,024 and
+ * kv-head among the 16 tokens (positions 16 i .. 16 i + 15) it lies in, as far
+ * as this query or one within 128 rows of its kv-head's sees them; a weight by
+ * 2^-11 of itself, plus 2^-32 of the weight of the row's largest score or of one
+ * up to 2^8 below it. So an output differs from the exact one by its bf16
+ * rounding plus a few 2^-11 of the values it averages, and more only where
+ * neighbouring tokens, or channel groups, differ in size by more than about
+ * 2^10. Keys that no query of the call sees leave no trace. B is at most 1,024 and
  * total_q * Hq / Hkv below 2^31 - 128.
  */
 size_t nk_chunk_workspace_bytes(int32_t head_dim, int32_t num_ctas);

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int* last_mma = misc + 2;                             // block number of the last MMAs committed to pvdone / qkdone
   int* start = misc + 4;                                // [4] b, h, tile, v of the CTA's first block
   int* exps = misc + 32;                                // [4][K | V][4]: e of 16 keys of a block
-  volatile int* info = misc + 96;                       // [kStages] of a raw block: keys there | first of its segment << 8 | 16-key groups that were not copied << 16
+  volatile uint16_t* live = reinterpret_cast<volatile uint16_t*>(misc + 96);  // [kStages][4] of a raw block: the keys that count, a bit each
   int* last_raw = misc + 100;                           // raw blocks issued
   int* longest = misc + 101;                            // blocks of the longest tile
   int* sched = misc + 104;                              // [kMaxSched + 1] where the CTAs' shares of the last tiles begin
@@ -877,8 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     static_assert(kStages == 2, "a stage per parity");
     for (int j = odd; j < total; j += 2, ph ^= 1u) {
       wait_bar(&rfull[odd], ph);
-      const int inf = info[odd];
-      const int there = ((inf >> (16 + cw)) & 1) ? 0 : (inf & 0xff) - cw * 16;  // keys of this warp's 16 that exist
+      const uint32_t keys = live[odd * 4 + cw];  // of this warp's 16: those that count
       // ---- scales of K and V, and the exponents, which have to be there with the scores
       int es[2];
 #pragma unroll
@@ -889,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         float mx = 0.f, mn = INFINITY;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          if (!has_scale || (lane + 32 * i) / G64 >= there) s[i] = 0.f;  // no such key: stale codes count as zeros
+          if (!has_scale || !((keys >> ((lane + 32 * i) / G64)) & 1u)) s[i] = 0.f;  // (whatever the codes are)
           float a = fabsf(s[i]);
           if (!(a <= 3.4028234e38f)) {  // infinite of either sign or NaN, the append of a non-finite row: zeros too, flagged
             s[i] = a = 0.f;
@@ -1160,10 +1159,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (__any_sync(0xffffffffu, *abort_flag != 0)) break;  // no more copies
           const uint32_t bar = smem_u32(&rfull[st]);
           if (lane == 0) {
-            const int left = L - block_at(span, v0 + i) * kKeys;
+            // The keys that count: in the sequence, in pages that were copied, and seen by some token of the tile (from
+            // the window of its first token on, or a sink; not behind its last token). What nobody sees must neither set
+            // an exponent nor a flag.
+            const int k0 = block_at(span, v0 + i) * kKeys, end = min(span.p1 + 1 - k0, kKeys);  // (p1 < L)
+            uint64_t on = ~0ull >> (kKeys - end);
+            if (p.window > 0) {
+              const int from = max(p.sinks - k0, 0);  // hidden: from .. to
+              const int to = (int)min((int64_t)span.p0 - p.window - k0, (int64_t)(kKeys - 1));
+              if (from <= to) on &= ~((~0ull >> (kKeys - 1 - to)) & (~0ull << from));
+            }
             // bits 0, 4, 8, 12 of outb are the 16-key groups, bit 0 alone a whole block
-            const unsigned out = whole ? (outb ? 15u : 0u) : ((outb & 1u) | ((outb >> 3) & 2u) | ((outb >> 6) & 4u) | ((outb >> 9) & 8u));
-            info[st] = (left < kKeys ? left : kKeys) | (i == 0 ? 256 : 0) | (out << 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              live[st * 4 + c] = ((whole ? outb : outb >> (4 * c)) & 1u) ? 0 : (uint16_t)(on >> (16 * c));
             if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
             mbar_arrive_expect_tx(bar, __popc(okb) * per * kKeyBytes);
             *last_raw = q + 1;
