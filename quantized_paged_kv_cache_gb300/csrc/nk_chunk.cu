@@ -833,7 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       if (live && !finite) flag(p.status, NK_DEVFLAG_RANGE);
       if (!whole) {
-        if (half == 0) p.part_lse[slot * kRows + row] = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+        // (a row sum that is NaN, of a query that is not finite, stays NaN through the join)
+        if (half == 0) p.part_lse[slot * kRows + row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
         if (head) {
           // the tile's first blocks: this CTA leaves what the join needs
           have_desc = true;

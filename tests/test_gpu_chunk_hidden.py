@@ -69,3 +69,26 @@ def test_a_later_token_that_is_not_finite_leaves_the_tiles_before_it():
     v[33:] *= 2.0 ** 30
     v[40] = float("inf")
     assert torch.equal(run(k, v)[:32], want[:32])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_is_nan_however_the_work_is_split(value):
+    L, T, Hq, H, D = 2000, 9, 8, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(16)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    pool, bt = pool_of(r(L, H, D), r(L, H, D), 64)
+    q = r(T, Hq, D).bfloat16()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ctx, cu = i32([L]), i32([0, T])
+    for n in (1, 2, 7, 0):
+        status = i32([0])
+        run = lambda q: nk.paged_chunk_attn(pool, q, cu, bt, ctx, 0.1, L, num_ctas=n, status=status)  # noqa: B023, E731
+        want = run(q)
+        bad = q.clone()
+        bad[5, 3] = value
+        out = run(bad)
+        torch.cuda.synchronize()
+        assert int(status.item()) == nk.NK_DEVFLAG_RANGE
+        assert torch.isnan(out[5, 3]).all(), f"{n} CTAs"
+        out[5, 3] = want[5, 3]
+        assert torch.equal(out, want), "the other rows"
