@@ -448,10 +448,11 @@ def _one(t, what: str) -> None:
 
 
 def _clamped(max_ctx: int, window: int, sinks: int) -> tuple:
-    """A window or sinks past 2^31 - 1 tokens, which the C calls cannot take, mean the same as that many."""
-    if max_ctx > _I32_MAX:
+    """A window or sinks past 2^31 - 1 tokens, which the C calls cannot take, mean the same as that many; negative ones
+    stay negative, which the C calls refuse."""
+    if not -_I32_MAX <= max_ctx <= _I32_MAX:
         raise ValueError("max_ctx must be below 2^31")
-    return min(window, _I32_MAX), min(sinks, _I32_MAX)
+    return max(min(window, _I32_MAX), -1), max(min(sinks, _I32_MAX), -1)
 
 
 def _empty(stream, like, shape, dtype=None):
@@ -482,6 +483,8 @@ def step_tables(page_size: int, num_pages: int, start_pos, new_lens, free_pages,
     _need(torch.int64, slot_map)
     if used is not None:
         _one(used, "used")
+    if page_size > _I32_MAX or num_pages > _I32_MAX or page_size < -_I32_MAX or num_pages < -_I32_MAX:
+        raise ValueError("page_size and num_pages must be below 2^31")
     B, rows, shape = start_pos.numel(), min(slot_map.numel(), _I32_MAX), block_table.shape
     if new_lens.numel() != B or ctx_lens.numel() != B or cu_new.numel() != B + 1 or len(shape) != 2 or shape[0] != B:
         raise ValueError("start_pos, new_lens, ctx_lens and block_table hold one entry (row) per sequence, cu_new one more")
@@ -571,7 +574,7 @@ def paged_window_attn(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, m
     _need(torch.int32, block_table, ctx_lens, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    if max_ctx > _I32_MAX or window > _I32_MAX or sinks > _I32_MAX:
+    if not (0 <= max_ctx <= _I32_MAX and 0 <= window <= _I32_MAX and 0 <= sinks <= _I32_MAX):
         window, sinks = _clamped(max_ctx, window, sinks)
     B, T, Hq, D = q.shape
     shape = block_table.shape
@@ -608,7 +611,7 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
     _need(torch.int32, cu_q, block_table, ctx_lens, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    if max_ctx > _I32_MAX or window > _I32_MAX or sinks > _I32_MAX:
+    if not (0 <= max_ctx <= _I32_MAX and 0 <= window <= _I32_MAX and 0 <= sinks <= _I32_MAX):
         window, sinks = _clamped(max_ctx, window, sinks)
     total, Hq, D = q.shape
     B, shape = ctx_lens.numel(), block_table.shape

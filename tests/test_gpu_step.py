@@ -459,3 +459,25 @@ def test_slots_and_rows_past_32_bits():
     want = nk.mrope(x, y, pos, inv, (32,))
     nk.mrope(q, k, pos, inv, (32,), q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_negative_numbers_past_32_bits_are_refused():
+    """They must not come out as small positive ones on the way into the C calls."""
+    D, P, i32 = 64, 16, torch.int32
+    pool = nk.KVPool.empty(2, P, 2, D, fill=0)
+    table = torch.zeros(1, 2, dtype=i32, device="cuda")
+    ctx, cu = torch.tensor([1], dtype=i32, device="cuda"), torch.tensor([0, 1], dtype=i32, device="cuda")
+    x = torch.randn(1, 2, D, device="cuda").bfloat16()
+    for window, sinks in ((5 - 2**32, 0), (5, 5 - 2**32), (-5, 0), (5, -5)):
+        with pytest.raises(nk.NKError):
+            nk.paged_window_attn(pool, x.unsqueeze(0), table, ctx, 0.1, 32, window, sinks=sinks)
+        with pytest.raises(nk.NKError):
+            nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32, window=window, sinks=sinks)
+    with pytest.raises(ValueError):
+        nk.paged_window_attn(pool, x.unsqueeze(0), table, ctx, 0.1, 32 - 2**32, 5)
+    with pytest.raises(ValueError):
+        nk.paged_chunk_attn(pool, x, cu, table, ctx, 0.1, 32 - 2**32, window=5)
+    slots = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for page_size, pages in ((2**32 + 16, 2), (16, 2**32 + 2), (16 - 2**32, 2), (16, 2 - 2**32)):
+        with pytest.raises(ValueError):
+            nk.step_tables(page_size, pages, ctx, ctx, ctx, table, cu, ctx.clone(), slots)
