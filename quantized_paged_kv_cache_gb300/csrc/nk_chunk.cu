@@ -39,7 +39,8 @@
 //   warp 16     issues the MMAs: QK of block j + 1 goes out before PV of block
 //               j, so the tensor cores work while the softmax does;
 //   warp 17     walks the list, looks up the pages and fills a two-stage ring of
-//               raw blocks with bulk asynchronous copies (18 and 19 are idle).
+//               raw blocks with bulk asynchronous copies (18 and 19 have no
+//               part: setmaxnreg takes whole warpgroups).
 //
 // What bounds it: per 64-key block at head dim 256 the MMAs take 1,026 cycles
 // of the tensor cores, the copies, codes, fp16 tiles and MMA operands about
@@ -101,7 +102,6 @@ static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsMma == 5 * kLaunchRegs, "shar
 constexpr int kTmemCols = 512;
 constexpr int kStages = 2;  // raw blocks in flight (a third does not fit at head dim 256), one of each parity
 constexpr int kMaxSched = 160;  // CTAs of a call whose tiles are dealt out whole first (one per SM has fewer)
-constexpr int kMinBlocks = 1;  // blocks a CTA takes at least (fewer CTAs work on a small batch)
 
 // A segment: the blocks of one tile that fall into the CTA's range. The
 // producer warp, which walks the list, leaves them for the softmax and MMA
@@ -445,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   __syncthreads();
   const Tables tab{pre, tiles, cus, p.ctx, p.B};
   const int64_t W = pre[p.B];
-  const int64_t most = quot(W + kMinBlocks - 1, kMinBlocks);
-  const int nctas = most < p.n_ctas ? (int)most : p.n_ctas;  // CTAs that take part
+  const int nctas = W < p.n_ctas ? (int)W : p.n_ctas;  // CTAs that take part, a block each at least
   const int cta = blockIdx.x;
   const bool idle = cta >= nctas;
   // ---- whole tiles first: `waves` rounds of one tile a CTA
