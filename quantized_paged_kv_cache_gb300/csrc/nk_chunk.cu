@@ -47,9 +47,10 @@
 // 1,700 of shared memory, and about 4,800 warp instructions 1,200 issue slots
 // of each scheduler; a block takes about 2,050 cycles, so the hand-offs between
 // the roles count beside each of them. Eight chunks of 1,024 tokens at 8K to
-// 32K (24 q-heads over 4 kv-heads): 3,340 us, 1,118 TFLOP/s.
+// 32K (24 q-heads over 4 kv-heads): 3,525 us in a loop, under the power cap
+// (1,059 TFLOP/s), 3,320 for a few calls; four in a window of 4,096: 481.
 //
-// Taken against, on those eight chunks: codes loaded straight into the convert
+// Taken against, on those eight chunks (a few calls each): codes loaded straight into the convert
 // warps' registers instead of the ring, 7,345 us (4,720 with the ring, other
 // things equal); MMAs issued by one lane of a diverged warp 4,332 (3,518 from
 // a uniform one); two threads a row, 32 keys each, that exchange their maxima
