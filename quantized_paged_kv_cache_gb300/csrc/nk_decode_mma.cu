@@ -6,20 +6,6 @@
 namespace nk {
 namespace mma {
 
-// Warps per team (channel split) for a head_dim and a number of 8-row tiles:
-// chosen so one warp's Q fragments and output accumulator stay near 150
-// registers. rk8v4 rows carry a second (low) fp16 part, so its warps take
-// narrower slices.
-int channel_split(int D, int NT) {
-  if (D == 256) return NT <= 1 ? 1 : (NT <= 3 ? 2 : 4);
-  if (D == 128) return NT <= 3 ? 1 : 2;
-  return 1;
-}
-int channel_split_rk(int D, int NT) {
-  if (D == 256) return NT <= 1 ? 2 : 4;
-  return NT <= 1 ? 1 : 2;
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

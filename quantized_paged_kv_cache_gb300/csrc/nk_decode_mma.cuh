@@ -78,6 +78,7 @@ struct Geometry {
   int stage_bytes;   // one page: K|V boxes, then Ks, Vs (rounded to 1 KB)
   int stages;
   int max_stages;    // that barriers and counters have room for
+  bool gated;        // a wait for a page first asks whether it was issued
   int park_off;      // the teams' accumulators at a segment's end, -1: no room beside the ring
   int xch_off, xch_bytes;
   int merge_off, merge_bytes;
@@ -88,6 +89,34 @@ struct Geometry {
 };
 
 __host__ __device__ inline int round_up(int x, int a) { return (x + a - 1) / a * a; }
+
+// Warps per team (channel split) for a head_dim and a number of 8-row tiles:
+// chosen so one warp's Q fragments and output accumulator stay near 150
+// registers. rk8v4 rows carry a second (low) fp16 part, so its warps take
+// narrower slices.
+__host__ __device__ inline int channel_split(int D, int NT) {
+  if (D == 256) return NT <= 1 ? 1 : (NT <= 3 ? 2 : 4);
+  if (D == 128) return NT <= 3 ? 1 : 2;
+  return 1;
+}
+__host__ __device__ inline int channel_split_rk(int D, int NT) {
+  if (D == 256) return NT <= 1 ? 2 : 4;
+  return NT <= 1 ? 1 : 2;
+}
+
+// The page that a team waits for, q, shares its stage with page q - stages. The
+// wait goes by the parity of the stage's phase, so it must not begin before
+// that page has landed: two phases behind, the barrier would let it pass with
+// the data of page q - 2 stages. A team that reads both pages sees to that
+// itself. It does where a page has a block for every team, or where the ring
+// is a whole number of the teams' rounds over the blocks: its size is a
+// multiple of this.
+__host__ __device__ inline int ring_unit(int nteams, int bpp) {
+  if (bpp >= nteams) return 1;
+  int u = 1;
+  while (u * bpp % nteams != 0) ++u;  // (at most 8)
+  return u;
+}
 
 // Shared-memory plan. Needs the pool format, D, NT, CS, P (and B for the
 // prefix array). A bf16 pool stages 2-byte K|V values and no scales. With a
@@ -121,6 +150,12 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
     g.max_stages = ms;
     if (ms == kStagesWhole || s > kStagesWhole) break;
   }
+  // A ring of more than eight gives up the pages past the last whole round; a
+  // smaller one keeps them (48-, 80-, 96- and 112-key pages, 3 to 7 stages),
+  // and the waits ask first whether the page was issued.
+  const int unit = ring_unit(nteams, P / 16);
+  if (s > kStagesWhole) s -= s % unit;
+  g.gated = s % unit != 0;
   g.stages = s;
   int off = g.stages * g.stage_bytes;
   g.park_off = park ? off : -1;
@@ -774,13 +809,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
         issue_page_rk<D>(p, &tmap, &tmapv, pid[q], stage0 + q * geo.stage_bytes, smem_u32(&full_bar[q]));
       else
         issue_page<D, BF>(p, &tmap, pid[q], stage0 + q * geo.stage_bytes, smem_u32(&full_bar[q]));
+      if (geo.gated) __threadfence_block();
       icnt[q] = 1;
     }
   }
 
   const int bpp_sh = (BPP & (BPP - 1)) == 0 ? __ffs(BPP) - 1 : -1;  // blocks per page, as a shift
   int q_cur = 0, s_cur = 0;  // last page whose stage was located, and that stage
-  uint32_t par_cur = 0;
+  int round_cur = 0;         // pages that went through the stage before it
   int page_seq = 0;   // CTA page number of the current segment's first page
   int jn = team;       // next block of this team
   // With up to two row tiles the next unit's Q rows are fetched (one or two
@@ -836,16 +872,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
         ++q_cur;
         if (++s_cur == S) {
           s_cur = 0;
-          par_cur ^= 1u;
+          ++round_cur;
         }
       }
       const int s = s_cur;
-      const uint32_t par = par_cur;
+      const uint32_t par = (uint32_t)round_cur & 1u;
       const uint32_t st = stage0 + s * geo.stage_bytes;
       // [P][G_ALL] key scales (fp32 or fp16), then [P][GV_ALL] value scales
       const uint8_t* ks_s = smem + s * geo.stage_bytes + (RK ? 3 * P * D / 2 : 2 * P * D);
       const uint8_t* vs_s = ks_s + P * G_ALL * sb;
       {
+        if (geo.gated) {  // the page was issued, so the stage's previous one has landed
+          const volatile int* issued = icnt + s;
+          const unsigned long long t0 = clock64();
+          while (*issued <= round_cur && !*abort_flag) {
+            if (clock64() - t0 > p.wait_cycles) {
+              if (lane == 0) flag(p.status, NK_DEVFLAG_TIMEOUT);
+              *abort_flag = 1;
+            }
+          }
+          __threadfence_block();
+        }
         // after one wait of the CTA has run out, no wait blocks any more (the
         // blocks run without data and nothing more is issued; the end of the
         // kernel waits for the copies that were)
@@ -1209,6 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
                   issue_page_rk<D>(p, &tmap, &tmapv, zn, st, smem_u32(&full_bar[s]));
                 else
                   issue_page<D, BF>(p, &tmap, zn, st, smem_u32(&full_bar[s]));
+                if (geo.gated) __threadfence_block();
                 ++icnt[s];
               } else {
                 flag(p.status, NK_DEVFLAG_TIMEOUT);
