@@ -2,8 +2,9 @@
  * nk.h -- C ABI of the paged INT8 group-64 KV cache for one GB300 (sm_103a).
  *
  * Three operations on the cache, and beside them the operators of a serving
- * step (tables, rotary positions, windowed and ragged attention; described at
- * their declarations), all enqueued on a caller-supplied CUDA stream:
+ * step (tables, rotary positions, windowed and ragged attention) and of long
+ * caches (page bounds, selection, sparse attention, weights, eviction) and
+ * the verification of drafts, described at their declarations, all enqueued on a caller-supplied CUDA stream:
  *   nk_kv_append          quantize new bf16 K/V rows into 64-channel int8 groups
  *                         and scatter them into pages ("NInfer-3090" README,
  *                         introduction: the kv_cache_append Op owns KV
@@ -94,7 +95,9 @@ typedef enum {
                                        operands by powers of two, so no finite bf16 input
                                        leaves their range); rk8v4 append: a group scale
                                        saturated at the fp16 maximum, or a non-finite value */
-#define NK_DEVFLAG_NO_PAGES 0x20u   /* nk_step_tables: the free list is shorter than the step needs */
+#define NK_DEVFLAG_NO_PAGES 0x20u   /* nk_step_tables: the free list is shorter than the step needs;
+                                       nk_evict_pages: the list of freed pages is */
+#define NK_DEVFLAG_BAD_TOKEN 0x40u  /* nk_verify_drafts: a draft outside the vocabulary */
 
 /* Limits of the library. */
 #define NK_GROUP 64      /* channels per quantization group */
@@ -382,6 +385,179 @@ int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t
                         int32_t B, int32_t total_q, int32_t num_q_heads, float sm_scale, int32_t max_ctx,
                         int32_t window, int32_t sinks, int32_t num_ctas, void* workspace_dev, size_t workspace_bytes,
                         void* out_dev, int32_t* status_dev, void* stream);
+
+/*
+ * Long caches. The next five read less of a long cache, or keep less of it, and
+ * nk_verify_drafts ends a verify round; none has a counterpart on the pages.
+ *
+ * nk_page_bounds -- of each touched page and kv-head, the largest and smallest
+ * value hi[d], lo[d] of every key channel over the page's filled slots, so that
+ * nk_page_select can tell what the page's best score may be. Called after the
+ * step's nk_kv_append with its block table, start_pos and cu_new: it covers the
+ * pages that a new row falls in, over all of their slots up to start + new.
+ *   bounds_dev  nk_page_bounds_bytes(...) bytes, 16-byte aligned, owned by the
+ *               caller beside the pool (2 D + 4 bytes per page and kv-head, as
+ *               much as one key and value of the page):
+ *               codes [num_pages][Hkv][hi | lo][D] int8, then
+ *               scales [num_pages][Hkv] fp32.
+ * With v = fp32(code * scale) of the pool's keys, s = fp32(max(|hi|, |lo|) / 127)
+ * over all channels (1 when that is 0), codes = clamp(round_half_even(fp32(hi /
+ * s)), -127, 127), lo alike. Groups whose scale is not finite count as zeros
+ * (NK_DEVFLAG_RANGE). A sequence whose start or rows are negative or pass the
+ * table sets NK_DEVFLAG_BAD_POS and is skipped, a page outside the pool
+ * NK_DEVFLAG_BAD_PAGE. B is at most 1,024. A page that two sequences write in
+ * one call gets the bounds of one of them.
+ */
+size_t nk_page_bounds_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim);
+int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                   const int32_t* start_pos_dev, const int32_t* cu_new_dev, int32_t B, int32_t* status_dev,
+                   void* stream);
+
+/*
+ * nk_page_select -- the k pages of each query token and kv-head whose bounds
+ * promise the largest score, for nk_paged_sparse_attn.
+ *   q_dev, block_table_dev, ctx_lens_dev, B, T, num_q_heads, max_ctx
+ *                  as nk_paged_decode_attn: token t of sequence b, at position
+ *                  ctx_len - T + t, sees pages 0 .. position / P
+ *   sink_pages, recent_pages  the first and the last of them that are taken in
+ *                  any case; recent_pages >= 1 (the last pages are not full, and
+ *                  their bounds are not read), sink_pages + recent_pages <= k
+ *   workspace_dev  nk_page_select_workspace_bytes(...) bytes, 16-byte aligned;
+ *                  scratch. Calls that may overlap on the GPU need one each.
+ *   pages_dev      int32 [B][T][Hkv][k]: the pages' numbers in the sequence,
+ *                  ascending, -1 behind them where the token sees fewer than k
+ * The score of a page is s * max over the G query heads of
+ *   sum_d max(q8[d], 0) hi[d] + min(q8[d], 0) lo[d]
+ * with the bounds' codes and scale s, and q8 = clamp(round_half_even(fp32(q /
+ * s_q)), -127, 127), s_q = fp32(max |q| / 127) over the token's G heads (1 when
+ * that is 0): whole numbers times s, compared exactly. Of equal scores the lower
+ * page is taken. Query heads that are not finite choose as zeros would. Pages
+ * whose id is outside the pool (NK_DEVFLAG_BAD_PAGE) and bounds that are not
+ * finite come last. An invalid context length sets NK_DEVFLAG_BAD_CTX and leaves
+ * its sequence's lists as they were. G is at most 48, B * Hkv 65,535.
+ */
+size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_kv_heads, int32_t page_size, int32_t max_ctx);
+int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                   const void* q_dev, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                   const int32_t* ctx_lens_dev, int32_t B, int32_t T, int32_t num_q_heads, int32_t max_ctx, int32_t k,
+                   int32_t sink_pages, int32_t recent_pages, void* workspace_dev, size_t workspace_bytes,
+                   int32_t* pages_dev, int32_t* status_dev, void* stream);
+
+/*
+ * nk_paged_sparse_attn -- nk_paged_decode_attn over lists of pages: token t of
+ * sequence b sees, with the G query heads of kv-head h, the keys at positions up
+ * to its own in the pages pages[b][t][h][0 .. pages_per_list - 1]
+ * (nk_page_select's, or any others: in any order; entries that are negative or
+ * past the token's own page name none; a page listed twice counts twice). A row
+ * that sees no key is zeros. Only listed pages are read, and only their
+ * block-table entries. A list is scanned up to as many entries as the token sees
+ * pages, so put the ones that name no page behind the others.
+ * Other arguments, checks, device flags, ordering and ownership as
+ * nk_paged_decode_attn; the workspace holds nk_decode_workspace_bytes(B * T, 1,
+ * ...) bytes. B * T is at most 1,024, G 48.
+ */
+int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
+                         int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, const int32_t* pages_dev,
+                         int32_t pages_per_list, int32_t B, int32_t T, int32_t num_q_heads, float sm_scale,
+                         int32_t max_ctx, int32_t num_ctas, void* workspace_dev, size_t workspace_bytes, void* out_dev,
+                         int32_t* status_dev, void* stream);
+
+/*
+ * nk_page_weights -- the attention weight each page draws: of page i of sequence
+ * b and kv-head h, the sum over the T query columns, the G query heads and the
+ * page's keys of the softmax weights that nk_paged_decode_attn would give them
+ * (all pages of a sequence and kv-head: T * G). For a decode step T = 1; T up to
+ * 16 takes a prompt's last tokens as the witnesses of what it needs.
+ *   q_dev .. max_ctx  as nk_paged_decode_attn (the K half of the pool is read)
+ *   weights_dev    fp32 [num_pages][Hkv], written for the pages that the batch
+ *                  holds; every other entry stays as it was
+ *   prior_dev      fp32 [num_pages][Hkv] or NULL: earlier sums to add to (may be
+ *                  weights_dev itself, else must not overlap it)
+ *   seen_dev       int32 [B] or NULL: only pages that hold one of a sequence's
+ *                  first seen[b] tokens have an earlier sum; the others start
+ *                  here, whatever prior_dev holds (a page's last owner's). NULL:
+ *                  all have one.
+ *   workspace_dev  nk_page_weights_workspace_bytes(...) bytes, 16-byte aligned;
+ *                  scratch. Calls that may overlap on the GPU need one each.
+ * fp32 sums in a fixed order. An invalid context length sets NK_DEVFLAG_BAD_CTX,
+ * a page outside the pool NK_DEVFLAG_BAD_PAGE (it draws nothing). A page that
+ * several sequences hold gets the sum of one of them. A query that is not
+ * finite, or a visible key's scale, makes the weights its row touches NaN. The
+ * T * G rows of a kv-head must fit shared memory: NK_ERR_UNSUPPORTED past about
+ * 200 of them (head dim 256) to 400 (64).
+ */
+size_t nk_page_weights_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t page_size, int32_t max_ctx);
+int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
+                    int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, int32_t B, int32_t T, int32_t num_q_heads,
+                    float sm_scale, int32_t max_ctx, const float* prior_dev, const int32_t* seen_dev,
+                    void* workspace_dev, size_t workspace_bytes, float* weights_dev, int32_t* status_dev,
+                    void* stream);
+
+/*
+ * nk_evict_pages -- cuts sequences back to keep_pages pages: those with the
+ * largest weight, summed over the kv-heads (exactly: of equal sums the lower
+ * page stays), and in any case the first sink_pages and the last recent_pages
+ * (>= 1, so every page that goes is full; together at most keep_pages). The kept
+ * pages keep their order, so the cache's other calls go on with the new table
+ * and length; keys keep the rotary positions they were appended with.
+ *   weights_dev    fp32 [num_pages][Hkv] (nk_page_weights); NaN ranks last
+ *   block_table_dev, out_table_dev  int32 [B][max_pages_per_seq], at most 16,384
+ *                  wide; may be the same buffer, else must not overlap. Entries
+ *                  behind the kept pages that held one become -1, others are
+ *                  copied.
+ *   ctx_lens_dev   int32 [B]; new_ctx_dev int32 [B]: ctx - P * pages that went
+ *                  (not ctx_lens_dev itself)
+ *   freed_dev      int32 [max_freed]: the pages that went, sequence after
+ *                  sequence, ascending in each; entries behind stay as they were
+ *   num_freed_dev  int32 [1]: how many. More than max_freed set
+ *                  NK_DEVFLAG_NO_PAGES; the first max_freed are written.
+ * A length that is negative or past the table sets NK_DEVFLAG_BAD_CTX: new_ctx
+ * is 0 and the sequence's row of the output table stays as it was. A page id
+ * outside the pool sets NK_DEVFLAG_BAD_PAGE, weighs 0 and, where it goes, is
+ * listed as -1. B is at most 1,024.
+ */
+int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, const float* weights_dev,
+                   const int32_t* block_table_dev, int32_t* out_table_dev, int32_t max_pages_per_seq,
+                   const int32_t* ctx_lens_dev, int32_t B, int32_t keep_pages, int32_t sink_pages,
+                   int32_t recent_pages, int32_t* new_ctx_dev, int32_t* freed_dev, int32_t max_freed,
+                   int32_t* num_freed_dev, int32_t* status_dev, void* stream);
+
+/*
+ * nk_verify_drafts -- the end of a verify round of T = draft + 1 columns: how
+ * many of each sequence's drafted tokens stand, and the token that follows them,
+ * so that the tokens are distributed as the target's own.
+ *   target_dev     fp32 [B][T][vocab]: the target's probabilities after each
+ *                  column; rows target_row_stride >= vocab elements apart
+ *   draft_dev      fp32 [B][T - 1][vocab]: those each draft was drawn from, rows
+ *                  draft_row_stride apart; NULL: the drafts were certain (1 at
+ *                  the draft)
+ *   drafts_dev     int32 [B][T - 1]
+ *   num_drafts_dev int32 [B] or NULL: drafts of each sequence, 0 .. T - 1 (NULL:
+ *                  T - 1); the columns behind are not read
+ *   uniforms_dev   fp32 [B][T], each in [0, 1): u[t] decides on draft t, u[T - 1]
+ *                  draws the token
+ *   tokens_dev     int32 [B][T]: the accepted drafts, the token drawn, -1 behind
+ *   accepted_dev   int32 [B]: accepted drafts a
+ *   ctx_lens_dev, next_start_dev  int32 [B] or NULL: next_start = ctx - drafts +
+ *                  a, the cache rows that stand and so the start_pos of the next
+ *                  step (ctx counts the round's columns; may be one buffer)
+ * Draft t with token x is accepted when u[t] * q_t(x) < p_t(x) (exact) and all
+ * before it were. The token is the lowest i with r_0 + .. + r_i > u[T - 1] * R:
+ * r = max(p_a - q_a, 0), each difference rounded to fp32, where a draft was
+ * refused, and p_a where none was left or nothing is left of that; R the sum of
+ * r. The sums are whole multiples of 2^-62: the same in every run. NaN and
+ * negative weights count as 0, those above 1 as 1; a row without any, or whose
+ * sum is 2 or more, sets NK_DEVFLAG_RANGE and token -1. A draft outside the
+ * vocabulary sets NK_DEVFLAG_BAD_TOKEN and is refused, a count outside 0 .. T - 1
+ * NK_DEVFLAG_BAD_POS and is clamped; uniforms outside [0, 1) draw as the nearest
+ * inside. T is at most 16, vocab 2^30, B 65,535.
+ */
+int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const float* draft_dev,
+                     int64_t draft_row_stride, const int32_t* drafts_dev, const int32_t* num_drafts_dev,
+                     const float* uniforms_dev, int32_t B, int32_t T, int32_t vocab, const int32_t* ctx_lens_dev,
+                     int32_t* tokens_dev, int32_t* accepted_dev, int32_t* next_start_dev, int32_t* status_dev,
+                     void* stream);
 
 /* Same contract and result, computed by the fp32 CUDA-core kernel that the
  * tensor-core path is measured against. */

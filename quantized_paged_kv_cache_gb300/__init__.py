@@ -21,6 +21,7 @@ NK_DEVFLAG_BAD_CTX = 0x4
 NK_DEVFLAG_TIMEOUT = 0x8
 NK_DEVFLAG_RANGE = 0x10
 NK_DEVFLAG_NO_PAGES = 0x20
+NK_DEVFLAG_BAD_TOKEN = 0x40
 GROUP = 64
 MAX_T = 16
 
@@ -31,6 +32,8 @@ __all__ = [
     "rk8v4_decode_attn", "i8f16_chunk_bytes", "i8f16_pool_bytes", "i8f16_append", "i8f16_decode_attn",
     "bf16kv_chunk_bytes", "bf16kv_pool_bytes", "bf16kv_append", "bf16kv_decode_attn", "test_inject_copy_stall", "paged_prefill_attn",
     "step_tables", "mrope", "paged_window_attn", "chunk_workspace_bytes", "paged_chunk_attn",
+    "PageBounds", "page_bounds_bytes", "page_bounds", "page_select_workspace_bytes", "page_select", "paged_sparse_attn",
+    "page_weights_workspace_bytes", "page_weights", "evict_pages", "verify_drafts",
 ]
 
 
@@ -631,3 +634,264 @@ def paged_chunk_attn(pool: KVPool, q, cu_q, block_table, ctx_lens, sm_scale: flo
                                    workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_paged_chunk_attn")
     return out
+
+
+def page_bounds_bytes(num_pages: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().nk_page_bounds_bytes(num_pages, num_kv_heads, head_dim))
+
+
+@dataclass
+class PageBounds:
+    """The caller-owned bounds of a pool's keys: ``storage`` is a uint8 CUDA
+    tensor of ``page_bounds_bytes(...)`` bytes, codes [page][kv-head][hi, lo][D]
+    int8 followed by scales [page][kv-head] fp32 (nk_page_bounds)."""
+
+    storage: "object"
+    num_pages: int
+    num_kv_heads: int
+    head_dim: int
+
+    @classmethod
+    def empty(cls, pool: KVPool):
+        """Bounds for ``pool``, all zeros."""
+        import torch
+
+        n = page_bounds_bytes(pool.num_pages, pool.num_kv_heads, pool.head_dim)
+        return cls(torch.zeros(n, dtype=torch.uint8, device=pool.storage.device), pool.num_pages, pool.num_kv_heads,
+                   pool.head_dim)
+
+    def _codes_bytes(self) -> int:
+        return self.num_pages * self.num_kv_heads * 2 * self.head_dim
+
+    def codes(self):
+        """int8 [num_pages][Hkv][2][D], a view."""
+        import torch
+
+        n = self._codes_bytes()
+        return self.storage[:n].view(torch.int8).view(self.num_pages, self.num_kv_heads, 2, self.head_dim)
+
+    def scales(self):
+        """fp32 [num_pages][Hkv], a view."""
+        import torch
+
+        n = self._codes_bytes()
+        return self.storage[n:n + 4 * self.num_pages * self.num_kv_heads].view(torch.float32).view(
+            self.num_pages, self.num_kv_heads)
+
+    def values(self):
+        """fp32 [num_pages][Hkv][2][D]: the largest and smallest values that the codes stand for."""
+        return self.codes() * self.scales()[..., None, None]
+
+    def _check(self) -> None:
+        if self.storage.numel() * self.storage.element_size() < self._codes_bytes() + 4 * self.num_pages * self.num_kv_heads:
+            raise ValueError("the bounds' storage is smaller than page_bounds_bytes(...)")
+
+
+def page_bounds(pool: KVPool, bounds: PageBounds, block_table, start_pos, cu_new, status=None, stream=None) -> None:
+    """The bounds of the pages that a step's new rows fall in, after their
+    kv_append (nk_page_bounds); block_table, start_pos and cu_new as there."""
+    import torch
+
+    _need(torch.int32, block_table, start_pos, cu_new, status)
+    _need_scratch(pool.storage, bounds.storage)
+    pool.need("int8")
+    bounds._check()
+    if (bounds.num_pages, bounds.num_kv_heads, bounds.head_dim) != (pool.num_pages, pool.num_kv_heads, pool.head_dim):
+        raise ValueError("the bounds are of another pool's shape")
+    B, shape = start_pos.numel(), block_table.shape
+    if len(shape) != 2 or shape[0] != B or cu_new.numel() != B + 1:
+        raise ValueError("start_pos and block_table hold one entry (row) per sequence, cu_new one more")
+    rc = lib().nk_page_bounds(pool._struct(), bounds.storage.data_ptr(), block_table.data_ptr(), shape[1],
+                              start_pos.data_ptr(), cu_new.data_ptr(), B, _ptr(status), _stream(stream))
+    _check(rc, "nk_page_bounds")
+
+
+def page_select_workspace_bytes(B: int, T: int, num_kv_heads: int, page_size: int, max_ctx: int) -> int:
+    return int(lib().nk_page_select_workspace_bytes(B, T, num_kv_heads, page_size, max_ctx))
+
+
+def _small(what: str, *numbers_) -> None:
+    if not all(-_I32_MAX <= n <= _I32_MAX for n in numbers_):
+        raise ValueError(f"{what} must be below 2^31")
+
+
+def page_select(bounds: PageBounds, q, block_table, ctx_lens, page_size: int, max_ctx: int, k: int, sink_pages: int = 1,
+                recent_pages: int = 1, workspace=None, out=None, status=None, stream=None):
+    """The ``k`` pages of each query token and kv-head whose bounds promise the
+    largest scores (nk_page_select): ``q`` bf16 [B][T][Hq][D]; returns int32
+    [B][T][Hkv][k], ascending, -1 behind the last."""
+    import torch
+
+    _need(torch.bfloat16, q)
+    _need(torch.int32, block_table, ctx_lens, out, status)
+    _need_scratch(bounds.storage, workspace)
+    bounds._check()
+    _small("page_size, max_ctx, k, sink_pages and recent_pages", page_size, max_ctx, k, sink_pages, recent_pages)
+    B, T, Hq, D = q.shape
+    Hkv, shape = bounds.num_kv_heads, block_table.shape
+    if D != bounds.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
+        raise ValueError("q, block_table, ctx_lens and the bounds disagree on the batch or the head dim")
+    if out is None:
+        out = _empty(stream, block_table, (B, T, Hkv, max(k, 0)), torch.int32)
+    elif out.numel() != B * T * Hkv * k:
+        raise ValueError("out must be [B][T][kv-heads][k]")
+    if workspace is None:
+        wbytes = lib().nk_page_select_workspace_bytes(B, T, Hkv, page_size, max_ctx)
+        workspace = _empty(stream, q, max(wbytes, 16), torch.uint8)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_page_select(bounds.storage.data_ptr(), bounds.num_pages, page_size, Hkv, D, q.data_ptr(),
+                              block_table.data_ptr(), shape[1], ctx_lens.data_ptr(), B, T, Hq, max_ctx, k, sink_pages,
+                              recent_pages, workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
+    _check(rc, "nk_page_select")
+    return out
+
+
+def paged_sparse_attn(pool: KVPool, q, block_table, ctx_lens, pages, sm_scale: float, max_ctx: int, num_ctas: int = 0,
+                      workspace=None, out=None, status=None, stream=None):
+    """Decode / verify attention over the listed ``pages`` int32 [B][T][Hkv][k]
+    of each query token and kv-head (nk_paged_sparse_attn; page_select makes
+    such lists); returns out bf16 [B][T][Hq][D]."""
+    import torch
+
+    _need(torch.bfloat16, q, out)
+    _need(torch.int32, block_table, ctx_lens, pages, status)
+    _need_scratch(pool.storage, workspace)
+    pool.need("int8")
+    _small("max_ctx and num_ctas", max_ctx, num_ctas)
+    B, T, Hq, D = q.shape
+    shape, lists, Hkv = block_table.shape, pages.shape, pool.num_kv_heads
+    if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
+        raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
+    if len(lists) != 4 or lists[:3] != (B, T, Hkv):
+        raise ValueError("pages must be [B][T][kv-heads][pages]")
+    if out is None:
+        out = _empty(stream, q, q.shape)
+    elif out.numel() != q.numel():
+        raise ValueError("out must have the shape of q")
+    if workspace is None:
+        wbytes = max(lib().nk_decode_workspace_bytes(B * T, 1, Hq, Hkv, D, num_ctas), 256)
+        workspace = _empty(stream, q, wbytes, torch.uint8)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_paged_sparse_attn(pool._struct(), q.data_ptr(), block_table.data_ptr(), shape[1], ctx_lens.data_ptr(),
+                                    pages.data_ptr(), lists[3], B, T, Hq, sm_scale, max_ctx, num_ctas,
+                                    workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
+    _check(rc, "nk_paged_sparse_attn")
+    return out
+
+
+def page_weights_workspace_bytes(B: int, T: int, num_q_heads: int, num_kv_heads: int, page_size: int,
+                                 max_ctx: int) -> int:
+    return int(lib().nk_page_weights_workspace_bytes(B, T, num_q_heads, num_kv_heads, page_size, max_ctx))
+
+
+def page_weights(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, max_ctx: int, weights, prior=None, seen=None,
+                 workspace=None, status=None, stream=None):
+    """The attention weight that each page of the batch draws from ``q`` bf16
+    [B][T][Hq][D], added to ``prior`` (nk_page_weights): ``weights`` fp32
+    [num_pages][Hkv] is written for the batch's pages and returned; pass it as
+    ``prior`` too to accumulate in place, with ``seen`` int32 [B] the tokens that
+    earlier calls covered."""
+    import torch
+
+    _need(torch.bfloat16, q)
+    _need(torch.float32, weights, prior)
+    _need(torch.int32, block_table, ctx_lens, seen, status)
+    _need_scratch(pool.storage, workspace)
+    pool.need("int8")
+    _small("max_ctx", max_ctx)
+    B, T, Hq, D = q.shape
+    shape, Hkv = block_table.shape, pool.num_kv_heads
+    if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
+        raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
+    if seen is not None and seen.numel() != B:
+        raise ValueError("seen must hold one count per sequence")
+    for t in (weights, prior):
+        if t is not None and t.shape != (pool.num_pages, Hkv):
+            raise ValueError("weights and prior must be [num_pages][kv-heads]")
+    if workspace is None:
+        wbytes = lib().nk_page_weights_workspace_bytes(B, T, Hq, Hkv, pool.page_size, max_ctx)
+        workspace = _empty(stream, q, max(wbytes, 16), torch.uint8)
+    else:
+        wbytes = workspace.numel() * workspace.element_size()
+    rc = lib().nk_page_weights(pool._struct(), q.data_ptr(), block_table.data_ptr(), shape[1], ctx_lens.data_ptr(), B, T,
+                               Hq, sm_scale, max_ctx, _ptr(prior), _ptr(seen), workspace.data_ptr(), wbytes,
+                               weights.data_ptr(), _ptr(status), _stream(stream))
+    _check(rc, "nk_page_weights")
+    return weights
+
+
+def evict_pages(page_size: int, weights, block_table, ctx_lens, keep_pages: int, new_ctx, freed, num_freed,
+                sink_pages: int = 1, recent_pages: int = 1, out=None, status=None, stream=None):
+    """Cuts sequences back to the ``keep_pages`` pages that drew the most
+    attention (nk_evict_pages): ``weights`` fp32 [num_pages][Hkv], the compacted
+    table in ``out`` (default: ``block_table`` itself, in place), ``new_ctx``
+    int32 [B], the pages given back in ``freed`` int32 and their count in
+    ``num_freed`` int32 [1]. Returns the table."""
+    import torch
+
+    if out is None:
+        out = block_table
+    _need(torch.float32, weights)
+    _need(torch.int32, block_table, ctx_lens, new_ctx, freed, num_freed, out, status)
+    _small("page_size, keep_pages, sink_pages and recent_pages", page_size, keep_pages, sink_pages, recent_pages)
+    _one(num_freed, "num_freed")
+    B, shape = ctx_lens.numel(), block_table.shape
+    if len(shape) != 2 or shape[0] != B or out.shape != shape or new_ctx.numel() != B or weights.dim() != 2:
+        raise ValueError("block_table, out, ctx_lens and new_ctx hold one row (entry) per sequence, weights are [num_pages][kv-heads]")
+    rc = lib().nk_evict_pages(page_size, weights.shape[0], weights.shape[1], weights.data_ptr(), block_table.data_ptr(),
+                              out.data_ptr(), shape[1], ctx_lens.data_ptr(), B, keep_pages, sink_pages, recent_pages,
+                              new_ctx.data_ptr(), freed.data_ptr(), min(freed.numel(), _I32_MAX), num_freed.data_ptr(),
+                              _ptr(status), _stream(stream))
+    _check(rc, "nk_evict_pages")
+    return out
+
+
+def _vocab_stride(t, what: str) -> int:
+    """Elements between the rows of [B][rows][vocab], which must all be the same distance apart."""
+    (b, r, v), (s0, s1, s2) = t.shape, t.stride()
+    if v > 1 and s2 != 1:
+        raise ValueError(f"the entries of a row of {what} must be consecutive")
+    row = s1 if r > 1 else (s0 if b > 1 else v)
+    if b > 1 and r > 0 and s0 != r * row:
+        raise ValueError(f"the rows of {what} must all be the same distance apart")
+    return row
+
+
+def verify_drafts(target, draft, drafts, uniforms, num_drafts=None, ctx_lens=None, next_start=None, tokens=None,
+                  accepted=None, status=None, stream=None):
+    """Accepts or replaces drafted tokens (nk_verify_drafts): ``target`` fp32
+    [B][T][vocab] and ``draft`` [B][T-1][vocab] (None: certain drafts) are
+    probabilities, ``drafts`` int32 [B][T-1], ``uniforms`` fp32 [B][T]. Returns
+    (tokens int32 [B][T], accepted int32 [B]); with ``ctx_lens`` int32 [B],
+    ``next_start`` int32 [B] gets the cache rows that stand."""
+    import torch
+
+    shape = target.shape
+    if len(shape) != 3 or shape[1] < 1 or (draft is not None and draft.shape != (shape[0], shape[1] - 1, shape[2])):
+        raise ValueError("target must be [B][T][vocab] and draft [B][T-1][vocab]")
+    B, T, V = shape
+    here = _here()
+    for t in (target, draft):
+        if t is not None and not (t.get_device() == here and t.dtype == torch.float32):
+            _refuse(t, here, torch.float32)
+    _need(torch.float32, uniforms)
+    _need(torch.int32, drafts, num_drafts, ctx_lens, next_start, tokens, accepted, status)
+    if drafts.numel() != B * (T - 1) or uniforms.numel() != B * T:
+        raise ValueError("drafts must be [B][T-1] and uniforms [B][T]")
+    for t in (num_drafts, ctx_lens, next_start, accepted):
+        if t is not None and t.numel() != B:
+            raise ValueError("num_drafts, ctx_lens, next_start and accepted hold one entry per sequence")
+    if tokens is None:
+        tokens = _empty(stream, drafts, (B, T), torch.int32)
+    elif tokens.numel() != B * T:
+        raise ValueError("tokens must be [B][T]")
+    if accepted is None:
+        accepted = _empty(stream, drafts, (B,), torch.int32)
+    rc = lib().nk_verify_drafts(target.data_ptr(), _vocab_stride(target, "target"), _ptr(draft),
+                                0 if draft is None else _vocab_stride(draft, "draft"), drafts.data_ptr(),
+                                _ptr(num_drafts), uniforms.data_ptr(), B, T, V, _ptr(ctx_lens), tokens.data_ptr(),
+                                accepted.data_ptr(), _ptr(next_start), _ptr(status), _stream(stream))
+    _check(rc, "nk_verify_drafts")
+    return tokens, accepted

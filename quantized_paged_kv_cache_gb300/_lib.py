@@ -70,6 +70,15 @@ EXPORTS = (
     "nk_paged_window_attn",
     "nk_chunk_workspace_bytes",
     "nk_paged_chunk_attn",
+    "nk_page_bounds_bytes",
+    "nk_page_bounds",
+    "nk_page_select_workspace_bytes",
+    "nk_page_select",
+    "nk_paged_sparse_attn",
+    "nk_page_weights_workspace_bytes",
+    "nk_page_weights",
+    "nk_evict_pages",
+    "nk_verify_drafts",
 )
 
 
@@ -131,6 +140,24 @@ def lib() -> ctypes.CDLL:
             L.nk_chunk_workspace_bytes.argtypes, L.nk_chunk_workspace_bytes.restype = [I32, I32], Z
             L.nk_paged_chunk_attn.argtypes = [pool_p, P, P, P, I32, P, I32, I32, I32, F, I32, I32, I32, I32, P, Z, P, P, P]
             L.nk_paged_chunk_attn.restype = ctypes.c_int
+            L.nk_page_bounds_bytes.argtypes, L.nk_page_bounds_bytes.restype = [I32, I32, I32], Z
+            L.nk_page_bounds.argtypes = [pool_p, P, P, I32, P, P, I32, P, P]
+            L.nk_page_bounds.restype = ctypes.c_int
+            L.nk_page_select_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+            L.nk_page_select_workspace_bytes.restype = Z
+            L.nk_page_select.argtypes = [P, I32, I32, I32, I32, P, P, I32, P, I32, I32, I32, I32, I32, I32, I32, P, Z, P, P,
+                                         P]
+            L.nk_page_select.restype = ctypes.c_int
+            L.nk_paged_sparse_attn.argtypes = [pool_p, P, P, I32, P, P, I32, I32, I32, I32, F, I32, I32, P, Z, P, P, P]
+            L.nk_paged_sparse_attn.restype = ctypes.c_int
+            L.nk_page_weights_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+            L.nk_page_weights_workspace_bytes.restype = Z
+            L.nk_page_weights.argtypes = [pool_p, P, P, I32, P, I32, I32, I32, F, I32, P, P, P, Z, P, P, P]
+            L.nk_page_weights.restype = ctypes.c_int
+            L.nk_evict_pages.argtypes = [I32, I32, I32, P, P, P, I32, P, I32, I32, I32, I32, P, P, I32, P, P, P]
+            L.nk_evict_pages.restype = ctypes.c_int
+            L.nk_verify_drafts.argtypes = [P, I64, P, I64, P, P, P, I32, I32, I32, P, P, P, P, P, P]
+            L.nk_verify_drafts.restype = ctypes.c_int
             L.nk_attn_combine.argtypes = [P, P, I32, I32, I32, P, P]
             L.nk_attn_combine.restype = ctypes.c_int
             L.nk_status_string.argtypes, L.nk_status_string.restype = [ctypes.c_int], ctypes.c_char_p

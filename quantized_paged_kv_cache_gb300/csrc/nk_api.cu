@@ -7,6 +7,7 @@
 
 #include "nk_chunk.cuh"
 #include "nk_decode.cuh"
+#include "nk_host.cuh"
 #include "nk_ptx.cuh"
 #include "nk_rk8v4.cuh"
 
@@ -18,26 +19,18 @@ cudaError_t launch_kv_append(int sms, const nk_kv_pool& pool, int fmt, const int
 
 using namespace nk;
 
-namespace {
+namespace nk {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// nk_test_inject_copy_stall: withheld CTA page number (-1: none) and wait limit (0: the default)
-std::atomic<int> g_withhold{-1};
-std::atomic<unsigned long long> g_wait_cycles{0};
-
-bool pool_ok(const nk_kv_pool* pool, int* err) {
-  if (!pool || !pool->base_dev) { *err = NK_ERR_NULL; return false; }
+int check_pool(const nk_kv_pool* pool) {
+  if (!pool || !pool->base_dev) return NK_ERR_NULL;
   const int P = pool->page_size, D = pool->head_dim;
   if (pool->num_pages < 1 || pool->num_kv_heads < 1 || P < 16 || P > 256 || P % 16 != 0 ||
-      !(D == 64 || D == 128 || D == 256) || !aligned(pool->base_dev, 16)) {
-    *err = NK_ERR_SHAPE;
-    return false;
-  }
-  return true;
+      !(D == 64 || D == 128 || D == 256) || (reinterpret_cast<uintptr_t>(pool->base_dev) & 15) != 0)
+    return NK_ERR_SHAPE;
+  return NK_OK;
 }
 
-int sm_count() {
+int device_sms() {
   static std::atomic<int> cached[64];  // per device; 0 = not looked up yet
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) { (void)cudaGetLastError(); return 0; }
@@ -49,6 +42,23 @@ int sm_count() {
   if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+}  // namespace nk
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// nk_test_inject_copy_stall: withheld CTA page number (-1: none) and wait limit (0: the default)
+std::atomic<int> g_withhold{-1};
+std::atomic<unsigned long long> g_wait_cycles{0};
+
+bool pool_ok(const nk_kv_pool* pool, int* err) {
+  *err = check_pool(pool);
+  return *err == NK_OK;
+}
+
+int sm_count() { return device_sms(); }
 
 // The longest run of one kv-head's keys a CTA of the mma.sync decode kernels
 // may take: 4,096 pages of 64 keys measured 4.4e-4 to 7.0e-4 relative L2
@@ -206,6 +216,8 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   p.window = window;
   p.sinks = sinks;
   p.sink_pages = (int)(((int64_t)sinks + P - 1) / P);
+  p.lists = nullptr;
+  p.entries = p.tokens = 0;
   p.q = reinterpret_cast<const uint16_t*>(q);
   p.bt = bt;
   p.max_pages = max_pages;
@@ -442,6 +454,72 @@ int nk_paged_window_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
                                  Path::kWindow, &p, &empty, window, sinks < max_ctx ? sinks : max_ctx);
   if (err != NK_OK || empty) return err;
   return launch_decode(p, Path::kWindow, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
+                         int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, const int32_t* pages_dev,
+                         int32_t pages_per_list, int32_t B, int32_t T, int32_t num_q_heads, float sm_scale,
+                         int32_t max_ctx, int32_t num_ctas, void* workspace_dev, size_t workspace_bytes, void* out_dev,
+                         int32_t* status_dev, void* stream) {
+  const int err = check_pool(pool);
+  if (err != NK_OK) return err;
+  if (B < 0 || T < 1 || T > NK_MAX_T || num_q_heads < 1 || pages_per_list < 1) return NK_ERR_SHAPE;
+  if (B == 0) return NK_OK;
+  if (!q_dev || !block_table_dev || !ctx_lens_dev || !pages_dev || !out_dev) return NK_ERR_NULL;
+  const int Hkv = pool->num_kv_heads, D = pool->head_dim, P = pool->page_size;
+  if (num_q_heads % Hkv != 0) return NK_ERR_SHAPE;
+  const int G = num_q_heads / Hkv;
+  const int64_t tokens = (int64_t)B * T;
+  if (tokens > kMaxBatch || !decode_lists_supported(D, G, P)) return NK_ERR_UNSUPPORTED;
+  if (max_pages_per_seq < 1 || max_ctx < T || (int64_t)max_ctx > (int64_t)max_pages_per_seq * P) return NK_ERR_SHAPE;
+  if (!isfinite(sm_scale) || !aligned(q_dev, 16) || !aligned(out_dev, 16)) return NK_ERR_SHAPE;
+  DecodeParams p = {};
+  p.pool = reinterpret_cast<const uint8_t*>(pool->base_dev);
+  p.num_pages = pool->num_pages;
+  p.P = P;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.lay = layout_of(kFmtI8F32, P, D);
+  p.fmt = kFmtI8F32;
+  p.q = reinterpret_cast<const uint16_t*>(q_dev);
+  p.bt = block_table_dev;
+  p.max_pages = max_pages_per_seq;
+  p.ctx = ctx_lens_dev;
+  p.B = (int)tokens;  // a unit is one token's rows of one kv-head
+  p.T = p.qT = 1;
+  p.Hq = num_q_heads;
+  p.G = G;
+  p.sm_scale = sm_scale;
+  p.scale2 = sm_scale * kLog2e;
+  p.max_ctx = max_ctx;
+  p.lists = pages_dev;
+  p.entries = pages_per_list;
+  p.tokens = T;
+  const int64_t all = ((int64_t)max_ctx + P - 1) / P, unit = pages_per_list < all ? pages_per_list : all;
+  const int32_t keys = (int32_t)(unit * P < max_ctx ? unit * P : max_ctx);
+  int32_t n = num_ctas > 0 ? num_ctas : default_ctas(p.B, Hkv, keys, P, 1);
+  // as many CTAs as divide evenly over the units, as for windows (above)
+  const int64_t units = tokens * Hkv;
+  if (num_ctas <= 0) {
+    const int64_t even = units <= n ? n / units * units : 0;
+    if (5 * even >= 4 * (int64_t)n) n = (int32_t)even;
+  }
+  const int64_t per_cta = (units * unit + n - 1) / n;
+  if ((per_cta < unit ? per_cta : unit) * P > kMaxMmaRunKeys) return NK_ERR_UNSUPPORTED;
+  const size_t need = nk_decode_workspace_bytes(p.B, 1, num_q_heads, Hkv, D, n);
+  if (!workspace_dev || workspace_bytes < need || !aligned(workspace_dev, 16)) return NK_ERR_WORKSPACE;
+  p.n_ctas = n;
+  p.part_o = reinterpret_cast<float*>(workspace_dev);
+  p.part_lse = p.part_o + ((int64_t)n + units) * G * D;
+  p.out = reinterpret_cast<uint16_t*>(out_dev);
+  p.status = status_dev;
+  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
+  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
+  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_decode_mma(p, st);
+  if (e == cudaSuccess) e = launch_decode_combine(p, st);
+  return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
 size_t nk_rk8v4_chunk_bytes(int32_t page_size, int32_t head_dim) {

@@ -118,13 +118,13 @@ __device__ __forceinline__ void merge_row(int S, LseFn lse_of, RowFn row_of, uin
 // written directly by that CTA; the others merge the partial slots c + u of
 // the CTAs c their pages span (CTAs with an empty range wrote nothing).
 // Block = one (unit, row) and a slice of C channels.
-// WIN: the units' pages are those of a sliding window with sinks.
-template <int D, int C, bool WIN>
+// KEYS: which pages the units own.
+template <int D, int C, int KEYS>
 __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const DecodeParams p) {
   static_assert(D % C == 0, "whole slices");
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int warp_tot[8];
-  const auto sh = p.shape_of<WIN>();
+  const auto sh = p.shape_of<KEYS>();
   // The page prefix runs before the wait for the split kernel: this kernel
   // only ever follows the split kernel of the same call, which could start
   // only once its own predecessor had passed its wait (that predecessor is
@@ -160,18 +160,18 @@ __global__ void __launch_bounds__(kCombThreads) decode_combine_kernel(const Deco
   merge_row<C>(c1 - c0 + 1, lse_of, row_of, p.out + (((int64_t)b * p.qT + t) * p.Hq + h * p.G + hg) * D + c_off);
 }
 
-// The same for windows whose units span few CTAs: a warp per row, a lane for
+// The same for windows and lists whose units span few CTAs: a warp per row, a lane for
 // its channels (D / 32 of them), partial after partial. A block per row merges
 // with most of its threads idle then, and a batch's rows need several rounds of
 // blocks, each with the page prefix to form first; here eight rows share one.
-template <int D>
-__global__ void __launch_bounds__(kCombThreads) window_combine_kernel(const DecodeParams p) {
+template <int D, int KEYS>
+__global__ void __launch_bounds__(kCombThreads) short_combine_kernel(const DecodeParams p) {
   constexpr int V = D < 128 ? 2 : 4;  // channels of a load
   constexpr int NL = D / (32 * V);    // loads of a lane and partial
   constexpr int U = 4;                // partials in flight
   __shared__ int pre[kMaxBatch + 1];
   __shared__ int warp_tot[8];
-  const auto sh = p.shape_of<true>();
+  const auto sh = p.shape_of<KEYS>();
   block_page_prefix_short<true>(sh, p.ctx, p.trim, pre, warp_tot);  // before the wait, as above
   chain_wait();
   chain_release();
@@ -262,22 +262,29 @@ constexpr int kSliceRows = 256;
 // span of 10: 14.6 -> 14.0; one sequence, a span of 38: 12.1 -> 21.5).
 constexpr int kRowWarpSpan = 12;
 
-template <int D, bool WIN>
+template <int D, int KEYS>
 static cudaError_t launch_combine_w(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
   const dim3 b(kCombThreads);
   if (D > 64 && rows < kSliceRows)
-    return launch_chained(decode_combine_kernel<D, 64, WIN>, dim3((unsigned)(rows * (D / 64))), b, 0, stream, p);
-  return launch_chained(decode_combine_kernel<D, D, WIN>, dim3((unsigned)rows), b, 0, stream, p);
+    return launch_chained(decode_combine_kernel<D, 64, KEYS>, dim3((unsigned)(rows * (D / 64))), b, 0, stream, p);
+  return launch_chained(decode_combine_kernel<D, D, KEYS>, dim3((unsigned)rows), b, 0, stream, p);
+}
+
+template <int D, int KEYS>
+static cudaError_t launch_combine_short(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
+  if (p.n_ctas <= (int64_t)kRowWarpSpan * p.B * p.Hkv) {
+    const int64_t per = kCombThreads / 32;
+    return launch_chained(short_combine_kernel<D, KEYS>, dim3((unsigned)((rows + per - 1) / per)), dim3(kCombThreads),
+                          0, stream, p);
+  }
+  return launch_combine_w<D, KEYS>(p, rows, stream);
 }
 
 template <int D>
 static cudaError_t launch_combine_d(const DecodeParams& p, int64_t rows, cudaStream_t stream) {
-  if (p.window > 0 && p.n_ctas <= kRowWarpSpan * p.B * p.Hkv) {
-    const int64_t per = kCombThreads / 32;
-    return launch_chained(window_combine_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kCombThreads), 0,
-                          stream, p);
-  }
-  return p.window > 0 ? launch_combine_w<D, true>(p, rows, stream) : launch_combine_w<D, false>(p, rows, stream);
+  if (p.lists) return launch_combine_short<D, kKeysLists>(p, rows, stream);
+  if (p.window > 0) return launch_combine_short<D, kKeysWindow>(p, rows, stream);
+  return launch_combine_w<D, kKeysAll>(p, rows, stream);
 }
 
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {

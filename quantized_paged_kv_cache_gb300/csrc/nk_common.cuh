@@ -196,6 +196,33 @@ __device__ __forceinline__ int pages_of_len(const WindowShape& s, int L) {
   return all - first + lead;
 }
 
+// The same split over lists of pages: a "sequence" here is one query token bt =
+// b * tokens + t of sequence b, and a unit owns as many pages as its list has
+// entries that can name one, min(entries, pages the token sees). Its page
+// number i is entry i of the list.
+struct SparseShape : SplitShape {
+  int entries, tokens;
+};
+
+__device__ __forceinline__ int pages_of_len(const SparseShape& s, int L) {
+  if (L < 1) return 0;
+  const int all = (L - 1) / s.P + 1;
+  return all < s.entries ? all : s.entries;
+}
+
+// Length of sequence b of a shape: its context, for a token of a list the keys
+// that it sees (0 where the sequence's length is invalid).
+template <bool kL2Only, class Shape>
+__device__ __forceinline__ int len_of(const Shape& s, const int32_t* ctx_lens, int trim, int b) {
+  return (kL2Only ? __ldcg(ctx_lens + b) : ctx_lens[b]) - trim;
+}
+template <bool kL2Only>
+__device__ __forceinline__ int len_of(const SparseShape& s, const int32_t* ctx_lens, int, int bt) {
+  const int b = bt / s.tokens, L = kL2Only ? __ldcg(ctx_lens + b) : ctx_lens[b];
+  if (L < s.tokens || L > s.max_ctx || (int64_t)L > (int64_t)s.max_pages * s.P) return 0;
+  return L - s.tokens + (bt - b * s.tokens) + 1;
+}
+
 // Quotient of two numbers that are not negative. They nearly always fit 32
 // bits, where a division costs a tenth of the 64-bit one's hundreds of cycles;
 // several stand in the prologue of every decode kernel.
@@ -233,7 +260,7 @@ __device__ __forceinline__ void block_page_prefix(const Shape& s, const int32_t*
   for (int i = 0; i < 4; ++i) {
     const int b = tid * 4 + i;
     int L = 0;
-    if (b < s.B) L = (kL2Only ? __ldcg(ctx_lens + b) : ctx_lens[b]) - trim;
+    if (b < s.B) L = len_of<kL2Only>(s, ctx_lens, trim, b);
     v[i] = (b < s.B) ? pages_of_len(s, L) : 0;
     if (lens && b < s.B) lens[b] = L;
     sum += v[i];
@@ -277,7 +304,7 @@ __device__ __forceinline__ void block_page_prefix_short(const Shape& s, const in
   if (!one_warp || wid == 0) {
     int v = 0;
     if (tid < s.B) {
-      const int L = (kL2Only ? __ldcg(ctx_lens + tid) : ctx_lens[tid]) - trim;
+      const int L = len_of<kL2Only>(s, ctx_lens, trim, tid);
       v = pages_of_len(s, L);
       if (lens) lens[tid] = L;
     }

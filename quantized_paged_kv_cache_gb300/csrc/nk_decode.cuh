@@ -5,6 +5,10 @@
 
 namespace nk {
 
+// The keys a query sees: all of its context, a sliding window with sinks, or
+// the pages of a list.
+enum Keys : int { kKeysAll = 0, kKeysWindow = 1, kKeysLists = 2 };
+
 struct DecodeParams {
   const uint8_t* pool;
   int num_pages, P, Hkv, D;
@@ -37,6 +41,10 @@ struct DecodeParams {
   int fmt;  // KvFmt of the pool (the rk8v4 kernel ignores it)
   int window, sinks;  // sliding window and sinks (window 0: the whole context)
   int sink_pages;     // ceil(sinks / P)
+  // Lists of pages (nk_paged_sparse_attn; NULL: none): [B][Hkv][entries] logical
+  // pages, where B counts query tokens (`tokens` of each sequence; T is 1).
+  const int32_t* lists;
+  int entries, tokens;
   // Failure-detection tests (nk_test_inject_copy_stall): every bounded wait
   // gives up after wait_cycles, and the page copies of CTA page numbers
   // >= withhold are never issued (-1: all issued).
@@ -52,9 +60,17 @@ struct DecodeParams {
     s.sink_pages = sink_pages;
     return s;
   }
-  template <bool WIN>
+  __host__ __device__ SparseShape sparse_shape() const {
+    SparseShape s;
+    static_cast<SplitShape&>(s) = shape();
+    s.entries = entries;
+    s.tokens = tokens;
+    return s;
+  }
+  template <int KEYS>
   __host__ __device__ auto shape_of() const {
-    if constexpr (WIN) return window_shape();
+    if constexpr (KEYS == kKeysWindow) return window_shape();
+    else if constexpr (KEYS == kKeysLists) return sparse_shape();
     else return shape();
   }
 };
@@ -62,9 +78,10 @@ struct DecodeParams {
 // Flag invalid ctx lengths once (block 0 of a kernel).
 __device__ __forceinline__ void flag_bad_ctx(const DecodeParams& p) {
   if (blockIdx.x != 0) return;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+  const int n = p.lists ? p.B / p.tokens : p.B, T = p.lists ? p.tokens : p.T;
+  for (int b = threadIdx.x; b < n; b += blockDim.x) {
     const int L = p.ctx[b] - p.trim;
-    if (L < p.T || L > p.max_ctx || (int64_t)L > (int64_t)p.max_pages * p.P) flag(p.status, NK_DEVFLAG_BAD_CTX);
+    if (L < T || L > p.max_ctx || (int64_t)L > (int64_t)p.max_pages * p.P) flag(p.status, NK_DEVFLAG_BAD_CTX);
   }
 }
 
@@ -81,5 +98,6 @@ cudaError_t launch_attn_combine(const float* part_o, const float* part_lse, int 
 int decode_simt_ctas_per_sm(int D, int G);
 int decode_mma_ctas_per_sm(int D, int T, int G);
 bool decode_mma_supported(int fmt, int D, int T, int G, int P);
+bool decode_lists_supported(int D, int G, int P);
 
 }  // namespace nk

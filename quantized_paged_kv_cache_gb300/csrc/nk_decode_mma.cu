@@ -100,6 +100,7 @@ cudaError_t launch_d256(const CUtensorMap& map, const DecodeParams& p, int NT, c
 cudaError_t launch_d128(const CUtensorMap& map, const DecodeParams& p, int NT, cudaStream_t st);
 cudaError_t launch_d64(const CUtensorMap& map, const DecodeParams& p, int NT, cudaStream_t st);
 cudaError_t launch_window(const CUtensorMap& map, const DecodeParams& p, int NT, cudaStream_t st);
+cudaError_t launch_lists(const CUtensorMap& map, const DecodeParams& p, int NT, cudaStream_t st);
 cudaError_t launch_rk(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p, int NT, cudaStream_t st);
 
 }  // namespace mma
@@ -131,6 +132,7 @@ cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return mma::launch_rk(map, mapv, p, NT, stream);
   }
+  if (p.lists) return mma::launch_lists(map, p, NT, stream);
   if (p.window > 0) return mma::launch_window(map, p, NT, stream);
   if (p.D == 256) return mma::launch_d256(map, p, NT, stream);
   if (p.D == 128) return mma::launch_d128(map, p, NT, stream);

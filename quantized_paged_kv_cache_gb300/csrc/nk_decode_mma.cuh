@@ -120,9 +120,9 @@ __host__ __device__ inline int ring_unit(int nteams, int bpp) {
 
 // Shared-memory plan. Needs the pool format, D, NT, CS, P (and B for the
 // prefix array). A bf16 pool stages 2-byte K|V values and no scales. With a
-// window the accumulators have an area of their own where the ring keeps more
+// window (or lists, which are as short) the accumulators have an area of their own where the ring keeps more
 // than eight stages beside it (small pages).
-__host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int P, int B, bool win = false) {
+__host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int P, int B, int keys = kKeysAll) {
   Geometry g;
   const int nteams = kConsumerWarps / CS;
   // rk8v4: D key bytes and D / 2 value bytes per key, fp16 scales per 64
@@ -134,7 +134,8 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   g.xch_bytes = CS > 1 ? nteams * 2 * CS * NT * 4 * 32 * 4 : 0;
   const int mrows = NT * 8;
   g.merge_bytes = mrows * (D + 4) * 4 + 3 * nteams * mrows * 4 + mrows * 4;
-  const int pid_bytes = 1024 * 4;
+  const bool win = keys != kKeysAll;
+  const int pid_bytes = 1024 * 4 * (keys == kKeysLists ? 2 : 1);
   const int base = g.xch_bytes + g.merge_bytes + pid_bytes + 1024;
   const int park_bytes = nteams * mrows * (D + 4) * 4;
   int s = 0, pre_bytes = 0;
@@ -394,6 +395,33 @@ __device__ __forceinline__ int page_coord(const DecodeParams& p, const SplitShap
   return page_coord(p, sh, pre, x_begin, q);
 }
 
+// The same over lists of pages; `logical`: the entry's page in the sequence, -1
+// (and coordinate -2: nothing to load) where it names none that the token sees.
+__device__ __forceinline__ int page_coord(const DecodeParams& p, const SparseShape& sh, const int* pre, const int* lens,
+                                          int64_t x_begin, int q, int& logical) {
+  const int64_t x = x_begin + q;
+  int lo = 0, hi = sh.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)pre[mid] * sh.Hkv <= x) lo = mid; else hi = mid;
+  }
+  const int pages = pre[lo + 1] - pre[lo];
+  const int64_t off = x - (int64_t)pre[lo] * sh.Hkv;
+  const int h = (int)quot(off, pages), i = (int)(off - (int64_t)h * pages);
+  logical = __ldg(p.lists + ((int64_t)lo * sh.Hkv + h) * sh.entries + i);
+  if (logical < 0 || logical > (lens[lo] - 1) / sh.P) {
+    logical = -1;
+    return -2;
+  }
+  const int page = __ldg(p.bt + (int64_t)(lo / sh.tokens) * p.max_pages + logical);
+  return (page < 0 || page >= p.num_pages) ? -1 : page * p.Hkv + h;
+}
+__device__ __forceinline__ int page_coord(const DecodeParams& p, const SparseShape& sh, const int* pre, const int* lens,
+                                          int64_t x_begin, int q) {
+  int logical;
+  return page_coord(p, sh, pre, lens, x_begin, q, logical);
+}
+
 // Load the CTA's page number q into its stage: TMA boxes of the K|V codes
 // plus bulk copies of the two scale arrays, all completing on full_bar.
 template <int D, bool BF = false>
@@ -415,7 +443,7 @@ __device__ __forceinline__ void issue_page(const DecodeParams& p, const CUtensor
   const int kv_bytes = 2 * P * D;
   const int sc_bytes = P * (D / kGroup) * scale_bytes(p.fmt);
   if (z < 0) {
-    flag(p.status, NK_DEVFLAG_BAD_PAGE);
+    if (z == -1) flag(p.status, NK_DEVFLAG_BAD_PAGE);
     mbar_arrive(fb);  // release the consumers; the stage keeps stale data
     return;
   }
@@ -467,12 +495,16 @@ __device__ __forceinline__ void issue_page_rk(const DecodeParams& p, const CUten
 // WIN: sliding window with sinks. The units' pages are the visible ones
 // (WindowShape), blocks that straddle an end of the window or the sinks are
 // masked per column, blocks no column sees are passed over.
-template <int D, int NT, int CS, int FMT, bool WIN = false>
+// LISTS: the units' pages are the entries of lists (SparseShape); entries that
+// name no visible page are passed over.
+// SHORT: either of them.
+template <int D, int NT, int CS, int FMT, int KEYS = kKeysAll>
 __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                  const __grid_constant__ CUtensorMap tmapv,
                                                                  const DecodeParams p) {
   constexpr bool BF = FMT == kFmtBf16;
   constexpr bool RK = FMT == kFmtRk8v4;
+  constexpr bool WIN = KEYS == kKeysWindow, LISTS = KEYS == kKeysLists, SHORT = KEYS != kKeysAll;
   static_assert(!RK || D >= 128, "rk8v4: head_dim 128 or 256");
   // the tensor map is a launch parameter (no earlier kernel writes it): its
   // descriptor fetch can start before the wait for the previous kernel
@@ -493,17 +525,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const Geometry geo = geometry(FMT, D, NT, CS, p.P, p.B, WIN);
+  const Geometry geo = geometry(FMT, D, NT, CS, p.P, p.B, KEYS);
   const int S = geo.stages;
   constexpr int sb = (FMT == kFmtI8F16 || RK) ? 2 : 4;
   int* pre = reinterpret_cast<int*>(smem + geo.pre_off);
   int* warp_tot = pre + (p.B + 1);
   volatile int* abort_flag = pre + (p.B + 1) + 8;
-  const int ms = WIN ? geo.max_stages : kStagesWhole;
+  const int ms = SHORT ? geo.max_stages : kStagesWhole;
   int* cnt = pre + (p.B + 1) + 9;  // [ms] consumer count per stage
   int* lens = cnt + ms;            // [B] context lengths
   int* icnt = lens + p.B;          // [ms] copies issued into each stage
   int* pid = reinterpret_cast<int*>(smem + geo.pid_off);
+  int* lpid = pid + kPidCache;  // LISTS: the entries' logical pages
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + geo.bar_off);
   uint64_t* empty_bar = full_bar + ms;
   float* xch = reinterpret_cast<float*>(smem + geo.xch_off);
@@ -514,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = p.P, BPP = P / 16;
   const int per_stage = BPP * CS;  // consumer-warp arrivals per page
-  const auto sh = p.shape_of<WIN>();
+  const auto sh = p.shape_of<KEYS>();
 
   if (tid < S) {
     mbar_init(smem_u32(&full_bar[tid]), 1);
@@ -530,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   chain_release();
   flag_bad_ctx(p);
   // (both end with __syncthreads)
-  if constexpr (WIN) block_page_prefix_short(sh, p.ctx, p.trim, pre, warp_tot, lens);
+  if constexpr (SHORT) block_page_prefix_short(sh, p.ctx, p.trim, pre, warp_tot, lens);
   else block_page_prefix(sh, p.ctx, p.trim, pre, warp_tot, lens);
 
   const int64_t W = (int64_t)pre[p.B] * p.Hkv;
@@ -785,21 +818,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   bool have = next_segment(sh, pre, x, x_end, seg);
   if (have) fetch_q(seg);
   const int ncache = total < kPidCache ? total : kPidCache;
-  for (int q = tid; q < ncache; q += kThreads) pid[q] = page_coord(p, sh, pre, lens, x_begin, q);
+  for (int q = tid; q < ncache; q += kThreads) {
+    if constexpr (LISTS) pid[q] = page_coord(p, sh, pre, lens, x_begin, q, lpid[q]);
+    else pid[q] = page_coord(p, sh, pre, lens, x_begin, q);
+  }
   if (have) stage_q();
   __syncthreads();
   if (p.early) chain_wait();  // the pages may hold the preceding append's rows
   // The first S pages, issued in order by one thread (the copy unit then
   // completes page 0 first). Each issue waits until the unit accepts the
   // copy, so the issuer is the last warp, whose first block is in page 1.
-  // WIN: with many small pages (or few in all) the issue itself is what the
+  // SHORT: with many small pages (or few in all) the issue itself is what the
   // start waits for, and the lanes of four warps share it: 64 sequences with
   // windows of 1,000 on 16-key pages 32.5 -> 27.3 us, 8 with 3,000 on 128-key
   // pages 15.9 -> 14.5. With a ring of few large pages and more to come they
   // would all land late together (8 windows of 8,192 on 64-key pages 46.4 us in
   // order, 47.7 shared out).
   const int n0 = total < S ? total : S;
-  const bool shared_out = WIN && (S > 8 || total <= S);
+  const bool shared_out = SHORT && (S > 8 || total <= S);
   constexpr int kIssuers = 4;
   if (shared_out ? warp >= kConsumerWarps - kIssuers : tid == kThreads - 32) {
     const int q0 = shared_out ? lane * kIssuers + warp % kIssuers : 0, step = shared_out ? 32 * kIssuers : 1;
@@ -868,6 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
       const int kb = jn - q * BPP;                           // block in page
       int pi = seg.page_begin + (q - seg_first);
       if constexpr (WIN) pi += pi >= lead ? gap : 0;
+      if constexpr (LISTS) {
+        if (q < kPidCache) pi = lpid[q];
+        else (void)page_coord(p, sh, pre, lens, x_begin, q, pi);
+      }
       while (q_cur < q) {  // stage and phase of page q, advanced without a division
         ++q_cur;
         if (++s_cur == S) {
@@ -904,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
         const int pos0 = pi * P + key0;  // sequence position of the block's key 0
         bool seen = pos0 < L;
         // the first column's window starts after L - T - window
+        if constexpr (LISTS) seen = seen && pi >= 0;
         if constexpr (WIN) seen = seen && (pos0 + 15 > L - T - sh.window || pos0 < sh.sinks);
         if (seen) {
           // ---- QK: per-group fp32 partial dot products (GW*NT independent accumulators)
@@ -1320,10 +1361,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
     // After the CTA's last segment the stage ring is idle (every issued page
     // has been consumed), so each team can park its accumulator there and one
     // pass merges them; otherwise the teams add into mo one after another
-    // (WIN: unless the ring leaves an area to park them in at any time: 64
+    // (SHORT: unless the ring leaves an area to park them in at any time: 64
     // sequences, most with windows of 1,000 on 16-key pages, 45.7 -> 40.6 us).
     constexpr int kSlot = MROWS * (D + 4);
-    const bool own_area = WIN && geo.park_off >= 0;
+    const bool own_area = SHORT && geo.park_off >= 0;
     const bool parked = own_area || (last_seg && (size_t)NTEAMS * kSlot * 4 <= (size_t)S * geo.stage_bytes);
     float* const park = reinterpret_cast<float*>(smem + (own_area ? geo.park_off : 0));
     float* acc_buf = parked ? park + team * kSlot : mo;

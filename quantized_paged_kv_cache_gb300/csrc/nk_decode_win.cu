@@ -10,12 +10,12 @@ namespace mma {
 
 template <int D, int NT, int CS>
 static cudaError_t launch_w(const CUtensorMap& map, const DecodeParams& p, cudaStream_t st) {
-  const Geometry geo = geometry(kFmtI8F32, D, NT, CS, p.P, p.B, true);
+  const Geometry geo = geometry(kFmtI8F32, D, NT, CS, p.P, p.B, kKeysWindow);
   if (geo.stages < 2 || geo.total > kSmemLimit) return cudaErrorInvalidConfiguration;
   cudaError_t e =
-      set_smem_limit(reinterpret_cast<const void*>(decode_mma_kernel<D, NT, CS, kFmtI8F32, true>), geo.total);
+      set_smem_limit(reinterpret_cast<const void*>(decode_mma_kernel<D, NT, CS, kFmtI8F32, kKeysWindow>), geo.total);
   if (e != cudaSuccess) return e;
-  return launch_chained(decode_mma_kernel<D, NT, CS, kFmtI8F32, true>, dim3(p.n_ctas), dim3(kThreads), geo.total, st,
+  return launch_chained(decode_mma_kernel<D, NT, CS, kFmtI8F32, kKeysWindow>, dim3(p.n_ctas), dim3(kThreads), geo.total, st,
                         map, map, p);
 }
 

@@ -1,0 +1,601 @@
+// nk_select.cu -- which pages of a long cache a query attends to: the pages'
+// bounds (nk_page_bounds) and the choice by them (nk_page_select).
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "nk_common.cuh"
+#include "nk_host.cuh"
+#include "nk_topk.cuh"
+
+namespace nk {
+
+// ---------------------------------------------------------------------------
+// Bounds. Of each page and kv-head: hi[d] and lo[d], the largest and smallest
+// value fp32(code * scale) that key channel d takes in the page's filled slots,
+// as INT8 codes of one scale s = fp32(max(|hi|, |lo|) / 127), by the rounding of
+// the cache's own rows. No query's score over the page is above
+//   sum_d max(q_d hi_d, q_d lo_d) = sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d,
+// but for the codes' rounding.
+//   codes [num_pages][Hkv][hi | lo][D] int8, then scales [num_pages][Hkv] fp32.
+// ---------------------------------------------------------------------------
+struct BoundsView {
+  uint8_t* codes;
+  float* scales;
+};
+__host__ __device__ inline BoundsView bounds_view(void* base, int64_t num_pages, int Hkv, int D) {
+  uint8_t* b = reinterpret_cast<uint8_t*>(base);
+  return BoundsView{b, reinterpret_cast<float*>(b + num_pages * Hkv * 2 * D)};
+}
+
+// ---------------------------------------------------------------------------
+// nk_page_bounds: the touched pages of a step (those that a new row falls in),
+// from the codes that its append wrote. Every block forms the prefix of the
+// sequences' touched pages itself and takes (page, kv-head) items in turns; a
+// block goes over an item's keys, 16 bytes of a row a thread, each thread the
+// extremes of its 16 channels, merged by shuffles and through shared memory.
+//
+// Bounded by the K codes' and scales' bytes for prompts, by latency for a step
+// of single tokens (lengths, table, codes, then two block reductions).
+// ---------------------------------------------------------------------------
+struct BoundsParams {
+  const uint8_t* pool;
+  ChunkLayout lay;
+  int num_pages, P, Hkv;
+  const int32_t* bt;
+  int max_pages;
+  const int32_t* start;
+  const int32_t* cu;
+  int B;
+  BoundsView out;
+  int32_t* status;
+};
+
+constexpr int kBndThreads = 256, kBndWarps = kBndThreads / 32;
+constexpr int kBndLoads = 4;  // rows of a thread in flight
+
+template <int D>
+__global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsParams p) {
+  constexpr int LPR = D / 16;                 // threads of a row
+  constexpr int RPB = kBndThreads / LPR;      // rows at once
+  constexpr int GR = D / kGroup;
+  __shared__ int pre[kMaxBatch + 1];          // touched pages before sequence b
+  __shared__ int warp_tot[kBndWarps];
+  __shared__ __align__(16) float hi_s[kBndWarps][D], lo_s[kBndWarps][D];
+  __shared__ float top_s[kBndWarps];
+  chain_wait();
+  chain_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = p.P;
+  {
+    constexpr int PER = kMaxBatch / kBndThreads;
+    int v[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = tid * PER + i;
+      v[i] = 0;
+      if (b < p.B) {
+        const int64_t s = p.start[b], n = (int64_t)p.cu[b + 1] - p.cu[b];
+        if (s < 0 || n < 0 || s + n > (int64_t)p.max_pages * P || s + n > 0x7fffffff) {
+          if (blockIdx.x == 0) flag(p.status, NK_DEVFLAG_BAD_POS);
+        } else if (n > 0) {
+          v[i] = (int)((s + n + P - 1) / P - s / P);
+        }
+      }
+      sum += v[i];
+    }
+    int total;
+    int run = block_exclusive<kBndThreads>(sum, warp_tot, total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = tid * PER + i;
+      if (b < p.B) pre[b] = run;
+      run += v[i];
+    }
+    if (tid == 0) pre[p.B] = total;
+    __syncthreads();
+  }
+  const int64_t items = (int64_t)pre[p.B] * p.Hkv;
+  for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
+    const int k = (int)(x / p.Hkv), h = (int)(x - (int64_t)k * p.Hkv);
+    int b = 0, top = p.B;
+    while (top - b > 1) {
+      const int mid = (b + top) >> 1;
+      if (pre[mid] <= k) b = mid; else top = mid;
+    }
+    const int start = p.start[b];
+    const int64_t end = (int64_t)start + (p.cu[b + 1] - p.cu[b]);
+    const int logical = start / P + (k - pre[b]);
+    const int page = p.bt[(int64_t)b * p.max_pages + logical];
+    if (page < 0 || page >= p.num_pages) {  // (block-uniform)
+      if (tid == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+      continue;
+    }
+    const int64_t left = end - (int64_t)logical * P;
+    const int filled = left < P ? (int)left : P;
+    const uint8_t* chunk = p.pool + ((int64_t)page * p.Hkv + h) * p.lay.chunk;
+    const float* scales = reinterpret_cast<const float*>(chunk + p.lay.ks);
+    const int c0 = (tid % LPR) * 16;
+    float hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      hi[i] = -INFINITY;
+      lo[i] = INFINITY;
+    }
+    bool odd = false;
+    for (int r0 = tid / LPR; r0 < filled; r0 += RPB * kBndLoads) {
+      uint4 w[kBndLoads];
+      float sc[kBndLoads];
+#pragma unroll
+      for (int j = 0; j < kBndLoads; ++j) {
+        const int r = r0 + j * RPB;
+        w[j] = make_uint4(0, 0, 0, 0);
+        sc[j] = 0.f;
+        if (r < filled) {
+          w[j] = *reinterpret_cast<const uint4*>(chunk + (int64_t)r * D + c0);
+          sc[j] = scales[r * GR + c0 / kGroup];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBndLoads; ++j) {
+        if (r0 + j * RPB >= filled) continue;
+        float s = sc[j];
+        if (!(fabsf(s) < INFINITY)) {  // counts as zeros
+          odd = true;
+          s = 0.f;
+        }
+        const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float v = (float)(int8_t)(u[i / 4] >> (8 * (i & 3))) * s;
+          hi[i] = fmaxf(hi[i], v);
+          lo[i] = fminf(lo[i], v);
+        }
+      }
+    }
+    if (odd) flag(p.status, NK_DEVFLAG_RANGE);
+    // the rows of a warp share channels: lanes LPR apart
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      }
+    if (lane < LPR) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        *reinterpret_cast<float4*>(&hi_s[warp][c0 + i]) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+        *reinterpret_cast<float4*>(&lo_s[warp][c0 + i]) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+      }
+    }
+    __syncthreads();
+    float h1 = 0.f, l1 = 0.f;
+    if (tid < D) {
+      h1 = hi_s[0][tid];
+      l1 = lo_s[0][tid];
+#pragma unroll
+      for (int w2 = 1; w2 < kBndWarps; ++w2) {
+        h1 = fmaxf(h1, hi_s[w2][tid]);
+        l1 = fminf(l1, lo_s[w2][tid]);
+      }
+    }
+    float m = fmaxf(fabsf(h1), fabsf(l1));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) top_s[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w2 = 0; w2 < kBndWarps; ++w2) m = fmaxf(m, top_s[w2]);
+    float s = __fdiv_rn(m, 127.f);
+    if (s == 0.f) s = 1.f;
+    const int64_t rec = (int64_t)page * p.Hkv + h;
+    if (tid < D) {
+      uint8_t* dst = p.out.codes + rec * 2 * D + tid;
+      dst[0] = (uint8_t)(int8_t)fminf(fmaxf(rintf(__fdiv_rn(h1, s)), -127.f), 127.f);
+      dst[D] = (uint8_t)(int8_t)fminf(fmaxf(rintf(__fdiv_rn(l1, s)), -127.f), 127.f);
+    }
+    if (tid == 0) p.out.scales[rec] = s;
+    __syncthreads();  // (hi_s, top_s: the next item's)
+  }
+}
+
+// ---------------------------------------------------------------------------
+// nk_page_select, first kernel: the pages' scores. With one scale s_q for a
+// token's rows of a kv-head, q8 = clamp(rint(q / s_q)), page scale s:
+//   score = s * max over the G rows of sum_d max(q8_d, 0) hi_d + min(q8_d, 0) lo_d
+// (s_q > 0 orders nothing). The sum is a whole number below 127 * 127 * 256 <
+// 2^22, so fp16 operands with fp32 sums give it exactly on the tensor cores, and
+// its product with s is one 64-bit product: two scores never change places by
+// rounding.
+//
+// A warp takes 16 pages (the M of mma.m16n8k16; the token's rows are N) straight
+// from global memory: a page's record is 2 D consecutive bytes, and a thread
+// holds 16 consecutive channels of a group of 64, which in the product's K order
+// are four steps of four. The rows stay in shared memory as fp16 whole numbers;
+// their positive and negative parts are taken at the fragment. Bounded by the
+// records' bytes, for one sequence by latency.
+// ---------------------------------------------------------------------------
+struct SelectParams {
+  BoundsView bounds;
+  int64_t num_pages;
+  int Hkv, G;
+  const uint16_t* q;  // bf16 [B][T][Hq][D]
+  const int32_t* bt;
+  int max_pages;
+  const int32_t* ctx;
+  int B, T, P, max_ctx, k, sinks, recent;
+  int cols;           // tokens of a chunk of rows
+  uint64_t* scores;   // [B][T][Hkv][stride]
+  int64_t stride;     // pages of the longest context
+  int32_t* out;       // [B][T][Hkv][k]
+  int32_t* status;
+};
+
+__device__ __forceinline__ int select_len(const SelectParams& p, int b) {  // 0: refused
+  const int L = p.ctx[b];
+  return L < p.T || L > p.max_ctx || (int64_t)L > (int64_t)p.max_pages * p.P ? 0 : L;
+}
+
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kSelRows = 64;  // query rows of a chunk, at most
+
+__device__ __forceinline__ uint32_t sel_prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// two int8 codes (biased by ^ 0x80808080) as an exact fp16 pair
+__device__ __forceinline__ uint32_t sel_f16(uint32_t biased, uint32_t sel) {
+  const uint32_t h = sel_prmt(biased, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void sel_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_max0(uint32_t x) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), __halves2half2(__ushort_as_half(0), __ushort_as_half(0)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t half2_min0(uint32_t x) {
+  const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&x), __halves2half2(__ushort_as_half(0), __ushort_as_half(0)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Shared memory: rows [NT * 8][D / 2 + 2 words] fp16, then a warp's products [16][NT * 8 + 1] fp32.
+__host__ __device__ inline int select_smem(int D, int NT) {
+  return NT * 8 * (D * 2 + 8) + kSelWarps * 16 * (NT * 8 + 1) * 4;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectParams p) {
+  constexpr int ROWS = NT * 8;
+  constexpr int RS = D * 2 + 8;     // bytes of a row: 2 words past a multiple of 32, distinct banks for the fragments
+  constexpr int NC = D / 64;        // 64-channel parts of a record's half
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float top_s[kSelWarps];
+  chain_wait();
+  chain_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  const int t0 = blockIdx.z * p.cols, cols = min(p.cols, p.T - t0);
+  const int L = select_len(p, b);
+  if (L == 0) {
+    if (tid == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
+    return;
+  }
+  const int seen = (L - p.T + t0 + cols - 1) / p.P + 1;  // pages that the chunk's last token sees
+  if (seen <= p.k) return;                               // nothing to choose
+  const int blocks = (seen + 15) / 16, stride = gridDim.x * kSelWarps;
+  int blk = blockIdx.x * kSelWarps + warp;
+  // the first pages' records are on their way while the rows are made
+  uint4 rec[2][2][NC];  // [page g, g + 8][hi, lo][part]
+  float scale = 0.f;    // of page `lane`, lanes 0 to 15
+  bool there = true;
+  const auto load = [&](int bk) {
+    const int mine = bk * 16 + (lane & 15);
+    int page = -1;
+    there = true;
+    if (mine < seen) {
+      page = p.bt[(int64_t)b * p.max_pages + mine];
+      if (page < 0 || page >= p.num_pages) {
+        if (lane < 16) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+        page = -1;
+        there = false;
+      }
+    }
+    if (page >= 0) scale = p.bounds.scales[(int64_t)page * p.Hkv + h];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, g + 8 * i);
+      const uint4* src = reinterpret_cast<const uint4*>(p.bounds.codes + ((int64_t)(pg < 0 ? 0 : pg) * p.Hkv + h) * 2 * D);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) rec[i][s][c] = pg < 0 ? make_uint4(0, 0, 0, 0) : src[(s * D + 64 * c) / 16 + t4];
+    }
+  };
+  if (blk < blocks) load(blk);
+  // ---- the rows as whole numbers: a scale for each token
+  const int G = p.G, Hq = G * p.Hkv;
+  for (int i = tid; i < ROWS * (RS / 8); i += kSelThreads) reinterpret_cast<uint2*>(smem)[i] = make_uint2(0, 0);
+  __syncthreads();
+  for (int t = 0; t < cols; ++t) {
+    const uint16_t* src = p.q + ((int64_t)(b * p.T + t0 + t) * Hq + h * G) * D;  // G consecutive rows
+    float m = 0.f;
+    bool odd = false;
+    for (int i = tid; i < G * D / 8; i += kSelThreads) {
+      const uint4 v = *(reinterpret_cast<const uint4*>(src) + i);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = fabsf(bf16_lo(u[j])), c = fabsf(bf16_hi(u[j]));
+        odd |= !(a < INFINITY) || !(c < INFINITY);
+        m = fmaxf(m, fmaxf(a, c));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) top_s[warp] = m;
+    odd = __syncthreads_or(odd);
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) m = fmaxf(m, top_s[w]);
+    float s = __fdiv_rn(m, 127.f);
+    if (s == 0.f) s = 1.f;
+    if (!odd) {  // (rows that are not finite choose as zeros)
+      for (int i = tid; i < G * D / 8; i += kSelThreads) {
+        const uint4 v = *(reinterpret_cast<const uint4*>(src) + i);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(u[j]), s)), -127.f), 127.f);
+          const float c = fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(u[j]), s)), -127.f), 127.f);
+          const __half2 hh = __floats2half2_rn(a, c);
+          w[j] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        const int row = i / (D / 8), ch = (i % (D / 8)) * 8;
+        uint2* dst = reinterpret_cast<uint2*>(smem + (t * G + row) * RS + ch * 2);
+        dst[0] = make_uint2(w[0], w[1]);
+        dst[1] = make_uint2(w[2], w[3]);
+      }
+    }
+    __syncthreads();
+  }
+  float* prod = reinterpret_cast<float*>(smem + ROWS * RS) + warp * 16 * (ROWS + 1);
+  for (; blk < blocks; blk += stride) {  // (warp-uniform)
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a[2][4];  // [hi, lo]: rows g and g + 8 (pages), channels 4 j and 4 j + 2 of the thread's 16
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint4 r0 = rec[0][s][c], r1 = rec[1][s][c];
+          const uint32_t w0 = (j == 0 ? r0.x : j == 1 ? r0.y : j == 2 ? r0.z : r0.w) ^ 0x80808080u;
+          const uint32_t w1 = (j == 0 ? r1.x : j == 1 ? r1.y : j == 2 ? r1.z : r1.w) ^ 0x80808080u;
+          a[s][0] = sel_f16(w0, 0x4140);
+          a[s][1] = sel_f16(w1, 0x4140);
+          a[s][2] = sel_f16(w0, 0x4342);
+          a[s][3] = sel_f16(w1, 0x4342);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 q = *reinterpret_cast<const uint2*>(smem + (nt * 8 + g) * RS + (64 * c + 16 * t4 + 4 * j) * 2);
+          sel_mma(acc[nt], a[0][0], a[0][1], a[0][2], a[0][3], half2_max0(q.x), half2_max0(q.y));
+          sel_mma(acc[nt], a[1][0], a[1][1], a[1][2], a[1][3], half2_min0(q.x), half2_min0(q.y));
+        }
+      }
+    const float my_scale = scale;
+    const bool my_there = there;
+    const int base = blk * 16;
+    if (blk + stride < blocks) load(blk + stride);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) prod[(g + 8 * (k >> 1)) * (ROWS + 1) + nt * 8 + 2 * t4 + (k & 1)] = acc[nt][k];
+    __syncwarp();
+    // a lane keeps its page: 16 pages, two tokens at once
+    const int pg = lane & 15;
+    const double s = (double)my_scale;
+    if (base + pg < seen) {
+      for (int t = lane >> 4; t < cols; t += 2) {
+        const float* row = prod + pg * (ROWS + 1) + t * G;
+        float m = row[0];
+        for (int i = 1; i < G; ++i) m = fmaxf(m, row[i]);
+        double v = (double)m * s;
+        if (!my_there || !(fabs(v) < 1e300)) v = -1e300;  // no page, or bounds never made: last
+        p.scores[((int64_t)(b * p.T + t0 + t) * p.Hkv + h) * p.stride + base + pg] = ordered(v + 0.0);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Second kernel: of each (token, kv-head) the k pages, one block each. The first
+// `sinks` and the last `recent` pages that the token sees are always in; the
+// others by score (nk_topk.cuh). Keys are kept in shared memory where they fit.
+// ---------------------------------------------------------------------------
+constexpr int kPickThreads = 512;
+constexpr int kPickKeep = 16384;  // keys kept in shared memory, at most
+
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p, int room) {
+  extern __shared__ uint64_t keep[];
+  __shared__ TopSmem<kPickThreads> sm;
+  chain_wait();
+  chain_release();
+  const int tid = threadIdx.x;
+  const int bt = blockIdx.x / p.Hkv, b = bt / p.T, t = bt - b * p.T;
+  const int L = select_len(p, b);
+  if (L == 0) return;  // (flagged by the first kernel; the list is left as it was)
+  int32_t* out = p.out + (int64_t)blockIdx.x * p.k;
+  const int seen = (L - p.T + t) / p.P + 1;
+  if (seen <= p.k) {
+    for (int i = tid; i < p.k; i += kPickThreads) out[i] = i < seen ? i : -1;
+    return;
+  }
+  const int first = p.sinks, n = seen - p.sinks - p.recent, need = p.k - p.sinks - p.recent;  // need < n
+  for (int i = tid; i < p.sinks + p.recent; i += kPickThreads)
+    out[i < p.sinks ? i : i + need] = i < p.sinks ? i : seen - p.recent + (i - p.sinks);
+  if (need == 0) return;
+  const uint64_t* src = p.scores + (int64_t)blockIdx.x * p.stride + first;
+  const bool kept = n <= room;
+  if (kept) {
+    for (int i = tid; i < n; i += kPickThreads) keep[i] = __ldcg(src + i);
+    __syncthreads();
+  }
+  const uint64_t* keys = kept ? keep : src;
+  const auto key = [&](int i) { return keys[i]; };
+  uint64_t klo, khi, kt;
+  int it;
+  block_range<kPickThreads>(key, n, sm, klo, khi);
+  block_threshold<kPickThreads>(key, n, need, klo, khi, sm, kt, it);
+  const int per = top_run<kPickThreads>(n), a = tid * per, e = a + per < n ? a + per : n;
+  const auto taken = [&](int i) {
+    const uint64_t k = key(i);
+    return k > kt || (k == kt && i <= it);
+  };
+  int mine = 0, total;
+  for (int i = a; i < e; ++i) mine += taken(i);
+  int at = first + block_exclusive<kPickThreads>(mine, sm.warp, total);
+  for (int i = a; i < e; ++i)
+    if (taken(i)) out[at++] = first + i;
+}
+
+}  // namespace nk
+
+using namespace nk;
+
+namespace {
+
+template <int D, int NT>
+cudaError_t launch_scores(const SelectParams& p, dim3 grid, cudaStream_t st) {
+  const int smem = select_smem(D, NT);
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_score_kernel<D, NT>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(page_score_kernel<D, NT>, grid, dim3(kSelThreads), (size_t)smem, st, p);
+}
+
+template <int D>
+cudaError_t launch_scores_d(const SelectParams& p, int NT, dim3 grid, cudaStream_t st) {
+  switch (NT) {
+    case 1: return launch_scores<D, 1>(p, grid, st);
+    case 2: return launch_scores<D, 2>(p, grid, st);
+    case 3: return launch_scores<D, 3>(p, grid, st);
+    case 4: return launch_scores<D, 4>(p, grid, st);
+    case 5: case 6: return launch_scores<D, 6>(p, grid, st);
+    default: return launch_scores<D, 8>(p, grid, st);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nk_page_bounds_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t head_dim) {
+  if (num_pages < 1 || num_kv_heads < 1 || !(head_dim == 64 || head_dim == 128 || head_dim == 256)) return 0;
+  return (size_t)num_pages * num_kv_heads * (2 * (size_t)head_dim + 4);
+}
+
+int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                   const int32_t* start_pos_dev, const int32_t* cu_new_dev, int32_t B, int32_t* status_dev,
+                   void* stream) {
+  const int err = check_pool(pool);
+  if (err != NK_OK) return err;
+  if (B < 0 || max_pages_per_seq < 1) return NK_ERR_SHAPE;
+  if (B > kMaxBatch) return NK_ERR_UNSUPPORTED;
+  if (B == 0) return NK_OK;
+  if (!bounds_dev || !block_table_dev || !start_pos_dev || !cu_new_dev) return NK_ERR_NULL;
+  if (!aligned_to(bounds_dev, 16)) return NK_ERR_SHAPE;
+  const int P = pool->page_size, D = pool->head_dim;
+  const BoundsParams p{reinterpret_cast<const uint8_t*>(pool->base_dev), ChunkLayout::make(P, D), pool->num_pages, P,
+                       pool->num_kv_heads, block_table_dev, max_pages_per_seq, start_pos_dev, cu_new_dev, B,
+                       bounds_view(bounds_dev, pool->num_pages, pool->num_kv_heads, D), status_dev};
+  const int sms = device_sms();
+  int64_t grid = (int64_t)B * max_pages_per_seq * pool->num_kv_heads;
+  const int64_t most = (int64_t)(sms > 0 ? sms : 148) * 4;
+  if (grid > most) grid = most;
+  const dim3 g((unsigned)grid), t(kBndThreads);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 256   ? launch_chained(page_bounds_kernel<256>, g, t, 0, st, p)
+                        : D == 128 ? launch_chained(page_bounds_kernel<128>, g, t, 0, st, p)
+                                   : launch_chained(page_bounds_kernel<64>, g, t, 0, st, p);
+  return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
+}
+
+size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_kv_heads, int32_t page_size, int32_t max_ctx) {
+  if (B < 1 || T < 1 || T > NK_MAX_T || num_kv_heads < 1 || page_size < 1 || max_ctx < 1) return 0;
+  return (size_t)B * T * num_kv_heads * (((size_t)max_ctx + page_size - 1) / page_size) * 8;
+}
+
+int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                   const void* q_dev, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                   const int32_t* ctx_lens_dev, int32_t B, int32_t T, int32_t num_q_heads, int32_t max_ctx, int32_t k,
+                   int32_t sink_pages, int32_t recent_pages, void* workspace_dev, size_t workspace_bytes,
+                   int32_t* pages_dev, int32_t* status_dev, void* stream) {
+  if (num_pages < 1 || page_size < 1 || num_kv_heads < 1 || B < 0 || T < 1 || T > NK_MAX_T || num_q_heads < 1 ||
+      num_q_heads % num_kv_heads != 0 || !(head_dim == 64 || head_dim == 128 || head_dim == 256))
+    return NK_ERR_SHAPE;
+  if (k < 1 || sink_pages < 0 || recent_pages < 1 || (int64_t)sink_pages + recent_pages > k) return NK_ERR_SHAPE;
+  if (B == 0) return NK_OK;
+  if (!bounds_dev || !q_dev || !block_table_dev || !ctx_lens_dev || !pages_dev) return NK_ERR_NULL;
+  const int G = num_q_heads / num_kv_heads;
+  if (G > 48 || (int64_t)B * num_kv_heads > 65535) return NK_ERR_UNSUPPORTED;
+  if (max_pages_per_seq < 1 || max_ctx < T || (int64_t)max_ctx > (int64_t)max_pages_per_seq * page_size)
+    return NK_ERR_SHAPE;
+  if (!aligned_to(bounds_dev, 16) || !aligned_to(q_dev, 16)) return NK_ERR_SHAPE;
+  const size_t need = nk_page_select_workspace_bytes(B, T, num_kv_heads, page_size, max_ctx);
+  if (!workspace_dev || workspace_bytes < need || !aligned_to(workspace_dev, 16)) return NK_ERR_WORKSPACE;
+  SelectParams p = {};
+  p.bounds = bounds_view(const_cast<void*>(bounds_dev), num_pages, num_kv_heads, head_dim);
+  p.num_pages = num_pages;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.q = reinterpret_cast<const uint16_t*>(q_dev);
+  p.bt = block_table_dev;
+  p.max_pages = max_pages_per_seq;
+  p.ctx = ctx_lens_dev;
+  p.B = B;
+  p.T = T;
+  p.P = page_size;
+  p.max_ctx = max_ctx;
+  p.k = k;
+  p.sinks = sink_pages;
+  p.recent = recent_pages;
+  p.scores = reinterpret_cast<uint64_t*>(workspace_dev);
+  p.stride = ((int64_t)max_ctx + page_size - 1) / page_size;
+  p.out = pages_dev;
+  p.status = status_dev;
+  p.cols = kSelRows / G < 1 ? 1 : kSelRows / G;
+  if (p.cols > T) p.cols = T;
+  const int NT = (p.cols * G + 7) / 8;
+  const int64_t units = (int64_t)B * num_kv_heads;
+  const int sms = device_sms();
+  // eight warps of 16 pages a block; past four blocks an SM they take turns
+  int64_t gx = (p.stride + 16 * kSelWarps - 1) / (16 * kSelWarps), most = (int64_t)(sms > 0 ? sms : 148) * 4 / units;
+  if (most < 1) most = 1;
+  if (gx > most) gx = most;
+  const dim3 grid((unsigned)gx, (unsigned)units, (unsigned)((T + p.cols - 1) / p.cols));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = head_dim == 256   ? launch_scores_d<256>(p, NT, grid, st)
+                  : head_dim == 128 ? launch_scores_d<128>(p, NT, grid, st)
+                                    : launch_scores_d<64>(p, NT, grid, st);
+  if (e != cudaSuccess) return NK_ERR_CUDA;
+  const int room = (int)(p.stride < kPickKeep ? p.stride : kPickKeep);
+  e = set_smem_limit(reinterpret_cast<const void*>(page_pick_kernel), room * 8);
+  if (e != cudaSuccess) return NK_ERR_CUDA;
+  e = launch_chained(page_pick_kernel, dim3((unsigned)(units * T)), dim3(kPickThreads), (size_t)room * 8, st, p, room);
+  return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
+}
+
+}  // extern "C"

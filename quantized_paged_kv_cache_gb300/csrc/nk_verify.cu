@@ -1,0 +1,252 @@
+// nk_verify.cu -- the end of a verify round: drafted tokens accepted against
+// the target's probabilities, and the next token drawn (nk_verify_drafts).
+//
+// Draft t of a sequence, token x, is accepted when u_t q_t(x) < p_t(x), as far
+// as every one before it was; u_t q_t is exact in 64 bits. With a the number
+// accepted, the next token is drawn from r = max(p_a - q_a, 0) (each difference
+// rounded once to 32 bits) where draft a was refused, from p_a where none was
+// left: the lowest i with r_0 + .. + r_i > u R, R the sum of r. Such a sum over
+// a vocabulary does not survive 32 bits (a thousand tokens lie within its last
+// ones), and 64-bit floating point is slow on this chip. The r are summed as
+// whole multiples of 2^-62: exact to 2^-62 a token, in any order the same.
+//
+// One cluster a sequence, each CTA a slice of the vocabulary, each warp a part
+// of that: sums up, the slices' sums exchanged through distributed shared
+// memory, and the one part that the drawn number falls in is read again (from
+// L2) and summed ever finer: by 256 tokens a warp, then by 32, then by one.
+// Bounded by the two rows' bytes for many sequences, for few by latency: the
+// drafts, their probabilities, the rows, the exchange, the part again.
+#include <cooperative_groups.h>
+
+#include "nk_common.cuh"
+#include "nk_host.cuh"
+
+namespace nk {
+
+struct VerifyParams {
+  const float* p;
+  const float* q;  // may be NULL: the drafts are certain (q is 1 at the draft)
+  int64_t p_stride, q_stride;
+  const int32_t* drafts;  // [B][T-1]
+  const int32_t* num;     // [B] or NULL
+  const float* u;         // [B][T]
+  const int32_t* ctx;     // [B] or NULL
+  int T, V;
+  int32_t* tokens;    // [B][T]
+  int32_t* accepted;  // [B]
+  int32_t* next;      // [B] or NULL
+  int32_t* status;
+};
+
+constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
+constexpr int kVerUnroll = 8;
+constexpr float kVerOne = 4611686018427387904.f;  // 2^62: one, as a whole number
+constexpr uint64_t kVerCap = 0x7fffffffffffffffull;  // a sum of 2 or more ends here
+
+__device__ __forceinline__ uint64_t ver_add(uint64_t a, uint64_t b) {  // (both at most the cap)
+  const uint64_t s = a + b;
+  return s > kVerCap ? kVerCap : s;
+}
+__device__ __forceinline__ uint64_t ver_warp_sum(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = ver_add(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// r of one token; NaN and negative ones count as zero, more than one as one.
+__device__ __forceinline__ uint64_t ver_weight(float p, float q) {
+  return __float2ull_rz(fminf(fmaxf(p - q, 0.f), 1.f) * kVerOne);
+}
+
+template <int CL>
+__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams a) {
+  namespace cg = cooperative_groups;
+  __shared__ uint64_t part[kVerWarps];
+  __shared__ uint64_t slice[2][CL];  // [round]: the slices' sums
+  cg::cluster_group cluster = cg::this_cluster();
+  auto started = cluster.barrier_arrive();  // (awaited before the first write to another CTA's memory)
+  chain_wait();
+  chain_release();
+  const int rank = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int T = a.T, V = a.V;
+  // ---- the drafts, by every warp
+  int n = T - 1;
+  if (a.num) {
+    n = a.num[b];
+    if (n < 0 || n > T - 1) {
+      if (tid == 0 && rank == 0) flag(a.status, NK_DEVFLAG_BAD_POS);
+      n = n < 0 ? 0 : T - 1;
+    }
+  }
+  int x = -1;
+  bool good = false;
+  if (lane < n) {
+    x = a.drafts[(int64_t)b * (T - 1) + lane];
+    if (x >= 0 && x < V) {
+      const float px = a.p[((int64_t)b * T + lane) * a.p_stride + x];
+      const float qx = a.q ? a.q[((int64_t)b * (T - 1) + lane) * a.q_stride + x] : 1.f;
+      const float u = a.u[(int64_t)b * T + lane];
+      good = (double)u * (double)qx < (double)px;
+    } else if (rank == 0 && warp == 0) {
+      flag(a.status, NK_DEVFLAG_BAD_TOKEN);
+    }
+  }
+  const int acc = __ffs(~__ballot_sync(0xffffffffu, good)) - 1;  // (n <= 15: a lane is left)
+  const bool cut = acc < n;
+  const int refused = __shfl_sync(0xffffffffu, x, acc);
+  if (rank == 0 && warp == 0) {
+    if (lane < acc) a.tokens[(int64_t)b * T + lane] = x;
+    else if (lane > acc && lane < T) a.tokens[(int64_t)b * T + lane] = -1;
+    if (lane == 0) {
+      a.accepted[b] = acc;
+      if (a.next) a.next[b] = a.ctx[b] - n + acc;
+    }
+  }
+  // ---- the row
+  const float* prow = a.p + ((int64_t)b * T + acc) * a.p_stride;
+  const float* qrow = cut && a.q ? a.q + ((int64_t)b * (T - 1) + acc) * a.q_stride : nullptr;
+  int hole = cut && !a.q ? refused : -1;  // a certain draft that was refused
+  float uf = a.u[(int64_t)b * T + T - 1];
+  uf = fminf(fmaxf(uf, 0.f), 0.99999994f);
+  const uint64_t u64 = __float2ull_rz(uf * 18446744073709551616.f);
+  // parts of whole rounds: 32 lanes and kVerUnroll tokens each
+  const int per = (V + CL * kVerWarps - 1) / (CL * kVerWarps), step = (per + 31) / 32 * 32;
+  const auto begin_of = [&](int i) { return (int64_t)i * step < V ? i * step : V; };
+  const int lo = begin_of(rank * kVerWarps + warp), hi = begin_of(rank * kVerWarps + warp + 1);
+  const auto weight = [&](int i) {  // (i < V)
+    const float pv = i == hole ? 0.f : prow[i];
+    return ver_weight(pv, qrow ? qrow[i] : 0.f);
+  };
+  uint64_t total = 0, before = 0;  // of the row; of the slices before this one
+  for (int round = 0; round < 2; ++round) {
+    uint64_t sum = 0, over = 0;
+    int i = lo + lane;
+    for (; i + 32 * (kVerUnroll - 1) < hi; i += 32 * kVerUnroll) {
+      float pv[kVerUnroll], qv[kVerUnroll];
+#pragma unroll
+      for (int k = 0; k < kVerUnroll; ++k) pv[k] = prow[i + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kVerUnroll; ++k) qv[k] = qrow ? qrow[i + 32 * k] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kVerUnroll; ++k) {
+        // a token adds 2^62 at most, so a sum cannot pass 2^64 without bit 63 set once
+        sum += ver_weight(i + 32 * k == hole ? 0.f : pv[k], qv[k]);
+        over |= sum;
+      }
+    }
+    for (; i < hi; i += 32) {
+      sum += weight(i);
+      over |= sum;
+    }
+    if (over >> 63) sum = kVerCap;
+    sum = ver_warp_sum(sum);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (round == 0) cluster.barrier_wait(std::move(started));
+    if (warp == 0) {
+      uint64_t v = lane < kVerWarps ? part[lane] : 0;
+      v = ver_warp_sum(v);
+      if (lane < CL) *cluster.map_shared_rank(&slice[round][rank], lane) = v;
+    }
+    cluster.sync();
+    total = before = 0;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) {
+      if (c == rank) before = total;
+      total = ver_add(total, slice[round][c]);
+    }
+    // nothing left of p after q: the row itself (the same in every CTA)
+    if (total != 0 || !cut || round == 1) break;
+    qrow = nullptr;
+    hole = -1;
+  }
+  if (total == 0 || total == kVerCap) {  // no distribution
+    if (rank == 0 && tid == 0) {
+      a.tokens[(int64_t)b * T + acc] = -1;
+      flag(a.status, NK_DEVFLAG_RANGE);
+    }
+    return;
+  }
+  // ---- the token: the first whose sum passes u R, so the first above its whole part
+  const uint64_t want = __umul64hi(u64, total);
+  int w = -1;
+  uint64_t run = before;
+#pragma unroll
+  for (int k = 0; k < kVerWarps; ++k) {
+    if (w < 0) {
+      if (run + part[k] > want && run <= want) w = k;
+      else run += part[k];
+    }
+  }
+  if (w < 0) return;  // another slice's
+  // (block-uniform from here) the part's tokens, in runs of whole 32s, one a warp
+  const int plo = begin_of(rank * kVerWarps + w), phi = begin_of(rank * kVerWarps + w + 1);
+  const int len = (((phi - plo) + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;
+  const int a0 = plo + warp * len < phi ? plo + warp * len : phi, a1 = a0 + len < phi ? a0 + len : phi;
+  uint64_t sum = 0;
+#pragma unroll 8
+  for (int i = a0 + lane; i < a1; i += 32) sum += weight(i);
+  sum = ver_warp_sum(sum);
+  __syncthreads();  // part[] has been read
+  if (lane == 0) part[warp] = sum;
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) run += part[k];
+  if (!(run <= want && run + sum > want)) return;
+  for (int i0 = a0; i0 < a1; i0 += 32) {  // (warp-uniform)
+    const uint64_t v = i0 + lane < a1 ? weight(i0 + lane) : 0;
+    uint64_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, run + incl > want);
+    if (past) {
+      if (lane == 0) a.tokens[(int64_t)b * T + acc] = i0 + __ffs(past) - 1;
+      return;
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+}  // namespace nk
+
+using namespace nk;
+
+extern "C" {
+
+int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const float* draft_dev,
+                     int64_t draft_row_stride, const int32_t* drafts_dev, const int32_t* num_drafts_dev,
+                     const float* uniforms_dev, int32_t B, int32_t T, int32_t vocab, const int32_t* ctx_lens_dev,
+                     int32_t* tokens_dev, int32_t* accepted_dev, int32_t* next_start_dev, int32_t* status_dev,
+                     void* stream) {
+  if (B < 0 || T < 1 || T > NK_MAX_T || vocab < 1) return NK_ERR_SHAPE;
+  if (target_row_stride < vocab || (draft_dev && T > 1 && draft_row_stride < vocab)) return NK_ERR_SHAPE;
+  if (B > 65535 || vocab > (1 << 30)) return NK_ERR_UNSUPPORTED;
+  if (B == 0) return NK_OK;
+  if (!target_dev || !uniforms_dev || !tokens_dev || !accepted_dev || (T > 1 && !drafts_dev) ||
+      (next_start_dev && !ctx_lens_dev))
+    return NK_ERR_NULL;
+  // tokens and lengths are read by CTAs that others' results must not reach
+  if (tokens_dev == drafts_dev || tokens_dev == num_drafts_dev || accepted_dev == num_drafts_dev) return NK_ERR_SHAPE;
+  const VerifyParams p{target_dev, draft_dev, target_row_stride, draft_row_stride, drafts_dev, num_drafts_dev,
+                       uniforms_dev, ctx_lens_dev, T, vocab, tokens_dev, accepted_dev, next_start_dev, status_dev};
+  constexpr int CL = 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL, (unsigned)B);
+  cfg.blockDim = dim3(kVerThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<CL>, p);
+  return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
+}
+
+}  // extern "C"
