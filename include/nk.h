@@ -482,9 +482,8 @@ int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
  * fp32 sums in a fixed order. An invalid context length sets NK_DEVFLAG_BAD_CTX,
  * a page outside the pool NK_DEVFLAG_BAD_PAGE (it draws nothing). A page that
  * several sequences hold gets the sum of one of them. A query that is not
- * finite, or a visible key's scale, makes the weights its row touches NaN. The
- * T * G rows of a kv-head must fit shared memory: NK_ERR_UNSUPPORTED past about
- * 200 of them (head dim 256) to 400 (64).
+ * finite, or a visible key's scale, makes the weights its row touches NaN. B is at
+ * most 1,024, G 48.
  */
 size_t nk_page_weights_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
                                        int32_t page_size, int32_t max_ctx);

@@ -667,24 +667,27 @@ class PageBounds:
         """int8 [num_pages][Hkv][2][D], a view."""
         import torch
 
-        n = self._codes_bytes()
-        return self.storage[:n].view(torch.int8).view(self.num_pages, self.num_kv_heads, 2, self.head_dim)
+        n, h, d = self.num_pages, self.num_kv_heads, self.head_dim
+        return self.storage.view(torch.int8).as_strided((n, h, 2, d), (h * 2 * d, 2 * d, d, 1), 0)
+
+    def _scales(self, *ones):
+        import torch
+
+        n, h = self.num_pages, self.num_kv_heads
+        return self.storage.view(torch.float32).as_strided((n, h, *ones), (h, 1, *ones), self._codes_bytes() // 4)
 
     def scales(self):
         """fp32 [num_pages][Hkv], a view."""
-        import torch
-
-        n = self._codes_bytes()
-        return self.storage[n:n + 4 * self.num_pages * self.num_kv_heads].view(torch.float32).view(
-            self.num_pages, self.num_kv_heads)
+        return self._scales()
 
     def values(self):
         """fp32 [num_pages][Hkv][2][D]: the largest and smallest values that the codes stand for."""
-        return self.codes() * self.scales()[..., None, None]
+        return self.codes() * self._scales(1, 1)
 
     def _check(self) -> None:
-        if self.storage.numel() * self.storage.element_size() < self._codes_bytes() + 4 * self.num_pages * self.num_kv_heads:
-            raise ValueError("the bounds' storage is smaller than page_bounds_bytes(...)")
+        n = self.storage.numel()
+        if self.storage.element_size() != 1 or n % 4 != 0 or n < self._codes_bytes() + 4 * self.num_pages * self.num_kv_heads:
+            raise ValueError("the bounds' storage must be page_bounds_bytes(...) bytes (or more, in whole fours)")
 
 
 def page_bounds(pool: KVPool, bounds: PageBounds, block_table, start_pos, cu_new, status=None, stream=None) -> None:

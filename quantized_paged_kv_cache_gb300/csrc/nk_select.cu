@@ -30,12 +30,18 @@ __host__ __device__ inline BoundsView bounds_view(void* base, int64_t num_pages,
 // ---------------------------------------------------------------------------
 // nk_page_bounds: the touched pages of a step (those that a new row falls in),
 // from the codes that its append wrote. Every block forms the prefix of the
-// sequences' touched pages itself and takes (page, kv-head) items in turns; a
-// block goes over an item's keys, 16 bytes of a row a thread, each thread the
-// extremes of its 16 channels, merged by shuffles and through shared memory.
+// sequences' touched pages itself and takes (page, kv-head) items in turns.
 //
-// Bounded by the K codes' and scales' bytes for prompts, by latency for a step
-// of single tokens (lengths, table, codes, then two block reductions).
+// A thread reads 16 bytes of a row at a time and keeps the extremes of its 16
+// channels; D / 16 threads hold a row. With more items than blocks a warp takes
+// an item (no barrier, rows merged by shuffles); with fewer (a step of single
+// tokens) a block does, its warps' extremes merged through shared memory, so that
+// all of the item's bytes are on their way at once.
+//
+// Bounded by the K codes' and scales' bytes for prompts, by latency for a step of
+// single tokens (lengths, table, codes). Codes become fp32 by a byte permute (2^23
+// + 128 + code) and a packed subtraction: the conversion instruction takes an
+// eighth of their rate, and was the bound of the first form.
 // ---------------------------------------------------------------------------
 struct BoundsParams {
   const uint8_t* pool;
@@ -51,17 +57,92 @@ struct BoundsParams {
 };
 
 constexpr int kBndThreads = 256, kBndWarps = kBndThreads / 32;
-constexpr int kBndLoads = 4;  // rows of a thread in flight
+constexpr int kBndLoads = 8;  // rows of a thread in flight (of a whole warp's item)
+
+__device__ __forceinline__ uint32_t sel_prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// fp32(code * scale) of the four codes of w
+__device__ __forceinline__ void values4(uint32_t w, uint64_t scale2, float (&v)[4]) {
+  const uint64_t off = pack2(0xcb000080u, 0xcb000080u);  // -(2^23 + 128)
+  const uint32_t b = w ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t x = pack2(sel_prmt(b, 0x4b000000u, i == 0 ? 0x7440 : 0x7442),
+                             sel_prmt(b, 0x4b000000u, i == 0 ? 0x7441 : 0x7443));
+    const uint64_t y = mul2(add2(x, off), scale2);
+    v[2 * i] = __uint_as_float((uint32_t)y);
+    v[2 * i + 1] = __uint_as_float((uint32_t)(y >> 32));
+  }
+}
+
+// Extremes of rows r0, r0 + step, .. below `filled` at the thread's 16 channels;
+// true if a scale was not finite.
+template <int D, int LOADS>
+__device__ __forceinline__ bool row_extremes(const uint8_t* codes, const float* scales, int r0, int step, int filled,
+                                             float (&hi)[16], float (&lo)[16]) {
+  bool odd = false;
+  for (; r0 < filled; r0 += step * LOADS) {
+    uint4 w[LOADS];
+    float sc[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int r = min(r0 + j * step, filled - 1);  // (a row twice changes nothing)
+      w[j] = *reinterpret_cast<const uint4*>(codes + (int64_t)r * D);
+      sc[j] = scales[r * (D / kGroup)];
+    }
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      if (!(fabsf(sc[j]) < INFINITY)) {  // counts as zeros
+        odd = true;
+        sc[j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < LOADS; j += 2) {
+      const uint64_t s0 = pack2(__float_as_uint(sc[j]), __float_as_uint(sc[j]));
+      const uint64_t s1 = pack2(__float_as_uint(sc[j + 1]), __float_as_uint(sc[j + 1]));
+      const uint32_t u0[4] = {w[j].x, w[j].y, w[j].z, w[j].w}, u1[4] = {w[j + 1].x, w[j + 1].y, w[j + 1].z, w[j + 1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v0[4], v1[4];
+        values4(u0[i], s0, v0);
+        values4(u1[i], s1, v1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // (three-input extremes)
+          hi[4 * i + k] = fmaxf(hi[4 * i + k], fmaxf(v0[k], v1[k]));
+          lo[4 * i + k] = fminf(lo[4 * i + k], fminf(v0[k], v1[k]));
+        }
+      }
+    }
+  }
+  return odd;
+}
+
+__device__ __forceinline__ uint32_t bound_code(float x, float s) {
+  return (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f) & 0xffu;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsParams p) {
-  constexpr int LPR = D / 16;                 // threads of a row
-  constexpr int RPB = kBndThreads / LPR;      // rows at once
+  constexpr int LPR = D / 16;  // threads of a row
   constexpr int GR = D / kGroup;
-  __shared__ int pre[kMaxBatch + 1];          // touched pages before sequence b
+  __shared__ int pre[kMaxBatch + 1];  // touched pages before sequence b
   __shared__ int warp_tot[kBndWarps];
   __shared__ __align__(16) float hi_s[kBndWarps][D], lo_s[kBndWarps][D];
-  __shared__ float top_s[kBndWarps];
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,8 +176,12 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     __syncthreads();
   }
   const int64_t items = (int64_t)pre[p.B] * p.Hkv;
-  for (int64_t x = blockIdx.x; x < items; x += gridDim.x) {
-    const int k = (int)(x / p.Hkv), h = (int)(x - (int64_t)k * p.Hkv);
+  const bool wide = items <= gridDim.x;  // a block for each item
+  const int64_t first = wide ? blockIdx.x : (int64_t)blockIdx.x * kBndWarps + warp;
+  const int64_t stride = wide ? gridDim.x : (int64_t)gridDim.x * kBndWarps;
+  const int c0 = (lane % LPR) * 16;
+  for (int64_t x = first; x < items; x += stride) {  // (uniform over the item's threads)
+    const int k = (int)quot(x, p.Hkv), h = (int)(x - (int64_t)k * p.Hkv);
     int b = 0, top = p.B;
     while (top - b > 1) {
       const int mid = (b + top) >> 1;
@@ -106,52 +191,22 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     const int64_t end = (int64_t)start + (p.cu[b + 1] - p.cu[b]);
     const int logical = start / P + (k - pre[b]);
     const int page = p.bt[(int64_t)b * p.max_pages + logical];
-    if (page < 0 || page >= p.num_pages) {  // (block-uniform)
-      if (tid == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+    if (page < 0 || page >= p.num_pages) {
+      if (lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
       continue;
     }
     const int64_t left = end - (int64_t)logical * P;
     const int filled = left < P ? (int)left : P;
     const uint8_t* chunk = p.pool + ((int64_t)page * p.Hkv + h) * p.lay.chunk;
-    const float* scales = reinterpret_cast<const float*>(chunk + p.lay.ks);
-    const int c0 = (tid % LPR) * 16;
+    const float* scales = reinterpret_cast<const float*>(chunk + p.lay.ks) + c0 / kGroup;
     float hi[16], lo[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       hi[i] = -INFINITY;
       lo[i] = INFINITY;
     }
-    bool odd = false;
-    for (int r0 = tid / LPR; r0 < filled; r0 += RPB * kBndLoads) {
-      uint4 w[kBndLoads];
-      float sc[kBndLoads];
-#pragma unroll
-      for (int j = 0; j < kBndLoads; ++j) {
-        const int r = r0 + j * RPB;
-        w[j] = make_uint4(0, 0, 0, 0);
-        sc[j] = 0.f;
-        if (r < filled) {
-          w[j] = *reinterpret_cast<const uint4*>(chunk + (int64_t)r * D + c0);
-          sc[j] = scales[r * GR + c0 / kGroup];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBndLoads; ++j) {
-        if (r0 + j * RPB >= filled) continue;
-        float s = sc[j];
-        if (!(fabsf(s) < INFINITY)) {  // counts as zeros
-          odd = true;
-          s = 0.f;
-        }
-        const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = (float)(int8_t)(u[i / 4] >> (8 * (i & 3))) * s;
-          hi[i] = fmaxf(hi[i], v);
-          lo[i] = fminf(lo[i], v);
-        }
-      }
-    }
+    const bool odd = wide ? row_extremes<D, 4>(chunk + c0, scales, tid / LPR, kBndThreads / LPR, filled, hi, lo)
+                          : row_extremes<D, kBndLoads>(chunk + c0, scales, lane / LPR, 32 / LPR, filled, hi, lo);
     if (odd) flag(p.status, NK_DEVFLAG_RANGE);
     // the rows of a warp share channels: lanes LPR apart
 #pragma unroll
@@ -161,41 +216,45 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
         hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
         lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
       }
-    if (lane < LPR) {
+    if (wide) {
+      if (lane < LPR) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        *reinterpret_cast<float4*>(&hi_s[warp][c0 + i]) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
-        *reinterpret_cast<float4*>(&lo_s[warp][c0 + i]) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+        for (int i = 0; i < 16; i += 4) {
+          *reinterpret_cast<float4*>(&hi_s[warp][c0 + i]) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+          *reinterpret_cast<float4*>(&lo_s[warp][c0 + i]) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+        }
       }
+      __syncthreads();  // (one item a block)
+      if (warp > 0) return;
+#pragma unroll
+      for (int w = 0; w < kBndWarps; ++w)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          hi[i] = fmaxf(hi[i], hi_s[w][c0 + i]);
+          lo[i] = fminf(lo[i], lo_s[w][c0 + i]);
+        }
     }
-    __syncthreads();
-    float h1 = 0.f, l1 = 0.f;
-    if (tid < D) {
-      h1 = hi_s[0][tid];
-      l1 = lo_s[0][tid];
+    float m = 0.f;
 #pragma unroll
-      for (int w2 = 1; w2 < kBndWarps; ++w2) {
-        h1 = fmaxf(h1, hi_s[w2][tid]);
-        l1 = fminf(l1, lo_s[w2][tid]);
-      }
-    }
-    float m = fmaxf(fabsf(h1), fabsf(l1));
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) top_s[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w2 = 0; w2 < kBndWarps; ++w2) m = fmaxf(m, top_s[w2]);
+    for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s = __fdiv_rn(m, 127.f);
     if (s == 0.f) s = 1.f;
     const int64_t rec = (int64_t)page * p.Hkv + h;
-    if (tid < D) {
-      uint8_t* dst = p.out.codes + rec * 2 * D + tid;
-      dst[0] = (uint8_t)(int8_t)fminf(fmaxf(rintf(__fdiv_rn(h1, s)), -127.f), 127.f);
-      dst[D] = (uint8_t)(int8_t)fminf(fmaxf(rintf(__fdiv_rn(l1, s)), -127.f), 127.f);
+    // lanes below LPR write hi, the next LPR (or, at D = 256, the same half of a warp's) lo
+    const bool low = lane >= LPR;
+    if (lane < 2 * LPR) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i] |= bound_code(low ? lo[4 * i + j] : hi[4 * i + j], s) << (8 * j);
+      }
+      *reinterpret_cast<uint4*>(p.out.codes + rec * 2 * D + (low ? D : 0) + c0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (tid == 0) p.out.scales[rec] = s;
-    __syncthreads();  // (hi_s, top_s: the next item's)
+    if (lane == 0) p.out.scales[rec] = s;
   }
 }
 
@@ -239,11 +298,6 @@ __device__ __forceinline__ int select_len(const SelectParams& p, int b) {  // 0:
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelRows = 64;  // query rows of a chunk, at most
 
-__device__ __forceinline__ uint32_t sel_prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
 // two int8 codes (biased by ^ 0x80808080) as an exact fp16 pair
 __device__ __forceinline__ uint32_t sel_f16(uint32_t biased, uint32_t sel) {
   const uint32_t h = sel_prmt(biased, 0x64646464u, sel);

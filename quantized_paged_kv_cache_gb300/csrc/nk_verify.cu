@@ -39,7 +39,7 @@ struct VerifyParams {
 };
 
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
-constexpr int kVerUnroll = 8;
+constexpr int kVerUnroll = 16;
 constexpr float kVerOne = 4611686018427387904.f;  // 2^62: one, as a whole number
 constexpr uint64_t kVerCap = 0x7fffffffffffffffull;  // a sum of 2 or more ends here
 

@@ -6,6 +6,7 @@
 #include "nk_common.cuh"
 #include "nk_host.cuh"
 #include "nk_topk.cuh"
+#include "nk_weights.cuh"
 
 namespace nk {
 
@@ -18,248 +19,292 @@ namespace nk {
 // the rows' lse and adds up exp(page's - lse).
 //
 // First kernel: the flat list of (sequence, kv-head, page) items is cut into one
-// range a CTA (nk_common.cuh), a warp takes a page of the segment at a time, 16
-// keys straight from global memory into registers: a thread's 16 bytes of a row
-// are, in the product's K order, four steps of four channels. Codes enter
-// mma.m16n8k16 as exact fp16, the query rows as fp16 scaled by a power of two
-// each (exact for channels within 2^24 of the row's largest), fp32 sums by
-// 64-channel group, then the group's scale. Keys are M and query rows N, so a
-// decode step pads six rows to eight. Bounded by the K half of the cache, and by
-// mma.sync for the T = 16 of a window over a prompt.
+// range a CTA (nk_common.cuh), a warp takes a page of the segment at a time, KB
+// times 16 keys a step. Each warp has a ring of steps in shared memory that it
+// fills with asynchronous copies of 16 bytes a thread: what a thread copies is
+// what it reads again, 16 consecutive channels of a key, in the product's K order
+// four steps of four, so the layout is the lanes' own and needs no swizzle, and no
+// warp waits for another. Codes enter mma.m16n8k16 as exact fp16, the query rows
+// as fp16 scaled by a power of two each (exact for channels within 2^24 of the
+// row's largest), fp32 sums by 64-channel group, then the group's scale. Keys are M
+// and query rows N, so a decode step pads six rows to eight; more than 48 rows run
+// as chunks, in CTAs beside one another that find each other's keys in L2. Bounded
+// by the K half of the cache, and by mma.sync for the T = 16 of a window over a
+// prompt.
 // ---------------------------------------------------------------------------
-struct WeightParams {
-  const uint8_t* pool;
-  ChunkLayout lay;
-  int num_pages;
-  const uint16_t* q;  // bf16 [B][T][Hq][D]
-  const int32_t* bt;
-  const int32_t* ctx;
-  SplitShape sh;
-  int G, rows;        // rows: T * G rounded up to whole tiles of eight
-  float scale2;       // sm_scale * log2(e)
-  int n_ctas;
-  float* page_lse;    // [item][rows], base 2, -inf: no key seen
-  float* seg_lse;     // [n_ctas + B * Hkv][rows]
-  const float* prior; // may be NULL
-  const int32_t* seen;  // may be NULL
-  float* out;         // [num_pages][Hkv]
-  int32_t* status;
-};
-
 constexpr int kWgtThreads = 256, kWgtWarps = kWgtThreads / 32;
 
-__device__ __forceinline__ float wgt_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// A step of a warp in its ring: KB times 16 keys' codes, a lane's pieces 512 bytes
+// apart, then their scales.
+template <int D, int KB>
+struct KeyStep {
+  static constexpr int NG = D / kGroup;
+  static constexpr int kCodes = KB * 2 * NG * 512;
+  static constexpr int kBytes = kCodes + KB * 16 * NG * 4;
+};
+
+// Shared memory: each warp's running log-sums of the segment [rows] float2, the
+// rows' powers of two [rows], the chunk's rows as fp16 [rows][D / 2 + 2 words],
+// the rings.
+__host__ __device__ inline int weight_ring_off(int D, int chunk) {
+  return (kWgtWarps * chunk * 8 + chunk * 4 + chunk * (D * 2 + 8) + 15) / 16 * 16;
 }
-__device__ __forceinline__ uint32_t wgt_prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint32_t wgt_f16(uint32_t biased, uint32_t sel) {
-  const uint32_t h = wgt_prmt(biased, 0x64646464u, sel);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ void wgt_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Steps in a warp's ring: three where 227 KB hold them.
+template <int D, int NT, int KB>
+constexpr int weight_stages() {
+  return (kWgtWarps * NT * 64 + NT * 32 + NT * 8 * (D * 2 + 8) + 16 + kWgtWarps * 3 * KeyStep<D, KB>::kBytes +
+          (2 * kMaxBatch + 16) * 4 <= 227 * 1024)
+             ? 3
+             : 2;
 }
 
-// log-sums (m: largest, l: sum of 2^(s - m); l is 0 while m is -inf)
-__device__ __forceinline__ void lse_join(float& m, float& l, float m2, float l2) {
-  const float mx = fmaxf(m, m2);
-  if (mx == -INFINITY) {
-    l += l2;  // nothing, or NaN, which stays
-    return;
-  }
-  l = l * wgt_ex2(m - mx) + l2 * wgt_ex2(m2 - mx);
-  m = mx;
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
-
-// Shared memory: the unit's rows as fp16 [rows][D / 2 + 2 words], their powers
-// of two [rows], then a warp's running log-sums: of the page, a lane its own two
-// rows of a tile [rows / 8][32] float4, and of the segment [rows] float2.
-__host__ __device__ inline int weight_smem(int D, int rows) {
-  return rows * (D * 2 + 8) + rows * 4 + kWgtWarps * (rows / 8 * 32 * 16 + rows * 8);
+template <int BYTES>
+__device__ __forceinline__ void copy_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWgtThreads) page_lse_kernel(const WeightParams p) {
+template <int D, int NT, int KB>
+__global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightParams p) {
   constexpr int RS = D * 2 + 8;
   constexpr int NG = D / kGroup;
+  constexpr int ROWS = NT * 8;
+  constexpr int S = weight_stages<D, NT, KB>();
+  using Step = KeyStep<D, KB>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int pre[kMaxBatch + 1], lens[kMaxBatch], warp_tot[kWgtWarps];
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const SplitShape& sh = p.sh;
-  const int P = sh.P, Hkv = sh.Hkv, T = sh.T, G = p.G, M = T * G, rows = p.rows, tiles = rows / 8;
-  if (blockIdx.x == 0)
+  const int P = sh.P, Hkv = sh.Hkv, T = sh.T, G = p.G, M = T * G;
+  const int row0 = blockIdx.x * ROWS;  // the CTA's chunk of rows
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = tid; b < sh.B; b += kWgtThreads)
       if (pages_of_len(sh, p.ctx[b]) == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
   block_page_prefix_short(sh, p.ctx, 0, pre, warp_tot, lens);
   const int64_t W = (int64_t)pre[sh.B] * Hkv;
   if (W == 0) return;
-  float4* page_st = reinterpret_cast<float4*>(smem) + warp * tiles * 32;
-  uint8_t* rest = smem + kWgtWarps * tiles * 32 * 16;
-  float2* seg_st = reinterpret_cast<float2*>(rest);  // [warp][rows]
-  rest += kWgtWarps * rows * 8;
-  float* undo = reinterpret_cast<float*>(rest);      // sm_scale log2(e) / the row's power of two
-  uint8_t* qs = rest + rows * 4;
-  int64_t x = cta_begin(W, p.n_ctas, blockIdx.x);
-  const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.x + 1);
+  float2* seg_st = reinterpret_cast<float2*>(smem) + warp * ROWS;
+  float* undo = reinterpret_cast<float*>(smem + kWgtWarps * ROWS * 8);  // sm_scale log2(e) / the row's power of two
+  uint8_t* qs = reinterpret_cast<uint8_t*>(undo + ROWS);
+  uint8_t* ring = smem + weight_ring_off(D, ROWS) + warp * S * Step::kBytes;
+  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+  int64_t x = cta_begin(W, p.n_ctas, blockIdx.y);
+  const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.y + 1);
   Segment seg;
   int64_t item = x;  // of the segment's first page
   while (next_segment(sh, pre, x, x_end, seg)) {
-    const int L = lens[seg.b];
+    const int L = lens[seg.b], pages = seg.page_end - seg.page_begin;
+    const int32_t* row_bt = p.bt + (int64_t)seg.b * sh.max_pages + seg.page_begin;
+    const auto live_of = [&](int pg) { return min(P, L - (seg.page_begin + pg) * P); };
+    // ---- the copies: page and step of the next one, its page id, the one after's
+    int c_pg = warp, c_st = 0, c_slot = 0;
+    uint32_t none = 0, c_bit = 1;  // steps in flight whose page is none (a bit each, in turn)
+    int id = c_pg < pages ? row_bt[c_pg] : 0, id_next = c_pg + kWgtWarps < pages ? row_bt[c_pg + kWgtWarps] : 0;
+    const auto issue = [&]() {
+      if (c_pg < pages) {
+        const bool bad = id < 0 || id >= p.num_pages;
+        none = bad ? none | c_bit : none & ~c_bit;
+        c_bit = c_bit << 1 | c_bit >> 31;
+        const uint8_t* chunk = p.pool + ((int64_t)(bad ? 0 : id) * Hkv + seg.h) * p.lay.chunk;
+        const uint32_t dst = ring_u32 + c_slot * Step::kBytes;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = min(c_st * 16 * KB + 16 * kb, P - 16) + g + 8 * i;  // (past the page: its last 16, masked later)
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
+              copy_async16(dst + ((kb * 2 + i) * NG + c) * 512 + lane * 16, chunk + key * D + 64 * c + 16 * t4);
+          }
+        if (lane < 16 * KB) {
+          const int key = min(c_st * 16 * KB + (lane & ~15), P - 16) + (lane & 15);
+          const uint8_t* src = chunk + p.lay.ks + key * (NG * 4);
+          const uint32_t to = dst + Step::kCodes + lane * (NG * 4);
+          if constexpr (NG == 4) copy_async16(to, src);
+          else copy_async_small<NG * 4>(to, src);
+        }
+        if (++c_slot == S) c_slot = 0;
+        if ((++c_st) * 16 * KB >= live_of(c_pg)) {
+          c_st = 0;
+          c_pg += kWgtWarps;
+          id = id_next;
+          if (c_pg + kWgtWarps < pages) id_next = row_bt[c_pg + kWgtWarps];
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue();
     // ---- the unit's rows: a warp each, scaled into [2^14, 2^15)
-    for (int r = warp; r < rows; r += kWgtWarps) {
-      const int t = r / G, hg = r - t * G;
+    for (int r = warp; r < ROWS; r += kWgtWarps) {
+      const int row = row0 + r, t = row / G, hg = row - t * G;
       const uint16_t* src = p.q + (((int64_t)seg.b * T + t) * (G * Hkv) + seg.h * G + hg) * D;
       constexpr int PER = D / 64;  // words of a lane
       uint32_t w[PER];
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        w[i] = r < M ? reinterpret_cast<const uint32_t*>(src)[lane + 32 * i] : 0u;
+        w[i] = row < M ? reinterpret_cast<const uint32_t*>(src)[lane + 32 * i] : 0u;
         m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int e = 0;
-      if (m > 0.f) {
-        e = 14 - ((int)((__float_as_uint(m) >> 23) & 0xffu) - 127);
-        e = e > 110 ? 110 : (e < -113 ? -113 : e);
-      }
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const int e = wgt_row_exp(m);
+      const float up = wgt_pow2(e);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const __half2 hh = __floats2half2_rn(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
         reinterpret_cast<uint32_t*>(qs + r * RS)[lane + 32 * i] = *reinterpret_cast<const uint32_t*>(&hh);
       }
-      if (lane == 0) undo[r] = p.scale2 * __uint_as_float((uint32_t)(127 - e) << 23);
+      if (lane == 0) undo[r] = p.scale2 * wgt_pow2(-e);
     }
-    for (int i = lane; i < rows; i += 32) seg_st[warp * rows + i] = make_float2(-INFINITY, 0.f);
+    for (int i = lane; i < ROWS; i += 32) seg_st[i] = make_float2(-INFINITY, 0.f);
     __syncthreads();
-    const int pages = seg.page_end - seg.page_begin;
+    int slot = 0;
+    uint32_t bit = 1;
     for (int pg = warp; pg < pages; pg += kWgtWarps) {  // (warp-uniform)
-      const int logical = seg.page_begin + pg;
-      const int page = p.bt[(int64_t)seg.b * sh.max_pages + logical];
-      const bool bad = page < 0 || page >= p.num_pages;
-      if (bad && lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
-      const uint8_t* chunk = p.pool + ((int64_t)(bad ? 0 : page) * Hkv + seg.h) * p.lay.chunk;
-      const float* scales = reinterpret_cast<const float*>(chunk + p.lay.ks);
-      for (int i = 0; i < tiles; ++i) page_st[i * 32 + lane] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-      const int live = bad ? 0 : min(P, L - logical * P);
-      for (int k0 = 0; k0 < live; k0 += 16) {
-        uint4 raw[2][NG];
-        float sc[2][NG];
+      const int logical = seg.page_begin + pg, live = live_of(pg);
+      float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            const int key = k0 + g + 8 * i;  // (a page holds whole 16s)
-            raw[i][c] = *reinterpret_cast<const uint4*>(chunk + (int64_t)key * D + 64 * c + 16 * t4);
-            sc[i][c] = scales[key * NG + c];
-          }
-        uint32_t a[NG][4][4];
-#pragma unroll
-        for (int c = 0; c < NG; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 r0 = raw[0][c], r1 = raw[1][c];
-            const uint32_t w0 = (j == 0 ? r0.x : j == 1 ? r0.y : j == 2 ? r0.z : r0.w) ^ 0x80808080u;
-            const uint32_t w1 = (j == 0 ? r1.x : j == 1 ? r1.y : j == 2 ? r1.z : r1.w) ^ 0x80808080u;
-            a[c][j][0] = wgt_f16(w0, 0x4140);
-            a[c][j][1] = wgt_f16(w1, 0x4140);
-            a[c][j][2] = wgt_f16(w0, 0x4342);
-            a[c][j][3] = wgt_f16(w1, 0x4342);
-          }
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+        }
+      for (int k0 = 0; k0 < live; k0 += 16 * KB) {
+        issue();
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        const bool bad = (none & bit) != 0;
+        bit = bit << 1 | bit >> 31;
+        if (bad && lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+        const uint8_t* step = ring + slot * Step::kBytes;
+        if (++slot == S) slot = 0;
         const int pos0 = logical * P + k0;
-        const bool edge = pos0 + 15 > L - T;  // some row does not see some key
-        for (int nt = 0; nt < tiles; ++nt) {
-          float acc[NG][4];
+        const bool edge = bad || k0 + 16 * KB > live || pos0 + 16 * KB - 1 > L - T;  // some row does not see some key
+        float s[NT][KB][4];
 #pragma unroll
-          for (int c = 0; c < NG; ++c)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[c][k] = 0.f;
-          const uint8_t* qrow = qs + (nt * 8 + g) * RS + 32 * t4;
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+            for (int k = 0; k < 4; ++k) s[nt][kb][k] = 0.f;
 #pragma unroll
-            for (int c = 0; c < NG; ++c) {
-              const uint2 b = *reinterpret_cast<const uint2*>(qrow + 128 * c + 8 * j);
-              wgt_mma(acc[c], a[c][j][0], a[c][j][1], a[c][j][2], a[c][j][3], b.x, b.y);
+        for (int c = 0; c < NG; ++c) {
+          uint32_t a[KB][4][4];
+          float sc[KB][2];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            const uint4 r0 = *reinterpret_cast<const uint4*>(step + ((kb * 2 + 0) * NG + c) * 512 + lane * 16);
+            const uint4 r1 = *reinterpret_cast<const uint4*>(step + ((kb * 2 + 1) * NG + c) * 512 + lane * 16);
+            const float* scales = reinterpret_cast<const float*>(step + Step::kCodes) + (kb * 16 + g) * NG + c;
+            sc[kb][0] = scales[0];
+            sc[kb][1] = scales[8 * NG];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w0 = (j == 0 ? r0.x : j == 1 ? r0.y : j == 2 ? r0.z : r0.w) ^ 0x80808080u;
+              const uint32_t w1 = (j == 0 ? r1.x : j == 1 ? r1.y : j == 2 ? r1.z : r1.w) ^ 0x80808080u;
+              a[kb][j][0] = wgt_f16(w0, 0x4140);
+              a[kb][j][1] = wgt_f16(w1, 0x4140);
+              a[kb][j][2] = wgt_f16(w0, 0x4342);
+              a[kb][j][3] = wgt_f16(w1, 0x4342);
             }
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            s[0] = fmaf(sc[0][c], acc[c][0], s[0]);
-            s[1] = fmaf(sc[0][c], acc[c][1], s[1]);
-            s[2] = fmaf(sc[1][c], acc[c][2], s[2]);
-            s[3] = fmaf(sc[1][c], acc[c][3], s[3]);
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[KB][4];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[kb][k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint2 b = *reinterpret_cast<const uint2*>(qs + (nt * 8 + g) * RS + 32 * t4 + 128 * c + 8 * j);
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+                wgt_mma(acc[kb], a[kb][j][0], a[kb][j][1], a[kb][j][2], a[kb][j][3], b.x, b.y);
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              s[nt][kb][0] = fmaf(sc[kb][0], acc[kb][0], s[nt][kb][0]);
+              s[nt][kb][1] = fmaf(sc[kb][0], acc[kb][1], s[nt][kb][1]);
+              s[nt][kb][2] = fmaf(sc[kb][1], acc[kb][2], s[nt][kb][2]);
+              s[nt][kb][3] = fmaf(sc[kb][1], acc[kb][3], s[nt][kb][3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           const int r0 = nt * 8 + 2 * t4;
           const float2 un = *reinterpret_cast<const float2*>(undo + r0);
-          s[0] *= un.x;
-          s[1] *= un.y;
-          s[2] *= un.x;
-          s[3] *= un.y;
-          if (edge) {
-            const int p0 = L - T + r0 / G, p1 = L - T + (r0 + 1) / G, n0 = pos0 + g, n1 = n0 + 8;
-            if (n0 > p0 || n0 >= L) s[0] = -INFINITY;
-            if (n0 > p1 || n0 >= L) s[1] = -INFINITY;
-            if (n1 > p0 || n1 >= L) s[2] = -INFINITY;
-            if (n1 > p1 || n1 >= L) s[3] = -INFINITY;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            s[nt][kb][0] *= un.x;
+            s[nt][kb][1] *= un.y;
+            s[nt][kb][2] *= un.x;
+            s[nt][kb][3] *= un.y;
           }
-          float4 st = page_st[nt * 32 + lane];
-          const float m0 = fmaxf(st.x, fmaxf(s[0], s[2])), m1 = fmaxf(st.z, fmaxf(s[1], s[3]));
-          const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-          st.y = st.y * wgt_ex2(st.x - u0) + (wgt_ex2(s[0] - u0) + wgt_ex2(s[2] - u0));
-          st.w = st.w * wgt_ex2(st.z - u1) + (wgt_ex2(s[1] - u1) + wgt_ex2(s[3] - u1));
-          st.x = m0;
-          st.z = m1;
-          page_st[nt * 32 + lane] = st;
+          if (edge) {
+            // the last position each row sees; keys past the page's live ones are another page's
+            const int end = bad ? -1 : logical * P + live - 1;
+            const int p0 = min(L - T + (row0 + r0) / G, end), p1 = min(L - T + (row0 + r0 + 1) / G, end);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              const int n0 = pos0 + 16 * kb + g, n1 = n0 + 8;
+              if (n0 > p0) s[nt][kb][0] = -INFINITY;
+              if (n0 > p1) s[nt][kb][1] = -INFINITY;
+              if (n1 > p0) s[nt][kb][2] = -INFINITY;
+              if (n1 > p1) s[nt][kb][3] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = m[nt][e];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) mx = fmaxf(mx, fmaxf(s[nt][kb][e], s[nt][kb][e + 2]));
+            const float u = mx == -INFINITY ? 0.f : mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) sum += wgt_ex2(s[nt][kb][e] - u) + wgt_ex2(s[nt][kb][e + 2] - u);
+            l[nt][e] = fmaf(l[nt][e], wgt_ex2(m[nt][e] - u), sum);
+            m[nt][e] = mx;
+          }
         }
+        __syncwarp();  // (the next copies go where this step lay S steps ago)
       }
       // ---- the page's log-sums: eight lanes hold a row's keys
-      float* dst = p.page_lse + (item + pg) * rows;
-      for (int nt = 0; nt < tiles; ++nt) {
-        float4 st = page_st[nt * 32 + lane];
+      float* dst = p.page_lse + (item + pg) * p.rows + row0;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          const float mx = __shfl_xor_sync(0xffffffffu, st.x, o), lx = __shfl_xor_sync(0xffffffffu, st.y, o);
-          const float mz = __shfl_xor_sync(0xffffffffu, st.z, o), lz = __shfl_xor_sync(0xffffffffu, st.w, o);
-          lse_join(st.x, st.y, mx, lx);
-          lse_join(st.z, st.w, mz, lz);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[nt][e], o), l2 = __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+            lse_join(m[nt][e], l[nt][e], m2, l2);
+          }
         if (g == 0) {
           const int r0 = nt * 8 + 2 * t4;
-          *reinterpret_cast<float2*>(dst + r0) = make_float2(lse_of(st.x, st.y), lse_of(st.z, st.w));
-          float2* sg = seg_st + warp * rows + r0;
-          float2 s0 = sg[0], s1 = sg[1];
-          lse_join(s0.x, s0.y, st.x, st.y);
-          lse_join(s1.x, s1.y, st.z, st.w);
-          sg[0] = s0;
-          sg[1] = s1;
+          *reinterpret_cast<float2*>(dst + r0) = make_float2(lse_of(m[nt][0], l[nt][0]), lse_of(m[nt][1], l[nt][1]));
+          float2 s0 = seg_st[r0], s1 = seg_st[r0 + 1];
+          lse_join(s0.x, s0.y, m[nt][0], l[nt][0]);
+          lse_join(s1.x, s1.y, m[nt][1], l[nt][1]);
+          seg_st[r0] = s0;
+          seg_st[r0 + 1] = s1;
         }
       }
     }
     __syncthreads();
-    for (int r = tid; r < rows; r += kWgtThreads) {
+    const float2* all = reinterpret_cast<const float2*>(smem);
+    for (int r = tid; r < ROWS; r += kWgtThreads) {
       float m = -INFINITY, l = 0.f;
-      for (int w = 0; w < kWgtWarps; ++w) {
-        const float2 s = seg_st[w * rows + r];
-        lse_join(m, l, s.x, s.y);
-      }
-      p.seg_lse[((int64_t)blockIdx.x + seg.u) * rows + r] = lse_of(m, l);
+      for (int w = 0; w < kWgtWarps; ++w) lse_join(m, l, all[w * ROWS + r].x, all[w * ROWS + r].y);
+      p.seg_lse[((int64_t)blockIdx.y + seg.u) * p.rows + row0 + r] = lse_of(m, l);
     }
     item += pages;
     __syncthreads();
@@ -290,8 +335,10 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
     for (int c = c0 + lane; c <= c1; c += 32) {
       // (a CTA owns no item only when there are fewer items than CTAs)
       if (W < p.n_ctas && cta_begin(W, p.n_ctas, c) == cta_begin(W, p.n_ctas, c + 1)) continue;
-      const float s = p.seg_lse[((int64_t)c + u) * rows + r];
-      if (s != -INFINITY) lse_join(m, l, s, s == s ? 1.f : s);
+      for (int k = 0; k < p.takes; ++k) {
+        const float s = p.seg_lse[(((int64_t)c + u) * p.takes + k) * rows + r];
+        if (s != -INFINITY) lse_join(m, l, s, s == s ? 1.f : s);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -304,12 +351,13 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
   int seen = 0x7fffffff;
   if (p.seen) seen = p.seen[b];
   for (int64_t j = (int64_t)blockIdx.x * per + tid / 8; j < pages; j += (int64_t)gridDim.x * per) {
-    const float* src = p.page_lse + (x0 + j) * rows;
+    const float* src = p.page_lse + (x0 + j) * p.parts * rows;
     float sum = 0.f;
-    for (int r = tid & 7; r < M; r += 8) {
-      const float s = src[r], t = lse[r];
-      if (s != -INFINITY) sum += wgt_ex2(s - t);
-    }
+    for (int k = 0; k < p.parts; ++k, src += rows)
+      for (int r = tid & 7; r < M; r += 8) {
+        const float s = src[r], t = lse[r];
+        if (s != -INFINITY) sum += wgt_ex2(s - t);
+      }
     const uint32_t mask = 0xffu << (lane & 24);
     sum += __shfl_xor_sync(mask, sum, 1);
     sum += __shfl_xor_sync(mask, sum, 2);
@@ -468,12 +516,63 @@ using namespace nk;
 
 namespace {
 
-int weight_rows(int T, int G) { return (T * G + 7) / 8 * 8; }
+// From how many rows on the tcgen05 kernel takes a call.
+constexpr int kTcRows = 25;
 
-int weight_ctas(int64_t items) {
+// Row tiles of the mma.sync kernel's instances: 1, 2, 3, 4, 6; with 16-key pages
+// (steps of 16 keys) 1, 3, 6.
+int weight_tiles(int tiles, int P) {
+  if (P == 16) return tiles <= 1 ? 1 : (tiles <= 3 ? 3 : 6);
+  return tiles == 5 ? 6 : tiles;
+}
+
+// Chunks of rows, alike in size: at most 48 on mma.sync (six tiles of eight fill a
+// thread's registers), 128 on tcgen05 (the M of its product).
+struct WeightRows {
+  bool tc;
+  int chunks, chunk;  // rows of a chunk, a multiple of eight
+  int parts, takes;
+  int all() const { return chunks * chunk; }
+};
+WeightRows weight_rows(int T, int G, int P) {
+  const int M = T * G;
+  const bool tc = M >= kTcRows;
+  const int most = tc ? 128 : 48, n = (M + most - 1) / most, tiles = ((M + n - 1) / n + 7) / 8;
+  if (tc) return {true, n, tiles * 8, (P + 63) / 64, 2};
+  return {false, n, weight_tiles(tiles, P) * 8, 1, 1};
+}
+
+// CTAs along the pages: one an SM, shared by the chunks.
+int weight_ctas(int64_t items, const WeightRows& r) {
   const int sms = device_sms();
-  const int64_t n = (int64_t)(sms > 0 ? sms : 148) * 2;
+  int64_t n = (int64_t)(sms > 0 ? sms : 148) / r.chunks;
+  if (n < 1) n = 1;
   return (int)(items < n ? (items < 1 ? 1 : items) : n);
+}
+
+template <int D, int NT, int KB>
+cudaError_t launch_lse(const WeightParams& p, int chunks, cudaStream_t st) {
+  const int smem = weight_ring_off(D, NT * 8) + kWgtWarps * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes;
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_lse_kernel<D, NT, KB>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(kWgtThreads),
+                        (size_t)smem, st, p);
+}
+
+template <int D>
+cudaError_t launch_lse_d(const WeightParams& p, int chunks, cudaStream_t st) {
+  if (p.sh.P == 16) switch (p.chunk / 8) {
+      case 1: return launch_lse<D, 1, 1>(p, chunks, st);
+      case 3: return launch_lse<D, 3, 1>(p, chunks, st);
+      default: return launch_lse<D, 6, 1>(p, chunks, st);
+    }
+  switch (p.chunk / 8) {
+    case 1: return launch_lse<D, 1, 2>(p, chunks, st);
+    case 2: return launch_lse<D, 2, 2>(p, chunks, st);
+    case 3: return launch_lse<D, 3, 2>(p, chunks, st);
+    case 4: return launch_lse<D, 4, 2>(p, chunks, st);
+    default: return launch_lse<D, 6, 2>(p, chunks, st);
+  }
 }
 
 }  // namespace
@@ -485,8 +584,9 @@ size_t nk_page_weights_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads
   if (B < 1 || T < 1 || T > NK_MAX_T || num_kv_heads < 1 || num_q_heads < num_kv_heads || page_size < 1 || max_ctx < 1)
     return 0;
   const int64_t items = (int64_t)B * num_kv_heads * (((int64_t)max_ctx + page_size - 1) / page_size);
-  const int64_t slots = weight_ctas(items) + (int64_t)B * num_kv_heads;
-  return (size_t)(items + slots) * weight_rows(T, num_q_heads / num_kv_heads) * 4;
+  const WeightRows r = weight_rows(T, num_q_heads / num_kv_heads, page_size);
+  const int64_t slots = weight_ctas(items, r) + (int64_t)B * num_kv_heads;
+  return (size_t)(items * r.parts + slots * r.takes) * r.all() * 4;
 }
 
 int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
@@ -502,8 +602,8 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
   const int Hkv = pool->num_kv_heads, D = pool->head_dim, P = pool->page_size, G = num_q_heads / Hkv;
   if (max_pages_per_seq < 1 || max_ctx < T || (int64_t)max_ctx > (int64_t)max_pages_per_seq * P) return NK_ERR_SHAPE;
   if (!isfinite(sm_scale) || !aligned_to(q_dev, 16)) return NK_ERR_SHAPE;
-  const int rows = weight_rows(T, G), smem = weight_smem(D, rows);
-  if (B > kMaxBatch || (int64_t)B * Hkv > 65535 || smem > 200 * 1024) return NK_ERR_UNSUPPORTED;
+  if (B > kMaxBatch || (int64_t)B * Hkv > 65535 || G > 48) return NK_ERR_UNSUPPORTED;
+  const WeightRows r = weight_rows(T, G, P);
   const size_t need = nk_page_weights_workspace_bytes(B, T, num_q_heads, Hkv, P, max_ctx);
   if (!workspace_dev || workspace_bytes < need || !aligned_to(workspace_dev, 16)) return NK_ERR_WORKSPACE;
   const int64_t longest = ((int64_t)max_ctx + P - 1) / P, items = (int64_t)B * Hkv * longest;
@@ -511,36 +611,35 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
   p.pool = reinterpret_cast<const uint8_t*>(pool->base_dev);
   p.lay = ChunkLayout::make(P, D);
   p.num_pages = pool->num_pages;
+  p.D = D;
   p.q = reinterpret_cast<const uint16_t*>(q_dev);
   p.bt = block_table_dev;
   p.ctx = ctx_lens_dev;
   p.sh = SplitShape{B, Hkv, P, T, max_ctx, max_pages_per_seq};
   p.G = G;
-  p.rows = rows;
+  p.rows = r.all();
+  p.chunk = r.chunk;
+  p.parts = r.parts;
+  p.takes = r.takes;
   p.scale2 = sm_scale * kLog2e;
-  p.n_ctas = weight_ctas(items);
+  p.n_ctas = weight_ctas(items, r);
   p.page_lse = reinterpret_cast<float*>(workspace_dev);
-  p.seg_lse = p.page_lse + items * rows;
+  p.seg_lse = p.page_lse + items * r.parts * p.rows;
   p.prior = prior_dev;
   p.seen = seen_dev;
   p.out = weights_dev;
   p.status = status_dev;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 g((unsigned)p.n_ctas), t(kWgtThreads);
-  const void* fn = D == 256   ? reinterpret_cast<const void*>(page_lse_kernel<256>)
-                   : D == 128 ? reinterpret_cast<const void*>(page_lse_kernel<128>)
-                              : reinterpret_cast<const void*>(page_lse_kernel<64>);
-  cudaError_t e = set_smem_limit(fn, smem);
-  if (e != cudaSuccess) return NK_ERR_CUDA;
-  e = D == 256   ? launch_chained(page_lse_kernel<256>, g, t, (size_t)smem, st, p)
-      : D == 128 ? launch_chained(page_lse_kernel<128>, g, t, (size_t)smem, st, p)
-                 : launch_chained(page_lse_kernel<64>, g, t, (size_t)smem, st, p);
+  cudaError_t e = r.tc       ? launch_lse_tc(p, r.chunks, st)
+                  : D == 256 ? launch_lse_d<256>(p, r.chunks, st)
+                  : D == 128 ? launch_lse_d<128>(p, r.chunks, st)
+                             : launch_lse_d<64>(p, r.chunks, st);
   if (e != cudaSuccess) return NK_ERR_CUDA;
   const int64_t units = (int64_t)B * Hkv;
   int64_t gx = (longest + kWsmThreads / 8 - 1) / (kWsmThreads / 8), most = 2048 / units;
   if (most < 1) most = 1;
   if (gx > most) gx = most;
-  e = launch_chained(page_weight_kernel, dim3((unsigned)gx, (unsigned)units), dim3(kWsmThreads), (size_t)rows * 4, st,
+  e = launch_chained(page_weight_kernel, dim3((unsigned)gx, (unsigned)units), dim3(kWsmThreads), (size_t)p.rows * 4, st,
                      p);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
