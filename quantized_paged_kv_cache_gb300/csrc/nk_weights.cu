@@ -329,10 +329,15 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
   if (W == 0 || (int64_t)blockIdx.x * per >= pages) return;
   const int64_t x0 = (int64_t)pre[b] * sh.Hkv + (int64_t)h * pages;
   const int c0 = cta_of_item(W, p.n_ctas, x0), c1 = cta_of_item(W, p.n_ctas, x0 + pages - 1);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int r = warp; r < rows; r += kWsmThreads / 32) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  // `sub` lanes a row (a power of two, at most a warp), as many rows at once as fit
+  int sub = 32;
+  while (sub > 1 && rows * sub > kWsmThreads) sub >>= 1;
+  for (int r0 = 0; r0 < rows; r0 += kWsmThreads / sub) {  // (every thread: the shuffles below)
+    const int r = min(r0 + tid / sub, rows - 1);
     float m = -INFINITY, l = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
+#pragma unroll 4
+    for (int c = c0 + (tid & (sub - 1)); c <= c1; c += sub) {
       // (a CTA owns no item only when there are fewer items than CTAs)
       if (W < p.n_ctas && cta_begin(W, p.n_ctas, c) == cta_begin(W, p.n_ctas, c + 1)) continue;
       for (int k = 0; k < p.takes; ++k) {
@@ -340,12 +345,11 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
         if (s != -INFINITY) lse_join(m, l, s, s == s ? 1.f : s);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = sub >> 1; o > 0; o >>= 1) {
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
       lse_join(m, l, m2, l2);
     }
-    if (lane == 0) lse[r] = lse_of(m, l);
+    if ((tid & (sub - 1)) == 0) lse[r] = lse_of(m, l);
   }
   __syncthreads();
   int seen = 0x7fffffff;
@@ -354,10 +358,8 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
     const float* src = p.page_lse + (x0 + j) * p.parts * rows;
     float sum = 0.f;
     for (int k = 0; k < p.parts; ++k, src += rows)
-      for (int r = tid & 7; r < M; r += 8) {
-        const float s = src[r], t = lse[r];
-        if (s != -INFINITY) sum += wgt_ex2(s - t);
-      }
+#pragma unroll 4
+      for (int r = tid & 7; r < M; r += 8) sum += wgt_ex2(src[r] - lse[r]);  // (no key seen: 2^-inf is 0)
     const uint32_t mask = 0xffu << (lane & 24);
     sum += __shfl_xor_sync(mask, sum, 1);
     sum += __shfl_xor_sync(mask, sum, 2);
@@ -538,7 +540,7 @@ WeightRows weight_rows(int T, int G, int P) {
   const int M = T * G;
   const bool tc = M >= kTcRows;
   const int most = tc ? 128 : 48, n = (M + most - 1) / most, tiles = ((M + n - 1) / n + 7) / 8;
-  if (tc) return {true, n, tiles * 8, (P + 63) / 64, 2};
+  if (tc) return {true, n, tiles * 8, (P + 31) / 32, 4};
   return {false, n, weight_tiles(tiles, P) * 8, 1, 1};
 }
 
@@ -607,6 +609,7 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
   const size_t need = nk_page_weights_workspace_bytes(B, T, num_q_heads, Hkv, P, max_ctx);
   if (!workspace_dev || workspace_bytes < need || !aligned_to(workspace_dev, 16)) return NK_ERR_WORKSPACE;
   const int64_t longest = ((int64_t)max_ctx + P - 1) / P, items = (int64_t)B * Hkv * longest;
+  if (items * r.parts > 0x7fffffff) return NK_ERR_UNSUPPORTED;  // log-sums are numbered in 32 bits
   WeightParams p = {};
   p.pool = reinterpret_cast<const uint8_t*>(pool->base_dev);
   p.lay = ChunkLayout::make(P, D);

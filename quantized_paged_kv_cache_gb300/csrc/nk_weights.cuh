@@ -19,7 +19,7 @@ struct WeightParams {
   int G, rows, chunk; // rows: T * G in whole chunks of `chunk` rows (whole tiles of eight)
   float scale2;       // sm_scale * log2(e)
   int n_ctas;
-  int parts, takes;   // log-sums of a page; of a segment (the tcgen05 kernel: of 64 keys each, two)
+  int parts, takes;   // log-sums of a page; of a segment (the tcgen05 kernel: of 32 keys each, four)
   float* page_lse;    // [item][parts][rows], base 2, -inf: no key seen
   float* seg_lse;     // [n_ctas + B * Hkv][takes][rows]
   const float* prior; // may be NULL

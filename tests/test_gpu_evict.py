@@ -92,6 +92,22 @@ def test_weights(shape):
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("shape", [("many_t1", 2, 1, 6, 2, 64, 16, [100000, 60001]), ("many_t16", 1, 16, 8, 2, 64, 64, [200003]),
+                                   ("many_t16_p16", 1, 16, 8, 1, 64, 16, [99999]), ("many_t5_p128", 3, 5, 12, 2, 128, 128, [40000, 30001, 77]),
+                                   ("many_t16_p32", 2, 16, 14, 1, 64, 32, [70000, 12345]),
+                                   ("many_short", 300, 4, 16, 2, 64, 32, [4 + (37 * i) % 190 for i in range(300)]),
+                                   ("one_tile_each", 700, 2, 26, 2, 64, 64, [2 + (11 * i) % 63 for i in range(700)])], ids=lambda s: s[0])
+def test_weights_of_long_contexts(shape):
+    """Dozens of pages a CTA, so that every ring goes round; segments that end inside a CTA's range."""
+    c = make(shape)
+    w = c.w
+    want = ref.weights(c.pool.storage, w.num_pages, w.Hkv, w.P, w.D, c.bt_cpu.numpy(), w.ctx_lens, c.q, w.sm_scale)
+    out = torch.zeros((w.num_pages, w.Hkv), device="cuda")
+    got = nk.page_weights(c.pool, c.q, c.bt, c.ctx, w.sm_scale, w.max_ctx, out, status=c.status)
+    assert int(c.status.item()) == 0
+    check_weights(c, got, want, torch.zeros_like(out))
+
+
 @pytest.mark.parametrize("q_scale,k_scale", [(2.0 ** 60, 2.0 ** -60), (2.0 ** -80, 2.0 ** 80), (2.0 ** -30, 1.0)])
 def test_weights_far_off_unit_scale(q_scale, k_scale):
     c = make(("range", 2, 3, 6, 2, 128, 16, [200, 77]), q_scale=q_scale, k_scale=k_scale)
