@@ -5,6 +5,7 @@
 
 #include "nk_common.cuh"
 #include "nk_host.cuh"
+#include "nk_ptx.cuh"
 #include "nk_topk.cuh"
 
 namespace nk {
@@ -32,16 +33,20 @@ __host__ __device__ inline BoundsView bounds_view(void* base, int64_t num_pages,
 // from the codes that its append wrote. Every block forms the prefix of the
 // sequences' touched pages itself and takes (page, kv-head) items in turns.
 //
-// A thread reads 16 bytes of a row at a time and keeps the extremes of its 16
-// channels; D / 16 threads hold a row. With more items than blocks a warp takes
-// an item (no barrier, rows merged by shuffles); with fewer (a step of single
-// tokens) a block does, its warps' extremes merged through shared memory, so that
-// all of the item's bytes are on their way at once.
+// A thread takes 16 bytes of a row at a time and keeps the extremes of its 16
+// channels; D / 16 threads hold a row. With more items than blocks a warp takes an
+// item, from a ring of its own in shared memory that bulk asynchronous copies fill,
+// 32 keys a stage (no barrier between warps; rows merged by shuffles). With fewer
+// (a step of single tokens) a block does, straight from global memory, its warps'
+// extremes merged through shared memory, so that all of the item's bytes are on
+// their way at once.
 //
 // Bounded by the K codes' and scales' bytes for prompts, by latency for a step of
 // single tokens (lengths, table, codes). Codes become fp32 by a byte permute (2^23
 // + 128 + code) and a packed subtraction: the conversion instruction takes an
-// eighth of their rate, and was the bound of the first form.
+// eighth of their rate. Eight prompts of 8K to 16K tokens (101 MB): 65 us with
+// conversions and a block an item, 42 with packed ones and a warp an item that
+// loads into registers, too few of them in flight.
 // ---------------------------------------------------------------------------
 struct BoundsParams {
   const uint8_t* pool;
@@ -57,7 +62,11 @@ struct BoundsParams {
 };
 
 constexpr int kBndThreads = 256, kBndWarps = kBndThreads / 32;
-constexpr int kBndLoads = 8;  // rows of a thread in flight (of a whole warp's item)
+constexpr int kBndKeys = 32, kBndStages = 3;  // of a warp's ring
+template <int D>
+constexpr int bounds_stage() {  // codes, then scales
+  return kBndKeys * (D + D / kGroup * 4);
+}
 
 __device__ __forceinline__ uint32_t sel_prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
@@ -89,8 +98,8 @@ __device__ __forceinline__ void values4(uint32_t w, uint64_t scale2, float (&v)[
   }
 }
 
-// Extremes of rows r0, r0 + step, .. below `filled` at the thread's 16 channels;
-// true if a scale was not finite.
+// Extremes of rows r0, r0 + step, .. below `filled` at the thread's 16 channels,
+// from global or shared memory; true if a scale was not finite.
 template <int D, int LOADS>
 __device__ __forceinline__ bool row_extremes(const uint8_t* codes, const float* scales, int r0, int step, int filled,
                                              float (&hi)[16], float (&lo)[16]) {
@@ -140,9 +149,11 @@ template <int D>
 __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsParams p) {
   constexpr int LPR = D / 16;  // threads of a row
   constexpr int GR = D / kGroup;
-  __shared__ int pre[kMaxBatch + 1];  // touched pages before sequence b
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings
+  __shared__ int pre[kMaxBatch + 1];               // touched pages before sequence b
   __shared__ int warp_tot[kBndWarps];
-  __shared__ __align__(16) float hi_s[kBndWarps][D], lo_s[kBndWarps][D];
+  __shared__ uint64_t bars[kBndWarps][kBndStages];
+  __shared__ int4 meta[kBndWarps][kBndStages];     // record (two words), keys, the item's last
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -176,12 +187,10 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     __syncthreads();
   }
   const int64_t items = (int64_t)pre[p.B] * p.Hkv;
-  const bool wide = items <= gridDim.x;  // a block for each item
-  const int64_t first = wide ? blockIdx.x : (int64_t)blockIdx.x * kBndWarps + warp;
-  const int64_t stride = wide ? gridDim.x : (int64_t)gridDim.x * kBndWarps;
   const int c0 = (lane % LPR) * 16;
-  for (int64_t x = first; x < items; x += stride) {  // (uniform over the item's threads)
-    const int k = (int)quot(x, p.Hkv), h = (int)(x - (int64_t)k * p.Hkv);
+  // Item x: its page (-1: none, flagged) and filled slots
+  const auto look = [&](int64_t x, int& filled) {
+    const int k = (int)quot(x, p.Hkv);
     int b = 0, top = p.B;
     while (top - b > 1) {
       const int mid = (b + top) >> 1;
@@ -191,24 +200,21 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     const int64_t end = (int64_t)start + (p.cu[b + 1] - p.cu[b]);
     const int logical = start / P + (k - pre[b]);
     const int page = p.bt[(int64_t)b * p.max_pages + logical];
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
-      continue;
-    }
     const int64_t left = end - (int64_t)logical * P;
-    const int filled = left < P ? (int)left : P;
-    const uint8_t* chunk = p.pool + ((int64_t)page * p.Hkv + h) * p.lay.chunk;
-    const float* scales = reinterpret_cast<const float*>(chunk + p.lay.ks) + c0 / kGroup;
-    float hi[16], lo[16];
+    filled = left < P ? (int)left : P;
+    if (page >= 0 && page < p.num_pages) return page;
+    if (lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+    return -1;
+  };
+  float hi[16], lo[16];
+  const auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       hi[i] = -INFINITY;
       lo[i] = INFINITY;
     }
-    const bool odd = wide ? row_extremes<D, 4>(chunk + c0, scales, tid / LPR, kBndThreads / LPR, filled, hi, lo)
-                          : row_extremes<D, kBndLoads>(chunk + c0, scales, lane / LPR, 32 / LPR, filled, hi, lo);
-    if (odd) flag(p.status, NK_DEVFLAG_RANGE);
-    // the rows of a warp share channels: lanes LPR apart
+  };
+  const auto merge_lanes = [&]() {  // the rows of a warp share channels: lanes LPR apart
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -216,24 +222,8 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
         hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
         lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
       }
-    if (wide) {
-      if (lane < LPR) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          *reinterpret_cast<float4*>(&hi_s[warp][c0 + i]) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
-          *reinterpret_cast<float4*>(&lo_s[warp][c0 + i]) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
-        }
-      }
-      __syncthreads();  // (one item a block)
-      if (warp > 0) return;
-#pragma unroll
-      for (int w = 0; w < kBndWarps; ++w)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          hi[i] = fmaxf(hi[i], hi_s[w][c0 + i]);
-          lo[i] = fminf(lo[i], lo_s[w][c0 + i]);
-        }
-    }
+  };
+  const auto store = [&](int64_t rec) {  // by a warp
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
@@ -241,8 +231,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s = __fdiv_rn(m, 127.f);
     if (s == 0.f) s = 1.f;
-    const int64_t rec = (int64_t)page * p.Hkv + h;
-    // lanes below LPR write hi, the next LPR (or, at D = 256, the same half of a warp's) lo
+    // lanes below LPR write hi, the next LPR lo
     const bool low = lane >= LPR;
     if (lane < 2 * LPR) {
       uint32_t w[4];
@@ -255,6 +244,102 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
       *reinterpret_cast<uint4*>(p.out.codes + rec * 2 * D + (low ? D : 0) + c0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (lane == 0) p.out.scales[rec] = s;
+  };
+
+  if (items <= gridDim.x) {  // a block for each item
+    const int64_t x = blockIdx.x;
+    if (x >= items) return;
+    int filled;
+    const int page = look(x, filled);
+    if (page < 0) return;
+    const int64_t rec = (int64_t)page * p.Hkv + x % p.Hkv;
+    const uint8_t* chunk = p.pool + rec * p.lay.chunk;
+    clear();
+    if (row_extremes<D, 4>(chunk + c0, reinterpret_cast<const float*>(chunk + p.lay.ks) + c0 / kGroup, tid / LPR,
+                           kBndThreads / LPR, filled, hi, lo))
+      flag(p.status, NK_DEVFLAG_RANGE);
+    merge_lanes();
+    float* hi_s = reinterpret_cast<float*>(smem) + warp * 2 * D;
+    if (lane < LPR) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        *reinterpret_cast<float4*>(hi_s + c0 + i) = make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+        *reinterpret_cast<float4*>(hi_s + D + c0 + i) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
+      }
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 0; w < kBndWarps; ++w)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        hi[i] = fmaxf(hi[i], reinterpret_cast<const float*>(smem)[w * 2 * D + c0 + i]);
+        lo[i] = fminf(lo[i], reinterpret_cast<const float*>(smem)[w * 2 * D + D + c0 + i]);
+      }
+    store(rec);
+    return;
+  }
+
+  // ---- a warp for each item
+  constexpr int kStage = bounds_stage<D>();
+  uint8_t* ring = smem + warp * kBndStages * kStage;
+  const uint32_t bar0 = smem_u32(bars[warp]);
+  if (lane < kBndStages) {
+    mbar_init(bar0 + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  const int64_t stride = (int64_t)gridDim.x * kBndWarps;
+  int64_t x = (int64_t)blockIdx.x * kBndWarps + warp;  // the next item to copy
+  int page = -1, filled = 0, key = 0, issued = 0;
+  const auto next_page = [&]() {
+    for (; x < items; x += stride) {
+      page = look(x, filled);
+      if (page >= 0) break;
+    }
+    key = 0;
+  };
+  const auto issue = [&]() {
+    if (x >= items) return;
+    const int st = issued % kBndStages, rows = min(kBndKeys, filled - key), all = (rows + 15) / 16 * 16;
+    const int64_t rec = (int64_t)page * p.Hkv + x % p.Hkv;
+    if (lane == 0) {
+      meta[warp][st] = make_int4((int)(rec >> 31), (int)(rec & 0x7fffffff), rows, key + rows >= filled);
+      const uint8_t* chunk = p.pool + rec * p.lay.chunk;
+      const uint32_t dst = smem_u32(ring + st * kStage), bar = bar0 + 8 * st;
+      mbar_arrive_expect_tx(bar, all * (D + GR * 4));
+      bulk_load(dst, chunk + (int64_t)key * D, all * D, bar);
+      bulk_load(dst + kBndKeys * D, chunk + p.lay.ks + key * (GR * 4), all * (GR * 4), bar);
+    }
+    ++issued;
+    key += rows;
+    if (key >= filled) {
+      x += stride;
+      next_page();
+    }
+  };
+  next_page();
+  for (int i = 0; i < kBndStages - 1; ++i) issue();
+  clear();
+  for (int n = 0; n < issued; ++n) {
+    issue();
+    const int st = n % kBndStages;
+    if (!mbar_wait(bar0 + 8 * st, (uint32_t)(n / kBndStages) & 1u)) {  // (what follows is not waited for either)
+      flag(p.status, NK_DEVFLAG_TIMEOUT);
+      x = items;
+    }
+    __syncwarp();
+    const int4 m = meta[warp][st];
+    const uint8_t* codes = ring + st * kStage;
+    if (row_extremes<D, 4>(codes + c0, reinterpret_cast<const float*>(codes + kBndKeys * D) + c0 / kGroup, lane / LPR,
+                           32 / LPR, m.z, hi, lo))
+      flag(p.status, NK_DEVFLAG_RANGE);
+    if (m.w) {
+      merge_lanes();
+      store((int64_t)m.x << 31 | m.y);
+      clear();
+    }
+    __syncwarp();  // the stage's readers are done
   }
 }
 
@@ -532,6 +617,14 @@ using namespace nk;
 
 namespace {
 
+template <int D>
+cudaError_t launch_bounds(const BoundsParams& p, int grid, cudaStream_t st) {
+  constexpr int smem = kBndWarps * kBndStages * bounds_stage<D>();
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_bounds_kernel<D>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(page_bounds_kernel<D>, dim3((unsigned)grid), dim3(kBndThreads), (size_t)smem, st, p);
+}
+
 template <int D, int NT>
 cudaError_t launch_scores(const SelectParams& p, dim3 grid, cudaStream_t st) {
   const int smem = select_smem(D, NT);
@@ -577,13 +670,12 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
                        bounds_view(bounds_dev, pool->num_pages, pool->num_kv_heads, D), status_dev};
   const int sms = device_sms();
   int64_t grid = (int64_t)B * max_pages_per_seq * pool->num_kv_heads;
-  const int64_t most = (int64_t)(sms > 0 ? sms : 148) * 4;
+  const int64_t most = sms > 0 ? sms : 148;
   if (grid > most) grid = most;
-  const dim3 g((unsigned)grid), t(kBndThreads);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 256   ? launch_chained(page_bounds_kernel<256>, g, t, 0, st, p)
-                        : D == 128 ? launch_chained(page_bounds_kernel<128>, g, t, 0, st, p)
-                                   : launch_chained(page_bounds_kernel<64>, g, t, 0, st, p);
+  const cudaError_t e = D == 256   ? launch_bounds<256>(p, (int)grid, st)
+                        : D == 128 ? launch_bounds<128>(p, (int)grid, st)
+                                   : launch_bounds<64>(p, (int)grid, st);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 

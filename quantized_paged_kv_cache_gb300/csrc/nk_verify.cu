@@ -40,7 +40,6 @@ struct VerifyParams {
 
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
 constexpr int kVerUnroll = 16;
-constexpr float kVerOne = 4611686018427387904.f;  // 2^62: one, as a whole number
 constexpr uint64_t kVerCap = 0x7fffffffffffffffull;  // a sum of 2 or more ends here
 
 __device__ __forceinline__ uint64_t ver_add(uint64_t a, uint64_t b) {  // (both at most the cap)
@@ -53,9 +52,20 @@ __device__ __forceinline__ uint64_t ver_warp_sum(uint64_t v) {
   return v;
 }
 
-// r of one token; NaN and negative ones count as zero, more than one as one.
+// r of one token as a multiple of 2^-62, cut off below; NaN and negative ones
+// count as zero, more than one as one. With r = 2^(e - 127) 1.m that is 1.m at bit
+// 62, moved right by 127 - e: shifts, since the conversion to 64 bits was what the
+// first form waited for.
+__device__ __forceinline__ uint32_t shr_all(uint32_t x, uint32_t s) {  // (0 past 31)
+  uint32_t y;
+  asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(s));
+  return y;
+}
 __device__ __forceinline__ uint64_t ver_weight(float p, float q) {
-  return __float2ull_rz(fminf(fmaxf(p - q, 0.f), 1.f) * kVerOne);
+  const uint32_t b = __float_as_uint(fminf(fmaxf(p - q, 0.f), 1.f));
+  const uint32_t top = ((b << 7) & 0x3fffffffu) | 0x40000000u, s = 127u - (b >> 23);
+  const uint32_t hi = shr_all(top, s), lo = s < 32u ? __funnelshift_rc(0u, top, s) : shr_all(top, s - 32u);
+  return (uint64_t)hi << 32 | lo;
 }
 
 template <int CL>

@@ -32,7 +32,10 @@ namespace nk {
 // by the K half of the cache, and by mma.sync for the T = 16 of a window over a
 // prompt.
 // ---------------------------------------------------------------------------
-constexpr int kWgtThreads = 256, kWgtWarps = kWgtThreads / 32;
+// Warps of a CTA: for one tile of rows sixteen that take 16 keys a step (a step's
+// chain of wait, products and exponentials is longer than its time, and more warps
+// cover it), else eight that take 32, which halve the reads of the rows.
+constexpr int lse_warps(int NT) { return NT == 1 ? 16 : 8; }
 
 // A step of a warp in its ring: KB times 16 keys' codes, a lane's pieces 512 bytes
 // apart, then their scales.
@@ -47,12 +50,12 @@ struct KeyStep {
 // rows' powers of two [rows], the chunk's rows as fp16 [rows][D / 2 + 2 words],
 // the rings.
 __host__ __device__ inline int weight_ring_off(int D, int chunk) {
-  return (kWgtWarps * chunk * 8 + chunk * 4 + chunk * (D * 2 + 8) + 15) / 16 * 16;
+  return (lse_warps(chunk / 8) * chunk * 8 + chunk * 4 + chunk * (D * 2 + 8) + 15) / 16 * 16;
 }
 // Steps in a warp's ring: three where 227 KB hold them.
 template <int D, int NT, int KB>
 constexpr int weight_stages() {
-  return (kWgtWarps * NT * 64 + NT * 32 + NT * 8 * (D * 2 + 8) + 16 + kWgtWarps * 3 * KeyStep<D, KB>::kBytes +
+  return (lse_warps(NT) * (NT * 64 + 3 * KeyStep<D, KB>::kBytes) + NT * 32 + NT * 8 * (D * 2 + 8) + 16 +
           (2 * kMaxBatch + 16) * 4 <= 227 * 1024)
              ? 3
              : 2;
@@ -67,14 +70,15 @@ __device__ __forceinline__ void copy_async_small(uint32_t dst, const void* src) 
 }
 
 template <int D, int NT, int KB>
-__global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightParams p) {
+__global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const WeightParams p) {
+  constexpr int kWarps = lse_warps(NT), kThreads = kWarps * 32;
   constexpr int RS = D * 2 + 8;
   constexpr int NG = D / kGroup;
   constexpr int ROWS = NT * 8;
   constexpr int S = weight_stages<D, NT, KB>();
   using Step = KeyStep<D, KB>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int pre[kMaxBatch + 1], lens[kMaxBatch], warp_tot[kWgtWarps];
+  __shared__ int pre[kMaxBatch + 1], lens[kMaxBatch], warp_tot[kWarps];
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
@@ -82,13 +86,13 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
   const int P = sh.P, Hkv = sh.Hkv, T = sh.T, G = p.G, M = T * G;
   const int row0 = blockIdx.x * ROWS;  // the CTA's chunk of rows
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int b = tid; b < sh.B; b += kWgtThreads)
+    for (int b = tid; b < sh.B; b += kThreads)
       if (pages_of_len(sh, p.ctx[b]) == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
   block_page_prefix_short(sh, p.ctx, 0, pre, warp_tot, lens);
   const int64_t W = (int64_t)pre[sh.B] * Hkv;
   if (W == 0) return;
   float2* seg_st = reinterpret_cast<float2*>(smem) + warp * ROWS;
-  float* undo = reinterpret_cast<float*>(smem + kWgtWarps * ROWS * 8);  // sm_scale log2(e) / the row's power of two
+  float* undo = reinterpret_cast<float*>(smem + kWarps * ROWS * 8);  // sm_scale log2(e) / the row's power of two
   uint8_t* qs = reinterpret_cast<uint8_t*>(undo + ROWS);
   uint8_t* ring = smem + weight_ring_off(D, ROWS) + warp * S * Step::kBytes;
   const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
     // ---- the copies: page and step of the next one, its page id, the one after's
     int c_pg = warp, c_st = 0, c_slot = 0;
     uint32_t none = 0, c_bit = 1;  // steps in flight whose page is none (a bit each, in turn)
-    int id = c_pg < pages ? row_bt[c_pg] : 0, id_next = c_pg + kWgtWarps < pages ? row_bt[c_pg + kWgtWarps] : 0;
+    int id = c_pg < pages ? row_bt[c_pg] : 0, id_next = c_pg + kWarps < pages ? row_bt[c_pg + kWarps] : 0;
     const auto issue = [&]() {
       if (c_pg < pages) {
         const bool bad = id < 0 || id >= p.num_pages;
@@ -130,9 +134,9 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
         if (++c_slot == S) c_slot = 0;
         if ((++c_st) * 16 * KB >= live_of(c_pg)) {
           c_st = 0;
-          c_pg += kWgtWarps;
+          c_pg += kWarps;
           id = id_next;
-          if (c_pg + kWgtWarps < pages) id_next = row_bt[c_pg + kWgtWarps];
+          if (c_pg + kWarps < pages) id_next = row_bt[c_pg + kWarps];
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue();
     // ---- the unit's rows: a warp each, scaled into [2^14, 2^15)
-    for (int r = warp; r < ROWS; r += kWgtWarps) {
+    for (int r = warp; r < ROWS; r += kWarps) {
       const int row = row0 + r, t = row / G, hg = row - t * G;
       const uint16_t* src = p.q + (((int64_t)seg.b * T + t) * (G * Hkv) + seg.h * G + hg) * D;
       constexpr int PER = D / 64;  // words of a lane
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
     __syncthreads();
     int slot = 0;
     uint32_t bit = 1;
-    for (int pg = warp; pg < pages; pg += kWgtWarps) {  // (warp-uniform)
+    for (int pg = warp; pg < pages; pg += kWarps) {  // (warp-uniform)
       const int logical = seg.page_begin + pg, live = live_of(pg);
       float m[NT][2], l[NT][2];
 #pragma unroll
@@ -301,9 +305,9 @@ __global__ void __launch_bounds__(kWgtThreads, 1) page_lse_kernel(const WeightPa
     }
     __syncthreads();
     const float2* all = reinterpret_cast<const float2*>(smem);
-    for (int r = tid; r < ROWS; r += kWgtThreads) {
+    for (int r = tid; r < ROWS; r += kThreads) {
       float m = -INFINITY, l = 0.f;
-      for (int w = 0; w < kWgtWarps; ++w) lse_join(m, l, all[w * ROWS + r].x, all[w * ROWS + r].y);
+      for (int w = 0; w < kWarps; ++w) lse_join(m, l, all[w * ROWS + r].x, all[w * ROWS + r].y);
       p.seg_lse[((int64_t)blockIdx.y + seg.u) * p.rows + row0 + r] = lse_of(m, l);
     }
     item += pages;
@@ -518,8 +522,11 @@ using namespace nk;
 
 namespace {
 
-// From how many rows on the tcgen05 kernel takes a call.
-constexpr int kTcRows = 25;
+// From how many rows on the tcgen05 kernel takes a call: past one chunk of the
+// mma.sync kernel, which would read the keys once more for each (8 sequences at 8K
+// to 64K, 24 heads over 4: 48 rows 174 us on mma.sync and 194 on tcgen05, 72 rows
+// 322 and 209, 96 rows 323 and 215).
+constexpr int kTcRows = 49;
 
 // Row tiles of the mma.sync kernel's instances: 1, 2, 3, 4, 6; with 16-key pages
 // (steps of 16 keys) 1, 3, 6.
@@ -554,22 +561,21 @@ int weight_ctas(int64_t items, const WeightRows& r) {
 
 template <int D, int NT, int KB>
 cudaError_t launch_lse(const WeightParams& p, int chunks, cudaStream_t st) {
-  const int smem = weight_ring_off(D, NT * 8) + kWgtWarps * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes;
+  const int smem = weight_ring_off(D, NT * 8) + lse_warps(NT) * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes;
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_lse_kernel<D, NT, KB>), smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(kWgtThreads),
+  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(lse_warps(NT) * 32),
                         (size_t)smem, st, p);
 }
 
 template <int D>
 cudaError_t launch_lse_d(const WeightParams& p, int chunks, cudaStream_t st) {
+  if (p.chunk == 8) return launch_lse<D, 1, 1>(p, chunks, st);
   if (p.sh.P == 16) switch (p.chunk / 8) {
-      case 1: return launch_lse<D, 1, 1>(p, chunks, st);
       case 3: return launch_lse<D, 3, 1>(p, chunks, st);
       default: return launch_lse<D, 6, 1>(p, chunks, st);
     }
   switch (p.chunk / 8) {
-    case 1: return launch_lse<D, 1, 2>(p, chunks, st);
     case 2: return launch_lse<D, 2, 2>(p, chunks, st);
     case 3: return launch_lse<D, 3, 2>(p, chunks, st);
     case 4: return launch_lse<D, 4, 2>(p, chunks, st);

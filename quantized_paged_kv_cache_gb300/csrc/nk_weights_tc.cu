@@ -75,14 +75,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // K-major operand, 128-byte swizzle, atoms of 8 rows of 128 bytes, 1,024 bytes apart
-__device__ __forceinline__ uint64_t desc_of(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)1 << 16 |
-         (uint64_t)((1024 >> 4) | (1u << 14) | (2u << 29)) << 32;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -390,26 +389,31 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
     set_regs<kRegsRest>();
     if (warp == kMmaWarp) {
       // ------------------------------------------------------------ products
+      // The whole warp runs the loop and one elected lane issues. All 512 columns are
+      // this CTA's, so tensor memory starts at address 0: with that every operand of a
+      // product is a uniform register (a lane on its own, with the address from shared
+      // memory, took some 100 cycles for each).
+      const bool leader = elect_one();
       constexpr uint32_t id = idesc_f16(kRowsMost, kKeys);
       int done[2] = {0, 0};  // commits of each set
-      const uint64_t qa = desc_of(smem_u32(smem + SM::off_q)), kb = desc_of(smem_u32(smem + SM::off_b));
+      const uint32_t qa = desc_lo(smem_u32(smem + SM::off_q)), kb = desc_lo(smem_u32(smem + SM::off_b));
       for (int n = 0;; ++n) {
         const int buf = n & 1;
         wait(b_full(buf), (uint32_t)(n >> 1) & 1u);
-        const Tile* d = desc + n % kScales;
-        if (d->len == 0) break;
-        if (d->first) wait(rows_full(d->seg % kRowSets), (uint32_t)(d->seg / kRowSets) & 1u);
+        const Tile* t = desc + n % kScales;
+        if (t->len == 0) break;
+        if (t->first) wait(rows_full(t->seg % kRowSets), (uint32_t)(t->seg / kRowSets) & 1u);
         if (n >= 2) wait(acc_empty(buf), (uint32_t)((n >> 1) - 1) & 1u);
         if (__any_sync(0xffffffffu, *abort_flag != 0)) continue;
         ++done[buf];
-        fence_after();
-        if (elect_one()) {
+        if (leader) {
+          fence_after();
+          const uint32_t d = buf * NG * kKeys, k0 = kb + buf * ((NG * kKeys * 128) >> 4);
 #pragma unroll
           for (int c = 0; c < NG; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ss(tmem + buf * NG * kKeys + c * kKeys, qa + ((c * kRowsMost * 128 + k * 32) >> 4),
-                     kb + ((buf * NG * kKeys * 128 + c * kKeys * 128 + k * 32) >> 4), id, k > 0 ? 1u : 0u);
+              mma_ss(d + c * kKeys, qa + ((c * kRowsMost * 128 + k * 32) >> 4), k0 + ((c * kKeys * 128 + k * 32) >> 4), id, k > 0);
           mma_commit(b_empty(buf));
           mma_commit(acc_full(buf));
         }

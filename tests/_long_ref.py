@@ -181,7 +181,8 @@ def verify(p, q, drafts, u, num=None):
         r = np.clip(np.nan_to_num(r, nan=0.0), 0, 1)
         w = whole(r)
         total = sum(w)
-        ut = min(max(float(u[b, T - 1]), 0.0), 1 - 2.0 ** -24)
+        ut = float(u[b, T - 1])
+        ut = min(max(ut, 0.0), 1 - 2.0 ** -24) if ut == ut else 0.0
         num_u, run = int(ut * 2.0 ** 149) if ut < 2.0 ** -60 else int(ut * 2.0 ** 100) * 2 ** 49, 0
         for i, x in enumerate(w):
             run += x
