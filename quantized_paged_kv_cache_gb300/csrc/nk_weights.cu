@@ -5,6 +5,7 @@
 
 #include "nk_common.cuh"
 #include "nk_host.cuh"
+#include "nk_ptx.cuh"
 #include "nk_topk.cuh"
 #include "nk_weights.cuh"
 
@@ -20,70 +21,68 @@ namespace nk {
 //
 // First kernel: the flat list of (sequence, kv-head, page) items is cut into one
 // range a CTA (nk_common.cuh), a warp takes a page of the segment at a time, KB
-// times 16 keys a step. Each warp has a ring of steps in shared memory that it
-// fills with asynchronous copies of 16 bytes a thread: what a thread copies is
-// what it reads again, 16 consecutive channels of a key, in the product's K order
-// four steps of four, so the layout is the lanes' own and needs no swizzle, and no
-// warp waits for another. Codes enter mma.m16n8k16 as exact fp16, the query rows
-// as fp16 scaled by a power of two each (exact for channels within 2^24 of the
-// row's largest), fp32 sums by 64-channel group, then the group's scale. Keys are M
-// and query rows N, so a decode step pads six rows to eight; more than 48 rows run
-// as chunks, in CTAs beside one another that find each other's keys in L2. Bounded
-// by the K half of the cache, and by mma.sync for the T = 16 of a window over a
-// prompt.
+// times 16 keys a step, from a ring of its own in shared memory that bulk
+// asynchronous copies fill; no warp waits for another. A thread reads 16
+// consecutive channels of a key, in the product's K order four steps of four.
+// Codes enter mma.m16n8k16 as exact fp16, the query rows as fp16 scaled by a power
+// of two each (exact for channels within 2^24 of the row's largest), fp32 sums by
+// 64-channel group, then the group's scale. Keys are M and query rows N, so a
+// decode step pads six rows to eight (one tile, whose rows stay in registers); more
+// than 48 rows go to the tcgen05 kernel (nk_weights_tc.cu). Bounded by the K half
+// of the cache and, for several tiles of rows, by instructions.
 // ---------------------------------------------------------------------------
-// Warps of a CTA: for one tile of rows sixteen that take 16 keys a step (a step's
-// chain of wait, products and exponentials is longer than its time, and more warps
-// cover it), else eight that take 32, which halve the reads of the rows.
-constexpr int lse_warps(int NT) { return NT == 1 ? 16 : 8; }
+// ---------------------------------------------------------------------------
+constexpr int kWgtThreads = 256, kWgtWarps = kWgtThreads / 32;
 
-// A step of a warp in its ring: KB times 16 keys' codes, a lane's pieces 512 bytes
-// apart, then their scales.
+// A step of a warp in its ring: KB times 16 keys' codes, then their scales.
 template <int D, int KB>
 struct KeyStep {
   static constexpr int NG = D / kGroup;
-  static constexpr int kCodes = KB * 2 * NG * 512;
+  static constexpr int kCodes = KB * 16 * D;
   static constexpr int kBytes = kCodes + KB * 16 * NG * 4;
 };
 
 // Shared memory: each warp's running log-sums of the segment [rows] float2, the
 // rows' powers of two [rows], the chunk's rows as fp16 [rows][D / 2 + 2 words],
-// the rings.
+// the rings, the
+// page prefix and the lengths [2 B + 1].
 __host__ __device__ inline int weight_ring_off(int D, int chunk) {
-  return (lse_warps(chunk / 8) * chunk * 8 + chunk * 4 + chunk * (D * 2 + 8) + 15) / 16 * 16;
+  return (kWgtWarps * chunk * 8 + chunk * 4 + chunk * (D * 2 + 8) + 15) / 16 * 16;
 }
-// Steps in a warp's ring: three where 227 KB hold them.
+// Steps in a warp's ring: three where 227 KB hold them. One tile of rows takes
+// steps of 16 keys and two CTAs an SM: their chains of waits cover each other, and
+// the kernels before and behind find room beside one that ends.
 template <int D, int NT, int KB>
 constexpr int weight_stages() {
-  return (lse_warps(NT) * (NT * 64 + 3 * KeyStep<D, KB>::kBytes) + NT * 32 + NT * 8 * (D * 2 + 8) + 16 +
-          (2 * kMaxBatch + 16) * 4 <= 227 * 1024)
+  return (kWgtWarps * (NT * 64 + 3 * KeyStep<D, KB>::kBytes) + NT * 32 + NT * 8 * (D * 2 + 8) + 16 +
+          (2 * kMaxBatch + 32) * 4 + kWgtWarps * 3 * 8 <= 227 * 1024)
              ? 3
              : 2;
 }
-
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int BYTES>
-__device__ __forceinline__ void copy_async_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
+constexpr int lse_ctas(int NT) { return NT == 1 ? 2 : 1; }  // of an SM
 
 template <int D, int NT, int KB>
-__global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const WeightParams p) {
-  constexpr int kWarps = lse_warps(NT), kThreads = kWarps * 32;
+__global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(const WeightParams p) {
+  constexpr int kWarps = kWgtWarps, kThreads = kWgtThreads;
   constexpr int RS = D * 2 + 8;
   constexpr int NG = D / kGroup;
   constexpr int ROWS = NT * 8;
   constexpr int S = weight_stages<D, NT, KB>();
   using Step = KeyStep<D, KB>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int pre[kMaxBatch + 1], lens[kMaxBatch], warp_tot[kWarps];
+  __shared__ int warp_tot[kWarps];
+  __shared__ uint64_t bars[kWarps][S];
+  if (threadIdx.x < kWarps * S) {
+    mbar_init(smem_u32(&bars[0][0] + threadIdx.x), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const SplitShape& sh = p.sh;
   const int P = sh.P, Hkv = sh.Hkv, T = sh.T, G = p.G, M = T * G;
+  int* pre = reinterpret_cast<int*>(smem + weight_ring_off(D, ROWS) + kWarps * S * Step::kBytes);  // [B + 1]
+  int* lens = pre + sh.B + 1;                                                                     // [B]
   const int row0 = blockIdx.x * ROWS;  // the CTA's chunk of rows
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = tid; b < sh.B; b += kThreads)
@@ -95,51 +94,46 @@ __global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const W
   float* undo = reinterpret_cast<float*>(smem + kWarps * ROWS * 8);  // sm_scale log2(e) / the row's power of two
   uint8_t* qs = reinterpret_cast<uint8_t*>(undo + ROWS);
   uint8_t* ring = smem + weight_ring_off(D, ROWS) + warp * S * Step::kBytes;
-  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t ring_u32 = smem_u32(ring), bar0 = smem_u32(bars[warp]);
   int64_t x = cta_begin(W, p.n_ctas, blockIdx.y);
   const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.y + 1);
   Segment seg;
   int64_t item = x;  // of the segment's first page
+  int issued = 0, used = 0;  // steps
+  bool timed_out = false;
   while (next_segment(sh, pre, x, x_end, seg)) {
     const int L = lens[seg.b], pages = seg.page_end - seg.page_begin;
     const int32_t* row_bt = p.bt + (int64_t)seg.b * sh.max_pages + seg.page_begin;
     const auto live_of = [&](int pg) { return min(P, L - (seg.page_begin + pg) * P); };
     // ---- the copies: page and step of the next one, its page id, the one after's
-    int c_pg = warp, c_st = 0, c_slot = 0;
-    uint32_t none = 0, c_bit = 1;  // steps in flight whose page is none (a bit each, in turn)
+    int c_pg = warp, c_k = 0;
+    uint32_t none = 0;  // steps in flight whose page is none: a bit each, by their number in the CTA
     int id = c_pg < pages ? row_bt[c_pg] : 0, id_next = c_pg + kWarps < pages ? row_bt[c_pg + kWarps] : 0;
-    const auto issue = [&]() {
-      if (c_pg < pages) {
-        const bool bad = id < 0 || id >= p.num_pages;
-        none = bad ? none | c_bit : none & ~c_bit;
-        c_bit = c_bit << 1 | c_bit >> 31;
-        const uint8_t* chunk = p.pool + ((int64_t)(bad ? 0 : id) * Hkv + seg.h) * p.lay.chunk;
-        const uint32_t dst = ring_u32 + c_slot * Step::kBytes;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = min(c_st * 16 * KB + 16 * kb, P - 16) + g + 8 * i;  // (past the page: its last 16, masked later)
-#pragma unroll
-            for (int c = 0; c < NG; ++c)
-              copy_async16(dst + ((kb * 2 + i) * NG + c) * 512 + lane * 16, chunk + key * D + 64 * c + 16 * t4);
-          }
-        if (lane < 16 * KB) {
-          const int key = min(c_st * 16 * KB + (lane & ~15), P - 16) + (lane & 15);
-          const uint8_t* src = chunk + p.lay.ks + key * (NG * 4);
-          const uint32_t to = dst + Step::kCodes + lane * (NG * 4);
-          if constexpr (NG == 4) copy_async16(to, src);
-          else copy_async_small<NG * 4>(to, src);
-        }
-        if (++c_slot == S) c_slot = 0;
-        if ((++c_st) * 16 * KB >= live_of(c_pg)) {
-          c_st = 0;
-          c_pg += kWarps;
-          id = id_next;
-          if (c_pg + kWarps < pages) id_next = row_bt[c_pg + kWarps];
+    const auto issue = [&]() {  // (warp-uniform)
+      if (c_pg >= pages) return;
+      const int live = live_of(c_pg), slot = issued % S, keys = min(16 * KB, (live - c_k + 15) / 16 * 16);
+      const bool bad = id < 0 || id >= p.num_pages;
+      const uint32_t bit = 1u << (issued & 31);
+      none = bad ? none | bit : none & ~bit;
+      if (lane == 0) {
+        const uint32_t dst = ring_u32 + slot * Step::kBytes, bar = bar0 + 8 * slot;
+        if (bad || timed_out) {
+          mbar_arrive(bar);
+        } else {
+          const uint8_t* chunk = p.pool + ((int64_t)id * Hkv + seg.h) * p.lay.chunk;
+          mbar_arrive_expect_tx(bar, keys * (D + NG * 4));
+          bulk_load(dst, chunk + c_k * D, keys * D, bar);
+          bulk_load(dst + Step::kCodes, chunk + p.lay.ks + c_k * (NG * 4), keys * (NG * 4), bar);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++issued;
+      c_k += 16 * KB;
+      if (c_k >= live) {
+        c_k = 0;
+        c_pg += kWarps;
+        id = id_next;
+        if (c_pg + kWarps < pages) id_next = row_bt[c_pg + kWarps];
+      }
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue();
@@ -168,8 +162,13 @@ __global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const W
     }
     for (int i = lane; i < ROWS; i += 32) seg_st[i] = make_float2(-INFINITY, 0.f);
     __syncthreads();
-    int slot = 0;
-    uint32_t bit = 1;
+    uint2 bq[NT == 1 ? NG : 1][4];  // one tile: the rows as the products take them
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int c = 0; c < NG; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bq[c][j] = *reinterpret_cast<const uint2*>(qs + g * RS + 32 * t4 + 128 * c + 8 * j);
+    }
     for (int pg = warp; pg < pages; pg += kWarps) {  // (warp-uniform)
       const int logical = seg.page_begin + pg, live = live_of(pg);
       float m[NT][2], l[NT][2];
@@ -182,13 +181,17 @@ __global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const W
         }
       for (int k0 = 0; k0 < live; k0 += 16 * KB) {
         issue();
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        __syncwarp();
-        const bool bad = (none & bit) != 0;
-        bit = bit << 1 | bit >> 31;
+        const int slot = used % S;
+        // (after a wait that ran out nothing is copied, and nothing waited for but copies under way)
+        if (!mbar_wait(bar0 + 8 * slot, (uint32_t)(used / S) & 1u)) {
+          flag(p.status, NK_DEVFLAG_TIMEOUT);
+          timed_out = true;
+        }
+        timed_out = __any_sync(0xffffffffu, timed_out);
+        const bool bad = (none >> (used & 31)) & 1u;
+        ++used;
         if (bad && lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
         const uint8_t* step = ring + slot * Step::kBytes;
-        if (++slot == S) slot = 0;
         const int pos0 = logical * P + k0;
         const bool edge = bad || k0 + 16 * KB > live || pos0 + 16 * KB - 1 > L - T;  // some row does not see some key
         float s[NT][KB][4];
@@ -198,17 +201,29 @@ __global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const W
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[nt][kb][k] = 0.f;
+        float sc[KB][2][NG];  // the scales of keys g and g + 8
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float* f = reinterpret_cast<const float*>(step + Step::kCodes) + (kb * 16 + g + 8 * i) * NG;
+            if constexpr (NG == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(f);
+              sc[kb][i][0] = v.x, sc[kb][i][1] = v.y, sc[kb][i][2] = v.z, sc[kb][i][3] = v.w;
+            } else if constexpr (NG == 2) {
+              const float2 v = *reinterpret_cast<const float2*>(f);
+              sc[kb][i][0] = v.x, sc[kb][i][1] = v.y;
+            } else {
+              sc[kb][i][0] = *f;
+            }
+          }
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
           uint32_t a[KB][4][4];
-          float sc[KB][2];
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            const uint4 r0 = *reinterpret_cast<const uint4*>(step + ((kb * 2 + 0) * NG + c) * 512 + lane * 16);
-            const uint4 r1 = *reinterpret_cast<const uint4*>(step + ((kb * 2 + 1) * NG + c) * 512 + lane * 16);
-            const float* scales = reinterpret_cast<const float*>(step + Step::kCodes) + (kb * 16 + g) * NG + c;
-            sc[kb][0] = scales[0];
-            sc[kb][1] = scales[8 * NG];
+            const uint8_t* src = step + (kb * 16 + g) * D + 64 * c + 16 * t4;
+            const uint4 r0 = *reinterpret_cast<const uint4*>(src), r1 = *reinterpret_cast<const uint4*>(src + 8 * D);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t w0 = (j == 0 ? r0.x : j == 1 ? r0.y : j == 2 ? r0.z : r0.w) ^ 0x80808080u;
@@ -228,17 +243,19 @@ __global__ void __launch_bounds__(lse_warps(NT) * 32, 1) page_lse_kernel(const W
               for (int k = 0; k < 4; ++k) acc[kb][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint2 b = *reinterpret_cast<const uint2*>(qs + (nt * 8 + g) * RS + 32 * t4 + 128 * c + 8 * j);
+              uint2 b;
+              if constexpr (NT == 1) b = bq[c][j];
+              else b = *reinterpret_cast<const uint2*>(qs + (nt * 8 + g) * RS + 32 * t4 + 128 * c + 8 * j);
 #pragma unroll
               for (int kb = 0; kb < KB; ++kb)
                 wgt_mma(acc[kb], a[kb][j][0], a[kb][j][1], a[kb][j][2], a[kb][j][3], b.x, b.y);
             }
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-              s[nt][kb][0] = fmaf(sc[kb][0], acc[kb][0], s[nt][kb][0]);
-              s[nt][kb][1] = fmaf(sc[kb][0], acc[kb][1], s[nt][kb][1]);
-              s[nt][kb][2] = fmaf(sc[kb][1], acc[kb][2], s[nt][kb][2]);
-              s[nt][kb][3] = fmaf(sc[kb][1], acc[kb][3], s[nt][kb][3]);
+              s[nt][kb][0] = fmaf(sc[kb][0][c], acc[kb][0], s[nt][kb][0]);
+              s[nt][kb][1] = fmaf(sc[kb][0][c], acc[kb][1], s[nt][kb][1]);
+              s[nt][kb][2] = fmaf(sc[kb][1][c], acc[kb][2], s[nt][kb][2]);
+              s[nt][kb][3] = fmaf(sc[kb][1][c], acc[kb][3], s[nt][kb][3]);
             }
           }
         }
@@ -551,20 +568,21 @@ WeightRows weight_rows(int T, int G, int P) {
   return {false, n, weight_tiles(tiles, P) * 8, 1, 1};
 }
 
-// CTAs along the pages: one an SM, shared by the chunks.
+// CTAs along the pages: as many as an SM holds, shared by the chunks.
 int weight_ctas(int64_t items, const WeightRows& r) {
   const int sms = device_sms();
-  int64_t n = (int64_t)(sms > 0 ? sms : 148) / r.chunks;
+  int64_t n = (int64_t)(sms > 0 ? sms : 148) * (r.tc ? 1 : lse_ctas(r.chunk / 8)) / r.chunks;
   if (n < 1) n = 1;
   return (int)(items < n ? (items < 1 ? 1 : items) : n);
 }
 
 template <int D, int NT, int KB>
 cudaError_t launch_lse(const WeightParams& p, int chunks, cudaStream_t st) {
-  const int smem = weight_ring_off(D, NT * 8) + lse_warps(NT) * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes;
+  const int smem = weight_ring_off(D, NT * 8) + kWgtWarps * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes +
+                   (2 * p.sh.B + 1) * 4;
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_lse_kernel<D, NT, KB>), smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(lse_warps(NT) * 32),
+  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(kWgtThreads),
                         (size_t)smem, st, p);
 }
 
