@@ -387,7 +387,7 @@ int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t
                         void* out_dev, int32_t* status_dev, void* stream);
 
 /*
- * Long caches. The next five read less of a long cache, or keep less of it, and
+ * Long caches. The next calls read less of a long cache, or keep less of it, and
  * nk_verify_drafts ends a verify round; none has a counterpart on the pages.
  *
  * nk_page_bounds -- of each touched page and kv-head, the largest and smallest
@@ -413,6 +413,11 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
                    const int32_t* start_pos_dev, const int32_t* cu_new_dev, int32_t B, int32_t* status_dev,
                    void* stream);
 
+/* The values that the bounds stand for, code * scale: fp32
+ * [num_pages][Hkv][hi | lo][D], 16-byte aligned, for a choice by another rule. */
+int nk_page_bounds_values(const void* bounds_dev, int32_t num_pages, int32_t num_kv_heads, int32_t head_dim,
+                          float* values_dev, void* stream);
+
 /*
  * nk_page_select -- the k pages of each query token and kv-head whose bounds
  * promise the largest score, for nk_paged_sparse_attn.
@@ -423,7 +428,8 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
  *                  any case; recent_pages >= 1 (the last pages are not full, and
  *                  their bounds are not read), sink_pages + recent_pages <= k
  *   workspace_dev  nk_page_select_workspace_bytes(...) bytes, 16-byte aligned;
- *                  scratch. Calls that may overlap on the GPU need one each.
+ *                  scratch; 0 bytes (and no pointer) for most sizes. Calls that
+ *                  may overlap on the GPU need one each.
  *   pages_dev      int32 [B][T][Hkv][k]: the pages' numbers in the sequence,
  *                  ascending, -1 behind them where the token sees fewer than k
  * The score of a page is s * max over the G query heads of
@@ -436,7 +442,8 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
  * finite come last. An invalid context length sets NK_DEVFLAG_BAD_CTX and leaves
  * its sequence's lists as they were. G is at most 48, B * Hkv 65,535.
  */
-size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_kv_heads, int32_t page_size, int32_t max_ctx);
+size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t page_size, int32_t max_ctx);
 int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
                    const void* q_dev, const int32_t* block_table_dev, int32_t max_pages_per_seq,
                    const int32_t* ctx_lens_dev, int32_t B, int32_t T, int32_t num_q_heads, int32_t max_ctx, int32_t k,

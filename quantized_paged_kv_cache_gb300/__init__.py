@@ -667,27 +667,39 @@ class PageBounds:
         """int8 [num_pages][Hkv][2][D], a view."""
         import torch
 
-        n, h, d = self.num_pages, self.num_kv_heads, self.head_dim
-        return self.storage.view(torch.int8).as_strided((n, h, 2, d), (h * 2 * d, 2 * d, d, 1), 0)
-
-    def _scales(self, *ones):
-        import torch
-
-        n, h = self.num_pages, self.num_kv_heads
-        return self.storage.view(torch.float32).as_strided((n, h, *ones), (h, 1, *ones), self._codes_bytes() // 4)
+        n = self._codes_bytes()
+        return self.storage[:n].view(torch.int8).view(self.num_pages, self.num_kv_heads, 2, self.head_dim)
 
     def scales(self):
         """fp32 [num_pages][Hkv], a view."""
-        return self._scales()
+        import torch
 
-    def values(self):
-        """fp32 [num_pages][Hkv][2][D]: the largest and smallest values that the codes stand for."""
-        return self.codes() * self._scales(1, 1)
+        n = self._codes_bytes()
+        return self.storage[n:n + 4 * self.num_pages * self.num_kv_heads].view(torch.float32).view(
+            self.num_pages, self.num_kv_heads)
+
+    def values(self, out=None, stream=None):
+        """fp32 [num_pages][Hkv][2][D]: the largest and smallest values that the codes stand for (nk_page_bounds_values)."""
+        import torch
+
+        _need_scratch(self.storage, None)
+        self._check()
+        shape = (self.num_pages, self.num_kv_heads, 2, self.head_dim)
+        if out is None:
+            out = _empty(stream, self.storage, shape, torch.float32)
+        else:
+            _need(torch.float32, out)
+            if out.shape != shape:
+                raise ValueError("out must be [num_pages][kv-heads][2][head_dim]")
+        rc = lib().nk_page_bounds_values(self.storage.data_ptr(), self.num_pages, self.num_kv_heads, self.head_dim,
+                                         out.data_ptr(), _stream(stream))
+        _check(rc, "nk_page_bounds_values")
+        return out
 
     def _check(self) -> None:
-        n = self.storage.numel()
-        if self.storage.element_size() != 1 or n % 4 != 0 or n < self._codes_bytes() + 4 * self.num_pages * self.num_kv_heads:
-            raise ValueError("the bounds' storage must be page_bounds_bytes(...) bytes (or more, in whole fours)")
+        storage = self.storage
+        if storage.element_size() != 1 or storage.numel() < self.num_pages * self.num_kv_heads * (2 * self.head_dim + 4):
+            raise ValueError("the bounds' storage must be a tensor of page_bounds_bytes(...) bytes")
 
 
 def page_bounds(pool: KVPool, bounds: PageBounds, block_table, start_pos, cu_new, status=None, stream=None) -> None:
@@ -709,13 +721,13 @@ def page_bounds(pool: KVPool, bounds: PageBounds, block_table, start_pos, cu_new
     _check(rc, "nk_page_bounds")
 
 
-def page_select_workspace_bytes(B: int, T: int, num_kv_heads: int, page_size: int, max_ctx: int) -> int:
-    return int(lib().nk_page_select_workspace_bytes(B, T, num_kv_heads, page_size, max_ctx))
+def page_select_workspace_bytes(B: int, T: int, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int,
+                                max_ctx: int) -> int:
+    return int(lib().nk_page_select_workspace_bytes(B, T, num_q_heads, num_kv_heads, head_dim, page_size, max_ctx))
 
 
-def _small(what: str, *numbers_) -> None:
-    if not all(-_I32_MAX <= n <= _I32_MAX for n in numbers_):
-        raise ValueError(f"{what} must be below 2^31")
+def _large(*n):
+    raise ValueError(f"sizes and counts must lie between 0 and 2^31 - 1, not {n}")
 
 
 def page_select(bounds: PageBounds, q, block_table, ctx_lens, page_size: int, max_ctx: int, k: int, sink_pages: int = 1,
@@ -729,23 +741,26 @@ def page_select(bounds: PageBounds, q, block_table, ctx_lens, page_size: int, ma
     _need(torch.int32, block_table, ctx_lens, out, status)
     _need_scratch(bounds.storage, workspace)
     bounds._check()
-    _small("page_size, max_ctx, k, sink_pages and recent_pages", page_size, max_ctx, k, sink_pages, recent_pages)
+    if not (-1 < page_size <= _I32_MAX and -1 < max_ctx <= _I32_MAX and -1 < k <= _I32_MAX and -1 < sink_pages <= _I32_MAX
+            and -1 < recent_pages <= _I32_MAX):
+        _large(page_size, max_ctx, k, sink_pages, recent_pages)
     B, T, Hq, D = q.shape
     Hkv, shape = bounds.num_kv_heads, block_table.shape
     if D != bounds.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
         raise ValueError("q, block_table, ctx_lens and the bounds disagree on the batch or the head dim")
     if out is None:
-        out = _empty(stream, block_table, (B, T, Hkv, max(k, 0)), torch.int32)
+        out = _empty(stream, block_table, (B, T, Hkv, k), torch.int32)
     elif out.numel() != B * T * Hkv * k:
         raise ValueError("out must be [B][T][kv-heads][k]")
     if workspace is None:
-        wbytes = lib().nk_page_select_workspace_bytes(B, T, Hkv, page_size, max_ctx)
-        workspace = _empty(stream, q, max(wbytes, 16), torch.uint8)
+        wbytes = lib().nk_page_select_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_ctx)
+        if wbytes > 0:
+            workspace = _empty(stream, q, wbytes, torch.uint8)
     else:
         wbytes = workspace.numel() * workspace.element_size()
     rc = lib().nk_page_select(bounds.storage.data_ptr(), bounds.num_pages, page_size, Hkv, D, q.data_ptr(),
                               block_table.data_ptr(), shape[1], ctx_lens.data_ptr(), B, T, Hq, max_ctx, k, sink_pages,
-                              recent_pages, workspace.data_ptr(), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
+                              recent_pages, _ptr(workspace), wbytes, out.data_ptr(), _ptr(status), _stream(stream))
     _check(rc, "nk_page_select")
     return out
 
@@ -761,7 +776,8 @@ def paged_sparse_attn(pool: KVPool, q, block_table, ctx_lens, pages, sm_scale: f
     _need(torch.int32, block_table, ctx_lens, pages, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    _small("max_ctx and num_ctas", max_ctx, num_ctas)
+    if not (-1 < max_ctx <= _I32_MAX and -_I32_MAX <= num_ctas <= _I32_MAX):
+        _large(max_ctx, num_ctas)
     B, T, Hq, D = q.shape
     shape, lists, Hkv = block_table.shape, pages.shape, pool.num_kv_heads
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
@@ -803,7 +819,8 @@ def page_weights(pool: KVPool, q, block_table, ctx_lens, sm_scale: float, max_ct
     _need(torch.int32, block_table, ctx_lens, seen, status)
     _need_scratch(pool.storage, workspace)
     pool.need("int8")
-    _small("max_ctx", max_ctx)
+    if not -1 < max_ctx <= _I32_MAX:
+        _large(max_ctx)
     B, T, Hq, D = q.shape
     shape, Hkv = block_table.shape, pool.num_kv_heads
     if D != pool.head_dim or len(shape) != 2 or shape[0] != B or ctx_lens.numel() != B:
@@ -838,7 +855,9 @@ def evict_pages(page_size: int, weights, block_table, ctx_lens, keep_pages: int,
         out = block_table
     _need(torch.float32, weights)
     _need(torch.int32, block_table, ctx_lens, new_ctx, freed, num_freed, out, status)
-    _small("page_size, keep_pages, sink_pages and recent_pages", page_size, keep_pages, sink_pages, recent_pages)
+    if not (-1 < page_size <= _I32_MAX and -1 < keep_pages <= _I32_MAX and -1 < sink_pages <= _I32_MAX
+            and -1 < recent_pages <= _I32_MAX):
+        _large(page_size, keep_pages, sink_pages, recent_pages)
     _one(num_freed, "num_freed")
     B, shape = ctx_lens.numel(), block_table.shape
     if len(shape) != 2 or shape[0] != B or out.shape != shape or new_ctx.numel() != B or weights.dim() != 2:

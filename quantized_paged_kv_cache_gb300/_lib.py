@@ -72,6 +72,7 @@ EXPORTS = (
     "nk_paged_chunk_attn",
     "nk_page_bounds_bytes",
     "nk_page_bounds",
+    "nk_page_bounds_values",
     "nk_page_select_workspace_bytes",
     "nk_page_select",
     "nk_paged_sparse_attn",
@@ -143,7 +144,9 @@ def lib() -> ctypes.CDLL:
             L.nk_page_bounds_bytes.argtypes, L.nk_page_bounds_bytes.restype = [I32, I32, I32], Z
             L.nk_page_bounds.argtypes = [pool_p, P, P, I32, P, P, I32, P, P]
             L.nk_page_bounds.restype = ctypes.c_int
-            L.nk_page_select_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+            L.nk_page_bounds_values.argtypes = [P, I32, I32, I32, P, P]
+            L.nk_page_bounds_values.restype = ctypes.c_int
+            L.nk_page_select_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32, I32]
             L.nk_page_select_workspace_bytes.restype = Z
             L.nk_page_select.argtypes = [P, I32, I32, I32, I32, P, P, I32, P, I32, I32, I32, I32, I32, I32, I32, P, Z, P, P,
                                          P]

@@ -1,7 +1,10 @@
 // nk_select.cu -- which pages of a long cache a query attends to: the pages'
 // bounds (nk_page_bounds) and the choice by them (nk_page_select).
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "nk_common.cuh"
 #include "nk_host.cuh"
@@ -343,6 +346,24 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   }
 }
 
+// nk_page_bounds_values: 16 codes a thread, four stores of 16 bytes.
+__global__ void __launch_bounds__(256) bounds_values_kernel(BoundsView v, int64_t pieces, int per_rec, float* out) {
+  chain_wait();
+  chain_release();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+    const uint4 w = reinterpret_cast<const uint4*>(v.codes)[i];
+    const float s = v.scales[quot(i, per_rec)];
+    const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+      values4(u[j], s2, x);
+      reinterpret_cast<float4*>(out)[i * 4 + j] = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // nk_page_select, first kernel: the pages' scores. With one scale s_q for a
 // token's rows of a kv-head, q8 = clamp(rint(q / s_q)), page scale s:
@@ -410,27 +431,16 @@ __host__ __device__ inline int select_smem(int D, int NT) {
   return NT * 8 * (D * 2 + 8) + kSelWarps * 16 * (NT * 8 + 1) * 4;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectParams p) {
+// The scores of pages 0 .. seen - 1 of a (sequence, kv-head) for tokens t0 .. t0 +
+// cols - 1, 16 pages a warp from block `blk` on: store(t - t0, page, key).
+template <int D, int NT, class Store>
+__device__ __forceinline__ void score_pages(const SelectParams& p, uint8_t* smem, float* top_s, int b, int h, int t0,
+                                            int cols, int seen, int blk, int stride, const Store& store) {
   constexpr int ROWS = NT * 8;
   constexpr int RS = D * 2 + 8;     // bytes of a row: 2 words past a multiple of 32, distinct banks for the fragments
   constexpr int NC = D / 64;        // 64-channel parts of a record's half
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float top_s[kSelWarps];
-  chain_wait();
-  chain_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
-  const int t0 = blockIdx.z * p.cols, cols = min(p.cols, p.T - t0);
-  const int L = select_len(p, b);
-  if (L == 0) {
-    if (tid == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
-    return;
-  }
-  const int seen = (L - p.T + t0 + cols - 1) / p.P + 1;  // pages that the chunk's last token sees
-  if (seen <= p.k) return;                               // nothing to choose
-  const int blocks = (seen + 15) / 16, stride = gridDim.x * kSelWarps;
-  int blk = blockIdx.x * kSelWarps + warp;
+  const int blocks = (seen + 15) / 16;
   // the first pages' records are on their way while the rows are made
   uint4 rec[2][2][NC];  // [page g, g + 8][hi, lo][part]
   float scale = 0.f;    // of page `lane`, lanes 0 to 15
@@ -553,62 +563,144 @@ __global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectPar
         for (int i = 1; i < G; ++i) m = fmaxf(m, row[i]);
         double v = (double)m * s;
         if (!my_there || !(fabs(v) < 1e300)) v = -1e300;  // no page, or bounds never made: last
-        p.scores[((int64_t)(b * p.T + t0 + t) * p.Hkv + h) * p.stride + base + pg] = ordered(v + 0.0);
+        store(t, base + pg, ordered(v + 0.0));
       }
     }
     __syncwarp();
   }
 }
 
-// ---------------------------------------------------------------------------
-// Second kernel: of each (token, kv-head) the k pages, one block each. The first
-// `sinks` and the last `recent` pages that the token sees are always in; the
-// others by score (nk_topk.cuh). Keys are kept in shared memory where they fit.
-// ---------------------------------------------------------------------------
-constexpr int kPickThreads = 512;
-constexpr int kPickKeep = 16384;  // keys kept in shared memory, at most
-
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p, int room) {
-  extern __shared__ uint64_t keep[];
-  __shared__ TopSmem<kPickThreads> sm;
+// Two launches, for many query rows or pages: the scores through the workspace.
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float top_s[kSelWarps];
   chain_wait();
   chain_release();
-  const int tid = threadIdx.x;
-  const int bt = blockIdx.x / p.Hkv, b = bt / p.T, t = bt - b * p.T;
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  const int t0 = blockIdx.z * p.cols, cols = min(p.cols, p.T - t0);
   const int L = select_len(p, b);
-  if (L == 0) return;  // (flagged by the first kernel; the list is left as it was)
-  int32_t* out = p.out + (int64_t)blockIdx.x * p.k;
-  const int seen = (L - p.T + t) / p.P + 1;
+  if (L == 0) {
+    if (threadIdx.x == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
+    return;
+  }
+  const int seen = (L - p.T + t0 + cols - 1) / p.P + 1;  // pages that the chunk's last token sees
+  if (seen <= p.k) return;                               // nothing to choose
+  score_pages<D, NT>(p, smem, top_s, b, h, t0, cols, seen, (int)(blockIdx.x * kSelWarps + (threadIdx.x >> 5)),
+                     (int)gridDim.x * kSelWarps, [&](int t, int page, uint64_t key) {
+                       p.scores[((int64_t)(b * p.T + t0 + t) * p.Hkv + h) * p.stride + page] = key;
+                     });
+}
+
+// ---------------------------------------------------------------------------
+// The choice: of each (token, kv-head) the k pages, by one block. The first
+// `sinks` and the last `recent` pages that the token sees are always in; the
+// others by score (nk_topk.cuh). get(i): key of page i; up to `room` of them are
+// kept in shared memory, more are fetched anew in every pass.
+// ---------------------------------------------------------------------------
+constexpr int kPickKeep = 16384;  // keys kept in shared memory, at most
+
+template <int NTH, class Get>
+__device__ __forceinline__ void pick_pages(const SelectParams& p, int32_t* out, int seen, uint64_t* keep, int room,
+                                           TopSmem<NTH>& sm, const Get& get) {
+  const int tid = threadIdx.x;
   if (seen <= p.k) {
-    for (int i = tid; i < p.k; i += kPickThreads) out[i] = i < seen ? i : -1;
+    for (int i = tid; i < p.k; i += NTH) out[i] = i < seen ? i : -1;
     return;
   }
   const int first = p.sinks, n = seen - p.sinks - p.recent, need = p.k - p.sinks - p.recent;  // need < n
-  for (int i = tid; i < p.sinks + p.recent; i += kPickThreads)
+  for (int i = tid; i < p.sinks + p.recent; i += NTH)
     out[i < p.sinks ? i : i + need] = i < p.sinks ? i : seen - p.recent + (i - p.sinks);
   if (need == 0) return;
-  const uint64_t* src = p.scores + (int64_t)blockIdx.x * p.stride + first;
   const bool kept = n <= room;
   if (kept) {
-    for (int i = tid; i < n; i += kPickThreads) keep[i] = __ldcg(src + i);
+#pragma unroll 8
+    for (int i = tid; i < n; i += NTH) keep[i] = get(first + i);
     __syncthreads();
   }
-  const uint64_t* keys = kept ? keep : src;
-  const auto key = [&](int i) { return keys[i]; };
+  const auto key = [&](int i) { return kept ? keep[i] : get(first + i); };
   uint64_t klo, khi, kt;
   int it;
-  block_range<kPickThreads>(key, n, sm, klo, khi);
-  block_threshold<kPickThreads>(key, n, need, klo, khi, sm, kt, it);
-  const int per = top_run<kPickThreads>(n), a = tid * per, e = a + per < n ? a + per : n;
+  block_range<NTH>(key, n, sm, klo, khi);
+  block_threshold<NTH>(key, n, need, klo, khi, sm, kt, it);
+  const int per = top_run<NTH>(n), a = tid * per, e = a + per < n ? a + per : n;
   const auto taken = [&](int i) {
     const uint64_t k = key(i);
     return k > kt || (k == kt && i <= it);
   };
   int mine = 0, total;
   for (int i = a; i < e; ++i) mine += taken(i);
-  int at = first + block_exclusive<kPickThreads>(mine, sm.warp, total);
+  int at = first + block_exclusive<NTH>(mine, sm.warp, total);
   for (int i = a; i < e; ++i)
     if (taken(i)) out[at++] = first + i;
+}
+
+constexpr int kPickThreads = 512;
+
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p, int room) {
+  extern __shared__ uint64_t keep[];
+  __shared__ TopSmem<kPickThreads> sm;
+  chain_wait();
+  chain_release();
+  const int bt = blockIdx.x / p.Hkv, b = bt / p.T, t = bt - b * p.T;
+  const int L = select_len(p, b);
+  if (L == 0) return;  // (flagged by the first kernel; the list is left as it was)
+  const uint64_t* src = p.scores + (int64_t)blockIdx.x * p.stride;
+  pick_pages<kPickThreads>(p, p.out + (int64_t)blockIdx.x * p.k, (L - p.T + t) / p.P + 1, keep, room, sm,
+                           [&](int i) { return __ldcg(src + i); });
+}
+
+// ---------------------------------------------------------------------------
+// One launch: a cluster takes a (sequence, kv-head). Its CTAs share the blocks of
+// 16 pages out in turn and keep their keys; then each takes a token, fetches its
+// keys from all of them through distributed shared memory, and chooses. No
+// workspace, no second launch.
+// ---------------------------------------------------------------------------
+// Key slots of a token in a CTA of a cluster of `cl`, for so many pages.
+__host__ __device__ inline int cluster_slots(int64_t pages, int cl) {
+  const int64_t blocks = (pages + 15) / 16, per = (int64_t)cl * kSelWarps;
+  return (int)((blocks + per - 1) / per * kSelWarps * 16);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectParams p, int slots, int room) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float top_s[kSelWarps];
+  __shared__ TopSmem<kSelThreads> sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  chain_wait();
+  chain_release();
+  const int rank = (int)cluster.block_rank(), cl = (int)cluster.num_blocks();
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  const int L = select_len(p, b);
+  if (L == 0) {  // (the same in all of the cluster)
+    if (threadIdx.x == 0 && rank == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
+    return;
+  }
+  uint64_t* own = reinterpret_cast<uint64_t*>(smem + select_smem(D, NT));  // [T][slots]
+  uint64_t* keep = own + (int64_t)p.T * slots;                             // [room]
+  const int seen = (L - 1) / p.P + 1, turn = cl * kSelWarps;
+  const bool choose = seen > p.k;
+  if (choose) {
+    score_pages<D, NT>(p, smem, top_s, b, h, 0, p.T, seen, rank * kSelWarps + (int)(threadIdx.x >> 5), turn,
+                       [&](int t, int page, uint64_t key) {
+                         const int blk = page >> 4;
+                         own[t * slots + ((blk / turn) * kSelWarps + blk % kSelWarps) * 16 + (page & 15)] = key;
+                       });
+    cluster.sync();
+  }
+  for (int t = rank; t < p.T; t += cl) {  // (block-uniform)
+    pick_pages<kSelThreads>(p, p.out + ((int64_t)(b * p.T + t) * p.Hkv + h) * p.k, (L - p.T + t) / p.P + 1, keep, room, sm,
+                            [&](int page) {
+                              const int blk = page >> 4, w = blk % turn;
+                              return *cluster.map_shared_rank(
+                                  own + t * slots + ((blk / turn) * kSelWarps + w % kSelWarps) * 16 + (page & 15),
+                                  w / kSelWarps);
+                            });
+    __syncthreads();  // (keep and sm: the next token's)
+  }
+  if (choose) cluster.sync();  // nobody reads this CTA's keys any more
 }
 
 }  // namespace nk
@@ -625,8 +717,69 @@ cudaError_t launch_bounds(const BoundsParams& p, int grid, cudaStream_t st) {
   return launch_chained(page_bounds_kernel<D>, dim3((unsigned)grid), dim3(kBndThreads), (size_t)smem, st, p);
 }
 
+// How a call runs: in one launch where a cluster's CTA holds all rows, its keys
+// and a token's keys; else in two.
+constexpr int kSelSmem = 200 * 1024;
+int rows_tiles(int rows) {  // of the kernels' instances: 1, 2, 3, 4, 6, 8
+  const int nt = (rows + 7) / 8;
+  return nt == 5 ? 6 : (nt == 7 ? 8 : nt);
+}
+struct SelectPlan {
+  int cl;         // CTAs of a cluster; 0: two launches
+  int slots, room, smem;
+  int NT;
+};
+SelectPlan plan_select(int64_t units, int T, int G, int D, int64_t pages) {
+  SelectPlan s = {};
+  if (T * G > kSelRows || pages > kPickKeep) return s;
+  s.NT = rows_tiles(T * G);
+  // sixteen CTAs for each of a few units, else the portable eight, fewer where
+  // that many blocks of pages are not there
+  const int sms = device_sms();
+  s.cl = units * 16 <= (sms > 0 ? sms : 148) ? 16 : 8;
+  while (s.cl > 1 && (pages + 15) / 16 <= (int64_t)s.cl / 2 * kSelWarps) s.cl /= 2;
+  if (s.cl < T && T <= 8 && pages > 64) s.cl = T <= 2 ? 2 : (T <= 4 ? 4 : 8);  // a token each at once
+  s.slots = cluster_slots(pages, s.cl);
+  s.room = (int)pages;
+  const int64_t smem = select_smem(D, s.NT) + ((int64_t)T * s.slots + s.room) * 8;
+  if (smem > kSelSmem) return SelectPlan{};
+  s.smem = (int)smem;
+  return s;
+}
+
 template <int D, int NT>
-cudaError_t launch_scores(const SelectParams& p, dim3 grid, cudaStream_t st) {
+cudaError_t launch_scores(const SelectParams& p, dim3 grid, const SelectPlan& plan, cudaStream_t st) {
+  if (plan.cl > 0) {
+    const void* fn = reinterpret_cast<const void*>(page_select_kernel<D, NT>);
+    cudaError_t e = set_smem_limit(fn, plan.smem);
+    if (e != cudaSuccess) return e;
+    if (plan.cl > 8) {
+      static std::atomic<bool> allowed[64];  // per device
+      int dev = 0;
+      e = cudaGetDevice(&dev);
+      if (e != cudaSuccess) return e;
+      if (dev < 0 || dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+      }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)plan.cl, (unsigned)(p.B * p.Hkv));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)plan.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)plan.cl;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, page_select_kernel<D, NT>, p, plan.slots, plan.room);
+  }
   const int smem = select_smem(D, NT);
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_score_kernel<D, NT>), smem);
   if (e != cudaSuccess) return e;
@@ -634,14 +787,14 @@ cudaError_t launch_scores(const SelectParams& p, dim3 grid, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_scores_d(const SelectParams& p, int NT, dim3 grid, cudaStream_t st) {
+cudaError_t launch_scores_d(const SelectParams& p, int NT, dim3 grid, const SelectPlan& plan, cudaStream_t st) {
   switch (NT) {
-    case 1: return launch_scores<D, 1>(p, grid, st);
-    case 2: return launch_scores<D, 2>(p, grid, st);
-    case 3: return launch_scores<D, 3>(p, grid, st);
-    case 4: return launch_scores<D, 4>(p, grid, st);
-    case 5: case 6: return launch_scores<D, 6>(p, grid, st);
-    default: return launch_scores<D, 8>(p, grid, st);
+    case 1: return launch_scores<D, 1>(p, grid, plan, st);
+    case 2: return launch_scores<D, 2>(p, grid, plan, st);
+    case 3: return launch_scores<D, 3>(p, grid, plan, st);
+    case 4: return launch_scores<D, 4>(p, grid, plan, st);
+    case 6: return launch_scores<D, 6>(p, grid, plan, st);
+    default: return launch_scores<D, 8>(p, grid, plan, st);
   }
 }
 
@@ -679,9 +832,29 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
-size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_kv_heads, int32_t page_size, int32_t max_ctx) {
-  if (B < 1 || T < 1 || T > NK_MAX_T || num_kv_heads < 1 || page_size < 1 || max_ctx < 1) return 0;
-  return (size_t)B * T * num_kv_heads * (((size_t)max_ctx + page_size - 1) / page_size) * 8;
+int nk_page_bounds_values(const void* bounds_dev, int32_t num_pages, int32_t num_kv_heads, int32_t head_dim,
+                          float* values_dev, void* stream) {
+  if (num_pages < 1 || num_kv_heads < 1 || !(head_dim == 64 || head_dim == 128 || head_dim == 256)) return NK_ERR_SHAPE;
+  if (!bounds_dev || !values_dev) return NK_ERR_NULL;
+  if (!aligned_to(bounds_dev, 16) || !aligned_to(values_dev, 16)) return NK_ERR_SHAPE;
+  const int per_rec = 2 * head_dim / 16;
+  const int64_t pieces = (int64_t)num_pages * num_kv_heads * per_rec, blocks = (pieces + 255) / 256;
+  const int sms = device_sms();
+  const int64_t most = (int64_t)(sms > 0 ? sms : 148) * 8;
+  const cudaError_t e = launch_chained(bounds_values_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                                       reinterpret_cast<cudaStream_t>(stream),
+                                       bounds_view(const_cast<void*>(bounds_dev), num_pages, num_kv_heads, head_dim), pieces,
+                                       per_rec, values_dev);
+  return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
+}
+
+size_t nk_page_select_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t page_size, int32_t max_ctx) {
+  if (B < 1 || T < 1 || T > NK_MAX_T || num_kv_heads < 1 || num_q_heads < num_kv_heads || page_size < 1 || max_ctx < 1)
+    return 0;
+  const int64_t pages = ((int64_t)max_ctx + page_size - 1) / page_size;
+  if (plan_select((int64_t)B * num_kv_heads, T, num_q_heads / num_kv_heads, head_dim, pages).cl > 0) return 0;
+  return (size_t)B * T * num_kv_heads * pages * 8;
 }
 
 int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
@@ -700,8 +873,10 @@ int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size,
   if (max_pages_per_seq < 1 || max_ctx < T || (int64_t)max_ctx > (int64_t)max_pages_per_seq * page_size)
     return NK_ERR_SHAPE;
   if (!aligned_to(bounds_dev, 16) || !aligned_to(q_dev, 16)) return NK_ERR_SHAPE;
-  const size_t need = nk_page_select_workspace_bytes(B, T, num_kv_heads, page_size, max_ctx);
-  if (!workspace_dev || workspace_bytes < need || !aligned_to(workspace_dev, 16)) return NK_ERR_WORKSPACE;
+  const int64_t units = (int64_t)B * num_kv_heads, pages = ((int64_t)max_ctx + page_size - 1) / page_size;
+  const SelectPlan plan = plan_select(units, T, G, head_dim, pages);
+  const size_t need = plan.cl > 0 ? 0 : (size_t)units * T * pages * 8;
+  if (need > 0 && (!workspace_dev || workspace_bytes < need || !aligned_to(workspace_dev, 16))) return NK_ERR_WORKSPACE;
   SelectParams p = {};
   p.bounds = bounds_view(const_cast<void*>(bounds_dev), num_pages, num_kv_heads, head_dim);
   p.num_pages = num_pages;
@@ -719,25 +894,25 @@ int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size,
   p.sinks = sink_pages;
   p.recent = recent_pages;
   p.scores = reinterpret_cast<uint64_t*>(workspace_dev);
-  p.stride = ((int64_t)max_ctx + page_size - 1) / page_size;
+  p.stride = pages;
   p.out = pages_dev;
   p.status = status_dev;
   p.cols = kSelRows / G < 1 ? 1 : kSelRows / G;
   if (p.cols > T) p.cols = T;
-  const int NT = (p.cols * G + 7) / 8;
-  const int64_t units = (int64_t)B * num_kv_heads;
   const int sms = device_sms();
   // eight warps of 16 pages a block; past four blocks an SM they take turns
-  int64_t gx = (p.stride + 16 * kSelWarps - 1) / (16 * kSelWarps), most = (int64_t)(sms > 0 ? sms : 148) * 4 / units;
+  int64_t gx = (pages + 16 * kSelWarps - 1) / (16 * kSelWarps), most = (int64_t)(sms > 0 ? sms : 148) * 4 / units;
   if (most < 1) most = 1;
   if (gx > most) gx = most;
   const dim3 grid((unsigned)gx, (unsigned)units, (unsigned)((T + p.cols - 1) / p.cols));
+  const int NT = rows_tiles(p.cols * G);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = head_dim == 256   ? launch_scores_d<256>(p, NT, grid, st)
-                  : head_dim == 128 ? launch_scores_d<128>(p, NT, grid, st)
-                                    : launch_scores_d<64>(p, NT, grid, st);
+  cudaError_t e = head_dim == 256   ? launch_scores_d<256>(p, NT, grid, plan, st)
+                  : head_dim == 128 ? launch_scores_d<128>(p, NT, grid, plan, st)
+                                    : launch_scores_d<64>(p, NT, grid, plan, st);
+  if (e == cudaSuccess && plan.cl > 0) return NK_OK;
   if (e != cudaSuccess) return NK_ERR_CUDA;
-  const int room = (int)(p.stride < kPickKeep ? p.stride : kPickKeep);
+  const int room = (int)(pages < kPickKeep ? pages : kPickKeep);
   e = set_smem_limit(reinterpret_cast<const void*>(page_pick_kernel), room * 8);
   if (e != cudaSuccess) return NK_ERR_CUDA;
   e = launch_chained(page_pick_kernel, dim3((unsigned)(units * T)), dim3(kPickThreads), (size_t)room * 8, st, p, room);

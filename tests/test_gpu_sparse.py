@@ -52,6 +52,7 @@ def check_bounds(c, b, start, end, untouched):
     w = c.w
     kc, ks = ref.keys(c.pool.storage, w.num_pages, w.Hkv, w.P, w.D)
     codes, scales = b.codes().cpu().numpy(), b.scales().cpu().numpy()
+    assert np.array_equal(b.values().cpu().numpy(), codes.astype(np.float32) * scales[..., None, None], equal_nan=True)
     left = np.ones(w.num_pages, bool)
     for s, (a, e) in enumerate(zip(start, end)):
         for i in range(a // w.P, -(-e // w.P) if e > a else 0):

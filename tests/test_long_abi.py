@@ -21,8 +21,10 @@ def ref(p):
 def test_sizes():
     assert nk.page_bounds_bytes(10, 4, 256) == 10 * 4 * (2 * 256 + 4) and nk.page_bounds_bytes(10, 4, 96) == 0
     assert nk.page_bounds_bytes(1 << 24, 8, 256) == (1 << 27) * 516
-    assert nk.page_select_workspace_bytes(8, 4, 4, 64, 65536) == 8 * 4 * 4 * 1024 * 8
-    assert nk.page_select_workspace_bytes(1, 1, 1, 16, 17) == 16 and nk.page_select_workspace_bytes(0, 1, 1, 16, 17) == 0
+    assert nk.page_select_workspace_bytes(8, 4, 24, 4, 256, 64, 65536) == 0  # in one launch
+    assert nk.page_select_workspace_bytes(8, 16, 24, 4, 256, 64, 65536) == 8 * 16 * 4 * 1024 * 8  # 96 rows of a kv-head
+    assert nk.page_select_workspace_bytes(1, 1, 4, 2, 64, 16, 20000 * 16) == 2 * 20000 * 8  # more pages than stay on chip
+    assert nk.page_select_workspace_bytes(0, 1, 1, 1, 64, 16, 17) == 0
     one = nk.page_weights_workspace_bytes(1, 1, 6, 1, 16, 100)
     assert one == (7 + 7 + 1) * 8 * 4  # seven pages, as many CTAs, one unit, six rows in a tile of eight
     assert nk.page_weights_workspace_bytes(1, 17, 6, 1, 16, 100) == 0
@@ -39,9 +41,17 @@ def test_bounds_refusals():
     assert call(B=1025) == 3 and call(B=0) == 0
 
 
+def test_bounds_values_refusals():
+    def call(bounds=FAKE, pages=2, H=1, D=64, out=FAKE):
+        return nk.lib().nk_page_bounds_values(bounds, pages, H, D, out, None)
+
+    assert call(bounds=None) == 1 and call(out=None) == 1
+    assert call(pages=0) == 2 and call(H=0) == 2 and call(D=96) == 2 and call(bounds=FAKE + 8) == 2 and call(out=FAKE + 4) == 2
+
+
 def test_select_refusals():
     def call(bounds=FAKE, pages=16, P=16, Hkv=2, D=64, q=FAKE, bt=FAKE, width=8, ctx=FAKE, B=2, T=2, Hq=4, max_ctx=128, k=4, sinks=1,
-             recent=1, ws=FAKE, wsb=2 * 2 * 2 * 8 * 8, out=FAKE):
+             recent=1, ws=None, wsb=0, out=FAKE):
         return nk.lib().nk_page_select(bounds, pages, P, Hkv, D, q, bt, width, ctx, B, T, Hq, max_ctx, k, sinks, recent, ws, wsb, out, None, None)
 
     for name in ("bounds", "q", "bt", "ctx", "out"):
@@ -51,7 +61,8 @@ def test_select_refusals():
                 dict(q=FAKE + 2)):
         assert call(**bad) == 2, bad
     assert call(Hq=2 * 49) == 3 and call(B=40000) == 3 and call(B=0) == 0
-    assert call(ws=None) == 4 and call(wsb=511) == 4 and call(ws=FAKE + 8) == 4
+    many = dict(T=16, Hq=2 * 5, wsb=2 * 16 * 2 * 8 * 8, ws=FAKE)  # 80 rows: two launches, which need a workspace
+    assert call(**many | dict(ws=None)) == 4 and call(**many | dict(wsb=4095)) == 4 and call(**many | dict(ws=FAKE + 8)) == 4
 
 
 def test_sparse_refusals():
