@@ -427,14 +427,14 @@ __device__ __forceinline__ uint32_t half2_min0(uint32_t x) {
 }
 
 // Shared memory: rows [NT * 8][D / 2 + 2 words] fp16, then a warp's products [16][NT * 8 + 1] fp32.
-__host__ __device__ inline int select_smem(int D, int NT) {
-  return NT * 8 * (D * 2 + 8) + kSelWarps * 16 * (NT * 8 + 1) * 4;
+__host__ __device__ inline int select_smem(int D, int NT, int warps) {
+  return NT * 8 * (D * 2 + 8) + warps * 16 * (NT * 8 + 1) * 4;
 }
 
 // The scores of pages 0 .. seen - 1 of a (sequence, kv-head) for tokens t0 .. t0 +
 // cols - 1, 16 pages a warp from block `blk` on: store(t - t0, page, key).
-template <int D, int NT, class Store>
-__device__ __forceinline__ void score_pages(const SelectParams& p, uint8_t* smem, float* top_s, int b, int h, int t0,
+template <int D, int NT, int WARPS, class Store>
+__device__ __forceinline__ void score_pages(const SelectParams& p, uint8_t* smem, uint32_t* top_s, int b, int h, int t0,
                                             int cols, int seen, int blk, int stride, const Store& store) {
   constexpr int ROWS = NT * 8;
   constexpr int RS = D * 2 + 8;     // bytes of a row: 2 words past a multiple of 32, distinct banks for the fragments
@@ -469,52 +469,56 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, uint8_t* smem
     }
   };
   if (blk < blocks) load(blk);
-  // ---- the rows as whole numbers: a scale for each token
-  const int G = p.G, Hq = G * p.Hkv;
-  for (int i = tid; i < ROWS * (RS / 8); i += kSelThreads) reinterpret_cast<uint2*>(smem)[i] = make_uint2(0, 0);
+  // ---- the rows as whole numbers: a scale for each token. The pieces of all rows
+  // stay in registers between the search for the largest and the division.
+  const int G = p.G, rows = cols * G;
+  constexpr int PER = D / 8;                                          // 16-byte pieces of a row
+  constexpr int PCS = (ROWS * PER + WARPS * 32 - 1) / (WARPS * 32);  // of a thread
+  uint4 piece[PCS];
+  if (tid < NK_MAX_T) top_s[tid] = 0;
   __syncthreads();
-  for (int t = 0; t < cols; ++t) {
-    const uint16_t* src = p.q + ((int64_t)(b * p.T + t0 + t) * Hq + h * G) * D;  // G consecutive rows
-    float m = 0.f;
-    bool odd = false;
-    for (int i = tid; i < G * D / 8; i += kSelThreads) {
-      const uint4 v = *(reinterpret_cast<const uint4*>(src) + i);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < PCS; ++k) {
+    const int i = tid + k * WARPS * 32, row = i / PER, t = row / G;
+    piece[k] = make_uint4(0, 0, 0, 0);
+    uint32_t m = 0;  // |q| as bits: their order is that of the numbers, infinity and NaN past all
+    if (row < rows) {
+      const uint16_t* src = p.q + (((int64_t)(b * p.T + t0 + t) * p.Hkv + h) * G + (row - t * G)) * D;
+      piece[k] = reinterpret_cast<const uint4*>(src)[i % PER];
+      const uint32_t u[4] = {piece[k].x, piece[k].y, piece[k].z, piece[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
+    }
+    // (a row is a whole number of eight lanes)
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    if ((lane & 7) == 0 && row < rows) atomicMax(&top_s[t], m);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < PCS; ++k) {
+    const int i = tid + k * WARPS * 32, row = i / PER, t = row / G;
+    if (row >= ROWS) continue;
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint32_t top = row < rows ? top_s[t] : 0x7f800000u;
+    if (top < 0x7f800000u) {  // (rows that are not finite choose as zeros)
+      float s = __fdiv_rn(__uint_as_float(top), 127.f);
+      if (s == 0.f) s = 1.f;
+      const uint32_t u[4] = {piece[k].x, piece[k].y, piece[k].z, piece[k].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = fabsf(bf16_lo(u[j])), c = fabsf(bf16_hi(u[j]));
-        odd |= !(a < INFINITY) || !(c < INFINITY);
-        m = fmaxf(m, fmaxf(a, c));
+        const float x = fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(u[j]), s)), -127.f), 127.f);
+        const float y = fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(u[j]), s)), -127.f), 127.f);
+        const __half2 hh = __floats2half2_rn(x, y);
+        w[j] = *reinterpret_cast<const uint32_t*>(&hh);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) top_s[warp] = m;
-    odd = __syncthreads_or(odd);
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) m = fmaxf(m, top_s[w]);
-    float s = __fdiv_rn(m, 127.f);
-    if (s == 0.f) s = 1.f;
-    if (!odd) {  // (rows that are not finite choose as zeros)
-      for (int i = tid; i < G * D / 8; i += kSelThreads) {
-        const uint4 v = *(reinterpret_cast<const uint4*>(src) + i);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(u[j]), s)), -127.f), 127.f);
-          const float c = fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(u[j]), s)), -127.f), 127.f);
-          const __half2 hh = __floats2half2_rn(a, c);
-          w[j] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-        const int row = i / (D / 8), ch = (i % (D / 8)) * 8;
-        uint2* dst = reinterpret_cast<uint2*>(smem + (t * G + row) * RS + ch * 2);
-        dst[0] = make_uint2(w[0], w[1]);
-        dst[1] = make_uint2(w[2], w[3]);
-      }
-    }
-    __syncthreads();
+    uint2* dst = reinterpret_cast<uint2*>(smem + row * RS + (i % PER) * 16);
+    dst[0] = make_uint2(w[0], w[1]);
+    dst[1] = make_uint2(w[2], w[3]);
   }
+  __syncthreads();
   float* prod = reinterpret_cast<float*>(smem + ROWS * RS) + warp * 16 * (ROWS + 1);
   for (; blk < blocks; blk += stride) {  // (warp-uniform)
     float acc[NT][4];
@@ -574,7 +578,7 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, uint8_t* smem
 template <int D, int NT>
 __global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float top_s[kSelWarps];
+  __shared__ uint32_t top_s[NK_MAX_T];
   chain_wait();
   chain_release();
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectPar
   }
   const int seen = (L - p.T + t0 + cols - 1) / p.P + 1;  // pages that the chunk's last token sees
   if (seen <= p.k) return;                               // nothing to choose
-  score_pages<D, NT>(p, smem, top_s, b, h, t0, cols, seen, (int)(blockIdx.x * kSelWarps + (threadIdx.x >> 5)),
+  score_pages<D, NT, kSelWarps>(p, smem, top_s, b, h, t0, cols, seen, (int)(blockIdx.x * kSelWarps + (threadIdx.x >> 5)),
                      (int)gridDim.x * kSelWarps, [&](int t, int page, uint64_t key) {
                        p.scores[((int64_t)(b * p.T + t0 + t) * p.Hkv + h) * p.stride + page] = key;
                      });
@@ -596,13 +600,14 @@ __global__ void __launch_bounds__(kSelThreads) page_score_kernel(const SelectPar
 // The choice: of each (token, kv-head) the k pages, by one block. The first
 // `sinks` and the last `recent` pages that the token sees are always in; the
 // others by score (nk_topk.cuh). get(i): key of page i; up to `room` of them are
-// kept in shared memory, more are fetched anew in every pass.
+// kept in shared memory, more are fetched anew in every pass. [klo, khi] holds all
+// of them where klo <= khi.
 // ---------------------------------------------------------------------------
 constexpr int kPickKeep = 16384;  // keys kept in shared memory, at most
 
 template <int NTH, class Get>
 __device__ __forceinline__ void pick_pages(const SelectParams& p, int32_t* out, int seen, uint64_t* keep, int room,
-                                           TopSmem<NTH>& sm, const Get& get) {
+                                           TopSmem<NTH>& sm, const Get& get, uint64_t klo = 1, uint64_t khi = 0) {
   const int tid = threadIdx.x;
   if (seen <= p.k) {
     for (int i = tid; i < p.k; i += NTH) out[i] = i < seen ? i : -1;
@@ -612,17 +617,29 @@ __device__ __forceinline__ void pick_pages(const SelectParams& p, int32_t* out, 
   for (int i = tid; i < p.sinks + p.recent; i += NTH)
     out[i < p.sinks ? i : i + need] = i < p.sinks ? i : seen - p.recent + (i - p.sinks);
   if (need == 0) return;
-  const bool kept = n <= room;
-  if (kept) {
+  const bool kept = n <= room, ranged = kept && klo <= khi;
+  if (ranged) {  // the first round's counts beside the fetching
+    for (int i = tid; i < kTopBins; i += NTH) sm.hist[i] = 0;
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    const int shift = top_shift(klo, khi);
+#pragma unroll 8
+    for (int i = tid; i < n; i += NTH) {
+      const uint64_t k = get(first + i);
+      keep[i] = k;
+      atomicAdd(&sm.hist[(int)((k - klo) >> shift)], 1u);
+    }
+    __syncthreads();
+  } else if (kept) {
 #pragma unroll 8
     for (int i = tid; i < n; i += NTH) keep[i] = get(first + i);
     __syncthreads();
   }
   const auto key = [&](int i) { return kept ? keep[i] : get(first + i); };
-  uint64_t klo, khi, kt;
+  uint64_t kt;
   int it;
-  block_range<NTH>(key, n, sm, klo, khi);
-  block_threshold<NTH>(key, n, need, klo, khi, sm, kt, it);
+  if (!ranged) block_range<NTH>(key, n, sm, klo, khi);
+  block_threshold<NTH>(key, n, need, klo, khi, sm, kt, it, ranged);
   const int per = top_run<NTH>(n), a = tid * per, e = a + per < n ? a + per : n;
   const auto taken = [&](int i) {
     const uint64_t k = key(i);
@@ -656,18 +673,21 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
 // keys from all of them through distributed shared memory, and chooses. No
 // workspace, no second launch.
 // ---------------------------------------------------------------------------
+constexpr int kCluThreads = 512, kCluWarps = kCluThreads / 32;
+
 // Key slots of a token in a CTA of a cluster of `cl`, for so many pages.
 __host__ __device__ inline int cluster_slots(int64_t pages, int cl) {
-  const int64_t blocks = (pages + 15) / 16, per = (int64_t)cl * kSelWarps;
-  return (int)((blocks + per - 1) / per * kSelWarps * 16);
+  const int64_t blocks = (pages + 15) / 16, per = (int64_t)cl * kCluWarps;
+  return (int)((blocks + per - 1) / per * kCluWarps * 16);
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectParams p, int slots, int room) {
+__global__ void __launch_bounds__(kCluThreads) page_select_kernel(const SelectParams p, int slots, int room) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float top_s[kSelWarps];
-  __shared__ TopSmem<kSelThreads> sm;
+  __shared__ uint32_t top_s[NK_MAX_T];
+  __shared__ TopSmem<kCluThreads> sm;
+  __shared__ uint32_t range[NK_MAX_T][2];  // least and largest upper half of this CTA's keys of a token
   cg::cluster_group cluster = cg::this_cluster();
   chain_wait();
   chain_release();
@@ -678,26 +698,40 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectPa
     if (threadIdx.x == 0 && rank == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
     return;
   }
-  uint64_t* own = reinterpret_cast<uint64_t*>(smem + select_smem(D, NT));  // [T][slots]
+  uint64_t* own = reinterpret_cast<uint64_t*>(smem + select_smem(D, NT, kCluWarps));  // [T][slots]
   uint64_t* keep = own + (int64_t)p.T * slots;                             // [room]
-  const int seen = (L - 1) / p.P + 1, turn = cl * kSelWarps;
+  const int seen = (L - 1) / p.P + 1, turn = cl * kCluWarps;
   const bool choose = seen > p.k;
   if (choose) {
-    score_pages<D, NT>(p, smem, top_s, b, h, 0, p.T, seen, rank * kSelWarps + (int)(threadIdx.x >> 5), turn,
-                       [&](int t, int page, uint64_t key) {
-                         const int blk = page >> 4;
-                         own[t * slots + ((blk / turn) * kSelWarps + blk % kSelWarps) * 16 + (page & 15)] = key;
-                       });
+    if (threadIdx.x < p.T) {
+      range[threadIdx.x][0] = 0xffffffffu;
+      range[threadIdx.x][1] = 0;
+    }
+    // (score_pages has a barrier before its first store)
+    score_pages<D, NT, kCluWarps>(p, smem, top_s, b, h, 0, p.T, seen, rank * kCluWarps + (int)(threadIdx.x >> 5), turn,
+                                  [&](int t, int page, uint64_t key) {
+                                    const int blk = page >> 4;
+                                    own[t * slots + ((blk / turn) * kCluWarps + blk % kCluWarps) * 16 + (page & 15)] = key;
+                                    atomicMin(&range[t][0], (uint32_t)(key >> 32));
+                                    atomicMax(&range[t][1], (uint32_t)(key >> 32));
+                                  });
     cluster.sync();
   }
   for (int t = rank; t < p.T; t += cl) {  // (block-uniform)
-    pick_pages<kSelThreads>(p, p.out + ((int64_t)(b * p.T + t) * p.Hkv + h) * p.k, (L - p.T + t) / p.P + 1, keep, room, sm,
+    uint32_t lo = 0xffffffffu, hi = 0;
+    if (choose) {
+      const uint32_t* of = cluster.map_shared_rank(&range[t][0], (threadIdx.x & 31) % cl);
+      lo = __reduce_min_sync(0xffffffffu, of[0]);
+      hi = __reduce_max_sync(0xffffffffu, of[1]);
+    }
+    pick_pages<kCluThreads>(p, p.out + ((int64_t)(b * p.T + t) * p.Hkv + h) * p.k, (L - p.T + t) / p.P + 1, keep, room, sm,
                             [&](int page) {
                               const int blk = page >> 4, w = blk % turn;
                               return *cluster.map_shared_rank(
-                                  own + t * slots + ((blk / turn) * kSelWarps + w % kSelWarps) * 16 + (page & 15),
-                                  w / kSelWarps);
-                            });
+                                  own + t * slots + ((blk / turn) * kCluWarps + w % kCluWarps) * 16 + (page & 15),
+                                  w / kCluWarps);
+                            },
+                            (uint64_t)lo << 32, (uint64_t)hi << 32 | 0xffffffffu);
     __syncthreads();  // (keep and sm: the next token's)
   }
   if (choose) cluster.sync();  // nobody reads this CTA's keys any more
@@ -733,15 +767,16 @@ SelectPlan plan_select(int64_t units, int T, int G, int D, int64_t pages) {
   SelectPlan s = {};
   if (T * G > kSelRows || pages > kPickKeep) return s;
   s.NT = rows_tiles(T * G);
-  // sixteen CTAs for each of a few units, else the portable eight, fewer where
-  // that many blocks of pages are not there
+  // as many CTAs for each unit, up to sixteen, as leave them all resident at once
+  // (one an SM: 8 verified sequences with eight each took 15.2 us, 256 CTAs in two
+  // rounds), no more than there are blocks of pages for
   const int sms = device_sms();
-  s.cl = units * 16 <= (sms > 0 ? sms : 148) ? 16 : 8;
-  while (s.cl > 1 && (pages + 15) / 16 <= (int64_t)s.cl / 2 * kSelWarps) s.cl /= 2;
-  if (s.cl < T && T <= 8 && pages > 64) s.cl = T <= 2 ? 2 : (T <= 4 ? 4 : 8);  // a token each at once
+  s.cl = 16;
+  while (s.cl > 1 && units * s.cl > (sms > 0 ? sms : 148)) s.cl /= 2;
+  while (s.cl > 1 && (pages + 15) / 16 <= (int64_t)s.cl / 2 * kCluWarps) s.cl /= 2;
   s.slots = cluster_slots(pages, s.cl);
   s.room = (int)pages;
-  const int64_t smem = select_smem(D, s.NT) + ((int64_t)T * s.slots + s.room) * 8;
+  const int64_t smem = select_smem(D, s.NT, kCluWarps) + ((int64_t)T * s.slots + s.room) * 8;
   if (smem > kSelSmem) return SelectPlan{};
   s.smem = (int)smem;
   return s;
@@ -766,7 +801,7 @@ cudaError_t launch_scores(const SelectParams& p, dim3 grid, const SelectPlan& pl
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)plan.cl, (unsigned)(p.B * p.Hkv));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(kCluThreads);
     cfg.dynamicSmemBytes = (size_t)plan.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -780,7 +815,7 @@ cudaError_t launch_scores(const SelectParams& p, dim3 grid, const SelectPlan& pl
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, page_select_kernel<D, NT>, p, plan.slots, plan.room);
   }
-  const int smem = select_smem(D, NT);
+  const int smem = select_smem(D, NT, kSelWarps);
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_score_kernel<D, NT>), smem);
   if (e != cudaSuccess) return e;
   return launch_chained(page_score_kernel<D, NT>, grid, dim3(kSelThreads), (size_t)smem, st, p);

@@ -68,28 +68,36 @@ __device__ __forceinline__ int top_run(int n) {
   return ((n + NTH - 1) / NTH) | 1;
 }
 
-// 1 <= need <= n; [klo, khi] must hold every key. Called by all NTH threads;
-// ends with a barrier.
+// Bin width of a round, as a shift, for keys between lo and hi.
+__device__ __forceinline__ int top_shift(uint64_t lo, uint64_t hi) {
+  const int bits = 64 - __clzll((long long)(hi - lo));
+  return bits > 11 ? bits - 11 : 0;
+}
+
+// 1 <= need <= n; [klo, khi] must hold every key. `counted`: sm.hist already holds
+// the first round's counts (and sm.count 0). Called by all NTH threads; ends with
+// a barrier.
 template <int NTH, class Key>
 __device__ void block_threshold(const Key& key, int n, int need, uint64_t klo, uint64_t khi, TopSmem<NTH>& sm,
-                                uint64_t& kt, int& it) {
+                                uint64_t& kt, int& it, bool counted = false) {
   const int tid = threadIdx.x;
   static_assert(kTopBins % NTH == 0, "whole bins per thread");
   constexpr int BPT = kTopBins / NTH;
   uint64_t lo = klo, hi = khi;
   for (;;) {
-    const uint64_t range = hi - lo;
-    const int bits = 64 - __clzll((long long)range);
-    const int shift = bits > 11 ? bits - 11 : 0;
+    const int shift = top_shift(lo, hi);
+    if (!counted) {
 #pragma unroll
-    for (int i = 0; i < BPT; ++i) sm.hist[tid + i * NTH] = 0;
-    if (tid == 0) sm.count = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += NTH) {
-      const uint64_t k = key(i);
-      if (k >= lo && k <= hi) atomicAdd(&sm.hist[(int)((k - lo) >> shift)], 1u);
+      for (int i = 0; i < BPT; ++i) sm.hist[tid + i * NTH] = 0;
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += NTH) {
+        const uint64_t k = key(i);
+        if (k >= lo && k <= hi) atomicAdd(&sm.hist[(int)((k - lo) >> shift)], 1u);
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    counted = false;
     // bins from the top: thread t holds bins kTopBins - 1 - t * BPT downwards
     int c[BPT], sum = 0;
 #pragma unroll
