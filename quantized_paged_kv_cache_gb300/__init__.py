@@ -872,6 +872,8 @@ def evict_pages(page_size: int, weights, block_table, ctx_lens, keep_pages: int,
 
 def _vocab_stride(t, what: str) -> int:
     """Elements between the rows of [B][rows][vocab], which must all be the same distance apart."""
+    if t.is_contiguous():
+        return t.shape[2]
     (b, r, v), (s0, s1, s2) = t.shape, t.stride()
     if v > 1 and s2 != 1:
         raise ValueError(f"the entries of a row of {what} must be consecutive")

@@ -178,15 +178,10 @@ __device__ void block_threshold(const Key& key, int n, int need, uint64_t klo, u
   __syncthreads();
 }
 
-// Smallest and largest of the block's keys (of n >= 1). Ends with a barrier.
-template <int NTH, class Key>
-__device__ void block_range(const Key& key, int n, TopSmem<NTH>& sm, uint64_t& klo, uint64_t& khi) {
-  uint64_t lo = ~0ull, hi = 0;
-  for (int i = threadIdx.x; i < n; i += NTH) {
-    const uint64_t k = key(i);
-    lo = k < lo ? k : lo;
-    hi = k > hi ? k : hi;
-  }
+// Smallest and largest of the block's keys: each thread's own into shared memory by
+// warps (top_range), and after a barrier those of all (range_of).
+template <int NTH>
+__device__ __forceinline__ void top_range(uint64_t lo, uint64_t hi, TopSmem<NTH>& sm) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const uint64_t l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
@@ -197,12 +192,28 @@ __device__ void block_range(const Key& key, int n, TopSmem<NTH>& sm, uint64_t& k
     sm.lo[threadIdx.x >> 5] = lo;
     sm.hi[threadIdx.x >> 5] = hi;
   }
-  __syncthreads();
+}
+template <int NTH>
+__device__ __forceinline__ void range_of(uint64_t& lo, uint64_t& hi, const TopSmem<NTH>& sm) {
 #pragma unroll
   for (int w = 0; w < NTH / 32; ++w) {
     lo = sm.lo[w] < lo ? sm.lo[w] : lo;
     hi = sm.hi[w] > hi ? sm.hi[w] : hi;
   }
+}
+
+// The same of n >= 1 keys. Ends with a barrier.
+template <int NTH, class Key>
+__device__ void block_range(const Key& key, int n, TopSmem<NTH>& sm, uint64_t& klo, uint64_t& khi) {
+  uint64_t lo = ~0ull, hi = 0;
+  for (int i = threadIdx.x; i < n; i += NTH) {
+    const uint64_t k = key(i);
+    lo = k < lo ? k : lo;
+    hi = k > hi ? k : hi;
+  }
+  top_range(lo, hi, sm);
+  __syncthreads();
+  range_of(lo, hi, sm);
   klo = lo;
   khi = hi;
   __syncthreads();

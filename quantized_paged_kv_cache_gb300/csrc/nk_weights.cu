@@ -435,6 +435,7 @@ __device__ __forceinline__ uint32_t ordered32(float x) {
 __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) {
   extern __shared__ uint64_t keys[];
   __shared__ TopSmem<kEvThreads> sm;
+  __shared__ int before_s[kEvThreads / 32], all_s[kEvThreads / 32];
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, b = blockIdx.x;
@@ -445,19 +446,28 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
     if (L < 0 || (int64_t)L > (int64_t)p.max_pages * p.P) return -1;
     return L == 0 ? 0 : (L - 1) / p.P + 1;
   };
-  int64_t before = 0, all = 0;
+  // (a warp's sums; whoever needs them adds those up behind a later barrier)
+  int before = 0, all = 0;
   for (int i = tid; i < p.B; i += kEvThreads) {
-    const int held = held_of(i), gone = held > p.keep ? held - p.keep : 0;
+    const int h = held_of(i), gone = h > p.keep ? h - p.keep : 0;
     all += gone;
     if (i < b) before += gone;
   }
-  int sum_before, sum_all;
-  (void)block_exclusive<kEvThreads>((int)before, sm.warp, sum_before);
-  (void)block_exclusive<kEvThreads>((int)all, sm.warp, sum_all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if ((tid & 31) == 0) {
+    before_s[tid >> 5] = before;
+    all_s[tid >> 5] = all;
+  }
   const int held = held_of(b);
-  if (b == 0 && tid == 0) {
-    *p.num_freed = sum_all;
-    if (sum_all > p.max_freed) flag(p.status, NK_DEVFLAG_NO_PAGES);
+  if (b == 0) {  // (block-uniform)
+    __syncthreads();
+    if (tid == 0) {
+      int sum = 0;
+      for (int w = 0; w < kEvThreads / 32; ++w) sum += all_s[w];
+      *p.num_freed = sum;
+      if (sum > p.max_freed) flag(p.status, NK_DEVFLAG_NO_PAGES);
+    }
   }
   if (held < 0) {
     if (tid == 0) {
@@ -474,39 +484,62 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
       for (int i = tid; i < p.max_pages; i += kEvThreads) p.out[row + i] = p.table[row + i];
     return;
   }
+  // pages of a thread in flight: their ids, then a head's weights of all of them
+  constexpr int U = 4;
   bool bad = false;
-  for (int i = tid; i < held; i += kEvThreads) {
-    const int page = p.table[row + i];
-    float hi = 0.f, lo = 0.f;
-    if (page < 0 || page >= p.num_pages) {
-      bad = true;
-    } else {
-      for (int h = 0; h < p.Hkv; ++h) {
-        const float v = fminf(fmaxf(p.w[(int64_t)page * p.Hkv + h], -1e36f), 1e36f);  // (NaN: last)
-        // hi + v exactly as a sum and its rounding error, the error joined to lo
-        const float s = hi + v, z = s - hi;
-        const float err = (hi - (s - z)) + (v - z);
-        hi = s;
-        lo += err;
-      }
-      const float s = hi + lo;
-      lo = lo - (s - hi);
-      hi = s;
+  uint64_t klo = ~0ull, khi = 0;
+  const int last = held - p.recent;  // one past the last page in question
+  for (int i0 = tid; i0 < held; i0 += kEvThreads * U) {
+    int page[U];
+    float hi[U], lo[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kEvThreads;
+      page[u] = i < held ? p.table[row + i] : 0;
+      hi[u] = lo[u] = 0.f;
     }
-    ids[i] = page;
-    // (+ 0: a negative zero has the order of a positive one)
-    keys[i] = ((uint64_t)ordered32(hi + 0.f) << 32) | ordered32(lo + 0.f);
+#pragma unroll 4
+    for (int h = 0; h < p.Hkv; ++h) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool there = page[u] >= 0 && page[u] < p.num_pages;
+        // (NaN: last)
+        const float v = there ? fminf(fmaxf(p.w[(int64_t)page[u] * p.Hkv + h], -1e36f), 1e36f) : 0.f;
+        // hi + v exactly as a sum and its rounding error, the error joined to lo
+        const float s = hi[u] + v, z = s - hi[u];
+        lo[u] += (hi[u] - (s - z)) + (v - z);
+        hi[u] = s;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kEvThreads;
+      if (i >= held) continue;
+      bad |= page[u] < 0 || page[u] >= p.num_pages;
+      const float s = hi[u] + lo[u], l = lo[u] - (s - hi[u]);
+      // (+ 0: a negative zero has the order of a positive one)
+      const uint64_t k = ((uint64_t)ordered32(s + 0.f) << 32) | ordered32(l + 0.f);
+      ids[i] = page[u];
+      keys[i] = k;
+      if (i >= p.sinks && i < last) {
+        klo = k < klo ? k : klo;
+        khi = k > khi ? k : khi;
+      }
+    }
   }
   if (bad) flag(p.status, NK_DEVFLAG_BAD_PAGE);
+  top_range(klo, khi, sm);
   __syncthreads();
-  const int n = held - p.sinks - p.recent, need = p.keep - p.sinks - p.recent;  // need < n
+  int sum_before = 0;
+#pragma unroll
+  for (int w = 0; w < kEvThreads / 32; ++w) sum_before += before_s[w];
+  const int n = last - p.sinks, need = p.keep - p.sinks - p.recent;  // need < n
   const uint64_t* mid = keys + p.sinks;
   const auto key = [&](int i) { return mid[i]; };
   uint64_t kt = ~0ull;
   int it = -1;
   if (need > 0) {
-    uint64_t klo, khi;
-    block_range<kEvThreads>(key, n, sm, klo, khi);
+    range_of(klo, khi, sm);
     block_threshold<kEvThreads>(key, n, need, klo, khi, sm, kt, it);
   }
   const int per = top_run<kEvThreads>(held), a = tid * per, e = a + per < held ? a + per : held;
