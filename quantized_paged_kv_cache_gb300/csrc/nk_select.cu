@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   constexpr int GR = D / kGroup;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings
   __shared__ int pre[kMaxBatch + 1];               // touched pages before sequence b
+  __shared__ int2 span[kMaxBatch];                 // its first new position, one past its last
   __shared__ int warp_tot[kBndWarps];
   __shared__ uint64_t bars[kBndWarps][kBndStages];
   __shared__ int4 meta[kBndWarps][kBndStages];     // record (two words), keys, the item's last
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
       v[i] = 0;
       if (b < p.B) {
         const int64_t s = p.start[b], n = (int64_t)p.cu[b + 1] - p.cu[b];
+        span[b] = make_int2((int)s, (int)(s + n));
         if (s < 0 || n < 0 || s + n > (int64_t)p.max_pages * P || s + n > 0x7fffffff) {
           if (blockIdx.x == 0) flag(p.status, NK_DEVFLAG_BAD_POS);
         } else if (n > 0) {
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   }
   const int64_t items = (int64_t)pre[p.B] * p.Hkv;
   const int c0 = (lane % LPR) * 16;
-  // Item x: its page (-1: none, flagged) and filled slots
+  // Item x: what the table says of its page, and its filled slots
   const auto look = [&](int64_t x, int& filled) {
     const int k = (int)quot(x, p.Hkv);
     int b = 0, top = p.B;
@@ -199,15 +201,15 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
       const int mid = (b + top) >> 1;
       if (pre[mid] <= k) b = mid; else top = mid;
     }
-    const int start = p.start[b];
-    const int64_t end = (int64_t)start + (p.cu[b + 1] - p.cu[b]);
-    const int logical = start / P + (k - pre[b]);
-    const int page = p.bt[(int64_t)b * p.max_pages + logical];
-    const int64_t left = end - (int64_t)logical * P;
-    filled = left < P ? (int)left : P;
-    if (page >= 0 && page < p.num_pages) return page;
+    const int2 s = span[b];
+    const int logical = s.x / P + (k - pre[b]);
+    filled = min(s.y - logical * P, P);
+    return p.bt[(int64_t)b * p.max_pages + logical];
+  };
+  const auto none = [&](int page) {
+    if (page >= 0 && page < p.num_pages) return false;
     if (lane == 0) flag(p.status, NK_DEVFLAG_BAD_PAGE);
-    return -1;
+    return true;
   };
   float hi[16], lo[16];
   const auto clear = [&]() {
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     if (x >= items) return;
     int filled;
     const int page = look(x, filled);
-    if (page < 0) return;
+    if (none(page)) return;
     const int64_t rec = (int64_t)page * p.Hkv + x % p.Hkv;
     const uint8_t* chunk = p.pool + rec * p.lay.chunk;
     clear();
@@ -293,16 +295,20 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   }
   __syncwarp();
   const int64_t stride = (int64_t)gridDim.x * kBndWarps;
-  int64_t x = (int64_t)blockIdx.x * kBndWarps + warp;  // the next item to copy
-  int page = -1, filled = 0, key = 0, issued = 0;
-  const auto next_page = [&]() {
-    for (; x < items; x += stride) {
-      page = look(x, filled);
-      if (page >= 0) break;
-    }
+  // the next item to copy, and the one behind it, whose page's number is on its way
+  int64_t x = (int64_t)blockIdx.x * kBndWarps + warp;
+  int page = 0, filled = 0, page_b = 0, filled_b = 0, key = 0, issued = 0;
+  if (x < items) page = look(x, filled);
+  if (x + stride < items) page_b = look(x + stride, filled_b);
+  const auto advance = [&]() {
+    x += stride;
+    page = page_b;
+    filled = filled_b;
     key = 0;
+    if (x + stride < items) page_b = look(x + stride, filled_b);
   };
   const auto issue = [&]() {
+    while (x < items && none(page)) advance();
     if (x >= items) return;
     const int st = issued % kBndStages, rows = min(kBndKeys, filled - key), all = (rows + 15) / 16 * 16;
     const int64_t rec = (int64_t)page * p.Hkv + x % p.Hkv;
@@ -316,12 +322,8 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     }
     ++issued;
     key += rows;
-    if (key >= filled) {
-      x += stride;
-      next_page();
-    }
+    if (key >= filled) advance();
   };
-  next_page();
   for (int i = 0; i < kBndStages - 1; ++i) issue();
   clear();
   for (int n = 0; n < issued; ++n) {
