@@ -39,7 +39,7 @@ __host__ __device__ inline BoundsView bounds_view(void* base, int64_t num_pages,
 // A thread takes 16 bytes of a row at a time and keeps the extremes of its 16
 // channels; D / 16 threads hold a row. With more items than blocks a warp takes an
 // item, from a ring of its own in shared memory that bulk asynchronous copies fill,
-// 32 keys a stage (no barrier between warps; rows merged by shuffles). With fewer
+// 16 keys a stage (no barrier between warps; rows merged by shuffles). With fewer
 // (a step of single tokens) a block does, straight from global memory, its warps'
 // extremes merged through shared memory, so that all of the item's bytes are on
 // their way at once.
@@ -49,7 +49,8 @@ __host__ __device__ inline BoundsView bounds_view(void* base, int64_t num_pages,
 // + 128 + code) and a packed subtraction: the conversion instruction takes an
 // eighth of their rate. Eight prompts of 8K to 16K tokens (101 MB): 65 us with
 // conversions and a block an item, 42 with packed ones and a warp an item that
-// loads into registers, too few of them in flight.
+// loads into registers, 33 with the rings, eight warps of 32 keys or sixteen of 16,
+// 28.7 with neighbouring items on different SMs (each warp has two or three).
 // ---------------------------------------------------------------------------
 struct BoundsParams {
   const uint8_t* pool;
@@ -64,8 +65,9 @@ struct BoundsParams {
   int32_t* status;
 };
 
-constexpr int kBndThreads = 256, kBndWarps = kBndThreads / 32;
-constexpr int kBndKeys = 32, kBndStages = 3;  // of a warp's ring
+constexpr int kBndThreads = 512, kBndWarps = kBndThreads / 32;
+constexpr int kBndWide = 256;  // threads that share an item
+constexpr int kBndKeys = 16, kBndStages = 3;  // of a stage, of a warp's ring
 template <int D>
 constexpr int bounds_stage() {  // codes, then scales
   return kBndKeys * (D + D / kGroup * 4);
@@ -101,6 +103,17 @@ __device__ __forceinline__ void values4(uint32_t w, uint64_t scale2, float (&v)[
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Extremes of rows r0, r0 + step, .. below `filled` at the thread's 16 channels,
 // from global or shared memory; true if a scale was not finite.
 template <int D, int LOADS>
@@ -134,9 +147,9 @@ __device__ __forceinline__ bool row_extremes(const uint8_t* codes, const float* 
         values4(u0[i], s0, v0);
         values4(u1[i], s1, v1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // (three-input extremes)
-          hi[4 * i + k] = fmaxf(hi[4 * i + k], fmaxf(v0[k], v1[k]));
-          lo[4 * i + k] = fminf(lo[4 * i + k], fminf(v0[k], v1[k]));
+        for (int k = 0; k < 4; ++k) {
+          hi[4 * i + k] = max3(hi[4 * i + k], v0[k], v1[k]);
+          lo[4 * i + k] = min3(lo[4 * i + k], v0[k], v1[k]);
         }
       }
     }
@@ -144,8 +157,14 @@ __device__ __forceinline__ bool row_extremes(const uint8_t* codes, const float* 
   return odd;
 }
 
-__device__ __forceinline__ uint32_t bound_code(float x, float s) {
-  return (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f) & 0xffu;
+// The code of x at scale s, with r = fp32(1 / s): the quotient by the reciprocal is
+// off by less than 2^-15 (three roundings of 2^-24 of at most 127), so only one that
+// near the border between two codes needs the division itself.
+__device__ __forceinline__ uint32_t bound_code(float x, float s, float r) {
+  float q = x * r;
+  const float n = rintf(q);
+  if (!(fabsf(q - n) < 0.4999f)) q = __fdiv_rn(x, s);
+  return (uint32_t)(int)fminf(fmaxf(rintf(q), -127.f), 127.f) & 0xffu;
 }
 
 template <int D>
@@ -236,6 +255,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s = __fdiv_rn(m, 127.f);
     if (s == 0.f) s = 1.f;
+    const float r = __frcp_rn(s);  // (infinite for the smallest: every quotient is then divided)
     // lanes below LPR write hi, the next LPR lo
     const bool low = lane >= LPR;
     if (lane < 2 * LPR) {
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
       for (int i = 0; i < 4; ++i) {
         w[i] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[i] |= bound_code(low ? lo[4 * i + j] : hi[4 * i + j], s) << (8 * j);
+        for (int j = 0; j < 4; ++j) w[i] |= bound_code(low ? lo[4 * i + j] : hi[4 * i + j], s, r) << (8 * j);
       }
       *reinterpret_cast<uint4*>(p.out.codes + rec * 2 * D + (low ? D : 0) + c0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
 
   if (items <= gridDim.x) {  // a block for each item
     const int64_t x = blockIdx.x;
-    if (x >= items) return;
+    if (x >= items || tid >= kBndWide) return;
     int filled;
     const int page = look(x, filled);
     if (none(page)) return;
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     const uint8_t* chunk = p.pool + rec * p.lay.chunk;
     clear();
     if (row_extremes<D, 4>(chunk + c0, reinterpret_cast<const float*>(chunk + p.lay.ks) + c0 / kGroup, tid / LPR,
-                           kBndThreads / LPR, filled, hi, lo))
+                           kBndWide / LPR, filled, hi, lo))
       flag(p.status, NK_DEVFLAG_RANGE);
     merge_lanes();
     float* hi_s = reinterpret_cast<float*>(smem) + warp * 2 * D;
@@ -272,10 +292,10 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
         *reinterpret_cast<float4*>(hi_s + D + c0 + i) = make_float4(lo[i], lo[i + 1], lo[i + 2], lo[i + 3]);
       }
     }
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"n"(kBndWide) : "memory");
     if (warp > 0) return;
 #pragma unroll
-    for (int w = 0; w < kBndWarps; ++w)
+    for (int w = 0; w < kBndWide / 32; ++w)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         hi[i] = fmaxf(hi[i], reinterpret_cast<const float*>(smem)[w * 2 * D + c0 + i]);
@@ -296,7 +316,8 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   __syncwarp();
   const int64_t stride = (int64_t)gridDim.x * kBndWarps;
   // the next item to copy, and the one behind it, whose page's number is on its way
-  int64_t x = (int64_t)blockIdx.x * kBndWarps + warp;
+  // (neighbouring items on different SMs, so that the last ones are spread over all)
+  int64_t x = (int64_t)warp * gridDim.x + blockIdx.x;
   int page = 0, filled = 0, page_b = 0, filled_b = 0, key = 0, issued = 0;
   if (x < items) page = look(x, filled);
   if (x + stride < items) page_b = look(x + stride, filled_b);
