@@ -43,15 +43,22 @@ int device_sms() {
   return n;
 }
 
+namespace {
+// nk_test_inject_copy_stall: withheld CTA page number (-1: none) and wait limit (0: the default)
+std::atomic<int> g_withhold{-1};
+std::atomic<unsigned long long> g_wait_cycles{0};
+}  // namespace
+
+WaitLimits wait_limits() {
+  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
+  return {wc > 0 ? wc : kWaitCycles, g_withhold.load(std::memory_order_relaxed)};
+}
+
 }  // namespace nk
 
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// nk_test_inject_copy_stall: withheld CTA page number (-1: none) and wait limit (0: the default)
-std::atomic<int> g_withhold{-1};
-std::atomic<unsigned long long> g_wait_cycles{0};
 
 bool pool_ok(const nk_kv_pool* pool, int* err) {
   *err = check_pool(pool);
@@ -238,9 +245,9 @@ int prepare_decode(const nk_kv_pool* pool, const void* q, const int32_t* bt, int
   p.qT = T;
   p.trim = 0;
   p.early = 0;
-  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
-  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
-  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  const WaitLimits limits = wait_limits();
+  p.wait_cycles = limits.cycles;
+  p.withhold = limits.withhold;
   *empty = false;
   return NK_OK;
 }
@@ -513,9 +520,9 @@ int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
   p.part_lse = p.part_o + ((int64_t)n + units) * G * D;
   p.out = reinterpret_cast<uint16_t*>(out_dev);
   p.status = status_dev;
-  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
-  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
-  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  const WaitLimits limits = wait_limits();
+  p.wait_cycles = limits.cycles;
+  p.withhold = limits.withhold;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_decode_mma(p, st);
   if (e == cudaSuccess) e = launch_decode_combine(p, st);
@@ -662,9 +669,9 @@ int nk_paged_prefill_attn(const nk_kv_pool* pool, const void* q_dev, const int32
   p.n_ctas = (int)grid;
   p.out = reinterpret_cast<uint16_t*>(out_dev);
   p.status = status_dev;
-  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
-  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
-  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  const WaitLimits limits = wait_limits();
+  p.wait_cycles = limits.cycles;
+  p.withhold = limits.withhold;
   return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
@@ -725,9 +732,9 @@ int nk_paged_chunk_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t
   p.desc = reinterpret_cast<int4*>(p.part_lse + slots);
   p.out = reinterpret_cast<uint16_t*>(out_dev);
   p.status = status_dev;
-  const unsigned long long wc = g_wait_cycles.load(std::memory_order_relaxed);
-  p.wait_cycles = wc > 0 ? wc : kWaitCycles;
-  p.withhold = g_withhold.load(std::memory_order_relaxed);
+  const WaitLimits limits = wait_limits();
+  p.wait_cycles = limits.cycles;
+  p.withhold = limits.withhold;
   return chunk::launch(p, D, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 

@@ -13,6 +13,14 @@ int check_pool(const nk_kv_pool* pool);
 // SMs of the current device (0 when it cannot be asked).
 int device_sms();
 
+// Limit of a bounded wait, and the number of the first copy withheld (-1: none) --
+// nk_test_inject_copy_stall.
+struct WaitLimits {
+  unsigned long long cycles;
+  int withhold;
+};
+WaitLimits wait_limits();
+
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace nk

@@ -63,6 +63,8 @@ struct BoundsParams {
   int B;
   BoundsView out;
   int32_t* status;
+  unsigned long long wait_cycles;  // of a bounded wait
+  int withhold;                    // a warp's copies from this number on are never made (-1: all are): tests
 };
 
 constexpr int kBndThreads = 512, kBndWarps = kBndThreads / 32;
@@ -334,12 +336,15 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
     const int st = issued % kBndStages, rows = min(kBndKeys, filled - key), all = (rows + 15) / 16 * 16;
     const int64_t rec = (int64_t)page * p.Hkv + x % p.Hkv;
     if (lane == 0) {
+      const bool held = p.withhold >= 0 && issued >= p.withhold;
       meta[warp][st] = make_int4((int)(rec >> 31), (int)(rec & 0x7fffffff), rows, key + rows >= filled);
       const uint8_t* chunk = p.pool + rec * p.lay.chunk;
       const uint32_t dst = smem_u32(ring + st * kStage), bar = bar0 + 8 * st;
-      mbar_arrive_expect_tx(bar, all * (D + GR * 4));
-      bulk_load(dst, chunk + (int64_t)key * D, all * D, bar);
-      bulk_load(dst + kBndKeys * D, chunk + p.lay.ks + key * (GR * 4), all * (GR * 4), bar);
+      if (!held) {
+        mbar_arrive_expect_tx(bar, all * (D + GR * 4));
+        bulk_load(dst, chunk + (int64_t)key * D, all * D, bar);
+        bulk_load(dst + kBndKeys * D, chunk + p.lay.ks + key * (GR * 4), all * (GR * 4), bar);
+      }
     }
     ++issued;
     key += rows;
@@ -350,11 +355,13 @@ __global__ void __launch_bounds__(kBndThreads) page_bounds_kernel(const BoundsPa
   for (int n = 0; n < issued; ++n) {
     issue();
     const int st = n % kBndStages;
-    if (!mbar_wait(bar0 + 8 * st, (uint32_t)(n / kBndStages) & 1u)) {  // (what follows is not waited for either)
+    // (after a wait that ran out nothing more is copied: the loop ends with the copies under way)
+    const bool late = !mbar_wait(bar0 + 8 * st, (uint32_t)(n / kBndStages) & 1u, p.wait_cycles);
+    if (__any_sync(0xffffffffu, late)) {
       flag(p.status, NK_DEVFLAG_TIMEOUT);
       x = items;
+      continue;
     }
-    __syncwarp();
     const int4 m = meta[warp][st];
     const uint8_t* codes = ring + st * kStage;
     if (row_extremes<D, 4>(codes + c0, reinterpret_cast<const float*>(codes + kBndKeys * D) + c0 / kGroup, lane / LPR,
@@ -876,9 +883,11 @@ int nk_page_bounds(const nk_kv_pool* pool, void* bounds_dev, const int32_t* bloc
   if (!bounds_dev || !block_table_dev || !start_pos_dev || !cu_new_dev) return NK_ERR_NULL;
   if (!aligned_to(bounds_dev, 16)) return NK_ERR_SHAPE;
   const int P = pool->page_size, D = pool->head_dim;
+  const WaitLimits limits = wait_limits();
   const BoundsParams p{reinterpret_cast<const uint8_t*>(pool->base_dev), ChunkLayout::make(P, D), pool->num_pages, P,
                        pool->num_kv_heads, block_table_dev, max_pages_per_seq, start_pos_dev, cu_new_dev, B,
-                       bounds_view(bounds_dev, pool->num_pages, pool->num_kv_heads, D), status_dev};
+                       bounds_view(bounds_dev, pool->num_pages, pool->num_kv_heads, D), status_dev, limits.cycles,
+                       limits.withhold};
   const int sms = device_sms();
   int64_t grid = (int64_t)B * max_pages_per_seq * pool->num_kv_heads;
   const int64_t most = sms > 0 ? sms : 148;

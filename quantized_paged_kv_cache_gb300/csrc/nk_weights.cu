@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
   const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.y + 1);
   Segment seg;
   int64_t item = x;  // of the segment's first page
-  int issued = 0, used = 0;  // steps
+  int issued = 0, used = 0, sent = 0;  // steps; one past the last that was copied
   bool timed_out = false;
   while (next_segment(sh, pre, x, x_end, seg)) {
     const int L = lens[seg.b], pages = seg.page_end - seg.page_begin;
@@ -117,15 +117,16 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
       none = bad ? none | bit : none & ~bit;
       if (lane == 0) {
         const uint32_t dst = ring_u32 + slot * Step::kBytes, bar = bar0 + 8 * slot;
-        if (bad || timed_out) {
+        if (bad) {
           mbar_arrive(bar);
-        } else {
+        } else if (!timed_out && !(p.withhold >= 0 && issued >= p.withhold)) {
           const uint8_t* chunk = p.pool + ((int64_t)id * Hkv + seg.h) * p.lay.chunk;
           mbar_arrive_expect_tx(bar, keys * (D + NG * 4));
           bulk_load(dst, chunk + c_k * D, keys * D, bar);
           bulk_load(dst + Step::kCodes, chunk + p.lay.ks + c_k * (NG * 4), keys * (NG * 4), bar);
         }
       }
+      if (!timed_out && !(p.withhold >= 0 && issued >= p.withhold)) sent = issued + 1;
       ++issued;
       c_k += 16 * KB;
       if (c_k >= live) {
@@ -182,8 +183,8 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
       for (int k0 = 0; k0 < live; k0 += 16 * KB) {
         issue();
         const int slot = used % S;
-        // (after a wait that ran out nothing is copied, and nothing waited for but copies under way)
-        if (!mbar_wait(bar0 + 8 * slot, (uint32_t)(used / S) & 1u)) {
+        // (after a wait of the warp has run out it copies nothing more and waits for nothing but, at the end, its copies)
+        if (!timed_out && !mbar_wait(bar0 + 8 * slot, (uint32_t)(used / S) & 1u, p.wait_cycles)) {
           flag(p.status, NK_DEVFLAG_TIMEOUT);
           timed_out = true;
         }
@@ -330,6 +331,8 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
     item += pages;
     __syncthreads();
   }
+  if (timed_out)
+    for (int i = max(0, sent - S); i < sent; ++i) (void)mbar_wait(bar0 + 8 * (i % S), (uint32_t)(i / S) & 1u, p.wait_cycles);
 }
 
 // Second kernel: block (x, unit) takes pages x * 32 .. of the unit; eight lanes
@@ -689,6 +692,9 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
   p.seen = seen_dev;
   p.out = weights_dev;
   p.status = status_dev;
+  const WaitLimits limits = wait_limits();
+  p.wait_cycles = limits.cycles;
+  p.withhold = limits.withhold;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = r.tc       ? launch_lse_tc(p, r.chunks, st)
                   : D == 256 ? launch_lse_d<256>(p, r.chunks, st)

@@ -26,6 +26,8 @@ struct WeightParams {
   const int32_t* seen;  // may be NULL
   float* out;         // [num_pages][Hkv]
   int32_t* status;
+  unsigned long long wait_cycles;  // of every bounded wait
+  int withhold;                    // steps from this number on are never copied (-1: all are): tests
 };
 
 __device__ __forceinline__ float wgt_ex2(float x) {

@@ -26,8 +26,8 @@
 // Only the copying warps know segments and tables: with the walk in every role the
 // registers spilled, and beside 217 KB of shared memory no L1 is left to hold a
 // spill (8 windows of 16 tokens at 8K to 64K: 204 us for this kernel then).
-// Every mbarrier wait is bounded; after one has run out nothing more is issued and
-// no wait blocks.
+// Every mbarrier wait is bounded; after one has run out every role ends at its next
+// wait, and the copies and products under way are waited for.
 #include <math.h>
 
 #include "nk_ptx.cuh"
@@ -194,12 +194,15 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
     __syncthreads();
   }
   const auto wait = [&](uint32_t bar, uint32_t parity) {  // by whole warps
-    if (!*abort_flag && !mbar_wait(bar, parity)) {
+    if (!*abort_flag && !mbar_wait(bar, parity, p.wait_cycles)) {
       flag(p.status, NK_DEVFLAG_TIMEOUT);
       *abort_flag = 1;
     }
     __syncwarp();
   };
+  // After a wait, by whole warps: one of the CTA's has run out, so this role ends where
+  // it is (what a wait has not confirmed is not read, least of all a tile's description).
+  const auto stopped = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
   if (warp < kSoft) {
     set_regs<kRegsSoft>();
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
     for (int n = set;; n += 2) {
       const int sl = n % kScales;
       wait(sc_full(sl), (uint32_t)(n / kScales) & 1u);
+      if (stopped()) break;
       const int4 d0 = *reinterpret_cast<const int4*>(desc + sl), d1 = *(reinterpret_cast<const int4*>(desc + sl) + 1);
       const int len = d0.z;
       if (len == 0 || d1.z != seg) {
@@ -232,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
         wait(rows_full(seg % kRowSets), (uint32_t)(seg / kRowSets) & 1u);
         un = reinterpret_cast<const float*>(smem + SM::off_undo)[(seg % kRowSets) * kRowsMost + row];
       }
+      if (stopped()) break;
       fence_after();
       if (act) {
         const float* scales = reinterpret_cast<const float*>(smem + SM::off_sc) + (sl * kKeys + half * (kKeys / 2)) * NG;
@@ -310,12 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
     for (int n = team;; n += 2) {
       const int rs = n % kRaw;
       wait(raw_full(rs), (uint32_t)(n / kRaw) & 1u);
+      if (stopped()) break;
       const int4 d0 = *reinterpret_cast<const int4*>(desc + n % kScales), d1 = *(reinterpret_cast<const int4*>(desc + n % kScales) + 1);
       if (d0.z == 0) {
         // (as for any tile, after the products over the buffer's last one: two phases ahead
         // of the wait for it, the barrier would hold that up for good)
         if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
-        if (lane == 0) mbar_arrive(b_full(team));
+        if (!stopped() && lane == 0) mbar_arrive(b_full(team));
         break;
       }
       if (d1.w) {
@@ -325,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
         if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
         if (n >= 3) wait(b_empty(team ^ 1), (uint32_t)((n - 3) >> 1) & 1u);
         if (n >= 1) wait(b_empty(team ^ 1), (uint32_t)((n - 1) >> 1) & 1u);
+        if (stopped()) break;
         const int T = p.sh.T, G = p.G, Hkv = p.sh.Hkv, b = d1.y / Hkv, h = d1.y - b * Hkv;
         float* undo = reinterpret_cast<float*>(smem + SM::off_undo) + (d1.z % kRowSets) * kRowsMost;
         const float sign = p.scale2 < 0.f ? -1.f : 1.f;
@@ -359,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(rows_full(d1.z % kRowSets));
       }
       if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
+      if (stopped()) break;
       const uint8_t* raw = smem + SM::off_raw + rs * (kKeys * D);
       uint8_t* dst = smem + SM::off_b + team * (NG * kKeys * 128);
       constexpr int PCS = D / 16;  // 16-code pieces of a key
@@ -400,11 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
       for (int n = 0;; ++n) {
         const int buf = n & 1;
         wait(b_full(buf), (uint32_t)(n >> 1) & 1u);
+        if (stopped()) break;
         const Tile* t = desc + n % kScales;
         if (t->len == 0) break;
         if (t->first) wait(rows_full(t->seg % kRowSets), (uint32_t)(t->seg / kRowSets) & 1u);
         if (n >= 2) wait(acc_empty(buf), (uint32_t)((n >> 1) - 1) & 1u);
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) continue;
+        if (stopped()) break;
         ++done[buf];
         if (leader) {
           fence_after();
@@ -422,21 +431,22 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
       // after a wait that ran out products may still be under way: they end before tensor memory is given back
       if (*abort_flag)
         for (int i = 0; i < 2; ++i)
-          if (done[i] > 0) (void)mbar_wait(b_empty(i), (uint32_t)(done[i] - 1) & 1u);
+          if (done[i] > 0) (void)mbar_wait(b_empty(i), (uint32_t)(done[i] - 1) & 1u, p.wait_cycles);
     } else if (warp < kCopyWarp + 2) {
       // ------------------------------------------------------------ copies
       const int P = p.sh.P, Hkv = p.sh.Hkv, odd = warp - kCopyWarp;
       const int share = P < kKeys ? kKeys / P : 1;
-      int n = 0, segs = 0, item = (int)x;
+      int n = 0, segs = 0, item = (int)x, sent = -1;  // sent: the last tile that was copied
       Segment seg;
-      while (next_segment(p.sh, pre, x, x_end, seg)) {
+      bool stop = false;
+      while (!stop && next_segment(p.sh, pre, x, x_end, seg)) {
         const int L = lens[seg.b], pages = seg.page_end - seg.page_begin;
         const int32_t* bt = p.bt + (int64_t)seg.b * p.sh.max_pages + seg.page_begin;
         // page ids of 32 pages of the segment, and the next 32
         int have = 0, ids = lane < pages ? bt[lane] : -1, ids2 = 32 + lane < pages ? bt[32 + lane] : -1;
         bool first = true;
-        for (int pg0 = 0; pg0 < pages; pg0 += share) {
-          for (int k0 = 0; k0 < P; k0 += kKeys, ++n, first = false) {
+        for (int pg0 = 0; pg0 < pages && !stop; pg0 += share) {
+          for (int k0 = 0; k0 < P && !stop; k0 += kKeys, ++n, first = false) {
             if ((n & 1) != odd) continue;
             const int rs = n % kRaw, sl = n % kScales;
             if (pg0 - have >= 32) {  // (32 is a whole number of a tile's pages: 4, 2 or 1)
@@ -458,13 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
             gone = __reduce_or_sync(0xffffffffu, gone);
             if (n >= kRaw) wait(raw_empty(rs), (uint32_t)(n / kRaw - 1) & 1u);
             if (n >= kScales) wait(sc_empty(sl), (uint32_t)(n / kScales - 1) & 1u);
-            const bool go = !__any_sync(0xffffffffu, *abort_flag != 0);
+            stop = stopped();
+            if (stop) continue;
+            const bool held = p.withhold >= 0 && n >= p.withhold;
+            if (!held) sent = n;
             if (lane == 0) {
               int4* d = reinterpret_cast<int4*>(desc + sl);
               const int there = min(min(P - k0, kKeys) * min(share, pages - pg0), kKeys);
               d[0] = make_int4((seg.page_begin + pg0) * P + k0, there, L, gone);
               d[1] = make_int4((item + pg0) * p.parts + k0 / (kKeys / 2), seg.u, segs, first);
-              if (go && all > 0) {
+              if (held) {
+                // (nobody arrives: a test of the waits)
+              } else if (all > 0) {
                 mbar_arrive_expect_tx(raw_full(rs), all * D);
                 mbar_arrive_expect_tx(sc_full(sl), all * NG * 4);
               } else {
@@ -473,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
               }
             }
             __syncwarp();
-            if (go && keys > 0) {
+            if (!held && keys > 0) {
               const uint8_t* chunk = p.pool + ((int64_t)id * Hkv + seg.h) * p.lay.chunk;
               const int at = lane * P;  // (lane 0 alone where pages have several tiles)
               bulk_load(smem_u32(smem + SM::off_raw + rs * (kKeys * D) + at * D), chunk + (int64_t)k0 * D, keys * D, raw_full(rs));
@@ -491,16 +506,17 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
       const int rs = n % kRaw, sl = n % kScales;
       if (n >= kRaw) wait(raw_empty(rs), (uint32_t)(n / kRaw - 1) & 1u);
       if (n >= kScales) wait(sc_empty(sl), (uint32_t)(n / kScales - 1) & 1u);
-      if (lane == 0) {
+      if (!stopped() && lane == 0) {
         desc[sl].len = 0;
         mbar_arrive(raw_full(rs));
         mbar_arrive(sc_full(sl));
       }
       // after a wait that ran out some copies may still be in flight: they land before the CTA ends
       if (*abort_flag) {
-        for (int i = n - 2; i >= 0 && i > n - kRaw; i -= 2) (void)mbar_wait(raw_full(i % kRaw), (uint32_t)(i / kRaw) & 1u);
-        for (int i = n - 2; i >= 0 && i > n - kScales; i -= 2)
-          (void)mbar_wait(sc_full(i % kScales), (uint32_t)(i / kScales) & 1u);
+        for (int i = sent; i >= 0 && i > sent - kRaw; i -= 2)
+          (void)mbar_wait(raw_full(i % kRaw), (uint32_t)(i / kRaw) & 1u, p.wait_cycles);
+        for (int i = sent; i >= 0 && i > sent - kScales; i -= 2)
+          (void)mbar_wait(sc_full(i % kScales), (uint32_t)(i / kScales) & 1u, p.wait_cycles);
       }
     }
   }
