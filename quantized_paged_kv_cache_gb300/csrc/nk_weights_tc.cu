@@ -97,15 +97,11 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void tm_ld8(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+__device__ __forceinline__ void tm_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
 }
 
 // What the other warps know of a tile.
@@ -241,47 +237,52 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
       if (act) {
         const float* scales = reinterpret_cast<const float*>(smem + SM::off_sc) + (sl * kKeys + half * (kKeys / 2)) * NG;
         float m = -INFINITY, l = 0.f;  // m: of the scores before their factor un
-#pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          const int ko = half * (kKeys / 2) + blk * 16;  // the block's first key in the tile
-          if (ko >= d0.y) break;
-          const int base = d0.x + ko;
-          if (base < len && !((d0.w >> (ko / 16)) & 1)) {
-            float s[16];
+        // four keys a round, the next round's accumulators on their way meanwhile (wait_ld
+        // waits for all of a thread's loads)
+        uint32_t v[2][NG][4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float v[NG][8];
+        for (int c = 0; c < NG; ++c) tm_ld4(acc + c * kKeys, v[0][c]);
+        float s[16];
 #pragma unroll
-              for (int c = 0; c < NG; ++c) tm_ld8(acc + c * kKeys + blk * 16 + e * 8, v[c]);
-              wait_ld();
+        for (int r = 0; r < 8; ++r) {
+          wait_ld();
+          if (r < 7) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float* f = scales + (blk * 16 + e * 8 + j) * NG;
-                float& y = s[e * 8 + j];
-                if constexpr (NG == 4) {
-                  const float4 q = *reinterpret_cast<const float4*>(f);
-                  y = fmaf(q.w, v[3][j], fmaf(q.z, v[2][j], fmaf(q.y, v[1][j], q.x * v[0][j])));
-                } else if constexpr (NG == 2) {
-                  const float2 q = *reinterpret_cast<const float2*>(f);
-                  y = fmaf(q.y, v[1][j], q.x * v[0][j]);
-                } else {
-                  y = f[0] * v[0][j];
-                }
-              }
+            for (int c = 0; c < NG; ++c) tm_ld4(acc + c * kKeys + 4 * (r + 1), v[(r + 1) & 1][c]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float* f = scales + (4 * r + j) * NG;
+            const auto at = [&](int c) { return __uint_as_float(v[r & 1][c][j]); };
+            float& y = s[(r & 3) * 4 + j];
+            if constexpr (NG == 4) {
+              const float4 q = *reinterpret_cast<const float4*>(f);
+              y = fmaf(q.w, at(3), fmaf(q.z, at(2), fmaf(q.y, at(1), q.x * at(0))));
+            } else if constexpr (NG == 2) {
+              const float2 q = *reinterpret_cast<const float2*>(f);
+              y = fmaf(q.y, at(1), q.x * at(0));
+            } else {
+              y = f[0] * at(0);
             }
+          }
+          if ((r & 3) != 3) continue;
+          // ---- a block of 16 keys
+          const int blk = r >> 2, ko = half * (kKeys / 2) + blk * 16, base = d0.x + ko;  // its first key in the tile; its position
+          if (ko >= d0.y) continue;
+          if (base < len && !((d0.w >> (ko / 16)) & 1)) {
             const int last = len - behind - base;  // keys past it are not seen
             if (base + 15 > len - p.sh.T) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 if (j > last) s[j] = -INFINITY;
             }
-            float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+            float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
 #pragma unroll
             for (int j = 4; j < 16; j += 4) {
-              a = fmaxf(a, fmaxf(s[j], s[j + 1]));
-              b = fmaxf(b, fmaxf(s[j + 2], s[j + 3]));
+              x0 = fmaxf(x0, fmaxf(s[j], s[j + 1]));
+              x1 = fmaxf(x1, fmaxf(s[j + 2], s[j + 3]));
             }
-            const float mx = fmaxf(m, fmaxf(a, b));
+            const float mx = fmaxf(m, fmaxf(x0, x1));
             const float off = mx == -INFINITY ? 0.f : -mx * un;
             float s0 = l * wgt_ex2(fmaf(m, un, off)), s1 = 0.f;
 #pragma unroll
