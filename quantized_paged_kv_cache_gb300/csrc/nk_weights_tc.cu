@@ -14,9 +14,9 @@
 // 28 warps, one CTA per SM:
 //   warps 0-15  four warpgroups: two halves of the keys for the tiles of even
 //               number, two for the odd (each parity has a set of accumulators);
-//   warps 16-23 codes from the ring to fp16 in the swizzled operand buffers, four
-//               warps for the tiles of even number, four for the odd (a tile's
-//               chain of wait, load and store is longer than its time); at a
+//   warps 16-23 codes from the ring to fp16 in the swizzled operand buffers, all
+//               eight at a tile (with four at the even and four at the odd ones a
+//               buffer's conversion and product follow each other, slower); at a
 //               segment's start the unit's rows, scaled into the fp16 range;
 //   warp 24     issues the MMAs;
 //   warps 25-26 walk the list, look up the pages, leave a description of every
@@ -152,19 +152,19 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
   if (tid == 32) {
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(raw_full(i), 1);
-      mbar_init(raw_empty(i), kConv / 2);
+      mbar_init(raw_empty(i), kConv);
     }
     for (int i = 0; i < kScales; ++i) {
       mbar_init(sc_full(i), 1);
       mbar_init(sc_empty(i), kSoft / 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(b_full(i), kConv / 2);
+      mbar_init(b_full(i), kConv);
       mbar_init(b_empty(i), 1);
       mbar_init(acc_full(i), 1);
       mbar_init(acc_empty(i), kSoft / 2);
     }
-    for (int i = 0; i < kRowSets; ++i) mbar_init(rows_full(i), kConv / 2);
+    for (int i = 0; i < kRowSets; ++i) mbar_init(rows_full(i), kConv);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -312,31 +312,29 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
   } else if (warp < kMmaWarp) {
     set_regs<kRegsConv>();
     // ------------------------------------------------------------ codes to fp16
-    const int cw = warp - kSoft, team = cw >> 2;  // four warps for the tiles of even number, four for the odd
-    for (int n = team;; n += 2) {
-      const int rs = n % kRaw;
+    const int cw = warp - kSoft;
+    for (int n = 0;; ++n) {
+      const int rs = n % kRaw, buf = n & 1;
       wait(raw_full(rs), (uint32_t)(n / kRaw) & 1u);
       if (stopped()) break;
       const int4 d0 = *reinterpret_cast<const int4*>(desc + n % kScales), d1 = *(reinterpret_cast<const int4*>(desc + n % kScales) + 1);
       if (d0.z == 0) {
         // (as for any tile, after the products over the buffer's last one: two phases ahead
         // of the wait for it, the barrier would hold that up for good)
-        if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
-        if (!stopped() && lane == 0) mbar_arrive(b_full(team));
+        if (n >= 2) wait(b_empty(buf), (uint32_t)((n >> 1) - 1) & 1u);
+        if (!stopped() && lane == 0) mbar_arrive(b_full(buf));
         break;
       }
       if (d1.w) {
-        // the unit's rows, once every product over the last unit's is done. A wait goes by
-        // parity, so it must not begin before the phase ahead of its own has ended: the
-        // other team's barrier is passed one phase after the other.
-        if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
-        if (n >= 3) wait(b_empty(team ^ 1), (uint32_t)((n - 3) >> 1) & 1u);
-        if (n >= 1) wait(b_empty(team ^ 1), (uint32_t)((n - 1) >> 1) & 1u);
+        // the unit's rows, once every product over the last unit's is done (a wait goes by
+        // parity and must not begin before the phase ahead of its own has ended: this
+        // one's was waited for at the tile before)
+        if (n >= 1) wait(b_empty(buf ^ 1), (uint32_t)((n - 1) >> 1) & 1u);
         if (stopped()) break;
         const int T = p.sh.T, G = p.G, Hkv = p.sh.Hkv, b = d1.y / Hkv, h = d1.y - b * Hkv;
         float* undo = reinterpret_cast<float*>(smem + SM::off_undo) + (d1.z % kRowSets) * kRowsMost;
         const float sign = p.scale2 < 0.f ? -1.f : 1.f;
-        for (int r = cw & 3; r < kRowsMost; r += kConv / 2) {
+        for (int r = cw; r < kRowsMost; r += kConv) {
           const int row = row0 + r, t = row / G, hg = row - t * G;
           const bool there = r < p.chunk && row < T * G;
           const uint16_t* src = p.q + (((int64_t)b * T + t) * (G * Hkv) + h * G + hg) * D;
@@ -366,13 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(rows_full(d1.z % kRowSets));
       }
-      if (n >= 2) wait(b_empty(team), (uint32_t)((n >> 1) - 1) & 1u);
+      if (n >= 2) wait(b_empty(buf), (uint32_t)((n >> 1) - 1) & 1u);
       if (stopped()) break;
       const uint8_t* raw = smem + SM::off_raw + rs * (kKeys * D);
-      uint8_t* dst = smem + SM::off_b + team * (NG * kKeys * 128);
+      uint8_t* dst = smem + SM::off_b + buf * (NG * kKeys * 128);
       constexpr int PCS = D / 16;  // 16-code pieces of a key
 #pragma unroll 4
-      for (int i = (cw & 3) * 32 + lane; i < kKeys * PCS; i += kConv / 2 * 32) {
+      for (int i = cw * 32 + lane; i < kKeys * PCS; i += kConv * 32) {
         const int key = i / PCS, j = i % PCS;
         const uint4 w = *reinterpret_cast<const uint4*>(raw + i * 16);
         const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
       fence_async();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(b_full(team));
+        mbar_arrive(b_full(buf));
         mbar_arrive(raw_empty(rs));
       }
     }
