@@ -29,7 +29,10 @@ namespace nk {
 // 64-channel group, then the group's scale. Keys are M and query rows N, so a
 // decode step pads six rows to eight (one tile, whose rows stay in registers); more
 // than 48 rows go to the tcgen05 kernel (nk_weights_tc.cu). Bounded by the K half
-// of the cache and, for several tiles of rows, by instructions.
+// of the cache (8 sequences, 274K tokens, 24 heads over 4 of 256: 65 us with the
+// second kernel, 4.6 TB/s) and, for several tiles of rows, by instructions (T = 4
+// 94 us, T = 8 149). Copies of 16 bytes a lane, which fill the queue of the memory
+// instructions, took 79, 116 and 174.
 // ---------------------------------------------------------------------------
 // ---------------------------------------------------------------------------
 constexpr int kWgtThreads = 256, kWgtWarps = kWgtThreads / 32;
@@ -409,7 +412,8 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
 //
 // A block each sequence: it forms the prefix of the freed counts from the
 // lengths itself, as no count depends on a weight; reads its row of the table
-// before it writes one. Bounded by latency.
+// before it writes one. Bounded by latency (8 sequences of up to 2,048 pages 9.8 us,
+// 512 of up to 1,250 pages 14 us).
 // ---------------------------------------------------------------------------
 struct EvictParams {
   const float* w;  // [num_pages][Hkv]
@@ -578,7 +582,7 @@ namespace {
 // From how many rows on the tcgen05 kernel takes a call: past one chunk of the
 // mma.sync kernel, which would read the keys once more for each (8 sequences at 8K
 // to 64K, 24 heads over 4: 48 rows 174 us on mma.sync and 194 on tcgen05, 72 rows
-// 322 and 209, 96 rows 323 and 215).
+// 322 and 209, 96 rows 323 and 215, before the mma.sync kernel's 48 rows came to 149).
 constexpr int kTcRows = 49;
 
 // Row tiles of the mma.sync kernel's instances: 1, 2, 3, 4, 6; with 16-key pages

@@ -26,6 +26,10 @@
 // Only the copying warps know segments and tables: with the walk in every role the
 // registers spilled, and beside 217 KB of shared memory no L1 is left to hold a
 // spill (8 windows of 16 tokens at 8K to 64K: 204 us for this kernel then).
+// Bounded by the hand-offs between the roles: 8 windows of 16 tokens at 8K to 64K (96
+// rows, 274K tokens, 4 kv-heads) take 198 us with the second kernel, 1.75 us a tile, where the
+// products are 0.45 and the codes' bytes 0.38.
+//
 // Every mbarrier wait is bounded; after one has run out every role ends at its next
 // wait, and the copies and products under way are waited for.
 #include <math.h>
