@@ -521,7 +521,7 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
  * A length that is negative or past the table sets NK_DEVFLAG_BAD_CTX: new_ctx
  * is 0 and the sequence's row of the output table stays as it was. A page id
  * outside the pool sets NK_DEVFLAG_BAD_PAGE, weighs 0 and, where it goes, is
- * listed as -1. B is at most 1,024.
+ * listed as -1. B is at most 1,024; with B 0 only num_freed is written (0).
  */
 int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, const float* weights_dev,
                    const int32_t* block_table_dev, int32_t* out_table_dev, int32_t max_pages_per_seq,
@@ -557,7 +557,8 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
  * sum is 2 or more, sets NK_DEVFLAG_RANGE and token -1. A draft outside the
  * vocabulary sets NK_DEVFLAG_BAD_TOKEN and is refused, a count outside 0 .. T - 1
  * NK_DEVFLAG_BAD_POS and is clamped; uniforms outside [0, 1) draw as the nearest
- * inside. T is at most 16, vocab 2^30, B 65,535.
+ * inside. The results must not overlap the inputs (but next_start ctx_lens). T is
+ * at most 16, vocab 2^30, B 65,535.
  */
 int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const float* draft_dev,
                      int64_t draft_row_stride, const int32_t* drafts_dev, const int32_t* num_drafts_dev,
@@ -743,12 +744,11 @@ int nk_version(void);
  * withheld_page >= 0, every tensor-core decode and prefill launched
  * afterwards by this process (nk_paged_decode_attn, nk_decode_step, the
  * no-alloc variant, the other formats' decodes, nk_paged_prefill_attn,
- * nk_paged_sparse_attn) never
- * issues the page copies of its CTA page numbers >= withheld_page (nk_page_weights
- * and nk_page_bounds: the copies of a CTA's or warp's ring from that number on),
- * and bounds
- * each of its waits by wait_cycles SM clock cycles (0 keeps the default of
- * about 2 s). A wait for a withheld page runs out, sets NK_DEVFLAG_TIMEOUT in
+ * nk_paged_sparse_attn) never issues the page copies of its CTA page numbers
+ * >= withheld_page (nk_page_weights and nk_page_bounds: the copies of a CTA's or
+ * warp's ring from that number on), and bounds each of its waits by wait_cycles
+ * SM clock cycles (0 keeps the default of about 2 s). A wait for a withheld page
+ * runs out, sets NK_DEVFLAG_TIMEOUT in
  * the status word, and the kernel runs on without blocking, issues nothing
  * more, lets the copies and tensor-core work it did issue complete, and
  * returns; the outputs of the call are then unspecified and the device stays

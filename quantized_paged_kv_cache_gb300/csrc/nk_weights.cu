@@ -446,6 +446,10 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
   chain_wait();
   chain_release();
   const int tid = threadIdx.x, b = blockIdx.x;
+  if (p.B == 0) {  // nothing goes
+    if (tid == 0) *p.num_freed = 0;
+    return;
+  }
   int32_t* ids = reinterpret_cast<int32_t*>(keys + p.max_pages);
   // freed pages of the sequences before this one (and of all)
   const auto held_of = [&](int i) {
@@ -724,18 +728,18 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
   if (sink_pages < 0 || recent_pages < 1 || (int64_t)sink_pages + recent_pages > keep_pages) return NK_ERR_SHAPE;
   // a row of the table and its keys stay in shared memory
   if (B > kMaxBatch || max_pages_per_seq > 16384) return NK_ERR_UNSUPPORTED;
-  if (B == 0) return NK_OK;
-  if (!weights_dev || !block_table_dev || !out_table_dev || !ctx_lens_dev || !new_ctx_dev || !num_freed_dev ||
-      (max_freed > 0 && !freed_dev))
+  // (a batch of no sequences still tells that no page went)
+  if (!num_freed_dev || (B > 0 && (!weights_dev || !block_table_dev || !out_table_dev || !ctx_lens_dev || !new_ctx_dev ||
+                                   (max_freed > 0 && !freed_dev))))
     return NK_ERR_NULL;
-  if (new_ctx_dev == ctx_lens_dev) return NK_ERR_SHAPE;  // every block reads the lengths while others write theirs
+  if (B > 0 && new_ctx_dev == ctx_lens_dev) return NK_ERR_SHAPE;  // every block reads the lengths while others write theirs
   const EvictParams p{weights_dev, num_pages, num_kv_heads, page_size, block_table_dev, out_table_dev,
                       max_pages_per_seq, ctx_lens_dev, B, keep_pages, sink_pages, recent_pages, new_ctx_dev, freed_dev,
                       max_freed, num_freed_dev, status_dev};
-  const int smem = (max_pages_per_seq + 1) / 2 * 2 * 12;
+  const int smem = B > 0 ? (max_pages_per_seq + 1) / 2 * 2 * 12 : 16;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(evict_kernel), smem);
   if (e != cudaSuccess) return NK_ERR_CUDA;
-  e = launch_chained(evict_kernel, dim3((unsigned)B), dim3(kEvThreads), (size_t)smem, reinterpret_cast<cudaStream_t>(stream),
+  e = launch_chained(evict_kernel, dim3((unsigned)(B > 0 ? B : 1)), dim3(kEvThreads), (size_t)smem, reinterpret_cast<cudaStream_t>(stream),
                      p);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }

@@ -97,6 +97,8 @@ def test_weights(shape):
                                    ("many_t16_p16", 1, 16, 8, 1, 64, 16, [99999]), ("many_t5_p128", 3, 5, 12, 2, 128, 128, [40000, 30001, 77]),
                                    ("many_t16_p32", 2, 16, 14, 1, 64, 32, [70000, 12345]),
                                    ("many_short", 300, 4, 16, 2, 64, 32, [4 + (37 * i) % 190 for i in range(300)]),
+                                   ("many_t16_p48", 1, 16, 8, 2, 128, 48, [30001]), ("many_t16_p80", 1, 16, 8, 1, 64, 80, [25003]),
+                                   ("many_t16_p256", 1, 16, 12, 2, 256, 256, [20011]), ("many_t4_p80", 1, 4, 12, 2, 128, 80, [20001]),
                                    ("one_tile_each", 700, 2, 26, 2, 64, 64, [2 + (11 * i) % 63 for i in range(700)])], ids=lambda s: s[0])
 def test_weights_of_long_contexts(shape):
     """Dozens of pages a CTA, so that every ring goes round; segments that end inside a CTA's range."""
@@ -219,6 +221,18 @@ def test_evict_ties_and_ranges(what):
         tb, new_ctx, count, lst = i32(table), i32([0] * 3), i32([0]), i32([-7] * len(freed))
         nk.evict_pages(16, torch.from_numpy(ws).cuda(), tb, i32(ctx), keep, new_ctx, lst, count, sink_pages=sinks, recent_pages=recent)
         assert np.array_equal(tb.cpu().numpy(), want) and lst.tolist() == freed, (keep, sinks, recent)
+
+
+def test_evict_nothing_and_the_widest_table():
+    count, none, f = i32([-5]), i32([]), torch.zeros((4, 2), device="cuda")
+    nk.evict_pages(16, f, i32(np.zeros((0, 4))), none, 3, none, i32([-7]), count)
+    assert count.tolist() == [0]
+    ctx, table, num, w, rng = table_case(1, 16, 2, 21, 16382 * 16 - 5)
+    assert table.shape[1] == 16384
+    want, lens, freed = ref.evict(w, table, ctx, 16, 900, 1, 2)
+    tb, new_ctx, lst = i32(table), i32([0]), i32([-7] * len(freed))
+    nk.evict_pages(16, torch.from_numpy(w).cuda(), tb, i32(ctx), 900, new_ctx, lst, count, sink_pages=1, recent_pages=2)
+    assert np.array_equal(tb.cpu().numpy(), want) and lst.tolist() == freed and new_ctx.tolist() == lens
 
 
 def test_evict_bad_data():

@@ -102,7 +102,7 @@ def test_evict_refusals():
     for bad in (dict(P=0), dict(pages=0), dict(Hkv=0), dict(B=-1), dict(width=0), dict(most=-1), dict(sinks=-1), dict(recent=0), dict(keep=1),
                 dict(sinks=2**31 - 1), dict(new=FAKE)):
         assert call(**bad) == 2, bad
-    assert call(B=1025) == 3 and call(width=16385) == 3 and call(B=0) == 0
+    assert call(B=1025) == 3 and call(width=16385) == 3 and call(B=0, count=None) == 1
 
 
 def test_verify_refusals():
