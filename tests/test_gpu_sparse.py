@@ -63,7 +63,12 @@ def check_bounds(c, b, start, end, untouched):
     assert np.array_equal(codes[left], untouched[0][left]) and np.array_equal(scales[left], untouched[1][left])
 
 
-@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+# pages that the sparse attention has no kernel for, or that end inside a copy; more items than blocks
+BOUNDS = SHAPES + [("d256_p256", 1, 1, 8, 2, 256, 256, [1300]), ("d64_p80", 2, 1, 4, 2, 64, 80, [999, 81]),
+                   ("many", 5, 1, 8, 8, 128, 16, [900, 333, 16, 1, 700]), ("many_d256", 2, 1, 4, 4, 256, 64, [6000, 4001])]
+
+
+@pytest.mark.parametrize("shape", BOUNDS, ids=[s[0] for s in BOUNDS])
 def test_bounds(shape):
     c = make(shape)
     w = c.w
@@ -187,6 +192,26 @@ def test_select_ties_and_ranges(what):
         got = selections(c, k, sinks, recent, b, q=q, bt=bt)
         assert np.array_equal(got.cpu().numpy(), expected(c, k, sinks, recent, b, q=q, bt=bt)), (k, sinks, recent)
     assert int(c.status.item()) == (nk.NK_DEVFLAG_BAD_PAGE if what == "bad_page" else 0)
+
+
+def test_select_captured_and_on_another_stream():
+    c = make(("graph", 2, 3, 8, 2, 128, 16, [1200, 400]))
+    w, b = c.w, made_bounds(c)
+    want = expected(c, 9, 1, 2, b)
+    out, g = torch.empty((2, 3, 2, 9), dtype=torch.int32, device="cuda"), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        selections(c, 9, 1, 2, b, out=out)
+        selections(c, 9, 1, 2, b, out=out)
+    g.replay()
+    g.replay()
+    assert np.array_equal(out.cpu().numpy(), want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = selections(c, 9, 1, 2, b, stream=st)
+    lists = nk.paged_sparse_attn(c.pool, c.q, c.bt, c.ctx, got, w.sm_scale, w.max_ctx, stream=st)
+    st.synchronize()
+    assert np.array_equal(got.cpu().numpy(), want)
+    assert torch.equal(lists, nk.paged_sparse_attn(c.pool, c.q, c.bt, c.ctx, got, w.sm_scale, w.max_ctx))
 
 
 def test_select_leaves_an_invalid_sequences_lists():
