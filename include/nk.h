@@ -488,7 +488,8 @@ int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
  *                  scratch. Calls that may overlap on the GPU need one each.
  * fp32 sums in a fixed order. An invalid context length sets NK_DEVFLAG_BAD_CTX,
  * a page outside the pool NK_DEVFLAG_BAD_PAGE (it draws nothing). A page that
- * several sequences hold gets the sum of one of them. A query that is not
+ * several sequences of the batch hold gets the sum of one of them (which one is not
+ * said; with weights_dev as prior_dev perhaps of more). A query that is not
  * finite, or a visible key's scale, makes the weights its row touches NaN. B is at
  * most 1,024, G 48.
  */
@@ -518,6 +519,8 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
  *                  sequence, ascending in each; entries behind stay as they were
  *   num_freed_dev  int32 [1]: how many. More than max_freed set
  *                  NK_DEVFLAG_NO_PAGES; the first max_freed are written.
+ * A page that several sequences hold is listed by each that lets it go: whoever
+ * shares pages counts their holders before giving one back.
  * A length that is negative or past the table sets NK_DEVFLAG_BAD_CTX: new_ctx
  * is 0 and the sequence's row of the output table stays as it was. A page id
  * outside the pool sets NK_DEVFLAG_BAD_PAGE, weighs 0 and, where it goes, is
@@ -556,9 +559,9 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
  * negative weights count as 0, those above 1 as 1; a row without any, or whose
  * sum is 2 or more, sets NK_DEVFLAG_RANGE and token -1. A draft outside the
  * vocabulary sets NK_DEVFLAG_BAD_TOKEN and is refused, a count outside 0 .. T - 1
- * NK_DEVFLAG_BAD_POS and is clamped; uniforms outside [0, 1) draw as the nearest
- * inside. The results must not overlap the inputs (but next_start ctx_lens). T is
- * at most 16, vocab 2^30, B 65,535.
+ * NK_DEVFLAG_BAD_POS and is clamped; uniforms outside [0, 1) count as the nearest
+ * inside, NaN as 0. The results must not overlap the inputs (but next_start
+ * ctx_lens). T is at most 16, vocab 2^30, B 65,535.
  */
 int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const float* draft_dev,
                      int64_t draft_row_stride, const int32_t* drafts_dev, const int32_t* num_drafts_dev,

@@ -784,6 +784,8 @@ def paged_sparse_attn(pool: KVPool, q, block_table, ctx_lens, pages, sm_scale: f
         raise ValueError("q, block_table, ctx_lens and the pool disagree on the batch or the head dim")
     if len(lists) != 4 or lists[:3] != (B, T, Hkv):
         raise ValueError("pages must be [B][T][kv-heads][pages]")
+    if lists[3] > _I32_MAX:
+        _large(lists[3])
     if out is None:
         out = _empty(stream, q, q.shape)
     elif out.numel() != q.numel():
@@ -896,6 +898,8 @@ def verify_drafts(target, draft, drafts, uniforms, num_drafts=None, ctx_lens=Non
     if len(shape) != 3 or shape[1] < 1 or (draft is not None and draft.shape != (shape[0], shape[1] - 1, shape[2])):
         raise ValueError("target must be [B][T][vocab] and draft [B][T-1][vocab]")
     B, T, V = shape
+    if V > _I32_MAX:
+        _large(V)
     here = _here()
     for t in (target, draft):
         if t is not None and not (t.get_device() == here and t.dtype == torch.float32):

@@ -69,6 +69,10 @@ __device__ __forceinline__ uint64_t ver_weight(float p, float q) {
   return (uint64_t)hi << 32 | lo;
 }
 
+__device__ __forceinline__ float ver_uniform(float u) {  // the nearest one in [0, 1); NaN: 0
+  return fminf(fmaxf(u, 0.f), 0.99999994f);
+}
+
 template <int CL>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams a) {
   namespace cg = cooperative_groups;
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     if (x >= 0 && x < V) {
       const float px = a.p[((int64_t)b * T + lane) * a.p_stride + x];
       const float qx = a.q ? a.q[((int64_t)b * (T - 1) + lane) * a.q_stride + x] : 1.f;
-      const float u = a.u[(int64_t)b * T + lane];
+      const float u = ver_uniform(a.u[(int64_t)b * T + lane]);
       good = (double)u * (double)qx < (double)px;
     } else if (rank == 0 && warp == 0) {
       flag(a.status, NK_DEVFLAG_BAD_TOKEN);
@@ -117,8 +121,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   const float* prow = a.p + ((int64_t)b * T + acc) * a.p_stride;
   const float* qrow = cut && a.q ? a.q + ((int64_t)b * (T - 1) + acc) * a.q_stride : nullptr;
   int hole = cut && !a.q ? refused : -1;  // a certain draft that was refused
-  float uf = a.u[(int64_t)b * T + T - 1];
-  uf = fminf(fmaxf(uf, 0.f), 0.99999994f);
+  const float uf = ver_uniform(a.u[(int64_t)b * T + T - 1]);
   const uint64_t u64 = __float2ull_rz(uf * 18446744073709551616.f);
   // parts of whole rounds: 32 lanes and kVerUnroll tokens each
   const int per = (V + CL * kVerWarps - 1) / (CL * kVerWarps), step = (per + 31) / 32 * 32;

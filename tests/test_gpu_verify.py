@@ -74,6 +74,15 @@ def test_uniforms_at_the_ends():
     assert t[:, 0].tolist() == [9, 94, 50, 94]
 
 
+def test_uniforms_outside_decide_as_the_nearest_inside():
+    p, _, d, u = case(4, 2, 100, 6)
+    p[:, 0].scatter_(1, d.long(), torch.tensor([[0.5], [0.0], [0.0], [0.5]], device="cuda"))
+    same = p[:, :1].clone().scatter_(2, d[..., None].long(), 0.5)
+    u[:, 0] = torch.tensor([1.0, -1.0, float("nan"), float("nan")], device="cuda")
+    _, acc = nk.verify_drafts(p, same, d, u)
+    assert acc.tolist() == [1, 0, 0, 1]  # (1 - 2^-24) 0.5 < 0.5; 0 < 0 is not
+
+
 def test_sums_that_32_bits_lose():
     """A hundred thousand equal weights below a large one: token i from u = (0.5 + i w) / R, between two of them."""
     V = 100001
