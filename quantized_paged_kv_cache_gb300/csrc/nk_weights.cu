@@ -46,7 +46,7 @@ struct KeyStep {
 };
 
 // Shared memory: each warp's running log-sums of the segment [rows] float2, the
-// rows' powers of two [rows], the chunk's rows as fp16 [rows][D / 2 + 2 words],
+// rows' powers of two [rows], the rows as fp16 [rows][D / 2 + 2 words],
 // the rings, the
 // page prefix and the lengths [2 B + 1].
 __host__ __device__ inline int weight_ring_off(int D, int chunk) {
@@ -86,8 +86,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
   const int P = sh.P, Hkv = sh.Hkv, T = sh.T, G = p.G, M = T * G;
   int* pre = reinterpret_cast<int*>(smem + weight_ring_off(D, ROWS) + kWarps * S * Step::kBytes);  // [B + 1]
   int* lens = pre + sh.B + 1;                                                                     // [B]
-  const int row0 = blockIdx.x * ROWS;  // the CTA's chunk of rows
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (blockIdx.x == 0)
     for (int b = tid; b < sh.B; b += kThreads)
       if (pages_of_len(sh, p.ctx[b]) == 0) flag(p.status, NK_DEVFLAG_BAD_CTX);
   block_page_prefix_short(sh, p.ctx, 0, pre, warp_tot, lens);
@@ -98,8 +97,8 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
   uint8_t* qs = reinterpret_cast<uint8_t*>(undo + ROWS);
   uint8_t* ring = smem + weight_ring_off(D, ROWS) + warp * S * Step::kBytes;
   const uint32_t ring_u32 = smem_u32(ring), bar0 = smem_u32(bars[warp]);
-  int64_t x = cta_begin(W, p.n_ctas, blockIdx.y);
-  const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.y + 1);
+  int64_t x = cta_begin(W, p.n_ctas, blockIdx.x);
+  const int64_t x_end = cta_begin(W, p.n_ctas, blockIdx.x + 1);
   Segment seg;
   int64_t item = x;  // of the segment's first page
   int issued = 0, used = 0, sent = 0;  // steps; one past the last that was copied
@@ -143,14 +142,14 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
     for (int i = 0; i < S - 1; ++i) issue();
     // ---- the unit's rows: a warp each, scaled into [2^14, 2^15)
     for (int r = warp; r < ROWS; r += kWarps) {
-      const int row = row0 + r, t = row / G, hg = row - t * G;
+      const int t = r / G, hg = r - t * G;
       const uint16_t* src = p.q + (((int64_t)seg.b * T + t) * (G * Hkv) + seg.h * G + hg) * D;
       constexpr int PER = D / 64;  // words of a lane
       uint32_t w[PER];
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        w[i] = row < M ? reinterpret_cast<const uint32_t*>(src)[lane + 32 * i] : 0u;
+        w[i] = r < M ? reinterpret_cast<const uint32_t*>(src)[lane + 32 * i] : 0u;
         m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
       }
 #pragma unroll
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
           if (edge) {
             // the last position each row sees; keys past the page's live ones are another page's
             const int end = bad ? -1 : logical * P + live - 1;
-            const int p0 = min(L - T + (row0 + r0) / G, end), p1 = min(L - T + (row0 + r0 + 1) / G, end);
+            const int p0 = min(L - T + r0 / G, end), p1 = min(L - T + (r0 + 1) / G, end);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
               const int n0 = pos0 + 16 * kb + g, n1 = n0 + 8;
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
         __syncwarp();  // (the next copies go where this step lay S steps ago)
       }
       // ---- the page's log-sums: eight lanes hold a row's keys
-      float* dst = p.page_lse + (item + pg) * p.rows + row0;
+      float* dst = p.page_lse + (item + pg) * ROWS;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
     for (int r = tid; r < ROWS; r += kThreads) {
       float m = -INFINITY, l = 0.f;
       for (int w = 0; w < kWarps; ++w) lse_join(m, l, all[w * ROWS + r].x, all[w * ROWS + r].y);
-      p.seg_lse[((int64_t)blockIdx.y + seg.u) * p.rows + row0 + r] = lse_of(m, l);
+      p.seg_lse[((int64_t)blockIdx.x + seg.u) * ROWS + r] = lse_of(m, l);
     }
     item += pages;
     __syncthreads();
@@ -596,8 +595,9 @@ int weight_tiles(int tiles, int P) {
   return tiles == 5 ? 6 : tiles;
 }
 
-// Chunks of rows, alike in size: at most 48 on mma.sync (six tiles of eight fill a
-// thread's registers), 128 on tcgen05 (the M of its product).
+// Rows of a unit: up to 48 in one chunk on mma.sync (six tiles of eight fill a
+// thread's registers), chunks of up to 128, alike in size, on tcgen05 (the M of its
+// product).
 struct WeightRows {
   bool tc;
   int chunks, chunk;  // rows of a chunk, a multiple of eight
@@ -607,9 +607,9 @@ struct WeightRows {
 WeightRows weight_rows(int T, int G, int P) {
   const int M = T * G;
   const bool tc = M >= kTcRows;
-  const int most = tc ? 128 : 48, n = (M + most - 1) / most, tiles = ((M + n - 1) / n + 7) / 8;
-  if (tc) return {true, n, tiles * 8, (P + 31) / 32, 4};
-  return {false, n, weight_tiles(tiles, P) * 8, 1, 1};
+  if (!tc) return {false, 1, weight_tiles((M + 7) / 8, P) * 8, 1, 1};
+  const int n = (M + 127) / 128, tiles = ((M + n - 1) / n + 7) / 8;
+  return {true, n, tiles * 8, (P + 31) / 32, 4};
 }
 
 // CTAs along the pages: as many as an SM holds, shared by the chunks.
@@ -621,27 +621,27 @@ int weight_ctas(int64_t items, const WeightRows& r) {
 }
 
 template <int D, int NT, int KB>
-cudaError_t launch_lse(const WeightParams& p, int chunks, cudaStream_t st) {
+cudaError_t launch_lse(const WeightParams& p, cudaStream_t st) {
   const int smem = weight_ring_off(D, NT * 8) + kWgtWarps * weight_stages<D, NT, KB>() * KeyStep<D, KB>::kBytes +
                    (2 * p.sh.B + 1) * 4;
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(page_lse_kernel<D, NT, KB>), smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)chunks, (unsigned)p.n_ctas), dim3(kWgtThreads),
-                        (size_t)smem, st, p);
+  return launch_chained(page_lse_kernel<D, NT, KB>, dim3((unsigned)p.n_ctas), dim3(kWgtThreads), (size_t)smem,
+                        st, p);
 }
 
 template <int D>
-cudaError_t launch_lse_d(const WeightParams& p, int chunks, cudaStream_t st) {
-  if (p.chunk == 8) return launch_lse<D, 1, 1>(p, chunks, st);
+cudaError_t launch_lse_d(const WeightParams& p, cudaStream_t st) {
+  if (p.chunk == 8) return launch_lse<D, 1, 1>(p, st);
   if (p.sh.P == 16) switch (p.chunk / 8) {
-      case 3: return launch_lse<D, 3, 1>(p, chunks, st);
-      default: return launch_lse<D, 6, 1>(p, chunks, st);
+      case 3: return launch_lse<D, 3, 1>(p, st);
+      default: return launch_lse<D, 6, 1>(p, st);
     }
   switch (p.chunk / 8) {
-    case 2: return launch_lse<D, 2, 2>(p, chunks, st);
-    case 3: return launch_lse<D, 3, 2>(p, chunks, st);
-    case 4: return launch_lse<D, 4, 2>(p, chunks, st);
-    default: return launch_lse<D, 6, 2>(p, chunks, st);
+    case 2: return launch_lse<D, 2, 2>(p, st);
+    case 3: return launch_lse<D, 3, 2>(p, st);
+    case 4: return launch_lse<D, 4, 2>(p, st);
+    default: return launch_lse<D, 6, 2>(p, st);
   }
 }
 
@@ -705,9 +705,9 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
   p.withhold = limits.withhold;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = r.tc       ? launch_lse_tc(p, r.chunks, st)
-                  : D == 256 ? launch_lse_d<256>(p, r.chunks, st)
-                  : D == 128 ? launch_lse_d<128>(p, r.chunks, st)
-                             : launch_lse_d<64>(p, r.chunks, st);
+                  : D == 256 ? launch_lse_d<256>(p, st)
+                  : D == 128 ? launch_lse_d<128>(p, st)
+                             : launch_lse_d<64>(p, st);
   if (e != cudaSuccess) return NK_ERR_CUDA;
   const int64_t units = (int64_t)B * Hkv;
   int64_t gx = (longest + kWsmThreads / 8 - 1) / (kWsmThreads / 8), most = 2048 / units;
@@ -739,8 +739,8 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
   const int smem = B > 0 ? (max_pages_per_seq + 1) / 2 * 2 * 12 : 16;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(evict_kernel), smem);
   if (e != cudaSuccess) return NK_ERR_CUDA;
-  e = launch_chained(evict_kernel, dim3((unsigned)(B > 0 ? B : 1)), dim3(kEvThreads), (size_t)smem, reinterpret_cast<cudaStream_t>(stream),
-                     p);
+  e = launch_chained(evict_kernel, dim3((unsigned)(B > 0 ? B : 1)), dim3(kEvThreads), (size_t)smem,
+                     reinterpret_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
