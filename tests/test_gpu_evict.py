@@ -235,6 +235,40 @@ def test_evict_nothing_and_the_widest_table():
     assert np.array_equal(tb.cpu().numpy(), want) and lst.tolist() == freed and new_ctx.tolist() == lens
 
 
+@pytest.mark.parametrize("T", [1, 16])
+def test_captured_and_on_another_stream(T):
+    c = make(("graph", 2, T, 24, 4, 256, 64, [3001, 900]))
+    w = c.w
+    want = torch.zeros((w.num_pages, w.Hkv), device="cuda")
+    nk.page_weights(c.pool, c.q, c.bt, c.ctx, w.sm_scale, w.max_ctx, want)
+    lists = [(torch.zeros_like(c.bt), i32([0] * w.B), i32([-7] * 50), i32([0])) for _ in range(3)]
+
+    def step(mass, out, new_ctx, freed, count, **kw):
+        nk.page_weights(c.pool, c.q, c.bt, c.ctx, w.sm_scale, w.max_ctx, mass, **kw)
+        nk.evict_pages(w.P, mass, c.bt, c.ctx, 9, new_ctx, freed, count, out=out, **kw)
+
+    mass = [torch.zeros_like(want) for _ in range(3)]
+    step(mass[0], *lists[0])
+    step(mass[2], *lists[2])  # (the kernels are loaded before the capture)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(mass[1], *lists[1])
+    for _ in range(2):
+        for t in (mass[1], *lists[1]):
+            t.fill_(-7)
+        g.replay()
+        touched = want != 0
+        assert torch.equal(mass[1][touched], want[touched])
+        for x, y in zip(lists[0][:2] + lists[0][3:], lists[1][:2] + lists[1][3:]):
+            assert torch.equal(x, y)
+        assert torch.equal(lists[0][2], lists[1][2])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    step(mass[2], *lists[2], stream=st)
+    st.synchronize()
+    assert torch.equal(mass[2], want) and all(torch.equal(x, y) for x, y in zip(lists[0], lists[2]))
+
+
 def test_evict_bad_data():
     ctx, table, num, w, rng = table_case(4, 16, 2, 4, 500)
     ctx[2], ctx[3] = -1, table.shape[1] * 16 + 1
