@@ -48,6 +48,23 @@ def test_verify(B, T, V, certain):
     check(p, q, d, u, num=[(3 * b) % T for b in range(B)])
 
 
+@pytest.mark.parametrize("V", [40004, 65536, 131072])
+@pytest.mark.parametrize("draft", ["certain", "aligned", "odd_rows"])
+def test_aligned_rows(V, draft):
+    """Rows that are read in pieces of four; with one side's rows off their 16 bytes; a refused draft of a large weight."""
+    p, q, d, u = case(3, 3, V, V)
+    p[:, 0] *= 0.6
+    p[:, 0].scatter_(1, d[:, :1].long(), 0.4)
+    u[:, 0] = torch.tensor([0.999999, 0.1, 0.999999], device="cuda")
+    if draft == "certain":
+        q = None
+    elif draft == "odd_rows":
+        q = torch.nn.functional.pad(q, (0, 1), value=float("nan"))[..., :V]
+    for last in (1 / 7, 0.7, 1 - 2.0 ** -24):
+        u[:, 2] = last
+        check(p, q, d, u)
+
+
 def test_all_accepted_and_none():
     p, q, d, u = case(6, 4, 500, 3)
     same = p[:, :3].contiguous()
