@@ -65,6 +65,24 @@ def test_aligned_rows(V, draft):
         check(p, q, d, u)
 
 
+def test_acceptance_is_exact():
+    """Products next to the target's probability: the rounded product equal to it, the exact one a half step aside; tiny ones."""
+    rng = np.random.default_rng(31)
+    n, V = 4000, 4
+    u = (rng.random((n, 2)) * (1 - 2.0 ** -24)).astype(np.float32)
+    qx = (rng.random(n) * 2.0 ** rng.choice([0, -1, -20, -70, -126], n)).astype(np.float32)
+    u[:, 0] *= rng.choice(np.float32([1, 2.0 ** -10, 2.0 ** -60]), n)
+    px = (u[:, 0].astype(np.float64) * qx).astype(np.float32)  # the rounded product
+    px = np.where(np.arange(n) % 5 == 0, np.nextafter(px, np.float32(1)), px)
+    px = np.where(np.arange(n) % 7 == 0, np.nextafter(px, np.float32(0)), px)
+    p, q = np.full((n, 2, V), 0.25, np.float32), np.full((n, 1, V), 0.25, np.float32)
+    p[:, 0, 2], q[:, 0, 2] = px, qx
+    p, q, u = (torch.from_numpy(x).cuda() for x in (p, q, u))
+    _, acc = nk.verify_drafts(p, q, i32(np.full((n, 1), 2)), u)
+    want = u[:, 0].double() * q[:, 0, 2].double() < p[:, 0, 2].double()
+    assert torch.equal(acc.bool(), want) and 0.2 < want.double().mean() < 0.8
+
+
 def test_all_accepted_and_none():
     p, q, d, u = case(6, 4, 500, 3)
     same = p[:, :3].contiguous()
