@@ -543,7 +543,7 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
  *                  the draft)
  *   drafts_dev     int32 [B][T - 1]
  *   num_drafts_dev int32 [B] or NULL: drafts of each sequence, 0 .. T - 1 (NULL:
- *                  T - 1); the columns behind are not read
+ *                  T - 1); the columns behind have no effect
  *   uniforms_dev   fp32 [B][T], each in [0, 1): u[t] decides on draft t, u[T - 1]
  *                  draws the token
  *   tokens_dev     int32 [B][T]: the accepted drafts, the token drawn, -1 behind

@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
   chain_release();
   const int rank = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int T = a.T, V = a.V;
-  // ---- the drafts, by every warp
+  // ---- the drafts, by every warp (beside their count, which says how many of them there are)
+  const float u_mine = lane < T ? ver_uniform(a.u[(int64_t)b * T + lane]) : 0.f;
+  const int x = lane < T - 1 ? a.drafts[(int64_t)b * (T - 1) + lane] : -1;
   int n = T - 1;
   if (a.num) {
     n = a.num[b];
@@ -114,15 +116,12 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
       n = n < 0 ? 0 : T - 1;
     }
   }
-  int x = -1;
   bool good = false;
   if (lane < n) {
-    x = a.drafts[(int64_t)b * (T - 1) + lane];
     if (x >= 0 && x < V) {
       const float px = a.p[((int64_t)b * T + lane) * a.p_stride + x];
       const float qx = a.q ? a.q[((int64_t)b * (T - 1) + lane) * a.q_stride + x] : 1.f;
-      const float u = ver_uniform(a.u[(int64_t)b * T + lane]);
-      good = ver_accept(u, qx, px);
+      good = ver_accept(u_mine, qx, px);
     } else if (rank == 0 && warp == 0) {
       flag(a.status, NK_DEVFLAG_BAD_TOKEN);
     }
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
   const float* prow = a.p + ((int64_t)b * T + acc) * a.p_stride;
   const float* qrow = cut && a.q ? a.q + ((int64_t)b * (T - 1) + acc) * a.q_stride : nullptr;
   int hole = cut && !a.q ? refused : -1;  // a certain draft that was refused
-  const float uf = ver_uniform(a.u[(int64_t)b * T + T - 1]);
+  const float uf = __shfl_sync(0xffffffffu, u_mine, T - 1);
   const uint64_t u64 = __float2ull_rz(uf * 18446744073709551616.f);
   // parts of whole rounds: 32 lanes and kVerUnroll tokens each
   const int per = (V + CL * kVerWarps - 1) / (CL * kVerWarps), step = (per + 31) / 32 * 32;
