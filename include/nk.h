@@ -487,11 +487,13 @@ int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_
  *   workspace_dev  nk_page_weights_workspace_bytes(...) bytes, 16-byte aligned;
  *                  scratch. Calls that may overlap on the GPU need one each.
  * fp32 sums in a fixed order. An invalid context length sets NK_DEVFLAG_BAD_CTX,
- * a page outside the pool NK_DEVFLAG_BAD_PAGE (it draws nothing). A page that
+ * a page outside the pool NK_DEVFLAG_BAD_PAGE (it draws nothing, and a query row
+ * whose visible pages are all outside adds nothing anywhere). A page that
  * several sequences of the batch hold gets the sum of one of them (which one is not
  * said; with weights_dev as prior_dev perhaps of more). A query that is not
- * finite, or a visible key's scale, makes the weights its row touches NaN. B is at
- * most 1,024, G 48.
+ * finite makes the weights of its sequence and kv-head NaN, and so does a visible
+ * key whose score is NaN or plus infinity (by a scale that is not finite); one
+ * whose score is minus infinity draws nothing. B is at most 1,024, G 48.
  */
 size_t nk_page_weights_workspace_bytes(int32_t B, int32_t T, int32_t num_q_heads, int32_t num_kv_heads,
                                        int32_t page_size, int32_t max_ctx);

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWgtThreads, lse_ctas(NT)) page_lse_kernel(con
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const int e = wgt_row_exp(m);
-      const float up = wgt_pow2(e);
+      const float up = wgt_row_factor(m, e);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const __half2 hh = __floats2half2_rn(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
@@ -375,7 +375,11 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
       lse_join(m, l, m2, l2);
     }
-    if ((tid & (sub - 1)) == 0) lse[r] = lse_of(m, l);
+    if ((tid & (sub - 1)) == 0) {
+      // a row that sees no key (its pages are none) draws nothing: 2^(s - inf) is 0 also where s is -inf
+      const float all = lse_of(m, l);
+      lse[r] = all == -INFINITY ? INFINITY : all;
+    }
   }
   __syncthreads();
   int seen = 0x7fffffff;

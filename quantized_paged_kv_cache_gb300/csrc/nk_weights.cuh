@@ -73,6 +73,12 @@ __device__ __forceinline__ int wgt_row_exp(float m) {
   return e > 110 ? 110 : (e < -113 ? -113 : e);
 }
 __device__ __forceinline__ float wgt_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// What a row with largest |q| m is multiplied by. An infinite one becomes NaN
+// throughout: its scores could all be minus infinity, as those of a row that sees
+// no key.
+__device__ __forceinline__ float wgt_row_factor(float m, int e) {
+  return m < INFINITY ? wgt_pow2(e) : __uint_as_float(0x7fffffffu);
+}
 
 // The first kernel on tcgen05 (nk_weights_tc.cu).
 cudaError_t launch_lse_tc(const WeightParams& p, int chunks, cudaStream_t st);

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) lse_tc_kernel(const __grid_consta
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const int e = wgt_row_exp(m);
-          const float up = sign * wgt_pow2(e);
+          const float up = sign * wgt_row_factor(m, e);
 #pragma unroll
           for (int i = 0; i < PER; ++i) {  // word lane + 32 i: channels 2 lane + 64 i, + 1, so group i
             const __half2 hh = __floats2half2_rn(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
