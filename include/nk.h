@@ -505,12 +505,17 @@ int nk_page_weights(const nk_kv_pool* pool, const void* q_dev, const int32_t* bl
 
 /*
  * nk_evict_pages -- cuts sequences back to keep_pages pages: those with the
- * largest weight, summed over the kv-heads (exactly: of equal sums the lower
- * page stays), and in any case the first sink_pages and the last recent_pages
+ * largest weight, summed over the kv-heads (of equal sums the lower page stays),
+ * and in any case the first sink_pages and the last recent_pages
  * (>= 1, so every page that goes is full; together at most keep_pages). The kept
  * pages keep their order, so the cache's other calls go on with the new table
  * and length; keys keep the rotary positions they were appended with.
- *   weights_dev    fp32 [num_pages][Hkv] (nk_page_weights); NaN ranks last
+ * A page's sum does not depend on the order of its heads: with 2^e the largest
+ * power of two in its weights and 2^c the least one that Hkv does not pass, each
+ * weight counts as a whole multiple of 2^(e + c - 61) (what is less is cut off), and
+ * sums are compared in their first 55 bits.
+ *   weights_dev    fp32 [num_pages][Hkv] (nk_page_weights); infinities count as
+ *                  2^128, a page with a NaN ranks last
  *   block_table_dev, out_table_dev  int32 [B][max_pages_per_seq], at most 16,384
  *                  wide; may be the same buffer, else must not overlap. Entries
  *                  behind the kept pages that held one become -1, others are

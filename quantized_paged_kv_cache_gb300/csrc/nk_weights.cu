@@ -409,14 +409,17 @@ __global__ void __launch_bounds__(kWsmThreads) page_weight_kernel(const WeightPa
 // nk_evict_pages. Of each sequence the `keep` pages with the largest weight,
 // summed over its kv-heads, stay (the first `sinks` and last `recent` ones in
 // any case; of equal ones the lower page), in their order; the others go to the
-// list of freed pages, sequence after sequence. The sums are carried as two fp32
-// numbers (48 bits, every step exact): 64-bit floating point is slow here, and a
-// single one would put pages of nearly equal weight in another order.
+// list of freed pages, sequence after sequence. A page's weights are summed as whole
+// multiples of 2^(e + c - 61), with 2^e the largest power of two in them and 2^c the
+// least that Hkv does not pass: the same sum in any order of the heads, which no
+// floating-point sum is (64-bit ones are slow here besides), cut to 55 significant
+// bits for its key. A sum as two fp32 numbers took 9.5 us where this takes 9.8, and
+// let equal sums differ.
 //
 // A block each sequence: it forms the prefix of the freed counts from the
 // lengths itself, as no count depends on a weight; reads its row of the table
 // before it writes one. Bounded by latency (8 sequences of up to 2,048 pages 9.8 us,
-// 512 of up to 1,250 pages 14 us).
+// 512 of up to 1,250 pages 14.1).
 // ---------------------------------------------------------------------------
 struct EvictParams {
   const float* w;  // [num_pages][Hkv]
@@ -435,14 +438,37 @@ struct EvictParams {
 
 constexpr int kEvThreads = 512;
 
-// Order of a fp32 that is not NaN, as a whole number.
-__device__ __forceinline__ uint32_t ordered32(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return (b >> 31) ? ~b : b | 0x80000000u;
+// A weight (the bits of a fp32 that is not NaN) in units of 2^(shift - 188), cut off
+// below; `shift` is top + c, with `top` at least the weight's exponent field. Its 24
+// bits stand at bit 38 and move right. Infinity is 2^128.
+__device__ __forceinline__ uint32_t ev_shr(uint32_t x, uint32_t s) {  // (0 past 31)
+  uint32_t y;
+  asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(s));
+  return y;
+}
+__device__ __forceinline__ int64_t weight_units(uint32_t bits, uint32_t shift) {
+  const uint32_t e = (bits >> 23) & 0xffu, s = shift - max(e, 1u);
+  const uint32_t m = ((bits << 6) & 0x1fffffc0u) | min(e, 1u) << 29;
+  const uint32_t hi = ev_shr(m, s), lo = ev_shr(__funnelshift_rc(0u, m, s), max(s, 32u) - 32u);
+  const int64_t x = (int64_t)((uint64_t)hi << 32 | lo);
+  return (int32_t)bits < 0 ? -x : x;
+}
+// Order of a sum of such units (below 2^63) as a whole number: sign, nine bits of
+// exponent, 54 bits behind the leading one. 0, below all of them, is a page's with a NaN.
+__device__ __forceinline__ uint64_t sum_key(int64_t sum, int top) {
+  constexpr uint64_t kSign = 1ull << 63;
+  if (sum == 0) return kSign;
+  const uint64_t size = (uint64_t)(sum < 0 ? -sum : sum);
+  const int n = 63 - __clzll((long long)size);
+  const uint64_t k = (uint64_t)(top + n) << 54 | ((size << (63 - n)) << 1) >> 10;
+  return sum < 0 ? ~(k | kSign) : k | kSign;
 }
 
-// Shared memory: keys [room] and the row of the table [room].
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) {
+// Shared memory: keys [room] and the row of the table [room]. W: weights of a page that
+// one load takes. MANY: three blocks an SM with two pages of a thread in flight, in place of
+// two with four.
+template <int W, bool MANY>
+__global__ void __launch_bounds__(kEvThreads, MANY ? 3 : 2) evict_kernel(const EvictParams p) {
   extern __shared__ uint64_t keys[];
   __shared__ TopSmem<kEvThreads> sm;
   __shared__ int before_s[kEvThreads / 32], all_s[kEvThreads / 32];
@@ -499,40 +525,63 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictParams p) 
     return;
   }
   // pages of a thread in flight: their ids, then a head's weights of all of them
-  constexpr int U = 4;
+  constexpr int U = MANY ? 2 : 4;
   bool bad = false;
   uint64_t klo = ~0ull, khi = 0;
   const int last = held - p.recent;  // one past the last page in question
+  const int heads_log2 = 32 - __clz(p.Hkv - 1);  // Hkv weights stay below 2^62 units
   for (int i0 = tid; i0 < held; i0 += kEvThreads * U) {
-    int page[U];
-    float hi[U], lo[U];
+    int page[U], top[U];
+    int64_t sum[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kEvThreads;
       page[u] = i < held ? p.table[row + i] : 0;
-      hi[u] = lo[u] = 0.f;
+      sum[u] = 0;
     }
-#pragma unroll 4
-    for (int h = 0; h < p.Hkv; ++h) {
+    // the largest weight without its sign (past infinity: a NaN), then the sum in units
+    // below it, W heads at a time (more are read once more, from L1)
+    uint32_t v[U][W], most[U] = {};
+    const auto fetch = [&](int h0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool there = page[u] >= 0 && page[u] < p.num_pages;
-        // (NaN: last)
-        const float v = there ? fminf(fmaxf(p.w[(int64_t)page[u] * p.Hkv + h], -1e36f), 1e36f) : 0.f;
-        // hi + v exactly as a sum and its rounding error, the error joined to lo
-        const float s = hi[u] + v, z = s - hi[u];
-        lo[u] += (hi[u] - (s - z)) + (v - z);
-        hi[u] = s;
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[u][j] = 0;
+        if (page[u] < 0 || page[u] >= p.num_pages) continue;
+        const float* src = p.w + (int64_t)page[u] * p.Hkv + h0;
+        if constexpr (W == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+        } else if constexpr (W == 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src);
+          v[u][0] = x.x, v[u][1] = x.y;
+        } else {
+          v[u][0] = __float_as_uint(*src);
+        }
       }
+    };
+    for (int h0 = 0; h0 < p.Hkv; h0 += W) {
+      fetch(h0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < W; ++j) most[u] = max(most[u], v[u][j] & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top[u] = max((int)(most[u] >> 23), 1);
+    for (int h0 = 0; h0 < p.Hkv; h0 += W) {
+      if (p.Hkv > W) fetch(h0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum[u] += weight_units(v[u][j], (uint32_t)(top[u] + heads_log2));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kEvThreads;
       if (i >= held) continue;
       bad |= page[u] < 0 || page[u] >= p.num_pages;
-      const float s = hi[u] + lo[u], l = lo[u] - (s - hi[u]);
-      // (+ 0: a negative zero has the order of a positive one)
-      const uint64_t k = ((uint64_t)ordered32(s + 0.f) << 32) | ordered32(l + 0.f);
+      const uint64_t k = most[u] > 0x7f800000u ? 0 : sum_key(sum[u], top[u]);
       ids[i] = page[u];
       keys[i] = k;
       if (i >= p.sinks && i < last) {
@@ -649,6 +698,17 @@ cudaError_t launch_lse_d(const WeightParams& p, cudaStream_t st) {
   }
 }
 
+// Past two blocks an SM the third is worth more than the loads in flight (512 sequences
+// 15.4 -> 14.1 us, on a slower box 18.9 -> 14.0, where 8 would go from 9.8 to 10.2).
+template <int W>
+cudaError_t launch_evict(const EvictParams& p, int smem, cudaStream_t st) {
+  const int sms = device_sms();
+  const auto kernel = p.B > 2 * (sms > 0 ? sms : 148) ? evict_kernel<W, true> : evict_kernel<W, false>;
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kernel, dim3((unsigned)(p.B > 0 ? p.B : 1)), dim3(kEvThreads), (size_t)smem, st, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -741,10 +801,11 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
                       max_pages_per_seq, ctx_lens_dev, B, keep_pages, sink_pages, recent_pages, new_ctx_dev, freed_dev,
                       max_freed, num_freed_dev, status_dev};
   const int smem = B > 0 ? (max_pages_per_seq + 1) / 2 * 2 * 12 : 16;
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(evict_kernel), smem);
-  if (e != cudaSuccess) return NK_ERR_CUDA;
-  e = launch_chained(evict_kernel, dim3((unsigned)(B > 0 ? B : 1)), dim3(kEvThreads), (size_t)smem,
-                     reinterpret_cast<cudaStream_t>(stream), p);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // four or two weights a load where every page's lie aligned to as many
+  const cudaError_t e = num_kv_heads % 4 == 0 && aligned_to(weights_dev, 16)  ? launch_evict<4>(p, smem, st)
+                        : num_kv_heads % 2 == 0 && aligned_to(weights_dev, 8) ? launch_evict<2>(p, smem, st)
+                                                                              : launch_evict<1>(p, smem, st);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;
 }
 
