@@ -99,30 +99,40 @@ __host__ __device__ inline ChunkLayout layout_of(int fmt, int P, int D) {
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Raises a kernel's dynamic shared-memory limit on the current device once
-// (the setting persists), instead of on every launch: the host side of a
-// decode step is on the critical path of a call that waits for its result.
+// Raises a kernel's dynamic shared-memory limit on the current device where it is
+// lower (the setting persists), instead of on every launch: the host side of a
+// decode step is on the critical path of a call that waits for its result. The
+// limit is set under the lock, so that of two threads' sizes the larger one stays.
 inline cudaError_t set_smem_limit(const void* kernel, int bytes) {
   struct Entry {
     const void* kernel;
     int device, bytes;
   };
+  constexpr unsigned kSlots = 4096;  // a slot for each kernel (some 200) and device
   static std::mutex mu;
-  static Entry seen[256];
-  static int count = 0;
+  static Entry seen[kSlots];
+  static unsigned count = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < count; ++i)
-      if (seen[i].kernel == kernel && seen[i].device == dev && seen[i].bytes >= bytes) return cudaSuccess;
-  }
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  unsigned at = (unsigned)((reinterpret_cast<uintptr_t>(kernel) * 0x9e3779b97f4a7c15ull) >> 40) + 61u * (unsigned)dev;
   std::lock_guard<std::mutex> lock(mu);
-  if (count < 256) seen[count++] = Entry{kernel, dev, bytes};
-  return cudaSuccess;
+  for (;; ++at) {  // (a slot is always free)
+    Entry& s = seen[at % kSlots];
+    if (s.kernel == kernel && s.device == dev) {
+      if (s.bytes >= bytes) return cudaSuccess;
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e == cudaSuccess) s.bytes = bytes;
+      return e;
+    }
+    if (s.kernel) continue;
+    if (count + 1 == kSlots) return cudaErrorMemoryAllocation;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    s = Entry{kernel, dev, bytes};
+    ++count;
+    return cudaSuccess;
+  }
 }
 
 template <typename... KArgs, typename... Args>

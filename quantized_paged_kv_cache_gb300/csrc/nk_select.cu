@@ -817,7 +817,7 @@ template <int D, int NT>
 cudaError_t launch_scores(const SelectParams& p, dim3 grid, const SelectPlan& plan, cudaStream_t st) {
   if (plan.cl > 0) {
     const void* fn = reinterpret_cast<const void*>(page_select_kernel<D, NT>);
-    cudaError_t e = set_smem_limit(fn, plan.smem);
+    cudaError_t e = set_smem_limit(fn, kSelSmem);  // (once, however the contexts grow)
     if (e != cudaSuccess) return e;
     if (plan.cl > 8) {
       static std::atomic<bool> allowed[64];  // per device
@@ -981,7 +981,7 @@ int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size,
   if (e == cudaSuccess && plan.cl > 0) return NK_OK;
   if (e != cudaSuccess) return NK_ERR_CUDA;
   const int room = (int)(pages < kPickKeep ? pages : kPickKeep);
-  e = set_smem_limit(reinterpret_cast<const void*>(page_pick_kernel), room * 8);
+  e = set_smem_limit(reinterpret_cast<const void*>(page_pick_kernel), kPickKeep * 8);
   if (e != cudaSuccess) return NK_ERR_CUDA;
   e = launch_chained(page_pick_kernel, dim3((unsigned)(units * T)), dim3(kPickThreads), (size_t)room * 8, st, p, room);
   return e == cudaSuccess ? NK_OK : NK_ERR_CUDA;

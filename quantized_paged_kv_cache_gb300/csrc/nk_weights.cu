@@ -437,6 +437,7 @@ struct EvictParams {
 };
 
 constexpr int kEvThreads = 512;
+constexpr int kEvPages = 16384;  // of a row of the table, at most: 12 bytes of shared memory each
 
 // A weight (the bits of a fp32 that is not NaN) in units of 2^(shift - 188), cut off
 // below; `shift` is top + c, with `top` at least the weight's exponent field. Its 24
@@ -704,7 +705,7 @@ template <int W>
 cudaError_t launch_evict(const EvictParams& p, int smem, cudaStream_t st) {
   const int sms = device_sms();
   const auto kernel = p.B > 2 * (sms > 0 ? sms : 148) ? evict_kernel<W, true> : evict_kernel<W, false>;
-  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kEvPages * 12);
   if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3((unsigned)(p.B > 0 ? p.B : 1)), dim3(kEvThreads), (size_t)smem, st, p);
 }
@@ -791,7 +792,7 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
     return NK_ERR_SHAPE;
   if (sink_pages < 0 || recent_pages < 1 || (int64_t)sink_pages + recent_pages > keep_pages) return NK_ERR_SHAPE;
   // a row of the table and its keys stay in shared memory
-  if (B > kMaxBatch || max_pages_per_seq > 16384) return NK_ERR_UNSUPPORTED;
+  if (B > kMaxBatch || max_pages_per_seq > kEvPages) return NK_ERR_UNSUPPORTED;
   // (a batch of no sequences still tells that no page went)
   if (!num_freed_dev || (B > 0 && (!weights_dev || !block_table_dev || !out_table_dev || !ctx_lens_dev || !new_ctx_dev ||
                                    (max_freed > 0 && !freed_dev))))
