@@ -461,7 +461,10 @@ int nk_page_select(const void* bounds_dev, int32_t num_pages, int32_t page_size,
  * pages, so put the ones that name no page behind the others.
  * Other arguments, checks, device flags, ordering and ownership as
  * nk_paged_decode_attn; the workspace holds nk_decode_workspace_bytes(B * T, 1,
- * ...) bytes. B * T is at most 1,024, G 48.
+ * ...) bytes. B * T is at most 1,024, G 48; at head dim 256 G is at most 40 with
+ * 112-key pages, 32 with 128, 24 with 144, 16 with 160, 8 with 176 and 192, and
+ * larger pages are refused (NK_ERR_UNSUPPORTED): the pages whose two stages fit
+ * the kernel's ring.
  */
 int nk_paged_sparse_attn(const nk_kv_pool* pool, const void* q_dev, const int32_t* block_table_dev,
                          int32_t max_pages_per_seq, const int32_t* ctx_lens_dev, const int32_t* pages_dev,

@@ -73,6 +73,7 @@ constexpr int kSmemLimit = 232448;  // opt-in shared memory per block on sm_100/
 // with fp16 scales leave two stages beside 33 to 40 rows, and a few hundred
 // bytes more would cost one of them, so the shape.
 constexpr int kStagesWhole = 8, kStagesWindow = 32;
+constexpr int kPidCache = 1024;  // page coordinates cached in shared memory per CTA
 
 struct Geometry {
   int stage_bytes;   // one page: K|V boxes, then Ks, Vs (rounded to 1 KB)
@@ -84,6 +85,7 @@ struct Geometry {
   int merge_off, merge_bytes;
   int pre_off;
   int pid_off;
+  int pids;          // page coordinates cached
   int bar_off;
   int total;
 };
@@ -135,7 +137,14 @@ __host__ __device__ inline Geometry geometry(int fmt, int D, int NT, int CS, int
   const int mrows = NT * 8;
   g.merge_bytes = mrows * (D + 4) * 4 + 3 * nteams * mrows * 4 + mrows * 4;
   const bool win = keys != kKeysAll;
-  const int pid_bytes = 1024 * 4 * (keys == kKeysLists ? 2 : 1);
+  // Lists keep two numbers of a page, so half as many pages' where a second stage needs
+  // the room (256-key pages at head dim 128, 192-key ones at 256).
+  g.pids = kPidCache;
+  if (keys == kKeysLists) {
+    const int rest = g.xch_bytes + g.merge_bytes + 1024 + round_up((2 * B + 10 + 2 * kStagesWhole) * 4, 16) + 2 * kStagesWhole * 8;
+    if ((kSmemLimit - rest - kPidCache * 8) / g.stage_bytes < 2) g.pids = kPidCache / 2;
+  }
+  const int pid_bytes = g.pids * (keys == kKeysLists ? 8 : 4);
   const int base = g.xch_bytes + g.merge_bytes + pid_bytes + 1024;
   const int park_bytes = nteams * mrows * (D + 4) * 4;
   int s = 0, pre_bytes = 0;
@@ -354,7 +363,6 @@ __device__ __forceinline__ uint32_t box_off(int P, int kv, int key, int ch16) {
 // ---------------------------------------------------------------------------
 // page loads
 // ---------------------------------------------------------------------------
-constexpr int kPidCache = 1024;  // page coordinates cached in shared memory per CTA
 
 // Coordinate z = page * Hkv + h of the CTA's page number q (-1 for a page id
 // outside the pool), from the cache or, past it, from the block table.
@@ -536,7 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   int* lens = cnt + ms;            // [B] context lengths
   int* icnt = lens + p.B;          // [ms] copies issued into each stage
   int* pid = reinterpret_cast<int*>(smem + geo.pid_off);
-  int* lpid = pid + kPidCache;  // LISTS: the entries' logical pages
+  const int pids = LISTS ? geo.pids : kPidCache;
+  int* lpid = pid + pids;  // LISTS: the entries' logical pages
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + geo.bar_off);
   uint64_t* empty_bar = full_bar + ms;
   float* xch = reinterpret_cast<float*>(smem + geo.xch_off);
@@ -817,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
   Segment seg;
   bool have = next_segment(sh, pre, x, x_end, seg);
   if (have) fetch_q(seg);
-  const int ncache = total < kPidCache ? total : kPidCache;
+  const int ncache = total < pids ? total : pids;
   for (int q = tid; q < ncache; q += kThreads) {
     if constexpr (LISTS) pid[q] = page_coord(p, sh, pre, lens, x_begin, q, lpid[q]);
     else pid[q] = page_coord(p, sh, pre, lens, x_begin, q);
@@ -905,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
       int pi = seg.page_begin + (q - seg_first);
       if constexpr (WIN) pi += pi >= lead ? gap : 0;
       if constexpr (LISTS) {
-        if (q < kPidCache) pi = lpid[q];
+        if (q < pids) pi = lpid[q];
         else (void)page_coord(p, sh, pre, lens, x_begin, q, pi);
       }
       while (q_cur < q) {  // stage and phase of page q, advanced without a division
@@ -1292,7 +1301,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const __grid_co
             if (qn < total && p.issuable(qn) && !*abort_flag) {
               // every reader arrived before its increment: the phase is complete
               if (mbar_wait(smem_u32(&empty_bar[s]), par, p.wait_cycles)) {
-                const int zn = qn < kPidCache ? pid[qn] : page_coord(p, sh, pre, lens, x_begin, qn);
+                const int zn = qn < pids ? pid[qn] : page_coord(p, sh, pre, lens, x_begin, qn);
                 if constexpr (RK)
                   issue_page_rk<D>(p, &tmap, &tmapv, zn, st, smem_u32(&full_bar[s]));
                 else
