@@ -794,15 +794,52 @@ struct SelectPlan {
   int slots, room, smem;
   int NT;
 };
+// Sixteen, which is past the portable size, where the largest instance with all of
+// its shared memory fits one of the device's groups of SMs sixteen times; else eight.
+// Without a device sixteen (nothing can be launched then).
+int largest_cluster() {
+  static std::atomic<int> known[64];  // per device; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 16;
+  }
+  if (dev >= 0 && dev < 64) {
+    const int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  const auto kernel = page_select_kernel<256, 8>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  int clusters = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kCluThreads);
+  cfg.dynamicSmemBytes = kSelSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const bool fits = set_smem_limit(fn, kSelSmem) == cudaSuccess &&
+                    cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+  if (!fits) (void)cudaGetLastError();
+  const int n = fits ? 16 : 8;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 SelectPlan plan_select(int64_t units, int T, int G, int D, int64_t pages) {
   SelectPlan s = {};
   if (T * G > kSelRows || pages > kPickKeep) return s;
   s.NT = rows_tiles(T * G);
-  // as many CTAs for each unit, up to sixteen, as leave them all resident at once
+  // as many CTAs for each unit, up to sixteen (eight where the device holds no cluster of
+  // sixteen), as leave them all resident at once
   // (one an SM: 8 verified sequences with eight each took 15.2 us, 256 CTAs in two
   // rounds), no more than there are blocks of pages for
   const int sms = device_sms();
-  s.cl = 16;
+  s.cl = largest_cluster();
   while (s.cl > 1 && units * s.cl > (sms > 0 ? sms : 148)) s.cl /= 2;
   while (s.cl > 1 && (pages + 15) / 16 <= (int64_t)s.cl / 2 * kCluWarps) s.cl /= 2;
   s.slots = cluster_slots(pages, s.cl);
