@@ -570,8 +570,9 @@ int nk_evict_pages(int32_t page_size, int32_t num_pages, int32_t num_kv_heads, c
  * sum is 2 or more, sets NK_DEVFLAG_RANGE and token -1. A draft outside the
  * vocabulary sets NK_DEVFLAG_BAD_TOKEN and is refused, a count outside 0 .. T - 1
  * NK_DEVFLAG_BAD_POS and is clamped; uniforms outside [0, 1) count as the nearest
- * inside, NaN as 0. The results must not overlap the inputs (but next_start
- * ctx_lens). T is at most 16, vocab 2^30, B 65,535.
+ * inside, NaN as 0. Results that overlap an input (but next_start ctx_lens, where
+ * they are one buffer) or each other are refused (NK_ERR_SHAPE). T is at most 16,
+ * vocab 2^30, B 65,535.
  */
 int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const float* draft_dev,
                      int64_t draft_row_stride, const int32_t* drafts_dev, const int32_t* num_drafts_dev,

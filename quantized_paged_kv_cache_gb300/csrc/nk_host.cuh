@@ -23,4 +23,14 @@ WaitLimits wait_limits();
 
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Bytes that a call reads or writes; ranges that share one.
+struct Range {
+  const void* at;
+  uint64_t bytes;
+};
+inline bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+
 }  // namespace nk

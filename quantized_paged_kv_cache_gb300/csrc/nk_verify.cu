@@ -280,8 +280,19 @@ int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const f
   if (!target_dev || !uniforms_dev || !tokens_dev || !accepted_dev || (T > 1 && !drafts_dev) ||
       (next_start_dev && !ctx_lens_dev))
     return NK_ERR_NULL;
-  // tokens and lengths are read by CTAs that others' results must not reach
-  if (tokens_dev == drafts_dev || tokens_dev == num_drafts_dev || accepted_dev == num_drafts_dev) return NK_ERR_SHAPE;
+  // all CTAs of a sequence read the inputs while one writes the results
+  const uint64_t rows = (uint64_t)B * T, drafted = (uint64_t)B * (T - 1), each = (uint64_t)B * 4;
+  const Range results[] = {{tokens_dev, rows * 4}, {accepted_dev, each}, {next_start_dev, next_start_dev ? each : 0}};
+  const Range inputs[] = {{target_dev, ((rows - 1) * target_row_stride + vocab) * 4},
+                          {draft_dev, draft_dev && T > 1 ? ((drafted - 1) * draft_row_stride + vocab) * 4 : 0},
+                          {drafts_dev, drafted * 4},
+                          {num_drafts_dev, num_drafts_dev ? each : 0},
+                          {uniforms_dev, rows * 4},
+                          {ctx_lens_dev, next_start_dev ? each : 0}};
+  for (const Range& r : results)
+    for (const Range& in : inputs)
+      if (overlap(r, in) && !(&r == &results[2] && &in == &inputs[5] && r.at == in.at)) return NK_ERR_SHAPE;
+  if (overlap(results[0], results[1]) || overlap(results[0], results[2]) || overlap(results[1], results[2])) return NK_ERR_SHAPE;
   const VerifyParams p{target_dev, draft_dev, target_row_stride, draft_row_stride, drafts_dev, num_drafts_dev,
                        uniforms_dev, ctx_lens_dev, T, vocab, tokens_dev, accepted_dev, next_start_dev, status_dev};
   constexpr int CL = 8;
