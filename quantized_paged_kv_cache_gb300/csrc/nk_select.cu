@@ -783,7 +783,8 @@ cudaError_t launch_bounds(const BoundsParams& p, int grid, cudaStream_t st) {
 }
 
 // How a call runs: in one launch where a cluster's CTA holds all rows, its keys
-// and a token's keys; else in two.
+// and a token's keys; else in two (8 sequences of 16 tokens at 4K to 64K, 96 rows: 34.3
+// us; one of 20,480 pages 58.2, where 16,384 in one launch take 30.0).
 constexpr int kSelSmem = 200 * 1024;
 int rows_tiles(int rows) {  // of the kernels' instances: 1, 2, 3, 4, 6, 8
   const int nt = (rows + 7) / 8;

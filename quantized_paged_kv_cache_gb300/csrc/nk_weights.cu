@@ -34,7 +34,6 @@ namespace nk {
 // 94 us, T = 8 149). Copies of 16 bytes a lane, which fill the queue of the memory
 // instructions, took 79, 116 and 174.
 // ---------------------------------------------------------------------------
-// ---------------------------------------------------------------------------
 constexpr int kWgtThreads = 256, kWgtWarps = kWgtThreads / 32;
 
 // A step of a warp in its ring: KB times 16 keys' codes, then their scales.
@@ -637,9 +636,12 @@ using namespace nk;
 namespace {
 
 // From how many rows on the tcgen05 kernel takes a call: past one chunk of the
-// mma.sync kernel, which would read the keys once more for each (8 sequences at 8K
-// to 64K, 24 heads over 4: 48 rows 174 us on mma.sync and 194 on tcgen05, 72 rows
-// 322 and 209, 96 rows 323 and 215, before the mma.sync kernel's 48 rows came to 149).
+// mma.sync kernel, which would read the keys once more for each. Both kernels, 8
+// sequences of 13K to 64K over 4 kv-heads, us on mma.sync / on tcgen05:
+//   rows          16           32          48       56
+//   head dim  64  62.8/114.2   71.0/115.3   93.1/119.6   -/120.5
+//            128  60.0/129.4   86.6/131.4  112.3/138.2   -/139.7
+//            256  76.4/175.1  112.1/177.1  151.9/183.9   -/185.6
 constexpr int kTcRows = 49;
 
 // Row tiles of the mma.sync kernel's instances: 1, 2, 3, 4, 6; with 16-key pages
