@@ -283,8 +283,8 @@ int nk_verify_drafts(const float* target_dev, int64_t target_row_stride, const f
   // all CTAs of a sequence read the inputs while one writes the results
   const uint64_t rows = (uint64_t)B * T, drafted = (uint64_t)B * (T - 1), each = (uint64_t)B * 4;
   const Range results[] = {{tokens_dev, rows * 4}, {accepted_dev, each}, {next_start_dev, next_start_dev ? each : 0}};
-  const Range inputs[] = {{target_dev, ((rows - 1) * target_row_stride + vocab) * 4},
-                          {draft_dev, draft_dev && T > 1 ? ((drafted - 1) * draft_row_stride + vocab) * 4 : 0},
+  const Range inputs[] = {{target_dev, (uint64_t)vocab * 4, rows, (uint64_t)target_row_stride * 4},
+                          {draft_dev, draft_dev && T > 1 ? (uint64_t)vocab * 4 : 0, drafted, (uint64_t)draft_row_stride * 4},
                           {drafts_dev, drafted * 4},
                           {num_drafts_dev, num_drafts_dev ? each : 0},
                           {uniforms_dev, rows * 4},
