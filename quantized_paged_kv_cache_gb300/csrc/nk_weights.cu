@@ -702,7 +702,7 @@ cudaError_t launch_lse_d(const WeightParams& p, cudaStream_t st) {
 }
 
 // Past two blocks an SM the third is worth more than the loads in flight (512 sequences
-// 15.4 -> 14.1 us, on a slower box 18.9 -> 14.0, where 8 would go from 9.8 to 10.2).
+// 15.4 -> 14.1 us, on a slower machine 18.9 -> 14.0, where 8 would go from 9.8 to 10.2).
 template <int W>
 cudaError_t launch_evict(const EvictParams& p, int smem, cudaStream_t st) {
   const int sms = device_sms();

@@ -1,4 +1,4 @@
-// How nk_page_select is launched on devices that hold no cluster of sixteen blocks, on the host with a fake driver.
+// How nk_page_select is launched on devices that hold no cluster of sixteen blocks, on the host with a fake CUDA runtime.
 //   cluster_check <clusters of sixteen that the device holds>: prints the cluster, the shared memory and the workspace of a
 //   few calls, and "bad" where a launch would not fit.
 #include <cooperative_groups.h>

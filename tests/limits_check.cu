@@ -1,4 +1,4 @@
-// The shared-memory limits of kernels (set_smem_limit), on the host with a fake driver: prints "good" or what is wrong.
+// The shared-memory limits of kernels (set_smem_limit), on the host with a fake CUDA runtime: prints "good" or what is wrong.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -11,7 +11,7 @@
 
 static std::atomic<int> calls{0}, device{0};
 static std::mutex mu;
-static std::map<std::pair<const void*, int>, int> limits;  // what the driver holds
+static std::map<std::pair<const void*, int>, int> limits;  // what the runtime holds
 
 static cudaError_t fake_device(int* dev) {
   *dev = device;

@@ -1,4 +1,4 @@
-// Which results nk_verify_drafts takes beside inputs whose rows lie apart, on the host with a fake driver: prints "good" or
+// Which results nk_verify_drafts takes beside inputs whose rows lie apart, on the host with a fake CUDA runtime: prints "good" or
 // what is wrong. Nothing is launched, and no pointer is followed.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

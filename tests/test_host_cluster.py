@@ -1,4 +1,4 @@
-"""How page selection is launched, against a fake driver (tests/cluster_check.cu), on the CPU."""
+"""How page selection is launched, against a fake CUDA runtime (tests/cluster_check.cu), on the CPU."""
 import os
 import subprocess
 

@@ -1,4 +1,4 @@
-"""The kernels' shared-memory limits against a fake driver (tests/limits_check.cu), on the CPU."""
+"""The kernels' shared-memory limits against a fake CUDA runtime (tests/limits_check.cu), on the CPU."""
 import os
 import subprocess
 

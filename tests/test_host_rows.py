@@ -1,4 +1,4 @@
-"""Results between the rows of strided inputs, against a fake driver (tests/rows_check.cu), on the CPU."""
+"""Results between the rows of strided inputs, against a fake CUDA runtime (tests/rows_check.cu), on the CPU."""
 import os
 import subprocess
 
